@@ -340,6 +340,185 @@ tq_status tq_f16_prompt_attn(const uint16_t *k, const uint16_t *v, int64_t n_cel
                              int n_q_heads, int n_kv_heads, int head_dim, float scale, int causal,
                              float *out, void *workspace, size_t workspace_bytes, tq_stream stream);
 
+/* ------------------------------------------------------------------------
+ * Paged 4-bit cache: K/V rows as plain 4-bit codes with a scale and an offset
+ * per row, in pages that sequences hold through block tables, with everything a
+ * serving step needs built and read on the device (lengths, block tables, slot
+ * maps), so that one captured graph serves every step.  The pages cited above
+ * have no counterpart: this is an addition of this library, next to the int8
+ * rows of tq_int8_prompt_attn.
+ *
+ * Conventions besides those at the head of this file: int32 arrays are 4-byte
+ * and int64 arrays 8-byte aligned; `max_pages` is the width of the block table
+ * (row stride in entries), entry j of a sequence's row the page of its cells
+ * j * page_size ..; entries beyond a sequence's length are never read.  Sequence
+ * lengths and row counts are read on the device when the call runs.  A workspace
+ * of these calls is 256-byte aligned, zero-filled before its first use and left
+ * ready by every call; calls of different shapes and kinds (decode, prefill,
+ * differential) may share one, one after the other, but not with calls above
+ * this section and not by calls that run at the same time.  Its status word is
+ * read by tq_workspace_status.
+ * ------------------------------------------------------------------------ */
+
+/* One paged 4-bit cache (K or V).  With D = head_dim rounded up to 64, 128 or 256:
+ *   codes   uint8    [n_pages][n_kv_heads][page_size][D / 2]
+ *           element i of a row in byte i / 2, low four bits for even i
+ *   scales  binary16 [n_pages][n_kv_heads][page_size][2]     (scale, offset)
+ * A row stands for scale * code + offset (code 0 .. 15).  head_dim is a multiple
+ * of 8, at most 256 (a dim that is not 64, 128 or 256 stores zero codes up to D);
+ * page_size a power of two, 16 .. 1024.  Cell c of the cache is row
+ * c % page_size of page c / page_size. */
+typedef struct tq_paged4 {
+  int32_t n_kv_heads;
+  int32_t head_dim;
+  int32_t page_size;
+  int32_t n_pages;
+  void *codes;         /* device */
+  void *scales;        /* device */
+} tq_paged4;
+
+/* Host only.  Bytes of the two planes.  Errors: TQ_ERR_INVALID_ARG. */
+tq_status tq_paged4_plane_bytes(int n_kv_heads, int head_dim, int page_size, int n_pages,
+                                size_t *codes_bytes, size_t *scales_bytes);
+
+/* Block tables and slot maps of a step, from request lengths: sequence s, which
+ * holds seq_len[s] cells, grows by n_new[s] cells (or shrinks by -n_new[s]: a
+ * request that ends passes -seq_len[s], rejected draft tokens their count).
+ * Pages that shrinking sequences no longer need go to the end of the free list,
+ * in the order of the sequences and of their cells; then growing sequences take
+ * theirs from its end, in the same order, into their block table rows.
+ *   new_len[s]    = seq_len[s] + n_new[s]
+ *   q_start[s]    = sum of max(n_new, 0) over the sequences before s  (n_seq + 1 values)
+ *   page_start[s] = sum of the pages taken by the sequences before s  (n_seq + 1 values)
+ *   slots[r], positions[r]  for the i-th new cell of s, r = q_start[s] + i: its cell
+ *                 in the cache (what tq_paged4_set_rows and tq_set_rows take) and
+ *                 its position seq_len[s] + i in the sequence; both -1 for the rows
+ *                 behind the last one, q_start[n_seq] <= r < n_rows
+ *   new_free_count = entries of free_pages in use afterwards (popped entries keep
+ *                 their values)
+ * new_len may be seq_len and new_free_count may be free_count (updated in place).
+ * A call that cannot be carried out -- a length below 0 or beyond
+ * max_pages * page_size before or after, more than n_rows new cells, too few free
+ * pages, a list longer than free_capacity -- changes no block table, free page or
+ * length, gives no slots (all -1, q_start and page_start 0) and stores
+ * TQ_ERR_DEVICE_CHECK in *dev_status (device int32 or NULL).
+ * All arrays device: seq_len, n_new, new_len int32 [n_seq]; block_table int32
+ * [n_seq][max_pages]; free_pages int32 [free_capacity]; free_count,
+ * new_free_count int32 [1]; q_start, page_start int32 [n_seq + 1]; slots int64
+ * [n_rows]; positions int32 [n_rows].  page_size: a power of two, 1 .. 65536.
+ * Errors: TQ_ERR_INVALID_ARG, TQ_ERR_CUDA. */
+tq_status tq_page_plan(const int32_t *seq_len, const int32_t *n_new, int n_seq, int page_size,
+                       int32_t *block_table, int max_pages, int32_t *free_pages, int64_t free_capacity,
+                       const int32_t *free_count, int32_t *new_len, int32_t *new_free_count,
+                       int32_t *q_start, int32_t *page_start, int64_t *slots, int32_t *positions,
+                       int64_t n_rows, int32_t *dev_status, tq_stream stream);
+
+/* Quantise-on-write of K and V rows, one launch.  Row r of every KV head goes to
+ * cell slots[r]:  offset = binary16(min x), scale = binary16((max x - min x) / 15),
+ * code_i = clamp(rint((x_i - offset) / scale), 0, 15), 0 where scale = 0 (ties to
+ * even, fp32).  A NaN counts as 0, magnitudes beyond 65504 as 65504.
+ * k_src  device, src_type (TQ_F32, TQ_F16, TQ_BF16): row r at element r * k_stride,
+ *        [k->n_kv_heads][k->head_dim] contiguous (v alike); 16-byte aligned, strides
+ *        multiples of 8 elements, at least a row -- slices of one projection's
+ *        output serve as they are
+ * slots  device int64 [n_rows], distinct; -1 skips the row; another slot outside
+ *        the cache skips it too and stores TQ_ERR_DEVICE_CHECK in *dev_status
+ *        (device int32 or NULL)
+ * Errors: TQ_ERR_INVALID_ARG, TQ_ERR_CUDA. */
+tq_status tq_paged4_set_rows(const tq_paged4 *k, const tq_paged4 *v, const void *k_src, int64_t k_stride,
+                             const void *v_src, int64_t v_stride, int src_type, const int64_t *slots,
+                             int64_t n_rows, int32_t *dev_status, tq_stream stream);
+
+/* The values that the cells of `slots` stand for, scale * code + offset in fp32
+ * rounded once to dst_type; rows as in tq_paged4_set_rows, a row whose slot is -1
+ * (or outside the cache, with the same report) is left as it was.
+ * Errors: TQ_ERR_INVALID_ARG, TQ_ERR_CUDA. */
+tq_status tq_paged4_get_rows(const tq_paged4 *k, const tq_paged4 *v, void *k_dst, int64_t k_stride,
+                             void *v_dst, int64_t v_stride, int dst_type, const int64_t *slots,
+                             int64_t n_rows, int32_t *dev_status, tq_stream stream);
+
+/* Bytes of workspace of the decode calls (plain and differential) for these caches,
+ * n_heads output heads and n_seq sequences; 0 if they are refused.  It depends
+ * neither on lengths nor on the number of sequences. */
+size_t tq_paged4_decode_workspace(const tq_paged4 *k, const tq_paged4 *v, int n_heads, int n_seq);
+
+/* Single-query decode of a batch over the pages:
+ *   out[s][h] = softmax_{t < seq_len[s]}(scale * q[s][h] . k_t) v_t
+ * with k_t, v_t the rows that sequence s's block table names and query head h
+ * reading KV head h / (n_q_heads / n_kv_heads).
+ * seq_len     device int32 [n_seq] (0: a zero output; a length beyond the table's
+ *             max_pages * page_size or below 0 is cut to that range and stores
+ *             TQ_ERR_DEVICE_CHECK in the workspace's status word)
+ * block_table device int32 [n_seq][max_pages]; a page id outside the cache reads
+ *             as zero rows and stores TQ_ERR_DEVICE_CHECK
+ * q           device, q_type (TQ_F16 or TQ_BF16): row s at element s * q_stride,
+ *             [n_q_heads][k->head_dim] contiguous; 16-byte aligned, q_stride a
+ *             multiple of 8
+ * out         device, q_type [n_seq][n_q_heads][v->head_dim], 16-byte aligned
+ * Stored row widths (K, V): (64, 64), (128, 128), (256, 128), (256, 256).
+ * Errors: TQ_ERR_INVALID_ARG, TQ_ERR_UNSUPPORTED (widths, q_type),
+ * TQ_ERR_WORKSPACE, TQ_ERR_CUDA. */
+tq_status tq_paged4_decode(const tq_paged4 *k, const tq_paged4 *v, const int32_t *block_table, int max_pages,
+                           const int32_t *seq_len, int n_seq, const void *q, int q_type, int64_t q_stride,
+                           int n_q_heads, float scale, void *out, void *workspace, size_t workspace_bytes,
+                           tq_stream stream);
+
+/* Bytes of workspace of the prefill calls (plain and differential) for at most
+ * n_rows query rows of n_seq sequences of at most max_len cells; 0 if refused. */
+size_t tq_paged4_prefill_workspace(const tq_paged4 *k, const tq_paged4 *v, int n_heads, int n_seq, int64_t n_rows,
+                                   int64_t max_len);
+
+/* Attention of several query rows per sequence (prompt chunks, verify batches),
+ * ragged: rows q_start[s] .. q_start[s + 1] - 1 of q are the last cells of
+ * sequence s, whose K/V rows are in the cache already:
+ *   out[r][h] = softmax_{t <= p_r}(scale * q[r][h] . k_t) v_t,
+ *   p_r = seq_len[s] - (q_start[s + 1] - q_start[s]) + (r - q_start[s]) when
+ *   causal, else every t < seq_len[s].  A row that sees no cell gets zeros.
+ * q_start  device int32 [n_seq + 1], from 0 up, at most n_rows; rows of q and out
+ *          behind q_start[n_seq] are neither read nor written.  A sequence with
+ *          rows outside 0 .. n_rows counts as without rows, and TQ_ERR_DEVICE_CHECK
+ *          is stored.
+ * n_rows   rows of q (row r at element r * q_stride) and out
+ * max_rows host: the most rows of one sequence, as far as the caller knows (0: not
+ *          known).  It only chooses the kernel.
+ * max_len  host: the longest sequence, as far as the caller knows (0: the table's
+ *          capacity).  It only chooses how many CTAs share a row's keys.
+ * Other arguments, results and errors as tq_paged4_decode; the workspace is what
+ * tq_paged4_prefill_workspace gives for the same n_rows, n_seq and max_len. */
+tq_status tq_paged4_prefill(const tq_paged4 *k, const tq_paged4 *v, const int32_t *block_table, int max_pages,
+                            const int32_t *seq_len, const int32_t *q_start, int n_seq, const void *q, int q_type,
+                            int64_t q_stride, int64_t n_rows, int n_q_heads, int64_t max_rows, int64_t max_len,
+                            float scale, int causal, void *out, void *workspace, size_t workspace_bytes,
+                            tq_stream stream);
+
+/* Differential attention, single query: two softmax maps over one set of values,
+ *   a_i = softmax_{t < seq_len[s]}(scale * q[s][2 h + i] . k_t[2 hv + i]) v_t[hv],   i = 0, 1
+ *   o   = a_0 - lambda[h] * a_1
+ *   out[s][h] = out_scale * o                                     without norm_weight,
+ *   out[s][h] = out_scale * norm_weight * o / sqrt(mean(o^2) + eps)   with it,
+ * hv = h / (n_heads / v->n_kv_heads); the mean is over the head's values.  K has
+ * two heads for each V head (2 hv and 2 hv + 1), q two for each output head.
+ * lambda      device f32 [n_heads]: the learned weights of the second map
+ * norm_weight device f32 [v->head_dim] or NULL
+ * q           [n_seq] rows of [2 n_heads][k->head_dim]
+ * out         [n_seq][n_heads][v->head_dim]
+ * Stored row widths (K, V): (64, 64), (64, 128), (128, 128), (128, 256).
+ * Other arguments, results and errors as tq_paged4_decode. */
+tq_status tq_paged4_diff_decode(const tq_paged4 *k, const tq_paged4 *v, const int32_t *block_table, int max_pages,
+                                const int32_t *seq_len, int n_seq, const void *q, int q_type, int64_t q_stride,
+                                int n_heads, const float *lambda, const float *norm_weight, float eps,
+                                float out_scale, float scale, void *out, void *workspace, size_t workspace_bytes,
+                                tq_stream stream);
+
+/* Differential attention of several query rows per sequence: rows and masks as
+ * tq_paged4_prefill, heads and result as tq_paged4_diff_decode. */
+tq_status tq_paged4_diff_prefill(const tq_paged4 *k, const tq_paged4 *v, const int32_t *block_table, int max_pages,
+                                 const int32_t *seq_len, const int32_t *q_start, int n_seq, const void *q,
+                                 int q_type, int64_t q_stride, int64_t n_rows, int n_heads, int64_t max_rows,
+                                 int64_t max_len, const float *lambda, const float *norm_weight, float eps,
+                                 float out_scale, float scale, int causal, void *out, void *workspace,
+                                 size_t workspace_bytes, tq_stream stream);
+
 /* Host only.  64-bit FNV-1a hash of n_bytes host bytes (offset basis
  * 0xcbf29ce484222325, prime 0x100000001b3), so that two builds' outputs can be
  * compared bit for bit from one printed number ([QSA#1821] "Measured": each

@@ -6,11 +6,12 @@ device memory and pass their pointers and the current CUDA stream through.
 """
 from __future__ import annotations
 
+import ctypes as C
 import math
 
 from . import _lib
 from ._lib import (TQ_BF16, TQ_DECODE_AUTO, TQ_DECODE_LUT, TQ_DECODE_MMA, TQ_F16, TQ_F32,
-                   TQ_TURBO2, TQ_TURBO3, TQ_TURBO4, TQError, tq_cache, tq_codebook)
+                   TQ_TURBO2, TQ_TURBO3, TQ_TURBO4, TQError, tq_cache, tq_codebook, tq_paged4)
 
 QS_BYTES = {2: 32, 3: 32, 4: 64}
 
@@ -184,3 +185,275 @@ def checksum(t) -> str:
     import numpy as np
     a = np.ascontiguousarray(t.detach().cpu().numpy())
     return f"{_lib.tq_checksum_fnv1a64(a.ctypes.data, a.nbytes):016x}"
+
+
+# ---- paged 4-bit cache (include/tq.h, "Paged 4-bit cache")
+
+def _need(ok, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+_ROW_TYPES: dict = {}
+
+
+def _row_type(t, what: str, dtypes=("float32", "float16", "bfloat16")) -> int:
+    """TQ_* type of a tensor of rows."""
+    if not _ROW_TYPES:
+        torch = _torch()
+        _ROW_TYPES.update({torch.float32: ("float32", TQ_F32), torch.float16: ("float16", TQ_F16),
+                           torch.bfloat16: ("bfloat16", TQ_BF16)})
+    name, code = _ROW_TYPES.get(t.dtype, ("", -1))
+    _need(name in dtypes, f"{what}: {t.dtype} is not one of {', '.join(dtypes)}")
+    return code
+
+
+def _here(device, *tensors):
+    """The call runs on the current device; every tensor has to be there."""
+    _need(device.type == "cuda" and device.index == _torch().cuda.current_device(),
+          "the cache is not on the current CUDA device")
+    for t in tensors:
+        _need(t is None or t.device == device, "tensors are on different devices")
+
+
+def _ints(t, dtype, shape, what: str):
+    _need(t.dtype == dtype and tuple(t.shape) == tuple(shape) and t.is_contiguous(),
+          f"{what}: a contiguous {dtype} tensor of shape {tuple(shape)} is expected")
+
+
+def _row_stride(t, shape, what: str) -> int:
+    """Elements between rows of t [n][heads][dim] whose rows are contiguous."""
+    _need(tuple(t.shape) == tuple(shape), f"{what}: shape {tuple(shape)} is expected, not {tuple(t.shape)}")
+    s0, s1, s2 = t.stride()
+    _need((s2 == 1 or shape[2] == 1) and (s1 == shape[2] or shape[1] == 1), f"{what}: a row's heads are contiguous")
+    return s0 if shape[0] > 1 else max(s0, shape[1] * shape[2])
+
+
+def _row_width(head_dim: int) -> int:
+    return 64 if head_dim <= 64 else 128 if head_dim <= 128 else 256
+
+
+class Paged4Cache:
+    """Planes of one paged 4-bit cache (K or V): codes [n_pages][n_kv_heads][page_size][D / 2] and
+    scales (scale, offset) [n_pages][n_kv_heads][page_size][2], D = head_dim rounded up to 64, 128 or 256."""
+
+    def __init__(self, n_kv_heads: int, head_dim: int, page_size: int, n_pages: int, device="cuda", _planes=None):
+        torch = _torch()
+        _lib.tq_paged4_plane_bytes(n_kv_heads, head_dim, page_size, n_pages)      # refuses what the library does
+        self.n_kv_heads, self.head_dim, self.page_size, self.n_pages = n_kv_heads, head_dim, page_size, n_pages
+        shape = (n_pages, n_kv_heads, page_size)
+        if _planes is None:
+            self.codes = torch.zeros((*shape, _row_width(head_dim) // 2), dtype=torch.uint8, device=device)
+            self.scales = torch.zeros((*shape, 2), dtype=torch.float16, device=device)
+        else:
+            self.codes, self.scales = _planes
+            _ints(self.codes, torch.uint8, (*shape, _row_width(head_dim) // 2), "codes")
+            _ints(self.scales, torch.float16, (*shape, 2), "scales")
+            _need(self.codes.device == self.scales.device, "tensors are on different devices")
+        self.device = self.codes.device
+        self.c = tq_paged4(n_kv_heads, head_dim, page_size, n_pages, self.codes.data_ptr(), self.scales.data_ptr())
+        self.ref = C.byref(self.c)
+
+    @classmethod
+    def from_planes(cls, codes, scales, head_dim: int):
+        """A cache over planes that exist already."""
+        n_pages, heads, page = codes.shape[:3]
+        return cls(heads, head_dim, page, n_pages, _planes=(codes, scales))
+
+
+class PagePlan:
+    """What page_plan fills: ``seq_len``, ``free_count``, ``q_start``, ``page_start``, ``slots``, ``positions``
+    (tq_page_plan in include/tq.h) for n_seq sequences and at most n_rows new cells."""
+
+    def __init__(self, n_seq: int, n_rows: int, device="cuda"):
+        torch = _torch()
+        i32 = lambda n: torch.zeros((n,), dtype=torch.int32, device=device)  # noqa: E731
+        self.n_seq, self.n_rows = n_seq, n_rows
+        self.seq_len, self.free_count = i32(n_seq), i32(1)
+        self.q_start, self.page_start = i32(n_seq + 1), i32(n_seq + 1)
+        self.slots = torch.full((n_rows,), -1, dtype=torch.int64, device=device)
+        self.positions = i32(n_rows)
+        self.device = self.slots.device
+        self._out = (self.q_start.data_ptr(), self.page_start.data_ptr(), self.slots.data_ptr(),
+                     self.positions.data_ptr())
+
+
+def page_plan(seq_len, n_new, page_size: int, block_table, free_pages, free_count, plan: PagePlan | None = None,
+              n_rows: int | None = None, in_place: bool = False, dev_status=None, stream=None) -> PagePlan:
+    """Pages, slots and positions of a step's new cells (tq_page_plan).  The block table and the free list are
+    updated; lengths and the free count go to ``plan``, or with ``in_place`` to seq_len and free_count themselves."""
+    torch = _torch()
+    n_seq, i32 = seq_len.shape[0], torch.int32
+    if plan is None:
+        _need(n_rows is not None, "page_plan needs a plan or n_rows")
+        plan = PagePlan(n_seq, n_rows, seq_len.device)
+    _need(plan.n_seq == n_seq, "the plan is for another number of sequences")
+    _ints(seq_len, i32, (n_seq,), "seq_len")
+    _ints(n_new, i32, (n_seq,), "n_new")
+    _need(block_table.dim() == 2 and block_table.shape[1] > 0, "block_table: [n_seq][max_pages]")
+    _ints(block_table, i32, (n_seq, block_table.shape[1]), "block_table")
+    _need(free_pages.dim() == 1, "free_pages: one dimension")
+    _ints(free_pages, i32, free_pages.shape, "free_pages")
+    _ints(free_count, i32, (1,), "free_count")
+    if dev_status is not None:
+        _ints(dev_status, i32, (1,), "dev_status")
+    _here(plan.device, seq_len, n_new, block_table, free_pages, free_count, dev_status)
+    st = _lib.tq_page_plan(seq_len.data_ptr(), n_new.data_ptr(), n_seq, page_size, block_table.data_ptr(),
+                           block_table.shape[1], free_pages.data_ptr(), free_pages.shape[0], free_count.data_ptr(),
+                           (seq_len if in_place else plan.seq_len).data_ptr(),
+                           (free_count if in_place else plan.free_count).data_ptr(), *plan._out, plan.n_rows,
+                           None if dev_status is None else dev_status.data_ptr(), _stream(stream))
+    _lib.check("tq_page_plan", st)
+    return plan
+
+
+def paged4_set_rows(kc: Paged4Cache, vc: Paged4Cache, k_src, v_src, slots, dev_status=None, stream=None):
+    """Quantise rows k_src, v_src [n][n_kv_heads][head_dim] (rows may be strided) into cells ``slots``
+    (device int64 [n]; -1: not stored)."""
+    n = slots.shape[0]
+    t = _row_type(k_src, "k_src")
+    _need(v_src.dtype == k_src.dtype, "k_src and v_src have different types")
+    _ints(slots, _torch().int64, (n,), "slots")
+    ks = _row_stride(k_src, (n, kc.n_kv_heads, kc.head_dim), "k_src")
+    vs = _row_stride(v_src, (n, vc.n_kv_heads, vc.head_dim), "v_src")
+    _here(kc.device, vc.codes, k_src, v_src, slots, dev_status)
+    st = _lib.tq_paged4_set_rows(kc.ref, vc.ref, k_src.data_ptr(), ks, v_src.data_ptr(), vs, t, slots.data_ptr(), n,
+                                 None if dev_status is None else dev_status.data_ptr(), _stream(stream))
+    _lib.check("tq_paged4_set_rows", st)
+
+
+def paged4_get_rows(kc: Paged4Cache, vc: Paged4Cache, slots, dtype=None, k_out=None, v_out=None, dev_status=None,
+                    stream=None):
+    """The values that cells ``slots`` stand for: (k, v) [n][n_kv_heads][head_dim] of ``dtype`` (default float16),
+    or in k_out and v_out (rows may be strided).  Rows whose slot is -1 stay as they were (new outputs: zeros)."""
+    torch = _torch()
+    n = slots.shape[0]
+    dtype = dtype or (k_out.dtype if k_out is not None else torch.float16)
+    if k_out is None:
+        k_out = torch.zeros((n, kc.n_kv_heads, kc.head_dim), dtype=dtype, device=slots.device)
+    if v_out is None:
+        v_out = torch.zeros((n, vc.n_kv_heads, vc.head_dim), dtype=dtype, device=slots.device)
+    t = _row_type(k_out, "k_out")
+    _need(v_out.dtype == k_out.dtype == dtype, "k_out, v_out and dtype differ")
+    _ints(slots, torch.int64, (n,), "slots")
+    ks = _row_stride(k_out, (n, kc.n_kv_heads, kc.head_dim), "k_out")
+    vs = _row_stride(v_out, (n, vc.n_kv_heads, vc.head_dim), "v_out")
+    _here(kc.device, vc.codes, k_out, v_out, slots, dev_status)
+    st = _lib.tq_paged4_get_rows(kc.ref, vc.ref, k_out.data_ptr(), ks, v_out.data_ptr(), vs, t, slots.data_ptr(), n,
+                                 None if dev_status is None else dev_status.data_ptr(), _stream(stream))
+    _lib.check("tq_paged4_get_rows", st)
+    return k_out, v_out
+
+
+def paged4_decode_workspace(kc: Paged4Cache, vc: Paged4Cache, n_heads: int, n_seq: int) -> int:
+    """Bytes of workspace of paged4_decode and, where K has two heads per V head, paged4_diff_decode."""
+    return _lib.tq_paged4_decode_workspace(kc.ref, vc.ref, n_heads, n_seq)
+
+
+def paged4_prefill_workspace(kc: Paged4Cache, vc: Paged4Cache, n_heads: int, n_seq: int, n_rows: int,
+                             max_len: int) -> int:
+    """Bytes of workspace of paged4_prefill and, where K has two heads per V head, paged4_diff_prefill."""
+    return _lib.tq_paged4_prefill_workspace(kc.ref, vc.ref, n_heads, n_seq, n_rows, max_len)
+
+
+def _paged4_args(kc, vc, block_table, seq_len, q, maps, out, extra=()):
+    """Checks shared by the attention calls -> (n_seq, max_pages, q type, q stride, output heads, out)."""
+    torch = _torch()
+    _need(block_table.dim() == 2 and block_table.shape[1] > 0, "block_table: [n_seq][max_pages]")
+    n_seq, max_pages = block_table.shape
+    _ints(block_table, torch.int32, (n_seq, max_pages), "block_table")
+    _ints(seq_len, torch.int32, (n_seq,), "seq_len")
+    t = _row_type(q, "q", ("float16", "bfloat16"))
+    _need(q.dim() == 3 and q.shape[1] % maps == 0, "q: [rows][heads][head_dim]")
+    rows, heads = q.shape[0], q.shape[1] // maps
+    stride = _row_stride(q, (rows, heads * maps, kc.head_dim), "q")
+    if out is None:
+        out = torch.empty((rows, heads, vc.head_dim), dtype=q.dtype, device=q.device)
+    else:
+        _ints(out, q.dtype, (rows, heads, vc.head_dim), "out")
+    _here(kc.device, vc.codes, block_table, seq_len, q, out, *extra)
+    return n_seq, max_pages, t, stride, heads, out
+
+
+def _diff_args(vc, heads, lam, norm_weight):
+    torch = _torch()
+    _ints(lam, torch.float32, (heads,), "lam")
+    if norm_weight is not None:
+        _ints(norm_weight, torch.float32, (vc.head_dim,), "norm_weight")
+    return lam.data_ptr(), None if norm_weight is None else norm_weight.data_ptr()
+
+
+def paged4_decode(kc: Paged4Cache, vc: Paged4Cache, block_table, seq_len, q, scale: float | None = None, out=None,
+                  ws=None, stream=None):
+    """One query row per sequence: q [n_seq][n_q_heads][Dk] (float16 or bfloat16, rows may be strided) over the
+    seq_len[s] cells (device int32) of block_table[s] -> [n_seq][n_q_heads][Dv] of q's type."""
+    n_seq, max_pages, t, stride, heads, out = _paged4_args(kc, vc, block_table, seq_len, q, 1, out, (ws,))
+    _need(q.shape[0] == n_seq, "q: one row per sequence")
+    scale = 1.0 / math.sqrt(kc.head_dim) if scale is None else scale
+    if ws is None:
+        ws = workspace(paged4_decode_workspace(kc, vc, heads, n_seq), q.device)
+    st = _lib.tq_paged4_decode(kc.ref, vc.ref, block_table.data_ptr(), max_pages, seq_len.data_ptr(), n_seq,
+                               q.data_ptr(), t, stride, heads, scale, out.data_ptr(), ws.data_ptr(), ws.numel(),
+                               _stream(stream))
+    _lib.check("tq_paged4_decode", st)
+    return out
+
+
+def paged4_prefill(kc: Paged4Cache, vc: Paged4Cache, block_table, seq_len, q, q_start, scale: float | None = None,
+                   causal: bool = True, max_rows: int = 0, max_len: int | None = None, out=None, ws=None,
+                   stream=None):
+    """Several query rows per sequence: rows q_start[s] .. q_start[s + 1] - 1 (device int32 [n_seq + 1]) of q
+    [n_rows][n_q_heads][Dk] are the last cells of sequence s.  max_rows and max_len (host): the most rows and cells
+    of one sequence, where known; they only choose the kernel.  A workspace for the call is
+    paged4_prefill_workspace(..., n_rows, max_len or the block table's capacity)."""
+    n_seq, max_pages, t, stride, heads, out = _paged4_args(kc, vc, block_table, seq_len, q, 1, out, (q_start, ws))
+    _ints(q_start, _torch().int32, (n_seq + 1,), "q_start")
+    scale = 1.0 / math.sqrt(kc.head_dim) if scale is None else scale
+    n_rows, max_len = q.shape[0], max_len or max_pages * kc.page_size
+    if ws is None:
+        ws = workspace(paged4_prefill_workspace(kc, vc, heads, n_seq, n_rows, max_len), q.device)
+    st = _lib.tq_paged4_prefill(kc.ref, vc.ref, block_table.data_ptr(), max_pages, seq_len.data_ptr(),
+                                q_start.data_ptr(), n_seq, q.data_ptr(), t, stride, n_rows, heads, max_rows, max_len,
+                                scale, int(causal), out.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream))
+    _lib.check("tq_paged4_prefill", st)
+    return out
+
+
+def paged4_diff_decode(kc: Paged4Cache, vc: Paged4Cache, block_table, seq_len, q, lam, scale: float | None = None,
+                       norm_weight=None, eps: float = 1e-5, out_scale: float = 1.0, out=None, ws=None, stream=None):
+    """Differential attention, one query row per sequence: q [n_seq][2 n_heads][Dk], K with two heads per V head,
+    lam (device float32 [n_heads]) the weights of the second map; optional RMS norm over each head's output."""
+    n_seq, max_pages, t, stride, heads, out = _paged4_args(kc, vc, block_table, seq_len, q, 2, out,
+                                                           (lam, norm_weight, ws))
+    _need(q.shape[0] == n_seq, "q: one row per sequence")
+    lam_p, norm_p = _diff_args(vc, heads, lam, norm_weight)
+    scale = 1.0 / math.sqrt(kc.head_dim) if scale is None else scale
+    if ws is None:
+        ws = workspace(paged4_decode_workspace(kc, vc, heads, n_seq), q.device)
+    st = _lib.tq_paged4_diff_decode(kc.ref, vc.ref, block_table.data_ptr(), max_pages, seq_len.data_ptr(), n_seq,
+                                    q.data_ptr(), t, stride, heads, lam_p, norm_p, eps, out_scale, scale,
+                                    out.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream))
+    _lib.check("tq_paged4_diff_decode", st)
+    return out
+
+
+def paged4_diff_prefill(kc: Paged4Cache, vc: Paged4Cache, block_table, seq_len, q, q_start, lam,
+                        scale: float | None = None, norm_weight=None, eps: float = 1e-5, out_scale: float = 1.0,
+                        causal: bool = True, max_rows: int = 0, max_len: int | None = None, out=None, ws=None,
+                        stream=None):
+    """Differential attention of several query rows per sequence: rows as paged4_prefill, heads as
+    paged4_diff_decode."""
+    n_seq, max_pages, t, stride, heads, out = _paged4_args(kc, vc, block_table, seq_len, q, 2, out,
+                                                           (q_start, lam, norm_weight, ws))
+    _ints(q_start, _torch().int32, (n_seq + 1,), "q_start")
+    lam_p, norm_p = _diff_args(vc, heads, lam, norm_weight)
+    scale = 1.0 / math.sqrt(kc.head_dim) if scale is None else scale
+    n_rows, max_len = q.shape[0], max_len or max_pages * kc.page_size
+    if ws is None:
+        ws = workspace(paged4_prefill_workspace(kc, vc, heads, n_seq, n_rows, max_len), q.device)
+    st = _lib.tq_paged4_diff_prefill(kc.ref, vc.ref, block_table.data_ptr(), max_pages, seq_len.data_ptr(),
+                                     q_start.data_ptr(), n_seq, q.data_ptr(), t, stride, n_rows, heads, max_rows,
+                                     max_len, lam_p, norm_p, eps, out_scale, scale, int(causal), out.data_ptr(),
+                                     ws.data_ptr(), ws.numel(), _stream(stream))
+    _lib.check("tq_paged4_diff_prefill", st)
+    return out

@@ -36,6 +36,11 @@ class tq_cache(C.Structure):
                 ("qs", C.c_void_p), ("signs", C.c_void_p)]
 
 
+class tq_paged4(C.Structure):
+    _fields_ = [("n_kv_heads", C.c_int32), ("head_dim", C.c_int32), ("page_size", C.c_int32),
+                ("n_pages", C.c_int32), ("codes", C.c_void_p), ("scales", C.c_void_p)]
+
+
 class TQError(RuntimeError):
     def __init__(self, fn: str, status: int):
         self.status = status
@@ -92,6 +97,28 @@ _SIGS = {
     "tq_fattn_decode_batch": (C.c_int, [C.POINTER(tq_cache), C.POINTER(tq_cache), C.POINTER(tq_codebook),
                                         C.POINTER(tq_codebook), _P, C.c_int, C.c_int, C.POINTER(C.c_int64),
                                         C.POINTER(C.c_int64), C.c_float, C.c_int, _P, _P, C.c_size_t, _P]),
+    "tq_paged4_plane_bytes": (C.c_int, [C.c_int, C.c_int, C.c_int, C.c_int, C.POINTER(C.c_size_t),
+                                        C.POINTER(C.c_size_t)]),
+    "tq_page_plan": (C.c_int, [_P, _P, C.c_int, C.c_int, _P, C.c_int, _P, C.c_int64, _P, _P, _P, _P, _P, _P, _P,
+                               C.c_int64, _P, _P]),
+    "tq_paged4_set_rows": (C.c_int, [C.POINTER(tq_paged4), C.POINTER(tq_paged4), _P, C.c_int64, _P, C.c_int64,
+                                     C.c_int, _P, C.c_int64, _P, _P]),
+    "tq_paged4_get_rows": (C.c_int, [C.POINTER(tq_paged4), C.POINTER(tq_paged4), _P, C.c_int64, _P, C.c_int64,
+                                     C.c_int, _P, C.c_int64, _P, _P]),
+    "tq_paged4_decode_workspace": (C.c_size_t, [C.POINTER(tq_paged4), C.POINTER(tq_paged4), C.c_int, C.c_int]),
+    "tq_paged4_decode": (C.c_int, [C.POINTER(tq_paged4), C.POINTER(tq_paged4), _P, C.c_int, _P, C.c_int, _P, C.c_int,
+                                   C.c_int64, C.c_int, C.c_float, _P, _P, C.c_size_t, _P]),
+    "tq_paged4_prefill_workspace": (C.c_size_t, [C.POINTER(tq_paged4), C.POINTER(tq_paged4), C.c_int, C.c_int,
+                                                 C.c_int64, C.c_int64]),
+    "tq_paged4_prefill": (C.c_int, [C.POINTER(tq_paged4), C.POINTER(tq_paged4), _P, C.c_int, _P, _P, C.c_int, _P,
+                                    C.c_int, C.c_int64, C.c_int64, C.c_int, C.c_int64, C.c_int64, C.c_float, C.c_int,
+                                    _P, _P, C.c_size_t, _P]),
+    "tq_paged4_diff_decode": (C.c_int, [C.POINTER(tq_paged4), C.POINTER(tq_paged4), _P, C.c_int, _P, C.c_int, _P,
+                                        C.c_int, C.c_int64, C.c_int, _P, _P, C.c_float, C.c_float, C.c_float, _P, _P,
+                                        C.c_size_t, _P]),
+    "tq_paged4_diff_prefill": (C.c_int, [C.POINTER(tq_paged4), C.POINTER(tq_paged4), _P, C.c_int, _P, _P, C.c_int, _P,
+                                         C.c_int, C.c_int64, C.c_int64, C.c_int, C.c_int64, C.c_int64, _P, _P,
+                                         C.c_float, C.c_float, C.c_float, C.c_int, _P, _P, C.c_size_t, _P]),
     # test hook (include/tq_testing.h)
     "tq_testing_decode_drop_split": (C.c_int, [C.POINTER(tq_cache), C.POINTER(tq_cache), C.POINTER(tq_codebook),
                                                C.POINTER(tq_codebook), _P, C.c_int, C.c_int64, C.c_float, C.c_int,
@@ -245,3 +272,23 @@ def tq_fattn_decode_batch(k: tq_cache, v: tq_cache, cbk: tq_codebook, cbv: tq_co
     ln = (C.c_int64 * n)(*[int(x) for x in seq_len])
     return lib.tq_fattn_decode_batch(C.byref(k), C.byref(v), C.byref(cbk), C.byref(cbv), q, n_q_heads, n, c0, ln,
                                      scale, algo, out, ws, ws_bytes, stream)
+
+
+def tq_paged4_plane_bytes(n_kv_heads: int, head_dim: int, page_size: int, n_pages: int):
+    a, b = C.c_size_t(), C.c_size_t()
+    check("tq_paged4_plane_bytes", lib.tq_paged4_plane_bytes(n_kv_heads, head_dim, page_size, n_pages, C.byref(a),
+                                                             C.byref(b)))
+    return a.value, b.value
+
+
+# The paged 4-bit calls take the caches as references (``C.byref`` of a tq_paged4, made
+# once per cache) and pass everything else through.
+tq_page_plan = lib.tq_page_plan
+tq_paged4_set_rows = lib.tq_paged4_set_rows
+tq_paged4_get_rows = lib.tq_paged4_get_rows
+tq_paged4_decode_workspace = lib.tq_paged4_decode_workspace
+tq_paged4_decode = lib.tq_paged4_decode
+tq_paged4_prefill_workspace = lib.tq_paged4_prefill_workspace
+tq_paged4_prefill = lib.tq_paged4_prefill
+tq_paged4_diff_decode = lib.tq_paged4_diff_decode
+tq_paged4_diff_prefill = lib.tq_paged4_diff_prefill

@@ -1,0 +1,307 @@
+// Host side of the paged 4-bit cache's C ABI: argument checks, workspace layout
+// and the choice of kernel.  Nothing here allocates or synchronises.
+#include <math.h>
+#include <string.h>
+
+#include "tq_paged4.cuh"
+
+namespace tq {
+namespace p4 {
+
+cudaError_t launch_few_plain(const AttnArgs &a, int columns, cudaStream_t s);
+cudaError_t launch_few_wide(const AttnArgs &a, int columns, cudaStream_t s);
+cudaError_t launch_few_diff(const AttnArgs &a, cudaStream_t s);
+
+cudaError_t launch_few(const AttnArgs &a, int columns, cudaStream_t s) {
+  if (a.diff) return launch_few_diff(a, s);
+  return a.wk == 256 ? launch_few_wide(a, columns, s) : launch_few_plain(a, columns, s);
+}
+
+static bool al(const void *p, uintptr_t n) { return p && (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+static size_t up(size_t x, size_t n) { return (x + n - 1) / n * n; }
+
+static int shift_of(int page_size, int lo, int hi) {
+  if (page_size < lo || page_size > hi || (page_size & (page_size - 1))) return -1;
+  int s = 0;
+  while ((1 << s) < page_size) ++s;
+  return s;
+}
+
+static bool shape_ok(int n_kv_heads, int head_dim, int page_size, int n_pages) {
+  return n_kv_heads > 0 && n_kv_heads <= 65536 && head_dim % 8 == 0 && row_width(head_dim) > 0 &&
+         shift_of(page_size, 16, 1024) >= 0 && n_pages > 0;
+}
+
+static bool cache_ok(const tq_paged4 *c) {
+  return c && shape_ok(c->n_kv_heads, c->head_dim, c->page_size, c->n_pages) && al(c->codes, 16) &&
+         al(c->scales, 16);
+}
+
+static bool pair_ok(const tq_paged4 *k, const tq_paged4 *v) {
+  return cache_ok(k) && cache_ok(v) && k->page_size == v->page_size && k->n_pages == v->n_pages;
+}
+
+static tq_status mapped(cudaError_t e) {
+  if (e == cudaSuccess) return TQ_OK;
+  cudaGetLastError();                 // the status reports it; leave no stale error behind
+  return TQ_ERR_CUDA;
+}
+
+// Shape checks common to the attention calls; `diff` from the caller.
+static tq_status heads_ok(const tq_paged4 *k, const tq_paged4 *v, int n_heads, int n_seq, bool diff) {
+  if (!pair_ok(k, v) || n_seq < 0 || n_seq > (1 << 24)) return TQ_ERR_INVALID_ARG;
+  if (k->n_kv_heads != (diff ? 2 : 1) * v->n_kv_heads) return TQ_ERR_INVALID_ARG;
+  if (n_heads <= 0 || n_heads > 65536 || n_heads % v->n_kv_heads) return TQ_ERR_INVALID_ARG;
+  return few_supported(row_width(k->head_dim), row_width(v->head_dim), diff) ? TQ_OK : TQ_ERR_UNSUPPORTED;
+}
+
+bool few_supported(int wk, int wv, bool diff) {
+  if (diff) return (wk == 64 && wv <= 128) || (wk == 128 && (wv == 128 || wv == 256));
+  return (wk == wv) || (wk == 256 && wv == 128);
+}
+
+// Workspace: status word, arrival counters (one per CTA, in a place that does not
+// depend on the shape, so that calls of different shapes can share it), partials.
+constexpr size_t kCountersOff = 256;
+struct Layout {
+  size_t part_off, total;
+};
+
+static Layout few_layout(int wv, bool diff) {
+  Layout L;
+  const size_t ctas = 2 * static_cast<size_t>(sm_count());         // at most two per SM
+  const size_t columns = 16, tiles = 2;                            // the larger of the two column widths
+  L.part_off = kCountersOff + up(sizeof(int32_t) * ctas, 256);
+  L.total = L.part_off + sizeof(float) * 2 * ctas * (4 * columns + tiles * (wv / 16) * 128);
+  (void)diff;
+  return L;
+}
+
+struct Call {
+  const tq_paged4 *k, *v;
+  const int32_t *block_table, *seq_len, *q_start;
+  const void *q;
+  const float *lam, *norm_weight;
+  void *out, *workspace;
+  size_t workspace_bytes;
+  int64_t q_stride, n_rows, max_rows, max_len;
+  int max_pages, n_seq, q_type, n_heads, causal;
+  float scale, eps, out_scale;
+  bool diff, ragged;
+  tq_stream stream;
+};
+
+static tq_status attend(const Call &c) {
+  tq_status st = heads_ok(c.k, c.v, c.n_heads, c.n_seq, c.diff);
+  if (st != TQ_OK) return st;
+  if (c.q_type == TQ_F32) return TQ_ERR_UNSUPPORTED;
+  if (c.q_type != TQ_F16 && c.q_type != TQ_BF16) return TQ_ERR_INVALID_ARG;
+  if (!isfinite(c.scale) || c.max_pages <= 0 || c.n_rows < 0 || c.max_rows < 0 || c.max_len < 0)
+    return TQ_ERR_INVALID_ARG;
+  if (c.diff && (!al(c.lam, 4) || (c.norm_weight && !al(c.norm_weight, 4)) || !isfinite(c.eps) || c.eps < 0.f ||
+                 !isfinite(c.out_scale)))
+    return TQ_ERR_INVALID_ARG;
+  const int64_t row = static_cast<int64_t>(c.diff ? 2 : 1) * c.n_heads * c.k->head_dim;
+  if (c.q_stride < row || c.q_stride % 8) return TQ_ERR_INVALID_ARG;
+  if (c.n_rows * (c.n_heads / c.v->n_kv_heads) > 0x7fffffffLL) return TQ_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(c.max_pages) * c.k->page_size > 0x7fffffffLL) return TQ_ERR_INVALID_ARG;
+  if (c.n_seq == 0 || c.n_rows == 0) return TQ_OK;
+  if (!al(c.block_table, 4) || !al(c.seq_len, 4) || (c.ragged && !al(c.q_start, 4)) || !al(c.q, 16) || !al(c.out, 16))
+    return TQ_ERR_INVALID_ARG;
+  const int wk = row_width(c.k->head_dim), wv = row_width(c.v->head_dim);
+  const Layout L = few_layout(wv, c.diff);
+  if (!al(c.workspace, 256) || c.workspace_bytes < L.total) return TQ_ERR_WORKSPACE;
+  AttnArgs a;
+  memset(&a, 0, sizeof(a));
+  a.k_codes = static_cast<const uint8_t *>(c.k->codes);
+  a.k_scales = static_cast<const uint16_t *>(c.k->scales);
+  a.v_codes = static_cast<const uint8_t *>(c.v->codes);
+  a.v_scales = static_cast<const uint16_t *>(c.v->scales);
+  a.block_table = c.block_table;
+  a.seq_len = c.seq_len;
+  a.q_start = c.ragged ? c.q_start : nullptr;
+  a.q = c.q;
+  a.out = c.out;
+  a.lam = c.lam;
+  a.norm_weight = c.norm_weight;
+  a.status = static_cast<int32_t *>(c.workspace);
+  a.counters = reinterpret_cast<int32_t *>(static_cast<char *>(c.workspace) + kCountersOff);
+  a.part = reinterpret_cast<float *>(static_cast<char *>(c.workspace) + L.part_off);
+  a.q_stride = c.q_stride;
+  a.n_rows = c.n_rows;
+  a.n_seq = c.n_seq;
+  a.max_pages = c.max_pages;
+  a.n_pages = c.k->n_pages;
+  a.page_shift = shift_of(c.k->page_size, 16, 1024);
+  a.n_heads = c.n_heads;
+  a.n_kv_heads = c.v->n_kv_heads;
+  a.group = c.n_heads / c.v->n_kv_heads;
+  a.dk = c.k->head_dim;
+  a.dv = c.v->head_dim;
+  a.wk = wk;
+  a.wv = wv;
+  a.bf16 = c.q_type == TQ_BF16;
+  a.causal = c.causal ? 1 : 0;
+  a.diff = c.diff;
+  a.scale_log2 = c.scale * 1.4426950408889634f;
+  a.eps = c.eps;
+  a.out_scale = c.out_scale;
+  const int64_t rows = c.ragged ? (c.max_rows ? c.max_rows : c.n_rows) : 1;
+  const int columns = rows * a.group > 8 ? 16 : 8;
+  return mapped(launch_few(a, columns, static_cast<cudaStream_t>(c.stream)));
+}
+
+static bool is_diff(const tq_paged4 *k, const tq_paged4 *v) { return k && v && k->n_kv_heads != v->n_kv_heads; }
+
+}  // namespace p4
+}  // namespace tq
+
+using namespace tq;
+using namespace tq::p4;
+
+extern "C" {
+
+tq_status tq_paged4_plane_bytes(int n_kv_heads, int head_dim, int page_size, int n_pages, size_t *codes_bytes,
+                                size_t *scales_bytes) {
+  if (!shape_ok(n_kv_heads, head_dim, page_size, n_pages) || !codes_bytes || !scales_bytes) return TQ_ERR_INVALID_ARG;
+  const size_t rows = static_cast<size_t>(n_pages) * n_kv_heads * page_size;
+  *codes_bytes = rows * (row_width(head_dim) / 2);
+  *scales_bytes = rows * 4;
+  return TQ_OK;
+}
+
+tq_status tq_page_plan(const int32_t *seq_len, const int32_t *n_new, int n_seq, int page_size, int32_t *block_table,
+                       int max_pages, int32_t *free_pages, int64_t free_capacity, const int32_t *free_count,
+                       int32_t *new_len, int32_t *new_free_count, int32_t *q_start, int32_t *page_start,
+                       int64_t *slots, int32_t *positions, int64_t n_rows, int32_t *dev_status, tq_stream stream) {
+  PlanArgs a;
+  a.page_shift = shift_of(page_size, 1, 65536);
+  if (a.page_shift < 0 || n_seq < 0 || max_pages <= 0 || free_capacity < 0 || free_capacity > 0x7fffffffLL ||
+      n_rows < 0 || n_rows > 0x7fffffffLL - 1)
+    return TQ_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(max_pages) * page_size > 0x7fffffffLL) return TQ_ERR_INVALID_ARG;
+  if (!al(free_count, 4) || !al(new_free_count, 4) || !al(q_start, 4) || !al(page_start, 4)) return TQ_ERR_INVALID_ARG;
+  if (n_seq > 0 && (!al(seq_len, 4) || !al(n_new, 4) || !al(block_table, 4) || !al(new_len, 4)))
+    return TQ_ERR_INVALID_ARG;
+  if (free_capacity > 0 && !al(free_pages, 4)) return TQ_ERR_INVALID_ARG;
+  if (n_rows > 0 && (!al(slots, 8) || !al(positions, 4))) return TQ_ERR_INVALID_ARG;
+  if (dev_status && !al(dev_status, 4)) return TQ_ERR_INVALID_ARG;
+  a.seq_len = seq_len;
+  a.n_new = n_new;
+  a.block_table = block_table;
+  a.free_pages = free_pages;
+  a.free_count = free_count;
+  a.new_len = new_len;
+  a.new_free_count = new_free_count;
+  a.q_start = q_start;
+  a.page_start = page_start;
+  a.slots = slots;
+  a.positions = positions;
+  a.status = dev_status;
+  a.n_rows = n_rows;
+  a.free_capacity = free_capacity;
+  a.n_seq = n_seq;
+  a.max_pages = max_pages;
+  return mapped(launch_page_plan(a, static_cast<cudaStream_t>(stream)));
+}
+
+static tq_status rows_call(bool set, const tq_paged4 *k, const tq_paged4 *v, const void *kp, int64_t k_stride,
+                           const void *vp, int64_t v_stride, int type, const int64_t *slots, int64_t n_rows,
+                           int32_t *dev_status, tq_stream stream) {
+  if (!pair_ok(k, v)) return TQ_ERR_INVALID_ARG;
+  if (type != TQ_F32 && type != TQ_F16 && type != TQ_BF16) return TQ_ERR_INVALID_ARG;
+  if (n_rows < 0 || k_stride % 8 || v_stride % 8 || k_stride < static_cast<int64_t>(k->n_kv_heads) * k->head_dim ||
+      v_stride < static_cast<int64_t>(v->n_kv_heads) * v->head_dim)
+    return TQ_ERR_INVALID_ARG;
+  if (n_rows == 0) return TQ_OK;
+  if (!al(kp, 16) || !al(vp, 16) || !al(slots, 8) || (dev_status && !al(dev_status, 4))) return TQ_ERR_INVALID_ARG;
+  if (n_rows > 0x7fffffffLL || n_rows * (k->n_kv_heads + v->n_kv_heads) > 0xfffffffffLL) return TQ_ERR_INVALID_ARG;
+  RowsArgs a;
+  const tq_paged4 *c[2] = {k, v};
+  const void *p[2] = {kp, vp};
+  const int64_t stride[2] = {k_stride, v_stride};
+  for (int i = 0; i < 2; ++i) {
+    a.src[i] = p[i];
+    a.dst[i] = const_cast<void *>(p[i]);
+    a.codes[i] = static_cast<uint8_t *>(c[i]->codes);
+    a.scales[i] = static_cast<uint16_t *>(c[i]->scales);
+    a.stride[i] = stride[i];
+    a.n_heads[i] = c[i]->n_kv_heads;
+    a.head_dim[i] = c[i]->head_dim;
+    a.width[i] = row_width(c[i]->head_dim);
+  }
+  a.slots = slots;
+  a.status = dev_status;
+  a.n_rows = n_rows;
+  a.page_shift = shift_of(k->page_size, 16, 1024);
+  a.n_cells = static_cast<int64_t>(k->n_pages) << a.page_shift;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return mapped(set ? launch_set_rows(type, a, s) : launch_get_rows(type, a, s));
+}
+
+tq_status tq_paged4_set_rows(const tq_paged4 *k, const tq_paged4 *v, const void *k_src, int64_t k_stride,
+                             const void *v_src, int64_t v_stride, int src_type, const int64_t *slots, int64_t n_rows,
+                             int32_t *dev_status, tq_stream stream) {
+  return rows_call(true, k, v, k_src, k_stride, v_src, v_stride, src_type, slots, n_rows, dev_status, stream);
+}
+
+tq_status tq_paged4_get_rows(const tq_paged4 *k, const tq_paged4 *v, void *k_dst, int64_t k_stride, void *v_dst,
+                             int64_t v_stride, int dst_type, const int64_t *slots, int64_t n_rows,
+                             int32_t *dev_status, tq_stream stream) {
+  return rows_call(false, k, v, k_dst, k_stride, v_dst, v_stride, dst_type, slots, n_rows, dev_status, stream);
+}
+
+size_t tq_paged4_decode_workspace(const tq_paged4 *k, const tq_paged4 *v, int n_heads, int n_seq) {
+  if (heads_ok(k, v, n_heads, n_seq, is_diff(k, v)) != TQ_OK) return 0;
+  return few_layout(row_width(v->head_dim), is_diff(k, v)).total;
+}
+
+size_t tq_paged4_prefill_workspace(const tq_paged4 *k, const tq_paged4 *v, int n_heads, int n_seq, int64_t n_rows,
+                                   int64_t max_len) {
+  if (heads_ok(k, v, n_heads, n_seq, is_diff(k, v)) != TQ_OK || n_rows < 0 || max_len < 0) return 0;
+  return few_layout(row_width(v->head_dim), is_diff(k, v)).total;
+}
+
+tq_status tq_paged4_decode(const tq_paged4 *k, const tq_paged4 *v, const int32_t *block_table, int max_pages,
+                           const int32_t *seq_len, int n_seq, const void *q, int q_type, int64_t q_stride,
+                           int n_q_heads, float scale, void *out, void *workspace, size_t workspace_bytes,
+                           tq_stream stream) {
+  Call c = {k, v, block_table, seq_len, nullptr, q, nullptr, nullptr, out, workspace, workspace_bytes, q_stride,
+            n_seq, 1, 0, max_pages, n_seq, q_type, n_q_heads, 1, scale, 0.f, 1.f, false, false, stream};
+  return attend(c);
+}
+
+tq_status tq_paged4_prefill(const tq_paged4 *k, const tq_paged4 *v, const int32_t *block_table, int max_pages,
+                            const int32_t *seq_len, const int32_t *q_start, int n_seq, const void *q, int q_type,
+                            int64_t q_stride, int64_t n_rows, int n_q_heads, int64_t max_rows, int64_t max_len,
+                            float scale, int causal, void *out, void *workspace, size_t workspace_bytes,
+                            tq_stream stream) {
+  Call c = {k, v, block_table, seq_len, q_start, q, nullptr, nullptr, out, workspace, workspace_bytes, q_stride,
+            n_rows, max_rows, max_len, max_pages, n_seq, q_type, n_q_heads, causal, scale, 0.f, 1.f, false, true,
+            stream};
+  return attend(c);
+}
+
+tq_status tq_paged4_diff_decode(const tq_paged4 *k, const tq_paged4 *v, const int32_t *block_table, int max_pages,
+                                const int32_t *seq_len, int n_seq, const void *q, int q_type, int64_t q_stride,
+                                int n_heads, const float *lambda, const float *norm_weight, float eps,
+                                float out_scale, float scale, void *out, void *workspace, size_t workspace_bytes,
+                                tq_stream stream) {
+  Call c = {k, v, block_table, seq_len, nullptr, q, lambda, norm_weight, out, workspace, workspace_bytes, q_stride,
+            n_seq, 1, 0, max_pages, n_seq, q_type, n_heads, 1, scale, eps, out_scale, true, false, stream};
+  return attend(c);
+}
+
+tq_status tq_paged4_diff_prefill(const tq_paged4 *k, const tq_paged4 *v, const int32_t *block_table, int max_pages,
+                                 const int32_t *seq_len, const int32_t *q_start, int n_seq, const void *q,
+                                 int q_type, int64_t q_stride, int64_t n_rows, int n_heads, int64_t max_rows,
+                                 int64_t max_len, const float *lambda, const float *norm_weight, float eps,
+                                 float out_scale, float scale, int causal, void *out, void *workspace,
+                                 size_t workspace_bytes, tq_stream stream) {
+  Call c = {k, v, block_table, seq_len, q_start, q, lambda, norm_weight, out, workspace, workspace_bytes, q_stride,
+            n_rows, max_rows, max_len, max_pages, n_seq, q_type, n_heads, causal, scale, eps, out_scale, true, true,
+            stream};
+  return attend(c);
+}
+
+}  // extern "C"
