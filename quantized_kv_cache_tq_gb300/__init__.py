@@ -189,43 +189,73 @@ def checksum(t) -> str:
 
 # ---- paged 4-bit cache (include/tq.h, "Paged 4-bit cache")
 
+# These calls also serve single decode steps, where the host's share counts: checks are plain comparisons.
+
+_T = None                        # torch's names used on every call, bound on the first one
+
+
+class _Torch:
+    def __init__(self):
+        torch = _torch()
+        self.int32, self.int64, self.float32, self.uint8 = torch.int32, torch.int64, torch.float32, torch.uint8
+        self.float16, self.empty, self.zeros = torch.float16, torch.empty, torch.zeros
+        self.row_types = {torch.float32: TQ_F32, torch.float16: TQ_F16, torch.bfloat16: TQ_BF16}
+        self.raw_stream = torch._C._cuda_getCurrentRawStream
+        self.current = torch.cuda.current_device
+
+
+def _t() -> _Torch:
+    global _T
+    if _T is None:
+        _T = _Torch()
+    return _T
+
+
 def _need(ok, what: str):
     if not ok:
         raise ValueError(what)
 
 
-_ROW_TYPES: dict = {}
-
-
-def _row_type(t, what: str, dtypes=("float32", "float16", "bfloat16")) -> int:
+def _row_type(t, what: str, f32: bool = True) -> int:
     """TQ_* type of a tensor of rows."""
-    if not _ROW_TYPES:
-        torch = _torch()
-        _ROW_TYPES.update({torch.float32: ("float32", TQ_F32), torch.float16: ("float16", TQ_F16),
-                           torch.bfloat16: ("bfloat16", TQ_BF16)})
-    name, code = _ROW_TYPES.get(t.dtype, ("", -1))
-    _need(name in dtypes, f"{what}: {t.dtype} is not one of {', '.join(dtypes)}")
+    code = _t().row_types.get(t.dtype, -1)
+    if code < 0 or (code == TQ_F32 and not f32):
+        raise ValueError(f"{what}: rows of {t.dtype} are not taken")
     return code
 
 
-def _here(device, *tensors):
-    """The call runs on the current device; every tensor has to be there."""
-    _need(device.type == "cuda" and device.index == _torch().cuda.current_device(),
-          "the cache is not on the current CUDA device")
+def _stream_here(stream, device: int, *tensors) -> int:
+    """The stream's handle.  The call runs on the current device, where every tensor has to be."""
+    if device < 0 or device != _t().current():
+        raise ValueError("the cache is not on the current CUDA device")
     for t in tensors:
-        _need(t is None or t.device == device, "tensors are on different devices")
+        if t is not None and t.get_device() != device:
+            raise ValueError("tensors are on different devices")
+    return _T.raw_stream(device) if stream is None else stream.cuda_stream
+
+
+def _made_on(stream, make):
+    """What a call allocates for itself is filled and reused in the order of the call's stream."""
+    if stream is None:
+        return make()
+    with _torch().cuda.stream(stream):
+        return make()
 
 
 def _ints(t, dtype, shape, what: str):
-    _need(t.dtype == dtype and tuple(t.shape) == tuple(shape) and t.is_contiguous(),
-          f"{what}: a contiguous {dtype} tensor of shape {tuple(shape)} is expected")
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{what}: a contiguous {dtype} tensor of shape {tuple(shape)} is expected")
 
 
 def _row_stride(t, shape, what: str) -> int:
     """Elements between rows of t [n][heads][dim] whose rows are contiguous."""
-    _need(tuple(t.shape) == tuple(shape), f"{what}: shape {tuple(shape)} is expected, not {tuple(t.shape)}")
+    if t.shape != shape:
+        raise ValueError(f"{what}: shape {tuple(shape)} is expected, not {tuple(t.shape)}")
+    if t.is_contiguous():
+        return shape[1] * shape[2]
     s0, s1, s2 = t.stride()
-    _need((s2 == 1 or shape[2] == 1) and (s1 == shape[2] or shape[1] == 1), f"{what}: a row's heads are contiguous")
+    if (s2 != 1 and shape[2] > 1) or (s1 != shape[2] and shape[1] > 1):
+        raise ValueError(f"{what}: a row's heads have to be contiguous")
     return s0 if shape[0] > 1 else max(s0, shape[1] * shape[2])
 
 
@@ -251,6 +281,7 @@ class Paged4Cache:
             _ints(self.scales, torch.float16, (*shape, 2), "scales")
             _need(self.codes.device == self.scales.device, "tensors are on different devices")
         self.device = self.codes.device
+        self.index = self.codes.get_device()
         self.c = tq_paged4(n_kv_heads, head_dim, page_size, n_pages, self.codes.data_ptr(), self.scales.data_ptr())
         self.ref = C.byref(self.c)
 
@@ -273,7 +304,8 @@ class PagePlan:
         self.q_start, self.page_start = i32(n_seq + 1), i32(n_seq + 1)
         self.slots = torch.full((n_rows,), -1, dtype=torch.int64, device=device)
         self.positions = i32(n_rows)
-        self.device = self.slots.device
+        self.index = self.slots.get_device()
+        self._len, self._count = self.seq_len.data_ptr(), self.free_count.data_ptr()
         self._out = (self.q_start.data_ptr(), self.page_start.data_ptr(), self.slots.data_ptr(),
                      self.positions.data_ptr())
 
@@ -282,28 +314,29 @@ def page_plan(seq_len, n_new, page_size: int, block_table, free_pages, free_coun
               n_rows: int | None = None, in_place: bool = False, dev_status=None, stream=None) -> PagePlan:
     """Pages, slots and positions of a step's new cells (tq_page_plan).  The block table and the free list are
     updated; lengths and the free count go to ``plan``, or with ``in_place`` to seq_len and free_count themselves."""
-    torch = _torch()
-    n_seq, i32 = seq_len.shape[0], torch.int32
+    n_seq, i32 = seq_len.shape[0], _t().int32
     if plan is None:
         _need(n_rows is not None, "page_plan needs a plan or n_rows")
-        plan = PagePlan(n_seq, n_rows, seq_len.device)
+        plan = _made_on(stream, lambda: PagePlan(n_seq, n_rows, seq_len.device))
     _need(plan.n_seq == n_seq, "the plan is for another number of sequences")
+    _need(block_table.dim() == 2 and free_pages.dim() == 1, "block_table: [n_seq][max_pages], free_pages: [capacity]")
+    width, capacity = block_table.shape[1], free_pages.shape[0]
     _ints(seq_len, i32, (n_seq,), "seq_len")
     _ints(n_new, i32, (n_seq,), "n_new")
-    _need(block_table.dim() == 2 and block_table.shape[1] > 0, "block_table: [n_seq][max_pages]")
-    _ints(block_table, i32, (n_seq, block_table.shape[1]), "block_table")
-    _need(free_pages.dim() == 1, "free_pages: one dimension")
-    _ints(free_pages, i32, free_pages.shape, "free_pages")
+    _ints(block_table, i32, (n_seq, width), "block_table")
+    _ints(free_pages, i32, (capacity,), "free_pages")
     _ints(free_count, i32, (1,), "free_count")
+    status = None
     if dev_status is not None:
         _ints(dev_status, i32, (1,), "dev_status")
-    _here(plan.device, seq_len, n_new, block_table, free_pages, free_count, dev_status)
-    st = _lib.tq_page_plan(seq_len.data_ptr(), n_new.data_ptr(), n_seq, page_size, block_table.data_ptr(),
-                           block_table.shape[1], free_pages.data_ptr(), free_pages.shape[0], free_count.data_ptr(),
-                           (seq_len if in_place else plan.seq_len).data_ptr(),
-                           (free_count if in_place else plan.free_count).data_ptr(), *plan._out, plan.n_rows,
-                           None if dev_status is None else dev_status.data_ptr(), _stream(stream))
-    _lib.check("tq_page_plan", st)
+        status = dev_status.data_ptr()
+    stream = _stream_here(stream, plan.index, seq_len, n_new, block_table, free_pages, free_count, dev_status)
+    len_p, count_p = seq_len.data_ptr(), free_count.data_ptr()
+    st = _lib.tq_page_plan(len_p, n_new.data_ptr(), n_seq, page_size, block_table.data_ptr(), width,
+                           free_pages.data_ptr(), capacity, count_p, len_p if in_place else plan._len,
+                           count_p if in_place else plan._count, *plan._out, plan.n_rows, status, stream)
+    if st:
+        _lib.check("tq_page_plan", st)
     return plan
 
 
@@ -312,36 +345,49 @@ def paged4_set_rows(kc: Paged4Cache, vc: Paged4Cache, k_src, v_src, slots, dev_s
     (device int64 [n]; -1: not stored)."""
     n = slots.shape[0]
     t = _row_type(k_src, "k_src")
-    _need(v_src.dtype == k_src.dtype, "k_src and v_src have different types")
-    _ints(slots, _torch().int64, (n,), "slots")
+    _need(v_src.dtype is k_src.dtype, "k_src and v_src have different types")
+    status = _rows_status(slots, n, dev_status)
     ks = _row_stride(k_src, (n, kc.n_kv_heads, kc.head_dim), "k_src")
     vs = _row_stride(v_src, (n, vc.n_kv_heads, vc.head_dim), "v_src")
-    _here(kc.device, vc.codes, k_src, v_src, slots, dev_status)
+    stream = _stream_here(stream, kc.index, vc.codes, k_src, v_src, slots, dev_status)
     st = _lib.tq_paged4_set_rows(kc.ref, vc.ref, k_src.data_ptr(), ks, v_src.data_ptr(), vs, t, slots.data_ptr(), n,
-                                 None if dev_status is None else dev_status.data_ptr(), _stream(stream))
-    _lib.check("tq_paged4_set_rows", st)
+                                 status, stream)
+    if st:
+        _lib.check("tq_paged4_set_rows", st)
+
+
+def _rows_status(slots, n, dev_status):
+    _ints(slots, _T.int64, (n,), "slots")
+    if dev_status is None:
+        return None
+    _ints(dev_status, _T.int32, (1,), "dev_status")
+    return dev_status.data_ptr()
 
 
 def paged4_get_rows(kc: Paged4Cache, vc: Paged4Cache, slots, dtype=None, k_out=None, v_out=None, dev_status=None,
                     stream=None):
     """The values that cells ``slots`` stand for: (k, v) [n][n_kv_heads][head_dim] of ``dtype`` (default float16),
     or in k_out and v_out (rows may be strided).  Rows whose slot is -1 stay as they were (new outputs: zeros)."""
-    torch = _torch()
     n = slots.shape[0]
-    dtype = dtype or (k_out.dtype if k_out is not None else torch.float16)
-    if k_out is None:
-        k_out = torch.zeros((n, kc.n_kv_heads, kc.head_dim), dtype=dtype, device=slots.device)
-    if v_out is None:
-        v_out = torch.zeros((n, vc.n_kv_heads, vc.head_dim), dtype=dtype, device=slots.device)
+    if k_out is None or v_out is None:
+        dtype = dtype or (k_out if k_out is not None else v_out if v_out is not None else None) or _t().float16
+        dtype = getattr(dtype, "dtype", dtype)
+        if k_out is None:
+            k_out = _made_on(stream, lambda: _t().zeros((n, kc.n_kv_heads, kc.head_dim), dtype=dtype,
+                                                        device=slots.device))
+        if v_out is None:
+            v_out = _made_on(stream, lambda: _t().zeros((n, vc.n_kv_heads, vc.head_dim), dtype=dtype,
+                                                        device=slots.device))
     t = _row_type(k_out, "k_out")
-    _need(v_out.dtype == k_out.dtype == dtype, "k_out, v_out and dtype differ")
-    _ints(slots, torch.int64, (n,), "slots")
+    _need(v_out.dtype is k_out.dtype and (dtype is None or dtype is k_out.dtype), "k_out, v_out and dtype differ")
+    status = _rows_status(slots, n, dev_status)
     ks = _row_stride(k_out, (n, kc.n_kv_heads, kc.head_dim), "k_out")
     vs = _row_stride(v_out, (n, vc.n_kv_heads, vc.head_dim), "v_out")
-    _here(kc.device, vc.codes, k_out, v_out, slots, dev_status)
+    stream = _stream_here(stream, kc.index, vc.codes, k_out, v_out, slots, dev_status)
     st = _lib.tq_paged4_get_rows(kc.ref, vc.ref, k_out.data_ptr(), ks, v_out.data_ptr(), vs, t, slots.data_ptr(), n,
-                                 None if dev_status is None else dev_status.data_ptr(), _stream(stream))
-    _lib.check("tq_paged4_get_rows", st)
+                                 status, stream)
+    if st:
+        _lib.check("tq_paged4_get_rows", st)
     return k_out, v_out
 
 
@@ -356,46 +402,47 @@ def paged4_prefill_workspace(kc: Paged4Cache, vc: Paged4Cache, n_heads: int, n_s
     return _lib.tq_paged4_prefill_workspace(kc.ref, vc.ref, n_heads, n_seq, n_rows, max_len)
 
 
-def _paged4_args(kc, vc, block_table, seq_len, q, maps, out, extra=()):
-    """Checks shared by the attention calls -> (n_seq, max_pages, q type, q stride, output heads, out)."""
-    torch = _torch()
-    _need(block_table.dim() == 2 and block_table.shape[1] > 0, "block_table: [n_seq][max_pages]")
+def _paged4_args(kc, vc, block_table, seq_len, q, maps, out, stream, *extra):
+    """Checks shared by the attention calls -> (n_seq, max_pages, q type, q stride, output heads, out, stream)."""
+    t = _row_type(q, "q", f32=False)
+    if block_table.dim() != 2 or q.dim() != 3 or q.shape[1] % maps:
+        raise ValueError("block_table: [n_seq][max_pages], q: [rows][heads][head_dim]")
     n_seq, max_pages = block_table.shape
-    _ints(block_table, torch.int32, (n_seq, max_pages), "block_table")
-    _ints(seq_len, torch.int32, (n_seq,), "seq_len")
-    t = _row_type(q, "q", ("float16", "bfloat16"))
-    _need(q.dim() == 3 and q.shape[1] % maps == 0, "q: [rows][heads][head_dim]")
-    rows, heads = q.shape[0], q.shape[1] // maps
-    stride = _row_stride(q, (rows, heads * maps, kc.head_dim), "q")
+    rows, heads, _ = q.shape
+    _ints(block_table, _T.int32, (n_seq, max_pages), "block_table")
+    _ints(seq_len, _T.int32, (n_seq,), "seq_len")
+    stride = _row_stride(q, (rows, heads, kc.head_dim), "q")
+    heads //= maps
     if out is None:
-        out = torch.empty((rows, heads, vc.head_dim), dtype=q.dtype, device=q.device)
+        out = _made_on(stream, lambda: _T.empty((rows, heads, vc.head_dim), dtype=q.dtype, device=q.device))
     else:
         _ints(out, q.dtype, (rows, heads, vc.head_dim), "out")
-    _here(kc.device, vc.codes, block_table, seq_len, q, out, *extra)
-    return n_seq, max_pages, t, stride, heads, out
+    return n_seq, max_pages, t, stride, heads, out, _stream_here(stream, kc.index, vc.codes, block_table, seq_len, q,
+                                                                 out, *extra)
 
 
 def _diff_args(vc, heads, lam, norm_weight):
-    torch = _torch()
-    _ints(lam, torch.float32, (heads,), "lam")
-    if norm_weight is not None:
-        _ints(norm_weight, torch.float32, (vc.head_dim,), "norm_weight")
-    return lam.data_ptr(), None if norm_weight is None else norm_weight.data_ptr()
+    _ints(lam, _T.float32, (heads,), "lam")
+    if norm_weight is None:
+        return lam.data_ptr(), None
+    _ints(norm_weight, _T.float32, (vc.head_dim,), "norm_weight")
+    return lam.data_ptr(), norm_weight.data_ptr()
 
 
 def paged4_decode(kc: Paged4Cache, vc: Paged4Cache, block_table, seq_len, q, scale: float | None = None, out=None,
                   ws=None, stream=None):
     """One query row per sequence: q [n_seq][n_q_heads][Dk] (float16 or bfloat16, rows may be strided) over the
     seq_len[s] cells (device int32) of block_table[s] -> [n_seq][n_q_heads][Dv] of q's type."""
-    n_seq, max_pages, t, stride, heads, out = _paged4_args(kc, vc, block_table, seq_len, q, 1, out, (ws,))
+    n_seq, max_pages, t, stride, heads, out, handle = _paged4_args(kc, vc, block_table, seq_len, q, 1, out, stream, ws)
     _need(q.shape[0] == n_seq, "q: one row per sequence")
     scale = 1.0 / math.sqrt(kc.head_dim) if scale is None else scale
     if ws is None:
-        ws = workspace(paged4_decode_workspace(kc, vc, heads, n_seq), q.device)
+        ws = _made_on(stream, lambda: workspace(paged4_decode_workspace(kc, vc, heads, n_seq), q.device))
     st = _lib.tq_paged4_decode(kc.ref, vc.ref, block_table.data_ptr(), max_pages, seq_len.data_ptr(), n_seq,
                                q.data_ptr(), t, stride, heads, scale, out.data_ptr(), ws.data_ptr(), ws.numel(),
-                               _stream(stream))
-    _lib.check("tq_paged4_decode", st)
+                               handle)
+    if st:
+        _lib.check("tq_paged4_decode", st)
     return out
 
 
@@ -406,16 +453,18 @@ def paged4_prefill(kc: Paged4Cache, vc: Paged4Cache, block_table, seq_len, q, q_
     [n_rows][n_q_heads][Dk] are the last cells of sequence s.  max_rows and max_len (host): the most rows and cells
     of one sequence, where known; they only choose the kernel.  A workspace for the call is
     paged4_prefill_workspace(..., n_rows, max_len or the block table's capacity)."""
-    n_seq, max_pages, t, stride, heads, out = _paged4_args(kc, vc, block_table, seq_len, q, 1, out, (q_start, ws))
-    _ints(q_start, _torch().int32, (n_seq + 1,), "q_start")
+    n_seq, max_pages, t, stride, heads, out, handle = _paged4_args(kc, vc, block_table, seq_len, q, 1, out, stream,
+                                                                   q_start, ws)
+    _ints(q_start, _T.int32, (n_seq + 1,), "q_start")
     scale = 1.0 / math.sqrt(kc.head_dim) if scale is None else scale
     n_rows, max_len = q.shape[0], max_len or max_pages * kc.page_size
     if ws is None:
-        ws = workspace(paged4_prefill_workspace(kc, vc, heads, n_seq, n_rows, max_len), q.device)
+        ws = _made_on(stream, lambda: workspace(paged4_prefill_workspace(kc, vc, heads, n_seq, n_rows, max_len), q.device))
     st = _lib.tq_paged4_prefill(kc.ref, vc.ref, block_table.data_ptr(), max_pages, seq_len.data_ptr(),
                                 q_start.data_ptr(), n_seq, q.data_ptr(), t, stride, n_rows, heads, max_rows, max_len,
-                                scale, int(causal), out.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream))
-    _lib.check("tq_paged4_prefill", st)
+                                scale, int(causal), out.data_ptr(), ws.data_ptr(), ws.numel(), handle)
+    if st:
+        _lib.check("tq_paged4_prefill", st)
     return out
 
 
@@ -423,17 +472,18 @@ def paged4_diff_decode(kc: Paged4Cache, vc: Paged4Cache, block_table, seq_len, q
                        norm_weight=None, eps: float = 1e-5, out_scale: float = 1.0, out=None, ws=None, stream=None):
     """Differential attention, one query row per sequence: q [n_seq][2 n_heads][Dk], K with two heads per V head,
     lam (device float32 [n_heads]) the weights of the second map; optional RMS norm over each head's output."""
-    n_seq, max_pages, t, stride, heads, out = _paged4_args(kc, vc, block_table, seq_len, q, 2, out,
-                                                           (lam, norm_weight, ws))
+    n_seq, max_pages, t, stride, heads, out, handle = _paged4_args(kc, vc, block_table, seq_len, q, 2, out, stream,
+                                                                   lam, norm_weight, ws)
     _need(q.shape[0] == n_seq, "q: one row per sequence")
     lam_p, norm_p = _diff_args(vc, heads, lam, norm_weight)
     scale = 1.0 / math.sqrt(kc.head_dim) if scale is None else scale
     if ws is None:
-        ws = workspace(paged4_decode_workspace(kc, vc, heads, n_seq), q.device)
+        ws = _made_on(stream, lambda: workspace(paged4_decode_workspace(kc, vc, heads, n_seq), q.device))
     st = _lib.tq_paged4_diff_decode(kc.ref, vc.ref, block_table.data_ptr(), max_pages, seq_len.data_ptr(), n_seq,
                                     q.data_ptr(), t, stride, heads, lam_p, norm_p, eps, out_scale, scale,
-                                    out.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream))
-    _lib.check("tq_paged4_diff_decode", st)
+                                    out.data_ptr(), ws.data_ptr(), ws.numel(), handle)
+    if st:
+        _lib.check("tq_paged4_diff_decode", st)
     return out
 
 
@@ -443,17 +493,18 @@ def paged4_diff_prefill(kc: Paged4Cache, vc: Paged4Cache, block_table, seq_len, 
                         stream=None):
     """Differential attention of several query rows per sequence: rows as paged4_prefill, heads as
     paged4_diff_decode."""
-    n_seq, max_pages, t, stride, heads, out = _paged4_args(kc, vc, block_table, seq_len, q, 2, out,
-                                                           (q_start, lam, norm_weight, ws))
-    _ints(q_start, _torch().int32, (n_seq + 1,), "q_start")
+    n_seq, max_pages, t, stride, heads, out, handle = _paged4_args(kc, vc, block_table, seq_len, q, 2, out, stream,
+                                                                   q_start, lam, norm_weight, ws)
+    _ints(q_start, _T.int32, (n_seq + 1,), "q_start")
     lam_p, norm_p = _diff_args(vc, heads, lam, norm_weight)
     scale = 1.0 / math.sqrt(kc.head_dim) if scale is None else scale
     n_rows, max_len = q.shape[0], max_len or max_pages * kc.page_size
     if ws is None:
-        ws = workspace(paged4_prefill_workspace(kc, vc, heads, n_seq, n_rows, max_len), q.device)
+        ws = _made_on(stream, lambda: workspace(paged4_prefill_workspace(kc, vc, heads, n_seq, n_rows, max_len), q.device))
     st = _lib.tq_paged4_diff_prefill(kc.ref, vc.ref, block_table.data_ptr(), max_pages, seq_len.data_ptr(),
                                      q_start.data_ptr(), n_seq, q.data_ptr(), t, stride, n_rows, heads, max_rows,
                                      max_len, lam_p, norm_p, eps, out_scale, scale, int(causal), out.data_ptr(),
-                                     ws.data_ptr(), ws.numel(), _stream(stream))
-    _lib.check("tq_paged4_diff_prefill", st)
+                                     ws.data_ptr(), ws.numel(), handle)
+    if st:
+        _lib.check("tq_paged4_diff_prefill", st)
     return out

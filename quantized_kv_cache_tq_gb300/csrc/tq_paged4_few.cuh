@@ -28,6 +28,12 @@
 //   x_t + exponent(s_t), so the largest weight lies in [1, 2^9] whatever the
 //   scales, and sums of p_t and p_t m_t stay in fp32.  R is raised only when it
 //   would grow by more than 2^8 (the sums are rescaled then).
+// - Codes count from a row's smallest value, so with w the rounded weight, sum w c
+//   + sum p m would carry the rounding of w times the whole range of the row.  The
+//   sum taken is sum w (c - c0) + sum p (m + s c0) with c0 = clamp(-m / s, 0, 15)
+//   per row, the code that stands for 0: the rounding then meets the values
+//   themselves (binary16 output error over 32768 keys: 7.2e-4 without, 2.2e-4 with;
+//   the plain fp32 form has 2.1e-4, the output's own rounding).
 //
 // Split of the work: the keys of all (sequence, V head, column chunk) items, in
 // units of 64, form one line that is cut into equal shares, one per CTA.  Shares
@@ -48,6 +54,7 @@ namespace p4 {
 
 constexpr int UNIT = 64;              // keys per unit of work
 constexpr int TILE = 32;              // keys per warp tile
+constexpr int MIN_SHARE = 4;          // units per CTA at least: one tile for each of eight warps
 
 // MAPS = 2: differential attention; tile n of the columns belongs to map n and
 // reads K head 2 hv + n.  MAPS = 1: NT tiles of eight columns read K head hv.
@@ -186,6 +193,37 @@ __device__ __forceinline__ SeqWork seq_work(const AttnArgs &a, int s, bool repor
   return w;
 }
 
+// Units of the sequences s0 .. s0 + threads - 1: this thread's sequence spans [lo, hi) of the
+// line that stands at `base` before them; returns their sum (to every thread).
+template <int COLS, int NW>
+__device__ __forceinline__ long long scan_chunk(const AttnArgs &a, int s0, long long base, long long *sums, bool report,
+                                                long long &lo, long long &hi) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  long long v = 0;
+  if (s0 + tid < a.n_seq) {
+    const SeqWork w = seq_work<COLS>(a, s0 + tid, report);
+    v = w.units * w.items;
+  }
+  long long x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();
+  if (lane == 31) sums[warp] = x;
+  __syncthreads();
+  long long all = 0;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) {
+    if (w == warp) x += all;
+    all += sums[w];
+  }
+  lo = base + x - v;
+  hi = base + x;
+  return all;
+}
+
 }  // namespace few
 
 template <int DK, int DV, int NT, int MAPS>
@@ -196,57 +234,34 @@ __global__ void __launch_bounds__(FewCfg<DK, DV, NT, MAPS>::THREADS, FewCfg<DK, 
   constexpr int NW = C::NW, KW = C::KW, VW = C::VW, MT = C::MT, NC = C::NC, COLS = C::COLS;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ long long s_scan[NW];
-  __shared__ long long s_total, s_pre;
+  __shared__ long long s_pre;
   __shared__ int s_seq, s_last;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
 
-  // ---- this CTA's share of the work line: [cur, end) of `total` units
-  long long total = 0, pre = 0;
-  int seq = 0;
-  for (int pass = 0; pass < 2; ++pass) {        // pass 0: the total; pass 1: the share's first sequence
-    long long carry = 0, begin = 0;
-    if (pass == 1) {
-      const long long n = total < gridDim.x ? total : gridDim.x;
-      if (blockIdx.x >= n) break;
-      begin = blockIdx.x * total / n;
-    }
-    for (int s0 = 0; s0 < a.n_seq; s0 += C::THREADS) {
-      long long v = 0;
-      if (s0 + tid < a.n_seq) {
-        const SeqWork w = seq_work<COLS>(a, s0 + tid, pass == 0 && blockIdx.x == 0);
-        v = w.units * w.items;
-      }
-      long long x = v;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      __syncthreads();
-      if (lane == 31) s_scan[warp] = x;
-      __syncthreads();
-      long long before = carry;
-      for (int w = 0; w < NW; ++w) {
-        if (w < warp) before += s_scan[w];
-        carry += s_scan[w];
-      }
-      x += before;
-      if (pass == 1 && v > 0 && x - v <= begin && begin < x) {
-        s_seq = s0 + tid;
-        s_pre = x - v;
-      }
-    }
-    if (pass == 0) total = carry;
-  }
-  const long long n_work = total < gridDim.x ? total : gridDim.x;
-  __syncthreads();
+  // ---- this CTA's share of the work line: units [cur, end) of `total`
+  long long total = 0, pre = 0, mine_lo = 0, mine_hi = 0;
+  for (int s0 = 0; s0 < a.n_seq; s0 += C::THREADS)
+    total += scan_chunk<COLS, NW>(a, s0, total, s_scan, blockIdx.x == 0, mine_lo, mine_hi);
+  const long long n_work = min(static_cast<long long>(gridDim.x), (total + MIN_SHARE - 1) / MIN_SHARE);
+  const bool works = blockIdx.x < n_work;
   long long cur = 0, end = 0;
-  if (blockIdx.x < n_work) {
-    seq = s_seq;
-    pre = s_pre;
+  int seq = 0;
+  if (works) {
     cur = blockIdx.x * total / n_work;
     end = (blockIdx.x + 1) * total / n_work;
+    long long at = 0;
+    for (int s0 = 0; s0 < a.n_seq; s0 += C::THREADS) {
+      // (a batch of one chunk still has its sums in registers)
+      if (a.n_seq > C::THREADS) at += scan_chunk<COLS, NW>(a, s0, at, s_scan, false, mine_lo, mine_hi);
+      if (mine_lo <= cur && cur < mine_hi) {
+        s_seq = s0 + tid;
+        s_pre = mine_lo;
+      }
+    }
+    __syncthreads();
+    seq = s_seq;
+    pre = s_pre;
   }
   const long long share0 = cur;
 
@@ -426,14 +441,16 @@ __global__ void __launch_bounds__(FewCfg<DK, DV, NT, MAPS>::THREADS, FewCfg<DK, 
       const bool masked = key0 + TILE > lim_min || key0 + TILE > k_end;
 
       // value scales and offsets of the lane's score rows (keys g + 8 j), exponents of the scales
-      float vs[4], vm[4], ve[4];
+      float vs[4], vm[4], ve[4], vc[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         uint32_t u;
         lds<1>(&u, sc + (MAPS * 32 + 8 * j + g) * 4);
         const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&u));
+        const float c0 = fminf(fmaxf(__fdividef(-f.y, f.x), 0.f), 15.f);     // (0 / 0 and NaN: 0)
         vs[j] = f.x;
-        vm[j] = f.y;
+        vc[j] = -c0;
+        vm[j] = fmaf(f.x, c0, f.y);
         ve[j] = f.x > 0.f ? static_cast<float>(static_cast<int>(__float_as_uint(f.x) >> 23) - 127) : -24.f;
       }
       uint32_t pb[NT][2][2];                // weights as B fragments [half][keys 0-7, 8-15]
@@ -522,8 +539,14 @@ __global__ void __launch_bounds__(FewCfg<DK, DV, NT, MAPS>::THREADS, FewCfg<DK, 
               z[nn][i] = fmaf(p, vm[j], z[nn][i]);
               wt[c] = p * vs[j];
             }
-            pb[nn][hf][0] = transpose8(half2_bits(wt[0], wt[1]));
-            pb[nn][hf][1] = transpose8(half2_bits(wt[2], wt[3]));
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const __half2 h = __floats2half2_rn(wt[2 * r], wt[2 * r + 1]);
+              const float2 f = __half22float2(h);
+              z[nn][0] = fmaf(f.x, vc[2 * hf + r], z[nn][0]);
+              z[nn][1] = fmaf(f.y, vc[2 * hf + r], z[nn][1]);
+              pb[nn][hf][r] = transpose8(*reinterpret_cast<const uint32_t *>(&h));
+            }
           }
         }
       }
@@ -635,24 +658,34 @@ __global__ void __launch_bounds__(FewCfg<DK, DV, NT, MAPS>::THREADS, FewCfg<DK, 
       if (finish) {
         __threadfence();
         if (tid == 0) a.counters[c0] = 0;
-        // partial of CTA c: slot 0 when the item's part begins the CTA's share, else slot 1
-        auto slot_of = [&](int c) {
-          return a.part + static_cast<int64_t>(2 * c + (c * total / n_work >= ia ? 0 : 1)) * C::PART;
+        // CTA c0's partial is in its slot 0 when the item's part begins its share, else in slot 1; the
+        // others' parts begin their shares
+        auto part_of = [&](int c) {
+          return a.part + static_cast<int64_t>(2 * (c0 + c) + (c == 0 && c0 * total / n_work < ia ? 1 : 0)) * C::PART;
         };
         const int n_con = c1 - c0 + 1;
-        if (tid < NC) {
-          float M = -INFINITY;
-          for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(slot_of(c) + 4 * tid));
-          float ls = 0.f, zs = 0.f;
-          for (int c = c0; c <= c1; ++c) {
-            const float4 p = __ldcg(reinterpret_cast<const float4 *>(slot_of(c)) + tid);
-            const float f = p.x == -INFINITY ? 0.f : exp2f(p.x - M);
-            ls += f * p.y;
-            zs += f * p.z;
+        float *cw = reinterpret_cast<float *>(smem);             // [CTA][column]: weight of its partial
+        for (int col = warp; col < NC; col += NW) {
+          float M = -INFINITY, ls = 0.f, zs = 0.f;
+          for (int c = lane; c < n_con; c += 32) {
+            const float r = __ldcg(part_of(c) + 4 * col);
+            cw[c * NC + col] = r;
+            M = fmaxf(M, r);
           }
-          wts[4 * tid] = M;
-          wts[4 * tid + 1] = ls;
-          wts[4 * tid + 2] = zs;
+          M = warp_max(M);
+          for (int c = lane; c < n_con; c += 32) {
+            const float4 p = __ldcg(reinterpret_cast<const float4 *>(part_of(c)) + col);
+            const float f = p.x == -INFINITY ? 0.f : exp2f(p.x - M);
+            cw[c * NC + col] = f;
+            ls = fmaf(f, p.y, ls);
+            zs = fmaf(f, p.z, zs);
+          }
+          ls = warp_sum(ls);
+          zs = warp_sum(zs);
+          if (lane == 0) {
+            wts[4 * col + 1] = ls;
+            wts[4 * col + 2] = zs;
+          }
         }
         __syncthreads();
 #pragma unroll
@@ -661,19 +694,17 @@ __global__ void __launch_bounds__(FewCfg<DK, DV, NT, MAPS>::THREADS, FewCfg<DK, 
           o4[k] = make_float4(0.f, 0.f, 0.f, 0.f);
           if (f < NF) {
             const int col = 8 * (f / (MT * 32)) + 2 * (f & 3);
-            const float M0 = wts[4 * col], M1 = wts[4 * col + 4];
-#pragma unroll 4
-            for (int c = 0; c < n_con; ++c) {
-              const float *p = slot_of(c0 + c);
-              const float4 v = __ldcg(reinterpret_cast<const float4 *>(p + 4 * NC) + f);
-              const float r0 = __ldcg(p + 4 * col), r1 = __ldcg(p + 4 * col + 4);
-              const float w0 = r0 == -INFINITY ? 0.f : exp2f(r0 - M0);
-              const float w1 = r1 == -INFINITY ? 0.f : exp2f(r1 - M1);
-              o4[k].x = fmaf(w0, v.x, o4[k].x);
-              o4[k].y = fmaf(w1, v.y, o4[k].y);
-              o4[k].z = fmaf(w0, v.z, o4[k].z);
-              o4[k].w = fmaf(w1, v.w, o4[k].w);
-            }
+            auto add = [&](int c, const float4 &v) {
+              const float2 w2 = *reinterpret_cast<const float2 *>(cw + c * NC + col);
+              o4[k].x = fmaf(w2.x, v.x, o4[k].x);
+              o4[k].y = fmaf(w2.y, v.y, o4[k].y);
+              o4[k].z = fmaf(w2.x, v.z, o4[k].z);
+              o4[k].w = fmaf(w2.y, v.w, o4[k].w);
+            };
+            add(0, __ldcg(reinterpret_cast<const float4 *>(part_of(0) + 4 * NC) + f));
+            const float4 *p = reinterpret_cast<const float4 *>(part_of(1) + 4 * NC) + f;
+#pragma unroll 8
+            for (int c = 1; c < n_con; ++c, p += 2 * C::PART / 4) add(c, __ldcg(p));
           }
         }
       }
