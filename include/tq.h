@@ -366,7 +366,7 @@ tq_status tq_f16_prompt_attn(const uint16_t *k, const uint16_t *v, int64_t n_cel
  *   scales  binary16 [n_pages][n_kv_heads][page_size][2]     (scale, offset)
  * A row stands for scale * code + offset (code 0 .. 15).  head_dim is a multiple
  * of 8, at most 256 (a dim that is not 64, 128 or 256 stores zero codes up to D);
- * page_size a power of two, 16 .. 1024.  Cell c of the cache is row
+ * page_size a power of two, 16 .. 1024; n_pages * n_kv_heads * page_size below 2^32.  Cell c of the cache is row
  * c % page_size of page c / page_size. */
 typedef struct tq_paged4 {
   int32_t n_kv_heads;

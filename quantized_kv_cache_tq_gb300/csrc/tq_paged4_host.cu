@@ -29,7 +29,8 @@ static int shift_of(int page_size, int lo, int hi) {
 
 static bool shape_ok(int n_kv_heads, int head_dim, int page_size, int n_pages) {
   return n_kv_heads > 0 && n_kv_heads <= 65536 && head_dim % 8 == 0 && row_width(head_dim) > 0 &&
-         shift_of(page_size, 16, 1024) >= 0 && n_pages > 0;
+         shift_of(page_size, 16, 1024) >= 0 && n_pages > 0 &&
+         static_cast<int64_t>(n_pages) * page_size < 0x100000000LL / n_kv_heads;     // 32-bit row numbers
 }
 
 static bool cache_ok(const tq_paged4 *c) {
@@ -103,7 +104,7 @@ static tq_status attend(const Call &c) {
     return TQ_ERR_INVALID_ARG;
   const int64_t row = static_cast<int64_t>(c.diff ? 2 : 1) * c.n_heads * c.k->head_dim;
   if (c.q_stride < row || c.q_stride % 8) return TQ_ERR_INVALID_ARG;
-  if (c.n_rows * (c.n_heads / c.v->n_kv_heads) > 0x7fffffffLL) return TQ_ERR_INVALID_ARG;
+  if (c.n_rows > 0x7fffffffLL / c.n_heads) return TQ_ERR_INVALID_ARG;
   if (static_cast<int64_t>(c.max_pages) * c.k->page_size > 0x7fffffffLL) return TQ_ERR_INVALID_ARG;
   if (c.n_seq == 0 || c.n_rows == 0) return TQ_OK;
   if (!al(c.block_table, 4) || !al(c.seq_len, 4) || (c.ragged && !al(c.q_start, 4)) || !al(c.q, 16) || !al(c.out, 16))
