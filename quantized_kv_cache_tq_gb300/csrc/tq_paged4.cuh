@@ -55,6 +55,7 @@ struct RowsArgs {
   int64_t n_rows;
   int64_t n_cells;
   int32_t page_shift;
+  uint32_t k_blocks;       // CTAs of the K rows (set at the launch)
 };
 cudaError_t launch_set_rows(int type, const RowsArgs &a, cudaStream_t s);
 cudaError_t launch_get_rows(int type, const RowsArgs &a, cudaStream_t s);

@@ -70,8 +70,11 @@ constexpr int TILE = 32;              // keys per warp tile
 constexpr int MIN_PIECE = 4;          // units of a piece at least: one tile for each of eight warps
 constexpr int SETUP = 8;              // units' worth of work that an item costs besides its keys
 
-// MAPS = 2: differential attention; tile n of the columns belongs to map n and
-// reads K head 2 hv + n.  MAPS = 1: NT tiles of eight columns read K head hv.
+// MAPS = 1: NT tiles of eight columns read K head hv.  MAPS = 2, differential
+// attention: one tile, columns 0 .. 3 of map 0 and 4 .. 7 of map 1 for the same four
+// (row, head) pairs.  Its scores add up both maps' products, each map's query
+// fragments holding zeros in the other's columns, so that everything after them --
+// softmax, weights, and the V rows, read once for both maps -- is that of one tile.
 template <int DK, int DV, int NT, int MAPS>
 struct FewCfg {
   static constexpr int KS = DK / 16;                      // k steps of the scores
@@ -79,16 +82,16 @@ struct FewCfg {
   static constexpr int NW = FEW_NW;                            // warps
   static constexpr int THREADS = NW * 32;
   static constexpr int KW = DK / 32;                      // words of a K row per lane
-  static constexpr int COLS = 8 * (MAPS == 2 ? 1 : NT);   // (row, head) columns per item
+  static constexpr int COLS = MAPS == 2 ? 4 : 8 * NT;     // (row, head) columns per item
   static constexpr int NC = 8 * NT;                       // columns incl. maps
   // per SM: two where value accumulators and query fragments leave room in 128 registers a thread
-  static constexpr int CTAS = FEW_NW == 8 && NT * (4 * MT + 2 * KS) <= 48 ? 2 : 1;
+  static constexpr int CTAS = FEW_NW == 8 && NT * (4 * MT + 2 * KS * MAPS) <= (DK == 128 && MAPS == 2 ? 64 : 48) ? 2 : 1;
   // one stage: K rows [map][key], V rows [key], scale pairs [K maps, V][key]
   static constexpr int K_BYTES = TILE * DK / 2;
   static constexpr int V_BYTES = TILE * DV / 2;
   static constexpr int SC = MAPS * K_BYTES + V_BYTES;
   static constexpr int STAGE = SC + (MAPS + 1) * TILE * 4;
-  static constexpr int PREP = TILE * (32 + 8 * (MAPS - 1));   // a warp's unpacked scales of one tile
+  static constexpr int PREP = TILE * (24 + 8 * MAPS);     // a warp's unpacked scales of one tile
   static constexpr int MERGE = NW * NT * MT * 512 + NW * NC * 12 + NC * 16;  // CTA merge, in the same place
   static constexpr int BUDGET = (CTAS == 2 ? 111 : 222) * 1024;
   static constexpr int FIT = (BUDGET - NW * PREP) / (NW * STAGE);
@@ -412,9 +415,9 @@ __global__ void __launch_bounds__(FewCfg<DK, DV, NT, MAPS>::THREADS, FewCfg<DK, 
     uint4 qraw[NT][KW];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const int c = c_base + (MAPS == 2 ? 0 : 8 * n) + g;
+      const int c = c_base + (MAPS == 2 ? g & 3 : 8 * n + g);
       const int row = c / a.group, head = hv * a.group + (c - row * a.group);
-      const int64_t qb = (w.row0 + row) * a.q_stride + static_cast<int64_t>(MAPS == 2 ? 2 * head + n : head) * a.dk;
+      const int64_t qb = (w.row0 + row) * a.q_stride + static_cast<int64_t>(MAPS == 2 ? 2 * head + (g >> 2) : head) * a.dk;
 #pragma unroll
       for (int i = 0; i < KW; ++i) {
         const int d0 = (i / 4) * 128 + KW4 * 8 * t + 8 * (i % 4);
@@ -506,7 +509,7 @@ __global__ void __launch_bounds__(FewCfg<DK, DV, NT, MAPS>::THREADS, FewCfg<DK, 
     pages_of(warp + (C::STAGES - 1) * NW, pn0, pn1);
 
     // ---- query fragments
-    uint32_t qf[NT][C::KS][2];
+    uint32_t qf[MAPS][NT][C::KS][2];
     float2 qx[NT], fx[NT];          // of columns 2t, 2t + 1: scale * log2(e) * sum(q), and the score factor
     int lim[NT][2];                 // their limits
 #pragma unroll
@@ -535,9 +538,14 @@ __global__ void __launch_bounds__(FewCfg<DK, DV, NT, MAPS>::THREADS, FewCfg<DK, 
       for (int i = 0; i < KW; ++i)
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
-          qf[n][2 * i + hf][0] = half2_bits(v[i][2 * hf] * s1 * s2, v[i][2 * hf + 4] * s1 * s2);
-          qf[n][2 * i + hf][1] =
-              half2_bits(v[i][2 * hf + 1] * s1 * s2 * 0.0625f, v[i][2 * hf + 5] * s1 * s2 * 0.0625f);
+          const uint32_t even = half2_bits(v[i][2 * hf] * s1 * s2, v[i][2 * hf + 4] * s1 * s2);
+          const uint32_t odd = half2_bits(v[i][2 * hf + 1] * s1 * s2 * 0.0625f, v[i][2 * hf + 5] * s1 * s2 * 0.0625f);
+#pragma unroll
+          for (int m = 0; m < MAPS; ++m) {
+            const bool here = MAPS == 1 || (g >> 2) == m;
+            qf[m][n][2 * i + hf][0] = here ? even : 0;
+            qf[m][n][2 * i + hf][1] = here ? odd : 0;
+          }
         }
       // this lane's softmax columns are 2t and 2t + 1: their values sit in lanes g = 2t, 2t + 1
       const float f = a.scale_log2 * exp2f(12.f + static_cast<float>(ex));          // 2^24 2^(ex - 12)
@@ -546,7 +554,7 @@ __global__ void __launch_bounds__(FewCfg<DK, DV, NT, MAPS>::THREADS, FewCfg<DK, 
       qx[n] = make_float2(__shfl_sync(0xffffffffu, qs, 8 * t), __shfl_sync(0xffffffffu, qs, 8 * t + 4));
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int cc = c_base + (MAPS == 2 ? 0 : 8 * n) + 2 * t + i;
+        const int cc = c_base + (MAPS == 2 ? (2 * t + i) & 3 : 8 * n + 2 * t + i);
         lim[n][i] = cc < cols_all ? limit_of(cc / a.group) : 0;
       }
     }
@@ -586,29 +594,34 @@ __global__ void __launch_bounds__(FewCfg<DK, DV, NT, MAPS>::THREADS, FewCfg<DK, 
         const float c0 = fminf(fmaxf(__fdividef(-v.y, v.x), 0.f), 15.f), vm = fmaf(v.x, c0, v.y);   // (0 / 0, NaN: 0)
         const float e = v.x != 0.f ? static_cast<float>(static_cast<int>(__float_as_uint(fabsf(v.x)) >> 23) - 127) : -24.f;
         sts4(prep + lane * 16, v.x, v.x, vm, vm);
-        sts4(prep + (TILE + lane) * 16, k.x, k.y, -c0, e);
+        sts2(prep + TILE * 16 + lane * 8, -c0, e);
+        sts2(prep + TILE * 24 + lane * 8, k.x, k.y);
         if (MAPS == 2) {
           const float2 k1 = pair(MAPS - 1);
-          sts2(prep + 2 * TILE * 16 + lane * 8, k1.x, k1.y);
+          sts2(prep + TILE * 32 + lane * 8, k1.x, k1.y);
         }
         __syncwarp();
       }
       const bool masked = key0 + TILE > lim_min || key0 + TILE > k_end;
 
-      float4 vsc[4], kce[4];      // of keys g + 8 j: V's (scale, scale, centred offset, the same); K's scale and offset,
-                                  // V's -c0 and exponent
+      float4 vsc[4];              // of keys g + 8 j: V's (scale, scale, centred offset, the same)
+      float2 vce[4], ksc[4];      // V's -c0 and exponent; K's scale and offset, of the map of the lane's columns
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         vsc[j] = lds4(prep + (8 * j + g) * 16);
-        kce[j] = lds4(prep + (TILE + 8 * j + g) * 16);
+        vce[j] = lds2(prep + TILE * 16 + (8 * j + g) * 8);
+        ksc[j] = lds2(prep + TILE * (MAPS == 2 ? 24 + 8 * (t >> 1) : 24) + (8 * j + g) * 8);
       }
       uint32_t pb[NT][2][2];                // weights as B fragments [half][keys 0-7, 8-15]
+      float s[NT][2][4];
 #pragma unroll
-      for (int m = 0; m < MAPS; ++m) {
-        constexpr int N1 = MAPS == 2 ? 1 : NT;
-        float s[N1][2][4];
+      for (int hf = 0; hf < 2; ++hf) {
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) s[n][hf][c] = 0.f;
+#pragma unroll
+        for (int m = 0; m < MAPS; ++m) {
           uint32_t kw[2][KW];
 #pragma unroll
           for (int r = 0; r < 2; ++r)
@@ -618,34 +631,26 @@ __global__ void __launch_bounds__(FewCfg<DK, DV, NT, MAPS>::THREADS, FewCfg<DK, 
               lds<W>(&kw[r][4 * c], st + m * C::K_BYTES + (16 * hf + 8 * r) * (DK / 2) + k_at[c]);
             }
 #pragma unroll
-          for (int n = 0; n < N1; ++n)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) s[n][hf][c] = 0.f;
-#pragma unroll
           for (int i = 0; i < KW; ++i) {
             const uint32_t a0 = kw[0][i], a1 = kw[1][i], b0 = a0 >> 8, b1 = a1 >> 8;
 #pragma unroll
-            for (int n = 0; n < N1; ++n) {
-              const int nn = MAPS == 2 ? m : n;
+            for (int n = 0; n < NT; ++n) {
               mma16816(s[n][hf], a0 & 0x000f000fu, a1 & 0x000f000fu, a0 & 0x00f000f0u, a1 & 0x00f000f0u,
-                       qf[nn][2 * i][0], qf[nn][2 * i][1]);
+                       qf[m][n][2 * i][0], qf[m][n][2 * i][1]);
               mma16816(s[n][hf], b0 & 0x000f000fu, b1 & 0x000f000fu, b0 & 0x00f000f0u, b1 & 0x00f000f0u,
-                       qf[nn][2 * i + 1][0], qf[nn][2 * i + 1][1]);
+                       qf[m][n][2 * i + 1][0], qf[m][n][2 * i + 1][1]);
             }
           }
         }
-        float2 ksc[4];                      // scale, offset
+      }
+      {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          ksc[j] = m == 0 ? make_float2(kce[j].x, kce[j].y) : lds2(prep + 2 * TILE * 16 + (8 * j + g) * 8);
-#pragma unroll
-        for (int n = 0; n < N1; ++n) {
-          const int nn = MAPS == 2 ? m : n;
-          float2 x[4];                      // scores of rows g + 8 j, columns 2t and 2t + 1
+        for (int nn = 0; nn < NT; ++nn) {
+          float2 x[4];                      // scores of keys g + 8 j, columns 2t and 2t + 1
           float mt[2] = {-INFINITY, -INFINITY};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const float2 sj = make_float2(s[n][j >> 1][2 * (j & 1)], s[n][j >> 1][2 * (j & 1) + 1]);
+            const float2 sj = make_float2(s[nn][j >> 1][2 * (j & 1)], s[nn][j >> 1][2 * (j & 1) + 1]);
             x[j] = fma2(mul2(make_float2(ksc[j].x, ksc[j].x), sj), fx[nn], mul2(make_float2(ksc[j].y, ksc[j].y), qx[nn]));
           }
           if (masked) {
@@ -658,8 +663,8 @@ __global__ void __launch_bounds__(FewCfg<DK, DV, NT, MAPS>::THREADS, FewCfg<DK, 
           }
 #pragma unroll
           for (int j = 0; j < 4; j += 2) {
-            const float2 u = add2(x[j], make_float2(kce[j].w, kce[j].w));
-            const float2 w = add2(x[j + 1], make_float2(kce[j + 1].w, kce[j + 1].w));
+            const float2 u = add2(x[j], make_float2(vce[j].y, vce[j].y));
+            const float2 w = add2(x[j + 1], make_float2(vce[j + 1].y, vce[j + 1].y));
             mt[0] = max3(mt[0], u.x, w.x);
             mt[1] = max3(mt[1], u.y, w.y);
           }
@@ -691,7 +696,7 @@ __global__ void __launch_bounds__(FewCfg<DK, DV, NT, MAPS>::THREADS, FewCfg<DK, 
             z[nn] = fma2(p, make_float2(vsc[j].z, vsc[j].w), z[nn]);
             const float2 w = mul2(p, make_float2(vsc[j].x, vsc[j].y));
             const __half2 h = __floats2half2_rn(w.x, w.y);
-            z[nn] = fma2(__half22float2(h), make_float2(kce[j].z, kce[j].z), z[nn]);
+            z[nn] = fma2(__half22float2(h), make_float2(vce[j].x, vce[j].x), z[nn]);
             pb[nn][j >> 1][j & 1] = transpose8(*reinterpret_cast<const uint32_t *>(&h));
           }
         }
@@ -766,12 +771,15 @@ __global__ void __launch_bounds__(FewCfg<DK, DV, NT, MAPS>::THREADS, FewCfg<DK, 
     }
     __syncthreads();
 
-    // Fragments with columns that exist: of each (tile, m tile), lanes (g, t) with t below 1, 2 or 4.  A thread
+    // Fragments with columns that exist: of each (tile, m tile), lanes (g, t) with 1, 2 or 4 of the t.  A thread
     // takes PER of them, or several threads one.
     const int n_cols = min(COLS, cols_all - c_base);
-    const int tsh = n_cols > 4 ? 2 : n_cols > 2 ? 1 : 0;
+    const int tsh = MAPS == 2 ? (n_cols > 2 ? 2 : 1) : n_cols > 4 ? 2 : n_cols > 2 ? 1 : 0;
     const int n_frag = NT * MT * (8 << tsh);
-    auto frag_at = [&](int v) { return (v >> (3 + tsh)) * 32 + ((v >> tsh) & 7) * 4 + (v & ((1 << tsh) - 1)); };
+    auto frag_at = [&](int v) {
+      const int low = v & ((1 << tsh) - 1);               // (two maps: t = 0 and 2)
+      return (v >> (3 + tsh)) * 32 + ((v >> tsh) & 7) * 4 + (MAPS == 2 && tsh == 1 ? 2 * low : low);
+    };
     constexpr int PER = (NT * MT * 32 + C::THREADS - 1) / C::THREADS;
     const bool whole = n_con == 1;
     float *mine = a.part + static_cast<int64_t>(2 * blockIdx.x + (even || share0 >= ia ? 0 : 1)) * C::PART;
@@ -812,7 +820,7 @@ __global__ void __launch_bounds__(FewCfg<DK, DV, NT, MAPS>::THREADS, FewCfg<DK, 
         // with few fragments, `teams` threads share one, each taking every teams-th partial
         const int teams = n_frag < C::THREADS ? C::THREADS / n_frag : 1, team = n_frag < C::THREADS ? tid / n_frag : 0;
         const int v0 = n_frag < C::THREADS ? tid - team * n_frag : tid;
-        constexpr int B = 8;                                     // loads in flight per thread
+        constexpr int B = C::CTAS == 2 ? 16 : 24;                // loads in flight per thread
         float4 p[B];
         auto fetch = [&](int c, int v) {
 #pragma unroll
@@ -827,6 +835,7 @@ __global__ void __launch_bounds__(FewCfg<DK, DV, NT, MAPS>::THREADS, FewCfg<DK, 
         float2 *clz = reinterpret_cast<float2 *>(cw + n_con * NC);
         for (int col = warp; col < NC; col += NW) {
           float M = -INFINITY, ls = 0.f, zs = 0.f;
+#pragma unroll 2
           for (int c = lane; c < n_con; c += 32) {
             const float4 r = __ldcg(reinterpret_cast<const float4 *>(part_of(c)) + col);
             cw[c * NC + col] = r.x;
@@ -889,7 +898,7 @@ __global__ void __launch_bounds__(FewCfg<DK, DV, NT, MAPS>::THREADS, FewCfg<DK, 
     if (finish) {
       // fragment f = (n, mt, lane): dims d, d + 1 of columns col, col + 1
       __syncthreads();                      // shared memory is free for the differential exchange
-      float *ex = reinterpret_cast<float *>(smem);               // [column 8][DV] of map 0, then of the difference
+      float *ex = reinterpret_cast<float *>(smem);               // [column][DV]
 #pragma unroll
       for (int k = 0; k < PER; ++k) {
         const int v = tid + k * C::THREADS;
@@ -919,7 +928,7 @@ __global__ void __launch_bounds__(FewCfg<DK, DV, NT, MAPS>::THREADS, FewCfg<DK, 
         }
       }
       if (MAPS == 2) {
-        // warp c: column c; o = map 0 - lambda map 1, RMS norm over the row, store
+        // warp c < 4: columns c and 4 + c; o = map 0 - lambda map 1, RMS norm over the row, store
         __syncthreads();
         const int c = c_base + warp;
         if (warp < COLS && c < cols_all) {
@@ -931,7 +940,7 @@ __global__ void __launch_bounds__(FewCfg<DK, DV, NT, MAPS>::THREADS, FewCfg<DK, 
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const int d = 64 * i + 2 * lane + e;
-              const float x = d < a.dv ? ex[warp * DV + d] - lam * ex[(8 + warp) * DV + d] : 0.f;
+              const float x = d < a.dv ? ex[warp * DV + d] - lam * ex[(4 + warp) * DV + d] : 0.f;
               y[2 * i + e] = x;
               ss = fmaf(x, x, ss);
             }
@@ -968,7 +977,7 @@ cudaError_t launch_few_t(const AttnArgs &a, cudaStream_t s) {
   static_assert(C::SMEM <= 227 * 1024, "shared memory");
   // weights and sums of every CTA's partial and the teams' sums, at the merge
   static_assert(C::SMEM >= 2 * 152 * C::NC * 12 + C::THREADS * 16 || C::CTAS == 1, "merge");
-  static_assert(MAPS == 1 || NT == 2, "differential: one tile of columns per map");
+  static_assert(MAPS == 1 || NT == 1, "differential: one tile of columns for both maps");
   auto kern = few_kernel<DK, DV, NT, MAPS>;
   cudaError_t e = set_dynamic_smem(reinterpret_cast<const void *>(kern), C::SMEM);
   if (e != cudaSuccess) return e;

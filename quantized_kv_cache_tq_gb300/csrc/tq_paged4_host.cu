@@ -216,7 +216,8 @@ static tq_status rows_call(bool set, const tq_paged4 *k, const tq_paged4 *v, con
     return TQ_ERR_INVALID_ARG;
   if (n_rows == 0) return TQ_OK;
   if (!al(kp, 16) || !al(vp, 16) || !al(slots, 8) || (dev_status && !al(dev_status, 4))) return TQ_ERR_INVALID_ARG;
-  if (n_rows > 0x7fffffffLL || n_rows * (k->n_kv_heads + v->n_kv_heads) > 0xfffffffffLL) return TQ_ERR_INVALID_ARG;
+  // (at most 16 lanes a row and head, 256 to a CTA, 2^31 - 1 CTAs)
+  if (n_rows > 0x7fffffffLL || n_rows * (k->n_kv_heads + v->n_kv_heads) > 0x7fffffe00LL) return TQ_ERR_INVALID_ARG;
   RowsArgs a;
   const tq_paged4 *c[2] = {k, v};
   const void *p[2] = {kp, vp};
@@ -234,6 +235,7 @@ static tq_status rows_call(bool set, const tq_paged4 *k, const tq_paged4 *v, con
   a.slots = slots;
   a.status = dev_status;
   a.n_rows = n_rows;
+  a.k_blocks = 0;
   a.page_shift = shift_of(k->page_size, 16, 1024);
   a.n_cells = static_cast<int64_t>(k->n_pages) << a.page_shift;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
