@@ -100,5 +100,9 @@ struct AttnArgs {
 bool few_supported(int wk, int wv, bool diff);
 cudaError_t launch_few(const AttnArgs &a, int columns, cudaStream_t s);
 
+// Prompt kernel: 256-row tiles on the tcgen05 tensor cores.
+bool prefill_supported(int wk, int wv);
+cudaError_t launch_prefill(const AttnArgs &a, cudaStream_t s);
+
 }  // namespace p4
 }  // namespace tq

@@ -61,20 +61,52 @@ bool few_supported(int wk, int wv, bool diff) {
   return (wk == wv) || (wk == 256 && wv == 128);
 }
 
-// Workspace: status word, arrival counters (one per CTA, in a place that does not
-// depend on the shape, so that calls of different shapes can share it), partials.
+// Workspace: status word, arrival counters of the few-row kernel (one per CTA, in a place that does not
+// depend on the shape, so that calls of different shapes can share it), partials of either kernel.
 constexpr size_t kCountersOff = 256;
 struct Layout {
   size_t part_off, total;
 };
 
-static Layout few_layout(int wv, bool diff) {
+static Layout few_layout(int wv) {
   Layout L;
   const size_t ctas = 2 * static_cast<size_t>(sm_count());         // at most two per SM
   const size_t columns = 16, tiles = 2;                            // the larger of the two column widths
   L.part_off = kCountersOff + up(sizeof(int32_t) * ctas, 256);
   L.total = L.part_off + sizeof(float) * 2 * ctas * (4 * columns + tiles * (wv / 16) * 128);
-  (void)diff;
+  return L;
+}
+
+// Key splits of the prompt kernel's row tiles: the count whose launch is estimated to end first, in key tiles
+// of one CTA: rounds of CTAs over the SMs times (key tiles per CTA + 6 for its set-up and epilogue, + 4 where
+// partial results are written and merged).
+constexpr int kMaxSplit = 16;
+static int prefill_splits(int64_t n_rows, int group, int k_heads, int64_t max_len) {
+  const int64_t ctas = (n_rows * group + 255) / 256 * k_heads, tiles = (max_len + 127) / 128, sms = sm_count();
+  int best = 1;
+  int64_t least = 0;
+  for (int c = 1; c <= kMaxSplit && (c == 1 || tiles / c >= 4); ++c) {
+    const int64_t cost = (ctas * c + sms - 1) / sms * ((tiles + c - 1) / c + 6 + (c > 1 ? 4 : 0));
+    if (c == 1 || cost < least) {
+      best = c;
+      least = cost;
+    }
+  }
+  return best;
+}
+
+// Whether a ragged call goes to the prompt kernel.  Up to 16 query columns per KV head (two tiles of the few-row
+// kernel) the 256-row tiles of the prompt kernel would stand nearly empty.
+static bool takes_prefill(const tq_paged4 *k, const tq_paged4 *v, int64_t rows_per_seq, int group) {
+  return prefill_supported(row_width(k->head_dim), row_width(v->head_dim)) && rows_per_seq * group > 16;
+}
+
+static Layout prefill_layout(const tq_paged4 *k, const tq_paged4 *v, int n_heads, int64_t n_rows, int n_split) {
+  const int wv = row_width(v->head_dim), maps = k->n_kv_heads / v->n_kv_heads;
+  Layout L = few_layout(wv);
+  if (!prefill_supported(row_width(k->head_dim), wv) || (n_split == 1 && maps == 1)) return L;
+  const size_t part = static_cast<size_t>(n_rows) * n_heads * maps * n_split * (wv + 4) * sizeof(float);
+  if (L.part_off + part > L.total) L.total = L.part_off + part;
   return L;
 }
 
@@ -110,7 +142,13 @@ static tq_status attend(const Call &c) {
   if (!al(c.block_table, 4) || !al(c.seq_len, 4) || (c.ragged && !al(c.q_start, 4)) || !al(c.q, 16) || !al(c.out, 16))
     return TQ_ERR_INVALID_ARG;
   const int wk = row_width(c.k->head_dim), wv = row_width(c.v->head_dim);
-  const Layout L = few_layout(wv, c.diff);
+  const int group = c.n_heads / c.v->n_kv_heads;
+  const int64_t rows = c.ragged ? (c.max_rows ? c.max_rows : c.n_rows) : 1;
+  const bool prompt = c.ragged && takes_prefill(c.k, c.v, rows, group);
+  const int n_split = prompt ? prefill_splits(c.n_rows, group, c.k->n_kv_heads,
+                                              c.max_len ? c.max_len : static_cast<int64_t>(c.max_pages) * c.k->page_size)
+                             : 1;
+  const Layout L = prompt ? prefill_layout(c.k, c.v, c.n_heads, c.n_rows, n_split) : few_layout(wv);
   if (!al(c.workspace, 256) || c.workspace_bytes < L.total) return TQ_ERR_WORKSPACE;
   AttnArgs a;
   memset(&a, 0, sizeof(a));
@@ -136,7 +174,7 @@ static tq_status attend(const Call &c) {
   a.page_shift = shift_of(c.k->page_size, 16, 1024);
   a.n_heads = c.n_heads;
   a.n_kv_heads = c.v->n_kv_heads;
-  a.group = c.n_heads / c.v->n_kv_heads;
+  a.group = group;
   a.dk = c.k->head_dim;
   a.dv = c.v->head_dim;
   a.wk = wk;
@@ -147,8 +185,15 @@ static tq_status attend(const Call &c) {
   a.scale_log2 = c.scale * 1.4426950408889634f;
   a.eps = c.eps;
   a.out_scale = c.out_scale;
-  const int64_t rows = c.ragged ? (c.max_rows ? c.max_rows : c.n_rows) : 1;
-  const int columns = rows * a.group > 8 ? 16 : 8;
+  a.n_split = n_split;
+  if (prompt) {
+    const int64_t tiles = c.n_rows * group / 256 + c.n_seq;        // upper bound over ragged sequences
+    if (tiles * n_split * c.k->n_kv_heads > 0x7fffffffLL || (c.n_rows * c.n_heads + 7) / 8 > 0x7fffffffLL)
+      return TQ_ERR_UNSUPPORTED;
+    a.n_tiles = static_cast<int32_t>(tiles);
+    return mapped(launch_prefill(a, static_cast<cudaStream_t>(c.stream)));
+  }
+  const int columns = rows * group > 8 ? 16 : 8;
   return mapped(launch_few(a, columns, static_cast<cudaStream_t>(c.stream)));
 }
 
@@ -256,13 +301,16 @@ tq_status tq_paged4_get_rows(const tq_paged4 *k, const tq_paged4 *v, void *k_dst
 
 size_t tq_paged4_decode_workspace(const tq_paged4 *k, const tq_paged4 *v, int n_heads, int n_seq) {
   if (heads_ok(k, v, n_heads, n_seq, is_diff(k, v)) != TQ_OK) return 0;
-  return few_layout(row_width(v->head_dim), is_diff(k, v)).total;
+  return few_layout(row_width(v->head_dim)).total;
 }
 
 size_t tq_paged4_prefill_workspace(const tq_paged4 *k, const tq_paged4 *v, int n_heads, int n_seq, int64_t n_rows,
                                    int64_t max_len) {
   if (heads_ok(k, v, n_heads, n_seq, is_diff(k, v)) != TQ_OK || n_rows < 0 || max_len < 0) return 0;
-  return few_layout(row_width(v->head_dim), is_diff(k, v)).total;
+  if (n_rows > 0x7fffffffLL / n_heads) return 0;
+  // (max_len 0, the call's "table's capacity": room for any split)
+  const int n_split = max_len ? prefill_splits(n_rows, n_heads / v->n_kv_heads, k->n_kv_heads, max_len) : kMaxSplit;
+  return prefill_layout(k, v, n_heads, n_rows, n_split).total;
 }
 
 tq_status tq_paged4_decode(const tq_paged4 *k, const tq_paged4 *v, const int32_t *block_table, int max_pages,
