@@ -5,13 +5,16 @@
 //
 // A CTA takes two tiles A, B of 128 rows -- a row is a (query, head) pair of one
 // sequence and KV head -- over key tiles of 128, which both tiles share, so that a
-// key tile is unpacked once for 256 rows.  16 warps:
-//   0-3, 4-7   softmax of tile A, B: one row per thread (TMEM lane);
-//   8-11       unpack: one key per thread, its packed rows held in registers one
+// key tile is unpacked once for 256 rows.  24 warps:
+//   0-7, 8-15  softmax of tile A, B: two threads per row (TMEM lane), 64 keys each;
+//   16-19      unpack: one key per thread, its packed rows held in registers one
 //              tile ahead, written as operand tiles (double buffered);
-//   12         one thread issues the products: S = Q K^T of both tiles into TMEM,
+//   20         one thread issues the products: S = Q K^T of both tiles into TMEM,
 //              O += P V with P written over S.  While one tile is in its softmax,
 //              the other one's products run.
+// The code of all roles has to stay small: with the products' loops unrolled, their
+// one warp waited for instructions (1390 against 1248 us at 2048 rows over 32768
+// cells, 8 KV heads, with one thread per row and its 128 keys unrolled).
 //
 // Numbers, so that 16-bit operands cost no accuracy beyond the output's own:
 // - Scores: K's operand is the code itself (a nibble masked in place reads as the
@@ -45,8 +48,10 @@ namespace p4 {
 namespace pre {
 
 constexpr int BM = 128, BN = 128;             // rows of a tile, keys of a key tile
-constexpr int NT = 512;
-constexpr int REG_SOFTMAX = 184, REG_UNPACK = 96, REG_MMA = 40;   // 2 x 184 + 96 + 40 <= 4 x 128
+constexpr int HK = BN / 2;                    // keys of a softmax thread
+constexpr int NT = 768;
+constexpr int W_UNPACK = 16, W_MMA = 20;      // first warps of the roles after the softmax
+constexpr int REG_SOFTMAX = 88, REG_UNPACK = 96, REG_MMA = 32;    // of 80 at the launch: 4 x 88 + 96 + 32 = 6 x 80
 
 template <int DK, int DV>
 struct Cfg {
@@ -59,14 +64,17 @@ struct Cfg {
   static constexpr uint32_t SQ = 0;
   static constexpr uint32_t SKV = 2 * Q_BYTES;                 // two buffers of (K, V)
   static constexpr uint32_t KV_BYTES = K_BYTES + V_BYTES;
-  static constexpr uint32_t SSC = SKV + 2 * KV_BYTES;          // [buffer][key] scale of a score
-  static constexpr uint32_t STAU = SSC + 2 * BN * 4;           // [buffer][32 keys] (tau, 2^-tau)
-  static constexpr uint32_t TOTAL = STAU + 2 * 4 * 8;
+  // (K of a tile may be written as soon as its buffer's scores are done, their softmax still running: four of these)
+  static constexpr uint32_t SSC = SKV + 2 * KV_BYTES;          // [j & 3][key] scale of a score
+  static constexpr uint32_t STAU = SSC + 4 * BN * 4;           // [j & 3][32 keys] (tau, 2^-tau)
+  static constexpr uint32_t SROW = STAU + 4 * 4 * 8;           // [tile][half][row] exchange between a row's threads
+  static constexpr uint32_t TOTAL = SROW + 2 * 2 * BM * 8;
   static constexpr int SKS = KC / 2, PKS = BN / 16;            // k steps of S and of PV
 };
 
 struct Bars {
-  uint64_t kv[2];         // key tile j (buffer j & 1) written            phase j >> 1
+  uint64_t k[2], v[2];    // K, V of key tile j (buffer j & 1) written    phase j >> 1
+  uint64_t kf[2];         // S_j of every row tile computed: K is free    phase j >> 1
   uint64_t s[2];          // S_j of tile X computed                       phase j
   uint64_t p[2];          // P_j of tile X written                        phase j
   uint64_t pv[2][2];      // PV_j of tile X (buffer j & 1) computed       phase j >> 1
@@ -80,13 +88,32 @@ __device__ __forceinline__ void mma_ta(uint32_t d, uint32_t a, uint64_t b, uint3
       "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(acc)));
 }
 
-__device__ __forceinline__ void st16(uint32_t taddr, const uint32_t *r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
-          taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
+__device__ __forceinline__ void st8(uint32_t taddr, const uint32_t *r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
+// Bounded wait for phase `parity` of `bar` by a whole warp.  Without a suspend-time hint: with one, a warp that
+// found the phase open slept on past its end, on every step of the chain score - softmax - product (WAIT_FIG).
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity) {
+  const uint32_t at = tc::smem_u32(bar);
+  for (int it = 0; it < (1 << 22); ++it) {
+    uint32_t ok;
+    asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+                 : "=r"(ok)
+                 : "r"(at), "r"(parity)
+                 : "memory");
+    if (__all_sync(0xffffffffu, ok != 0)) return true;
+  }
+  return false;
+}
+
+// one lane of the warp, the same every time
+__device__ __forceinline__ bool elect() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
 }
 
 __device__ __forceinline__ uint32_t bits(__half2 h) { return *reinterpret_cast<const uint32_t *>(&h); }
@@ -157,37 +184,43 @@ __global__ void __launch_bounds__(pre::NT, 1) prefill_kernel(const AttnArgs a) {
   const int t_lo = static_cast<int>(static_cast<long long>(tiles_all) * split / n_split);
   const int n_t = static_cast<int>(static_cast<long long>(tiles_all) * (split + 1) / n_split) - t_lo;
 
-  if (warp == 12) tc::tmem_alloc<512>(&tmem_slot);
+  if (warp == W_MMA) tc::tmem_alloc<512>(&tmem_slot);
   if (tid == NT - 1) {
     for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(&bars.kv[i], 4);
+      tc::mbar_init(&bars.k[i], 4);
+      tc::mbar_init(&bars.v[i], 4);
+      tc::mbar_init(&bars.kf[i], n_q);
       tc::mbar_init(&bars.s[i], 1);
-      tc::mbar_init(&bars.p[i], 4);
+      tc::mbar_init(&bars.p[i], 8);
       tc::mbar_init(&bars.pv[i][0], 1);
       tc::mbar_init(&bars.pv[i][1], 1);
     }
     tc::mbar_init_fence();
   }
 
-  // ---- Q: the softmax threads bring their rows
-  const int X = warp >> 2;                    // 0, 1: softmax of tile A, B
+  // ---- Q: the softmax threads bring their rows, half of the dims each
+  const int X = warp >> 3, half = (warp >> 2) & 1;                     // X 0, 1: softmax of tile A, B
   const int row = tid & (BM - 1);
   const int r = r0 + X * BM + row;            // row of the sequence
   const bool row_ok = X < n_q && r < rows_all;
   float fx = 1.f;                             // x = fx s_t (score), fx > 0
-  if (X < n_q) {
+  {
+    constexpr int NC = DK / 16;               // 8-element chunks of a thread
+    const bool here = X < n_q;
     const int qi = row_ok ? r / G : 0, head = hv * G + (row_ok ? r - qi * G : 0);
     const uint16_t *src = static_cast<const uint16_t *>(a.q) + (static_cast<int64_t>(sw.row0) + qi) * a.q_stride +
                           static_cast<int64_t>(maps * head + map) * a.dk;
-    uint4 raw[DK / 8];
-#pragma unroll
-    for (int c = 0; c < DK / 8; ++c) {
-      raw[c] = make_uint4(0, 0, 0, 0);
-      if (row_ok && 8 * c < a.dk) raw[c] = __ldg(reinterpret_cast<const uint4 *>(src + 8 * c));
-    }
+    float2 *ex = reinterpret_cast<float2 *>(smem + C::SROW) + (X & 1) * 2 * BM;     // [half][row]: (max, sum)
+    uint4 raw[NC];
     float mx = 0.f, sum = 0.f;
 #pragma unroll
-    for (int c = 0; c < DK / 8; ++c) {
+    for (int c = 0; c < NC; ++c) {
+      const int d = 8 * (half * NC + c);
+      raw[c] = make_uint4(0, 0, 0, 0);
+      if (row_ok && d < a.dk) raw[c] = __ldg(reinterpret_cast<const uint4 *>(src + d));
+    }
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
       float v[8];
       few::unpack8(raw[c], a.bf16, v);
 #pragma unroll
@@ -196,35 +229,46 @@ __global__ void __launch_bounds__(pre::NT, 1) prefill_kernel(const AttnArgs a) {
         sum += v[e];
       }
     }
-    // largest entry in [2^ex, 2^(ex + 1)) -> [2^12, 2^13); the scale's sign goes into q, a scale of 0 makes it 0
-    const int ex = mx > 0.f ? static_cast<int>(__float_as_uint(mx) >> 23) - 127 : 0;
-    const float s1 = __uint_as_float(static_cast<uint32_t>((12 - ex) / 2 + 127) << 23);
-    const float s2 = __uint_as_float(static_cast<uint32_t>((12 - ex) - (12 - ex) / 2 + 127) << 23) *
-                     (a.scale_log2 > 0.f ? 1.f : a.scale_log2 < 0.f ? -1.f : 0.f);
-    if (a.scale_log2 != 0.f) fx = fmaxf(fabsf(a.scale_log2) * exp2f(static_cast<float>(12 + ex)), 1e-37f);
-    unsigned char *dst = smem + C::SQ + X * C::Q_BYTES + (row >> 3) * 128 + (row & 7) * 16;
+    if (here) ex[half * BM + row] = make_float2(mx, sum);
+    __syncthreads();
+    if (here) {
+      const float2 e0 = ex[row], e1 = ex[BM + row];
+      mx = fmaxf(e0.x, e1.x);
+      sum = e0.y + e1.y;
+      // largest entry in [2^e, 2^(e + 1)) -> [2^12, 2^13); the scale's sign goes into q, a scale of 0 makes it 0
+      const int e = mx > 0.f ? static_cast<int>(__float_as_uint(mx) >> 23) - 127 : 0;
+      const float s1 = __uint_as_float(static_cast<uint32_t>((12 - e) / 2 + 127) << 23);
+      const float s2 = __uint_as_float(static_cast<uint32_t>((12 - e) - (12 - e) / 2 + 127) << 23) *
+                       (a.scale_log2 > 0.f ? 1.f : a.scale_log2 < 0.f ? -1.f : 0.f);
+      if (a.scale_log2 != 0.f) fx = fmaxf(fabsf(a.scale_log2) * exp2f(static_cast<float>(12 + e)), 1e-37f);
+      unsigned char *dst = smem + C::SQ + X * C::Q_BYTES + (row >> 3) * 128 + (row & 7) * 16;
 #pragma unroll
-    for (int c = 0; c < DK / 8; ++c) {
-      float v[8];
-      few::unpack8(raw[c], a.bf16, v);
+      for (int c = 0; c < NC; ++c) {
+        float v[8];
+        few::unpack8(raw[c], a.bf16, v);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = v[e] * s1 * s2 * ((e & 1) ? 0.0625f : 1.f);
-      // the order in which a code word unpacks: (0, 4), (1, 5), (2, 6), (3, 7)
-      *reinterpret_cast<uint4 *>(dst + c * 2048) =
-          make_uint4(few::half2_bits(v[0], v[4]), few::half2_bits(v[1], v[5]), few::half2_bits(v[2], v[6]),
-                     few::half2_bits(v[3], v[7]));
+        for (int i = 0; i < 8; ++i) v[i] = v[i] * s1 * s2 * ((i & 1) ? 0.0625f : 1.f);
+        // the order in which a code word unpacks: (0, 4), (1, 5), (2, 6), (3, 7)
+        *reinterpret_cast<uint4 *>(dst + (half * NC + c) * 2048) =
+            make_uint4(few::half2_bits(v[0], v[4]), few::half2_bits(v[1], v[5]), few::half2_bits(v[2], v[6]),
+                       few::half2_bits(v[3], v[7]));
+      }
+      if (half == 0) {
+        const float qs = sum * s1 * s2 * 0x1p-20f;
+        const __half h0 = __float2half_rn(qs);
+        const __half h1 = __float2half_rn(qs - __half2float(h0));
+        const __half h2 = __float2half_rn(qs - __half2float(h0) - __half2float(h1));
+        const __half z = __float2half_rn(0.f);
+        *reinterpret_cast<uint4 *>(dst + (DK / 8) * 2048) =
+            make_uint4(bits(__halves2half2(h0, h1)), bits(__halves2half2(h2, h0)), bits(__halves2half2(h1, z)), 0);
+      } else {
+        *reinterpret_cast<uint4 *>(dst + (DK / 8 + 1) * 2048) = make_uint4(0, 0, 0, 0);
+      }
     }
-    const float qs = sum * s1 * s2 * 0x1p-20f;
-    const __half h0 = __float2half_rn(qs);
-    const __half h1 = __float2half_rn(qs - __half2float(h0));
-    const __half h2 = __float2half_rn(qs - __half2float(h0) - __half2float(h1));
-    const __half z = __float2half_rn(0.f);
-    *reinterpret_cast<uint4 *>(dst + (DK / 8) * 2048) =
-        make_uint4(bits(__halves2half2(h0, h1)), bits(__halves2half2(h2, h0)), bits(__halves2half2(h1, z)), 0);
-    *reinterpret_cast<uint4 *>(dst + (DK / 8 + 1) * 2048) = make_uint4(0, 0, 0, 0);
-  } else if (warp >= 8 && warp < 12) {
+  }
+  if (warp >= W_UNPACK && warp < W_MMA) {
     // the unused half of the offset's k step
-    const int key = tid - 256;
+    const int key = tid - 32 * W_UNPACK;
 #pragma unroll
     for (int b = 0; b < 2; ++b)
       *reinterpret_cast<uint4 *>(smem + C::SKV + b * C::KV_BYTES + (key >> 3) * (C::KC * 128) + (DK / 8 + 1) * 128 +
@@ -239,48 +283,61 @@ __global__ void __launch_bounds__(pre::NT, 1) prefill_kernel(const AttnArgs a) {
   constexpr uint32_t TS = 0, TO = 256;        // TMEM columns: S / P of tile X at 128 X, O at 256 + 128 X
 
   float R = -INFINITY, l = 0.f;
-  if (warp >= 12) {
+  if (warp >= W_MMA) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_MMA));
-    if (warp == 12 && lane == 0 && n_t > 0) {
+    if (warp == W_MMA) {
       // ===================== products =====================
+      // The whole warp goes through the loop, so that descriptors stay in uniform registers; one lane issues.
       constexpr uint32_t ID_S = tc::idesc_f16(BM, BN, false, false);
       constexpr uint32_t ID_PV = tc::idesc_f16(BM, DV, false, true);
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      const bool one = elect();
+      const uint64_t q0 = tc::sdesc(sbase + C::SQ, 2048, 128);
+      const uint64_t k0 = tc::sdesc(sbase + C::SKV, 128, C::KC * 128);
+      const uint64_t v0 = tc::sdesc(sbase + C::SKV + C::K_BYTES, C::VC * 128, 128);
       bool ok = true;
-      auto issue_pv = [&](int x, int j) {
-        const uint64_t v = tc::sdesc(sbase + C::SKV + (j & 1) * C::KV_BYTES + C::K_BYTES, C::VC * 128, 128);
-#pragma unroll
-        for (int ks = 0; ks < C::PKS; ++ks)
-          mma_ta(tmem + TO + 128 * x, tmem + TS + 128 * x + 8 * ks, v + ((ks * 2 * C::VC * 128) >> 4), ID_PV,
-                 j > 0 || ks > 0);
-        tc::mma_commit(&bars.pv[x][j & 1]);
-      };
-      for (int j = 0; j <= n_t && ok; ++j)
-        for (int x = 0; x < n_q && ok; ++x) {
-          if (j > 0) {
-            ok = tc::mbar_wait(&bars.p[x], (j - 1) & 1);
+      for (int j = 0; j <= n_t && ok && n_t > 0; ++j) {
+        const uint64_t kv = static_cast<uint64_t>((j & 1) * (C::KV_BYTES >> 4));
+        const uint64_t kv_last = static_cast<uint64_t>(((j - 1) & 1) * (C::KV_BYTES >> 4));
+#pragma unroll 1
+        for (int x = 0; x < n_q; ++x) {
+          if (j > 0) {                        // PV of the tile before
+            ok = wait_warp(&bars.p[x], (j - 1) & 1);
+            if (ok && x == 0) ok = wait_warp(&bars.v[(j - 1) & 1], ((j - 1) >> 1) & 1);
             if (!ok) break;
             tc::fence_after_sync();
-            issue_pv(x, j - 1);
+            if (one) {
+#pragma unroll
+              for (int ks = 0; ks < C::PKS; ++ks)
+                mma_ta(tm + TO + 128 * x, tm + TS + 128 * x + 8 * ks, v0 + kv_last + ((ks * 2 * C::VC * 128) >> 4), ID_PV,
+                       j > 1 || ks > 0);
+              tc::mma_commit(&bars.pv[x][(j - 1) & 1]);
+            }
+            __syncwarp();
           }
           if (j == n_t) continue;
-          if (x == 0) ok = tc::mbar_wait(&bars.kv[j & 1], (j >> 1) & 1);
+          if (x == 0) ok = wait_warp(&bars.k[j & 1], (j >> 1) & 1);
           // S_j goes where P_{j-1} stands: its product has to be done
-          if (ok && j > 0) ok = tc::mbar_wait(&bars.pv[x][(j - 1) & 1], ((j - 1) >> 1) & 1);
+          if (ok && j > 0) ok = wait_warp(&bars.pv[x][(j - 1) & 1], ((j - 1) >> 1) & 1);
           if (!ok) break;
           tc::fence_after_sync();
-          const uint64_t q = tc::sdesc(sbase + C::SQ + x * C::Q_BYTES, 2048, 128);
-          const uint64_t k = tc::sdesc(sbase + C::SKV + (j & 1) * C::KV_BYTES, 128, C::KC * 128);
+          if (one) {
 #pragma unroll
-          for (int ks = 0; ks < C::SKS; ++ks)
-            tc::mma_f16(tmem + TS + 128 * x, q + ((ks * 4096) >> 4), k + ((ks * 256) >> 4), ID_S, ks > 0);
-          tc::mma_commit(&bars.s[x]);
+            for (int ks = 0; ks < C::SKS; ++ks)
+              tc::mma_f16(tm + TS + 128 * x, q0 + x * (C::Q_BYTES >> 4) + ((ks * 4096) >> 4), k0 + kv + ((ks * 256) >> 4),
+                          ID_S, ks > 0);
+            tc::mma_commit(&bars.s[x]);
+            tc::mma_commit(&bars.kf[j & 1]);
+          }
+          __syncwarp();
         }
+      }
       if (!ok) s_fail = 1;
     }
-  } else if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_UNPACK));
+  } else if (warp >= W_UNPACK) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REG_UNPACK));
     // ===================== unpack: one key of the tile per thread =====================
-    const int key = tid - 256;
+    const int key = tid - 32 * W_UNPACK;
     const int32_t *table = a.block_table + static_cast<int64_t>(s_seq) * a.max_pages;
     const int mask = (1 << a.page_shift) - 1;
     auto page_of = [&](int j) {
@@ -330,11 +387,18 @@ __global__ void __launch_bounds__(pre::NT, 1) prefill_kernel(const AttnArgs a) {
     bool ok = true;
     for (int j = 0; j < n_t; ++j) {
       const int b = j & 1;
-      if (j >= 2)                             // the buffer's last users
-        for (int x = 0; x < n_q && ok; ++x) ok = tc::mbar_wait(&bars.pv[x][b], ((j - 2) >> 1) & 1);
-      if (!__all_sync(0xffffffffu, ok)) { s_fail = 1; break; }
+      if (j >= 2) ok = wait_warp(&bars.kf[b], ((j - 2) >> 1) & 1);      // the K buffer's last users
+      if (!ok) { s_fail = 1; break; }
       unsigned char *kd = smem + C::SKV + b * C::KV_BYTES + (key >> 3) * (C::KC * 128) + (key & 7) * 16;
       unsigned char *vd = smem + C::SKV + b * C::KV_BYTES + C::K_BYTES + (key >> 3) * (C::VC * 128) + (key & 7) * 16;
+      // exponent of the 32 keys' values (with K: the softmax needs it)
+      const float2 vsc = __half22float2(as_half2(vsm));
+      const float top = fmaxf(fabsf(vsc.y), fabsf(fmaf(15.f, vsc.x, vsc.y)));
+      int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+      e = min(30, max(-30, __reduce_max_sync(0xffffffffu, e)));
+      const float dn = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);            // 2^-tau
+      if (lane == 0) 
+        reinterpret_cast<float2 *>(smem + C::STAU)[(j & 3) * 4 + (warp - W_UNPACK)] = make_float2(static_cast<float>(e), dn);
       {
         float2 sm = __half22float2(as_half2(ksm));
         float off = __fdividef(sm.y, sm.x);
@@ -349,7 +413,7 @@ __global__ void __launch_bounds__(pre::NT, 1) prefill_kernel(const AttnArgs a) {
         *reinterpret_cast<uint4 *>(kd + (DK / 8) * 128) =
             make_uint4(bits(__halves2half2(hi, hi)), bits(__halves2half2(hi, lo)),
                        bits(__halves2half2(lo, __float2half_rn(0.f))), 0);
-        reinterpret_cast<float *>(smem + C::SSC)[b * BN + key] = sm.x;
+        reinterpret_cast<float *>(smem + C::SSC)[(j & 3) * BN + key] = sm.x;
 #pragma unroll
         for (int i = 0; i < DK / 32; ++i) {
           const uint32_t w[4] = {kraw[i].x & keep, kraw[i].y & keep, kraw[i].z & keep, kraw[i].w & keep};
@@ -361,17 +425,16 @@ __global__ void __launch_bounds__(pre::NT, 1) prefill_kernel(const AttnArgs a) {
           }
         }
       }
+      tc::fence_async_smem();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&bars.k[b]);
       rw = row_of(j + 1, page);
       load_k(rw);                             // on its way while the values are unpacked
+      if (j >= 2)                             // the V buffer's last users
+        for (int x = 0; x < n_q && ok; ++x) ok = wait_warp(&bars.pv[x][b], ((j - 2) >> 1) & 1);
+      if (!ok) { s_fail = 1; break; }
       {
-        const float2 sm = __half22float2(as_half2(vsm));
-        const float top = fmaxf(fabsf(sm.y), fabsf(fmaf(15.f, sm.x, sm.y)));
-        int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
-        e = min(30, max(-30, __reduce_max_sync(0xffffffffu, e)));
-        const float dn = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);          // 2^-tau
-        if (lane == 0)
-          reinterpret_cast<float2 *>(smem + C::STAU)[b * 4 + (warp - 8)] = make_float2(static_cast<float>(e), dn);
-        const __half2 vs = __float2half2_rn(sm.x * dn), vm = __float2half2_rn(sm.y * dn);
+        const __half2 vs = __float2half2_rn(vsc.x * dn), vm = __float2half2_rn(vsc.y * dn);
         const __half2 k1024 = as_half2(0x64006400u), k16 = as_half2(0x2c002c00u), k64 = as_half2(0xd400d400u);
 #pragma unroll
         for (int i = 0; i < DV / 32; ++i) {
@@ -394,34 +457,39 @@ __global__ void __launch_bounds__(pre::NT, 1) prefill_kernel(const AttnArgs a) {
       page = page_of(j + 2);
       tc::fence_async_smem();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&bars.kv[b]);
+      if (lane == 0) tc::mbar_arrive(&bars.v[b]);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REG_SOFTMAX));
-    // ===================== softmax: one row per thread =====================
+    // ===================== softmax: 64 keys of a row per thread =====================
     const uint32_t lane_off = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const uint32_t ts = tmem + lane_off + TS + 128 * X, to = tmem + lane_off + TO + 128 * X;
+    const int pair = 1 + 4 * X + (warp & 3);                            // named barrier of the rows' two warps
+    float *ex = reinterpret_cast<float *>(smem + C::SROW) + X * 2 * BM; // [half][row]
     const int lim = row_ok ? limit_of(r) : 0;
     const float2 fx2 = make_float2(fx, fx);
     bool ok = true;
     for (int j = 0; j < (X < n_q ? n_t : 0); ++j) {
       const int b = j & 1;
-      ok = tc::mbar_wait(&bars.s[X], j & 1);
-      if (ok) ok = tc::mbar_wait(&bars.kv[b], (j >> 1) & 1);            // the tile's scales
-      if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+      if (ok) {
+        ok = wait_warp(&bars.s[X], j & 1);
+        if (ok) ok = wait_warp(&bars.k[b], (j >> 1) & 1);               // the tile's scales
+      }
+      if (!ok) {                              // a wait ran out: the row's other warp still meets this one
+        tc::named_sync(pair, 64);
+        continue;
+      }
       tc::fence_after_sync();
-      float y[BN];
+      float y[HK];
       {
         uint32_t *u = reinterpret_cast<uint32_t *>(y);
-        tc::tmem_ld32(ts, u);
-        tc::tmem_ld32(ts + 32, u + 32);
-        tc::tmem_ld32(ts + 64, u + 64);
-        tc::tmem_ld32(ts + 96, u + 96);
+        tc::tmem_ld32(ts + HK * half, u);
+        tc::tmem_ld32(ts + HK * half + 32, u + 32);
         tc::tmem_wait_ld();
       }
-      const float4 *sc = reinterpret_cast<const float4 *>(smem + C::SSC + b * BN * 4);
+      const float4 *sc = reinterpret_cast<const float4 *>(smem + C::SSC + ((j & 3) * BN + HK * half) * 4);
 #pragma unroll
-      for (int i = 0; i < BN / 4; ++i) {
+      for (int i = 0; i < HK / 4; ++i) {
         const float4 s4 = sc[i];
         const float2 u = mul2(make_float2(y[4 * i], y[4 * i + 1]), make_float2(s4.x, s4.y));
         const float2 w = mul2(make_float2(y[4 * i + 2], y[4 * i + 3]), make_float2(s4.z, s4.w));
@@ -430,16 +498,16 @@ __global__ void __launch_bounds__(pre::NT, 1) prefill_kernel(const AttnArgs a) {
         y[4 * i + 2] = w.x;
         y[4 * i + 3] = w.y;
       }
-      const int nvis = lim - (t_lo + j) * BN;                           // keys of the tile that the row sees
-      if (__any_sync(0xffffffffu, nvis < BN)) {
+      const int nvis = lim - (t_lo + j) * BN - HK * half;               // of the thread's keys, those that the row sees
+      if (__any_sync(0xffffffffu, nvis < HK)) {
 #pragma unroll
-        for (int i = 0; i < BN; ++i)
+        for (int i = 0; i < HK; ++i)
           if (i >= nvis) y[i] = -INFINITY;
       }
-      const float2 *tau = reinterpret_cast<const float2 *>(smem + C::STAU) + 4 * b;
+      const float2 *tau = reinterpret_cast<const float2 *>(smem + C::STAU) + 4 * (j & 3) + 2 * half;
       float top = -INFINITY;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
+      for (int c = 0; c < 2; ++c) {
         float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
         for (int i = 0; i < 32; i += 4) {
@@ -448,46 +516,54 @@ __global__ void __launch_bounds__(pre::NT, 1) prefill_kernel(const AttnArgs a) {
         }
         top = fmaxf(top, fmaf(fmaxf(m0, m1), fx, tau[c].x));
       }
+      // (the other thread read the last value before it wrote its weights, hence before this S)
+      ex[half * BM + row] = top;
+      tc::fence_before_sync();                // both warps' scores are read before either writes weights over them
+      tc::named_sync(pair, 64);
+      tc::fence_after_sync();
+      top = fmaxf(top, ex[(half ^ 1) * BM + row]);
       const bool raise = top > R + 8.f;
       if (__any_sync(0xffffffffu, raise)) {
         const float f = raise ? exp2f(R - top) : 1.f;                   // 0 at the first raise
         if (raise) R = top;
         l *= f;
         if (j > 0) {
-          ok = tc::mbar_wait(&bars.pv[X][(j - 1) & 1], ((j - 1) >> 1) & 1);    // O stands still
-          if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+          ok = wait_warp(&bars.pv[X][(j - 1) & 1], ((j - 1) >> 1) & 1);        // O stands still
+          if (!ok) continue;
           tc::fence_after_sync();
 #pragma unroll 1
-          for (int c = 0; c < DV; c += 16) {
-            uint32_t o[16];
-            asm volatile(
-                "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-                : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]), "=r"(o[7]),
-                  "=r"(o[8]), "=r"(o[9]), "=r"(o[10]), "=r"(o[11]), "=r"(o[12]), "=r"(o[13]), "=r"(o[14]), "=r"(o[15])
-                : "r"(to + c));
+          for (int c = half * (DV / 2); c < (half + 1) * (DV / 2); c += 8) {
+            uint32_t o[8];
+            asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                         : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]), "=r"(o[7])
+                         : "r"(to + c));
             tc::tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-            st16(to + c, o);
+            for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+            st8(to + c, o);
           }
         }
       }
       const float Rs = R == -INFINITY ? 0.f : R;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
+      for (int c = 0; c < 2; ++c) {
         const float2 t2 = tau[c];
         const float2 off = make_float2(t2.x - Rs, t2.x - Rs);
         float2 sum = make_float2(0.f, 0.f);
-        uint32_t p[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float2 e = fma2(make_float2(y[32 * c + 2 * i], y[32 * c + 2 * i + 1]), fx2, off);
-          const float2 w = make_float2(tc::ex2(e.x), tc::ex2(e.y));     // masked: 0
-          sum = add2(sum, w);
-          p[i] = few::half2_bits(w.x, w.y);
+        for (int h = 0; h < 2; ++h) {
+          uint32_t p[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int k = 32 * c + 16 * h + 2 * i;
+            const float2 e = fma2(make_float2(y[k], y[k + 1]), fx2, off);
+            const float2 w = make_float2(tc::ex2(e.x), tc::ex2(e.y));   // masked: 0
+            sum = add2(sum, w);
+            p[i] = few::half2_bits(w.x, w.y);
+          }
+          st8(ts + (HK / 2) * half + 16 * c + 8 * h, p);
         }
         l = fmaf(sum.x + sum.y, t2.y, l);
-        st16(ts + 16 * c, p);
       }
       tc::tmem_wait_st();
       tc::fence_before_sync();
@@ -496,21 +572,26 @@ __global__ void __launch_bounds__(pre::NT, 1) prefill_kernel(const AttnArgs a) {
     }
     // the last product has to be done before O is read
     if (ok && X < n_q && n_t > 0) {
-      ok = tc::mbar_wait(&bars.pv[X][(n_t - 1) & 1], ((n_t - 1) >> 1) & 1);
-      ok = __all_sync(0xffffffffu, ok);
+      ok = wait_warp(&bars.pv[X][(n_t - 1) & 1], ((n_t - 1) >> 1) & 1);
       tc::fence_after_sync();
     }
     if (!ok) s_fail = 1;
-    // ===================== epilogue: columns in the order of the code words =====================
+    // ===================== epilogue: columns in the order of the code words, half of them per thread =====================
+    if (X < n_q) {
+      tc::named_sync(pair, 64);                                         // the last exchange was read
+      ex[half * BM + row] = l;
+      tc::named_sync(pair, 64);
+      l += ex[(half ^ 1) * BM + row];
+    }
     if (ok && X < n_q) {
       const int qi = row_ok ? r / G : 0, head = hv * G + (row_ok ? r - qi * G : 0);
       const int64_t out_row = static_cast<int64_t>(sw.row0) + qi;
       const bool partial = n_split > 1 || a.diff;
       const float inv = l != 0.f ? 1.f / l : 0.f;                       // nothing visible: zeros (NaN stays NaN)
       float *part = a.part + (((out_row * a.n_heads + head) * maps + map) * n_split + split) * (DV + 4);
-      if (partial && row_ok) *reinterpret_cast<float4 *>(part) = make_float4(R, l, 0.f, 0.f);
+      if (partial && row_ok && half == 0) *reinterpret_cast<float4 *>(part) = make_float4(R, l, 0.f, 0.f);
 #pragma unroll 1
-      for (int c = 0; c < DV; c += 32) {
+      for (int c = half * (DV / 2); c < (half + 1) * (DV / 2); c += 32) {
         uint32_t o[32];
         if (n_t > 0) {
           tc::tmem_ld32(to + c, o);
@@ -553,7 +634,7 @@ __global__ void __launch_bounds__(pre::NT, 1) prefill_kernel(const AttnArgs a) {
   tc::fence_before_sync();
   __syncthreads();
   if (s_fail && tid == 0) set_status(a.status, TQ_ERR_TIMEOUT);
-  if (warp == 12) tc::tmem_dealloc<512>(tmem);
+  if (warp == W_MMA) tc::tmem_dealloc<512>(tmem);
 }
 
 // One warp per (row, output head): the key splits of each map together, then the difference and the norm.
@@ -624,7 +705,7 @@ template <int DK, int DV>
 cudaError_t launch_prefill_t(const AttnArgs &a, cudaStream_t s) {
   using C = pre::Cfg<DK, DV>;
   static_assert(C::TOTAL <= 227 * 1024, "shared memory");
-  static_assert(2 * pre::REG_SOFTMAX + pre::REG_UNPACK + pre::REG_MMA <= 512, "registers");
+  static_assert(4 * pre::REG_SOFTMAX + pre::REG_UNPACK + pre::REG_MMA <= 6 * 80, "registers");
   auto kern = prefill_kernel<DK, DV>;
   cudaError_t e = set_dynamic_smem(reinterpret_cast<const void *>(kern), C::TOTAL);
   if (e != cudaSuccess) return e;
