@@ -9,12 +9,16 @@
 //   0-7, 8-15  softmax of tile A, B: two threads per row (TMEM lane), 64 keys each;
 //   16-19      unpack: one key per thread, its packed rows held in registers one
 //              tile ahead, written as operand tiles (double buffered);
-//   20         one thread issues the products: S = Q K^T of both tiles into TMEM,
-//              O += P V with P written over S.  While one tile is in its softmax,
-//              the other one's products run.
-// The code of all roles has to stay small: with the products' loops unrolled, their
-// one warp waited for instructions (1390 against 1248 us at 2048 rows over 32768
-// cells, 8 KV heads, with one thread per row and its 128 keys unrolled).
+//   20         issues the products: S = Q K^T and O += P V.
+// Tensor memory holds O of both tiles (256 columns), their P as 16-bit pairs (128)
+// and ONE score buffer (128) that the tiles use in turn: it is free again as soon as
+// the softmax threads have read it into registers, so the next product of scores
+// runs beside the rest of the softmax and does not wait for P V.  (With a buffer per
+// tile and P written over it, a tile's scores had to wait for its P V: 1200 us at
+// 2048 rows over 32768 cells, 8 KV heads, against NEW_FIG.)
+// The code of all roles has to stay small: with the products' loops unrolled for one
+// thread and a whole row's 128 keys per softmax thread, the product warp waited for
+// instructions (1390 us in that form).
 //
 // Numbers, so that 16-bit operands cost no accuracy beyond the output's own:
 // - Scores: K's operand is the code itself (a nibble masked in place reads as the
@@ -76,6 +80,7 @@ struct Bars {
   uint64_t k[2], v[2];    // K, V of key tile j (buffer j & 1) written    phase j >> 1
   uint64_t kf[2];         // S_j of every row tile computed: K is free    phase j >> 1
   uint64_t s[2];          // S_j of tile X computed                       phase j
+  uint64_t rd[2];         // S_j of tile X read                           phase j
   uint64_t p[2];          // P_j of tile X written                        phase j
   uint64_t pv[2][2];      // PV_j of tile X (buffer j & 1) computed       phase j >> 1
 };
@@ -191,6 +196,7 @@ __global__ void __launch_bounds__(pre::NT, 1) prefill_kernel(const AttnArgs a) {
       tc::mbar_init(&bars.v[i], 4);
       tc::mbar_init(&bars.kf[i], n_q);
       tc::mbar_init(&bars.s[i], 1);
+      tc::mbar_init(&bars.rd[i], 8);
       tc::mbar_init(&bars.p[i], 8);
       tc::mbar_init(&bars.pv[i][0], 1);
       tc::mbar_init(&bars.pv[i][1], 1);
@@ -280,7 +286,7 @@ __global__ void __launch_bounds__(pre::NT, 1) prefill_kernel(const AttnArgs a) {
   tc::fence_after_sync();
   const uint32_t tmem = tmem_slot;
   const uint32_t sbase = tc::smem_u32(smem);
-  constexpr uint32_t TS = 0, TO = 256;        // TMEM columns: S / P of tile X at 128 X, O at 256 + 128 X
+  constexpr uint32_t TS = 0, TP = 128, TO = 256;        // TMEM columns: S, P of tile X at 128 + 64 X, O at 256 + 128 X
 
   float R = -INFINITY, l = 0.f;
   if (warp >= W_MMA) {
@@ -296,40 +302,42 @@ __global__ void __launch_bounds__(pre::NT, 1) prefill_kernel(const AttnArgs a) {
       const uint64_t k0 = tc::sdesc(sbase + C::SKV, 128, C::KC * 128);
       const uint64_t v0 = tc::sdesc(sbase + C::SKV + C::K_BYTES, C::VC * 128, 128);
       bool ok = true;
+      auto product = [&](int x, int j) {      // O += P V of row tile x, key tile j
+        if (x == 0) ok = wait_warp(&bars.v[j & 1], (j >> 1) & 1);
+        if (ok) ok = wait_warp(&bars.p[x], j & 1);
+        if (!ok) return;
+        tc::fence_after_sync();
+        const uint64_t v = v0 + static_cast<uint64_t>((j & 1) * (C::KV_BYTES >> 4));
+        if (one) {
+#pragma unroll
+          for (int ks = 0; ks < C::PKS; ++ks)
+            mma_ta(tm + TO + 128 * x, tm + TP + 64 * x + 8 * ks, v + ((ks * 2 * C::VC * 128) >> 4), ID_PV, j > 0 || ks > 0);
+          tc::mma_commit(&bars.pv[x][j & 1]);
+        }
+        __syncwarp();
+      };
+      // steps (j, x): scores once the step before has read its own, then the product of this row tile's step
+      // before.  (Its P is ready by the time that the scores are read: the same threads do both, in this order.)
       for (int j = 0; j <= n_t && ok && n_t > 0; ++j) {
-        const uint64_t kv = static_cast<uint64_t>((j & 1) * (C::KV_BYTES >> 4));
-        const uint64_t kv_last = static_cast<uint64_t>(((j - 1) & 1) * (C::KV_BYTES >> 4));
+        const uint64_t k = k0 + static_cast<uint64_t>((j & 1) * (C::KV_BYTES >> 4));
 #pragma unroll 1
-        for (int x = 0; x < n_q; ++x) {
-          if (j > 0) {                        // PV of the tile before
-            ok = wait_warp(&bars.p[x], (j - 1) & 1);
-            if (ok && x == 0) ok = wait_warp(&bars.v[(j - 1) & 1], ((j - 1) >> 1) & 1);
+        for (int x = 0; x < n_q && ok; ++x) {
+          if (j < n_t) {
+            if (x == 0) ok = wait_warp(&bars.k[j & 1], (j >> 1) & 1);
+            const int xl = x == 0 ? n_q - 1 : 0, jl = x == 0 ? j - 1 : j;              // the step before
+            if (ok && jl >= 0) ok = wait_warp(&bars.rd[xl], jl & 1);
             if (!ok) break;
             tc::fence_after_sync();
             if (one) {
 #pragma unroll
-              for (int ks = 0; ks < C::PKS; ++ks)
-                mma_ta(tm + TO + 128 * x, tm + TS + 128 * x + 8 * ks, v0 + kv_last + ((ks * 2 * C::VC * 128) >> 4), ID_PV,
-                       j > 1 || ks > 0);
-              tc::mma_commit(&bars.pv[x][(j - 1) & 1]);
+              for (int ks = 0; ks < C::SKS; ++ks)
+                tc::mma_f16(tm + TS, q0 + x * (C::Q_BYTES >> 4) + ((ks * 4096) >> 4), k + ((ks * 256) >> 4), ID_S, ks > 0);
+              tc::mma_commit(&bars.s[x]);
+              tc::mma_commit(&bars.kf[j & 1]);
             }
             __syncwarp();
           }
-          if (j == n_t) continue;
-          if (x == 0) ok = wait_warp(&bars.k[j & 1], (j >> 1) & 1);
-          // S_j goes where P_{j-1} stands: its product has to be done
-          if (ok && j > 0) ok = wait_warp(&bars.pv[x][(j - 1) & 1], ((j - 1) >> 1) & 1);
-          if (!ok) break;
-          tc::fence_after_sync();
-          if (one) {
-#pragma unroll
-            for (int ks = 0; ks < C::SKS; ++ks)
-              tc::mma_f16(tm + TS + 128 * x, q0 + x * (C::Q_BYTES >> 4) + ((ks * 4096) >> 4), k0 + kv + ((ks * 256) >> 4),
-                          ID_S, ks > 0);
-            tc::mma_commit(&bars.s[x]);
-            tc::mma_commit(&bars.kf[j & 1]);
-          }
-          __syncwarp();
+          if (j > 0) product(x, j - 1);
         }
       }
       if (!ok) s_fail = 1;
@@ -463,9 +471,10 @@ __global__ void __launch_bounds__(pre::NT, 1) prefill_kernel(const AttnArgs a) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REG_SOFTMAX));
     // ===================== softmax: 64 keys of a row per thread =====================
     const uint32_t lane_off = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-    const uint32_t ts = tmem + lane_off + TS + 128 * X, to = tmem + lane_off + TO + 128 * X;
+    const uint32_t ts = tmem + lane_off + TS + HK * half, tp = tmem + lane_off + TP + 64 * X + (HK / 2) * half;
+    const uint32_t to = tmem + lane_off + TO + 128 * X;
     const int pair = 1 + 4 * X + (warp & 3);                            // named barrier of the rows' two warps
-    float *ex = reinterpret_cast<float *>(smem + C::SROW) + X * 2 * BM; // [half][row]
+    float *ex = reinterpret_cast<float *>(smem + C::SROW) + X * 4 * BM; // [j & 1][half][row]
     const int lim = row_ok ? limit_of(r) : 0;
     const float2 fx2 = make_float2(fx, fx);
     bool ok = true;
@@ -483,9 +492,12 @@ __global__ void __launch_bounds__(pre::NT, 1) prefill_kernel(const AttnArgs a) {
       float y[HK];
       {
         uint32_t *u = reinterpret_cast<uint32_t *>(y);
-        tc::tmem_ld32(ts + HK * half, u);
-        tc::tmem_ld32(ts + HK * half + 32, u + 32);
+        tc::tmem_ld32(ts, u);
+        tc::tmem_ld32(ts + 32, u + 32);
         tc::tmem_wait_ld();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&bars.rd[X]);
       }
       const float4 *sc = reinterpret_cast<const float4 *>(smem + C::SSC + ((j & 3) * BN + HK * half) * 4);
 #pragma unroll
@@ -516,21 +528,21 @@ __global__ void __launch_bounds__(pre::NT, 1) prefill_kernel(const AttnArgs a) {
         }
         top = fmaxf(top, fmaf(fmaxf(m0, m1), fx, tau[c].x));
       }
-      // (the other thread read the last value before it wrote its weights, hence before this S)
-      ex[half * BM + row] = top;
-      tc::fence_before_sync();                // both warps' scores are read before either writes weights over them
+      // (two places in turn: the other thread may still be reading the last tile's)
+      ex[(2 * (j & 1) + half) * BM + row] = top;
       tc::named_sync(pair, 64);
-      tc::fence_after_sync();
-      top = fmaxf(top, ex[(half ^ 1) * BM + row]);
+      top = fmaxf(top, ex[(2 * (j & 1) + (half ^ 1)) * BM + row]);
+      if (j > 0) {                            // P and O stand still
+        ok = wait_warp(&bars.pv[X][(j - 1) & 1], ((j - 1) >> 1) & 1);
+        if (!ok) continue;
+        tc::fence_after_sync();
+      }
       const bool raise = top > R + 8.f;
       if (__any_sync(0xffffffffu, raise)) {
         const float f = raise ? exp2f(R - top) : 1.f;                   // 0 at the first raise
         if (raise) R = top;
         l *= f;
         if (j > 0) {
-          ok = wait_warp(&bars.pv[X][(j - 1) & 1], ((j - 1) >> 1) & 1);        // O stands still
-          if (!ok) continue;
-          tc::fence_after_sync();
 #pragma unroll 1
           for (int c = half * (DV / 2); c < (half + 1) * (DV / 2); c += 8) {
             uint32_t o[8];
@@ -561,7 +573,7 @@ __global__ void __launch_bounds__(pre::NT, 1) prefill_kernel(const AttnArgs a) {
             sum = add2(sum, w);
             p[i] = few::half2_bits(w.x, w.y);
           }
-          st8(ts + (HK / 2) * half + 16 * c + 8 * h, p);
+          st8(tp + 16 * c + 8 * h, p);
         }
         l = fmaf(sum.x + sum.y, t2.y, l);
       }
