@@ -27,9 +27,9 @@
 //   accumulation.
 // - The value weights p_t s_t are rounded to binary16 (relative 2^-11, an eighth
 //   of bfloat16's rounding of the output): R is a running maximum of
-//   x_t + exponent(s_t), so the largest weight lies in [1, 2^9] whatever the
+//   x_t + exponent(s_t), so the largest weight lies in [1, 2^13] whatever the
 //   scales, and sums of p_t and p_t m_t stay in fp32.  R is raised only when it
-//   would grow by more than 2^8 (the sums are rescaled then).
+//   would grow by more than 2^12 (the sums are rescaled then).
 // - Codes count from a row's smallest value, so with w the rounded weight, sum w c
 //   + sum p m would carry the rounding of w times the whole range of the row.  The
 //   sum taken is sum w (c - c0) + sum p (m + s c0) with c0 = clamp(-m / s, 0, 15)
@@ -65,6 +65,7 @@ namespace p4 {
 #ifndef FEW_NW
 #define FEW_NW 8
 #endif
+constexpr float RAISE = 12.f;         // growth of the maximum (log2) that rescales
 constexpr int UNIT = 64;              // keys per unit of work
 constexpr int TILE = 32;              // keys per warp tile
 constexpr int MIN_PIECE = 4;          // units of a piece at least: one tile for each of eight warps
@@ -668,12 +669,12 @@ __global__ void __launch_bounds__(FewCfg<DK, DV, NT, MAPS>::THREADS, FewCfg<DK, 
             mt[0] = max3(mt[0], u.x, w.x);
             mt[1] = max3(mt[1], u.y, w.y);
           }
-          const bool raise = mt[0] > R[nn].x + 8.f || mt[1] > R[nn].y + 8.f;
+          const bool raise = mt[0] > R[nn].x + RAISE || mt[1] > R[nn].y + RAISE;
           if (__any_sync(0xffffffffu, raise)) {
             auto lift = [&](float x, float &r, float &rs, float &lo, float &zo, int i) {
 #pragma unroll
               for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-              if (x > r + 8.f) {
+              if (x > r + RAISE) {
                 const float f = exp2f(r - x);             // 0 at the first raise
                 r = rs = x;
                 lo *= f;

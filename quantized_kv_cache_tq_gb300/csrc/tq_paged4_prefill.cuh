@@ -31,7 +31,8 @@
 // - Values: v_t 2^-tau rounded to binary16 (relative 2^-12 on average half), tau the
 //   largest exponent among 32 neighbouring keys; the weights p_t 2^tau are rounded
 //   to binary16 too.  Both roundings meet the values themselves.  R is a running
-//   maximum of x_t + tau, raised only when it would grow by more than 2^8.  Sums of
+//   maximum of x_t + tau, raised only when it would grow by more than 2^12 (which binary16 weights leave room
+//   for; with 2^8 the rescaling of O cost a tenth of the time).  Sums of
 //   weights stay in fp32.
 //
 // With few row tiles a tile's keys are split over several CTAs; the partial results
@@ -537,7 +538,7 @@ __global__ void __launch_bounds__(pre::NT, 1) prefill_kernel(const AttnArgs a) {
         if (!ok) continue;
         tc::fence_after_sync();
       }
-      const bool raise = top > R + 8.f;
+      const bool raise = top > R + RAISE;
       if (__any_sync(0xffffffffu, raise)) {
         const float f = raise ? exp2f(R - top) : 1.f;                   // 0 at the first raise
         if (raise) R = top;
