@@ -74,7 +74,8 @@ struct AttnArgs {
   const float *norm_weight;  // differential: RMS norm over each output row, or null
   int32_t *status;
   int32_t *counters;         // arrivals per work-sharing group, self-resetting
-  float *part;
+  float *part;               // partial results of items that CTAs share
+  float *row_part;           // prompt kernel: of rows [row][head][map][split][4 + width]: (R, l, 0, 0), values
   int64_t q_stride;          // elements between query rows
   int64_t n_rows;            // query rows in q / out
   int32_t n_seq;
@@ -92,6 +93,7 @@ struct AttnArgs {
   float scale_log2;
   float eps;
   float out_scale;
+  int32_t line;              // prompt kernel: one line of work over the SMs (else n_split CTAs per item)
   int32_t n_split;           // prompt kernel: key-range splits per tile
   int32_t n_tiles;           // prompt kernel: upper bound of row tiles over all sequences
 };

@@ -77,16 +77,25 @@ static Layout few_layout(int wv) {
   return L;
 }
 
-// Key splits of the prompt kernel's row tiles: the count whose launch is estimated to end first, in key tiles
-// of one CTA: rounds of CTAs over the SMs times (key tiles per CTA + 6 for its set-up and epilogue, + 4 where
-// partial results are written and merged).
+// How the prompt kernel shares its work out.  With half as many items (256-row tile, K head) as SMs or more,
+// one line over the SMs; with fewer, every item's keys are split: the count whose launch is estimated to end
+// first, in key tiles of one CTA: rounds of CTAs over the SMs times (key tiles per CTA + 4 for its set-up and
+// epilogue, + 4 where partial results are written and merged).
 constexpr int kMaxSplit = 16;
-static int prefill_splits(int64_t n_rows, int group, int k_heads, int64_t max_len) {
-  const int64_t ctas = (n_rows * group + 255) / 256 * k_heads, tiles = (max_len + 127) / 128, sms = sm_count();
+// (row tiles: full ones, and an unfilled one per sequence)
+static int64_t prefill_items(int64_t n_rows, int n_seq, int group, int k_heads) {
+  return ((n_rows * group + 255) / 256 + (n_seq < n_rows ? n_seq : n_rows) - 1) * k_heads;
+}
+static bool prefill_line(int64_t n_rows, int n_seq, int group, int k_heads) {
+  return 2 * prefill_items(n_rows, n_seq, group, k_heads) >= sm_count();
+}
+static int prefill_splits(int64_t n_rows, int n_seq, int group, int k_heads, int64_t max_len) {
+  if (prefill_line(n_rows, n_seq, group, k_heads)) return 1;
+  const int64_t ctas = prefill_items(n_rows, n_seq, group, k_heads), tiles = (max_len + 127) / 128, sms = sm_count();
   int best = 1;
   int64_t least = 0;
   for (int c = 1; c <= kMaxSplit && (c == 1 || tiles / c >= 4); ++c) {
-    const int64_t cost = (ctas * c + sms - 1) / sms * ((tiles + c - 1) / c + 6 + (c > 1 ? 4 : 0));
+    const int64_t cost = (ctas * c + sms - 1) / sms * ((tiles + c - 1) / c + 4 + (c > 1 ? 4 : 0));
     if (c == 1 || cost < least) {
       best = c;
       least = cost;
@@ -101,12 +110,17 @@ static bool takes_prefill(const tq_paged4 *k, const tq_paged4 *v, int64_t rows_p
   return prefill_supported(row_width(k->head_dim), row_width(v->head_dim)) && rows_per_seq * group > 16;
 }
 
-static Layout prefill_layout(const tq_paged4 *k, const tq_paged4 *v, int n_heads, int64_t n_rows, int n_split) {
+// row_off: where the rows' partial results begin (behind the shared items' partials in the line form).
+static Layout prefill_layout(const tq_paged4 *k, const tq_paged4 *v, int n_heads, int64_t n_rows, bool line, int n_split,
+                             size_t *row_off) {
   const int wv = row_width(v->head_dim), maps = k->n_kv_heads / v->n_kv_heads;
   Layout L = few_layout(wv);
-  if (!prefill_supported(row_width(k->head_dim), wv) || (n_split == 1 && maps == 1)) return L;
-  const size_t part = static_cast<size_t>(n_rows) * n_heads * maps * n_split * (wv + 4) * sizeof(float);
-  if (L.part_off + part > L.total) L.total = L.part_off + part;
+  *row_off = L.part_off;
+  if (!prefill_supported(row_width(k->head_dim), wv)) return L;
+  if (line) *row_off += up(sizeof(float) * 2 * sm_count() * 256 * (wv + 2), 256);       // two partials per CTA
+  size_t end = *row_off;
+  if (n_split > 1 || maps > 1) end += static_cast<size_t>(n_rows) * n_heads * maps * n_split * (wv + 4) * sizeof(float);
+  if (end > L.total) L.total = end;
   return L;
 }
 
@@ -145,10 +159,12 @@ static tq_status attend(const Call &c) {
   const int group = c.n_heads / c.v->n_kv_heads;
   const int64_t rows = c.ragged ? (c.max_rows ? c.max_rows : c.n_rows) : 1;
   const bool prompt = c.ragged && takes_prefill(c.k, c.v, rows, group);
-  const int n_split = prompt ? prefill_splits(c.n_rows, group, c.k->n_kv_heads,
+  const int n_split = prompt ? prefill_splits(c.n_rows, c.n_seq, group, c.k->n_kv_heads,
                                               c.max_len ? c.max_len : static_cast<int64_t>(c.max_pages) * c.k->page_size)
                              : 1;
-  const Layout L = prompt ? prefill_layout(c.k, c.v, c.n_heads, c.n_rows, n_split) : few_layout(wv);
+  const bool line = prompt && prefill_line(c.n_rows, c.n_seq, group, c.k->n_kv_heads);
+  size_t row_off = 0;
+  const Layout L = prompt ? prefill_layout(c.k, c.v, c.n_heads, c.n_rows, line, n_split, &row_off) : few_layout(wv);
   if (!al(c.workspace, 256) || c.workspace_bytes < L.total) return TQ_ERR_WORKSPACE;
   AttnArgs a;
   memset(&a, 0, sizeof(a));
@@ -186,6 +202,8 @@ static tq_status attend(const Call &c) {
   a.eps = c.eps;
   a.out_scale = c.out_scale;
   a.n_split = n_split;
+  a.line = line;
+  a.row_part = reinterpret_cast<float *>(static_cast<char *>(c.workspace) + row_off);
   if (prompt) {
     const int64_t tiles = c.n_rows * group / 256 + c.n_seq;        // upper bound over ragged sequences
     if (tiles * n_split * c.k->n_kv_heads > 0x7fffffffLL || (c.n_rows * c.n_heads + 7) / 8 > 0x7fffffffLL)
@@ -309,8 +327,10 @@ size_t tq_paged4_prefill_workspace(const tq_paged4 *k, const tq_paged4 *v, int n
   if (heads_ok(k, v, n_heads, n_seq, is_diff(k, v)) != TQ_OK || n_rows < 0 || max_len < 0) return 0;
   if (n_rows > 0x7fffffffLL / n_heads) return 0;
   // (max_len 0, the call's "table's capacity": room for any split)
-  const int n_split = max_len ? prefill_splits(n_rows, n_heads / v->n_kv_heads, k->n_kv_heads, max_len) : kMaxSplit;
-  return prefill_layout(k, v, n_heads, n_rows, n_split).total;
+  const int n_split = max_len ? prefill_splits(n_rows, n_seq, n_heads / v->n_kv_heads, k->n_kv_heads, max_len) : kMaxSplit;
+  size_t row_off = 0;
+  return prefill_layout(k, v, n_heads, n_rows, prefill_line(n_rows, n_seq, n_heads / v->n_kv_heads, k->n_kv_heads), n_split,
+                        &row_off).total;
 }
 
 tq_status tq_paged4_decode(const tq_paged4 *k, const tq_paged4 *v, const int32_t *block_table, int max_pages,
