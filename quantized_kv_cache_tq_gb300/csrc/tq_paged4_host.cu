@@ -77,27 +77,28 @@ static Layout few_layout(int wv) {
   return L;
 }
 
-// How the prompt kernel shares its work out.  With half as many items (256-row tile, K head) as SMs or more,
-// one line over the SMs; with fewer, every item's keys are split: the count whose launch is estimated to end
-// first, in key tiles of one CTA: rounds of CTAs over the SMs times (key tiles per CTA + 4 for its set-up and
-// epilogue, + 4 where partial results are written and merged).
+// How the prompt kernel shares its work out: one line over the SMs, or n_split CTAs per item (256-row tile, K
+// head), whichever is estimated to end first.  In key tiles of one CTA (2 us): a CTA costs its key tiles + 4 for
+// set-up and epilogue, + 4 where rows' partial results are written and merged; a line costs its share, and 14 for
+// finding it and for the items cut at its ends.  Measured, line against split: 2048 rows over 32768 cells 847 /
+// 969 us, over 4096 cells 127 / 118 us, three differential chunks of up to 700 rows 97 / 111 us, five chunks of up
+// to 300 rows 54 / 38 us.
 constexpr int kMaxSplit = 16;
-// (row tiles: full ones, and an unfilled one per sequence)
-static int64_t prefill_items(int64_t n_rows, int n_seq, int group, int k_heads) {
-  return ((n_rows * group + 255) / 256 + (n_seq < n_rows ? n_seq : n_rows) - 1) * k_heads;
-}
-static bool prefill_line(int64_t n_rows, int n_seq, int group, int k_heads) {
-  return 2 * prefill_items(n_rows, n_seq, group, k_heads) >= sm_count();
-}
-static int prefill_splits(int64_t n_rows, int n_seq, int group, int k_heads, int64_t max_len) {
-  if (prefill_line(n_rows, n_seq, group, k_heads)) return 1;
-  const int64_t ctas = prefill_items(n_rows, n_seq, group, k_heads), tiles = (max_len + 127) / 128, sms = sm_count();
-  int best = 1;
-  int64_t least = 0;
+struct Share {
+  bool line;
+  int n_split;
+};
+static Share prefill_share(int64_t n_rows, int n_seq, int group, int k_heads, int maps, int64_t max_len) {
+  const int64_t sms = sm_count(), tiles = (max_len + 127) / 128;
+  // (row tiles: the full ones and about half a tile per sequence)
+  int64_t items = (n_rows * group + 128 * (n_seq < n_rows ? n_seq : n_rows)) / 256 * k_heads;
+  if (items < k_heads) items = k_heads;
+  Share best = {true, 1};
+  int64_t least = (items * (tiles + 4) + sms - 1) / sms + 14;
   for (int c = 1; c <= kMaxSplit && (c == 1 || tiles / c >= 4); ++c) {
-    const int64_t cost = (ctas * c + sms - 1) / sms * ((tiles + c - 1) / c + 4 + (c > 1 ? 4 : 0));
-    if (c == 1 || cost < least) {
-      best = c;
+    const int64_t cost = (items * c + sms - 1) / sms * ((tiles + c - 1) / c + 4 + (c > 1 || maps > 1 ? 4 : 0));
+    if (cost < least) {
+      best = {false, c};
       least = cost;
     }
   }
@@ -159,10 +160,12 @@ static tq_status attend(const Call &c) {
   const int group = c.n_heads / c.v->n_kv_heads;
   const int64_t rows = c.ragged ? (c.max_rows ? c.max_rows : c.n_rows) : 1;
   const bool prompt = c.ragged && takes_prefill(c.k, c.v, rows, group);
-  const int n_split = prompt ? prefill_splits(c.n_rows, c.n_seq, group, c.k->n_kv_heads,
-                                              c.max_len ? c.max_len : static_cast<int64_t>(c.max_pages) * c.k->page_size)
-                             : 1;
-  const bool line = prompt && prefill_line(c.n_rows, c.n_seq, group, c.k->n_kv_heads);
+  Share share = {false, 1};
+  if (prompt)
+    share = prefill_share(c.n_rows, c.n_seq, group, c.k->n_kv_heads, c.diff ? 2 : 1,
+                          c.max_len ? c.max_len : static_cast<int64_t>(c.max_pages) * c.k->page_size);
+  const bool line = share.line;
+  const int n_split = share.n_split;
   size_t row_off = 0;
   const Layout L = prompt ? prefill_layout(c.k, c.v, c.n_heads, c.n_rows, line, n_split, &row_off) : few_layout(wv);
   if (!al(c.workspace, 256) || c.workspace_bytes < L.total) return TQ_ERR_WORKSPACE;
@@ -327,10 +330,11 @@ size_t tq_paged4_prefill_workspace(const tq_paged4 *k, const tq_paged4 *v, int n
   if (heads_ok(k, v, n_heads, n_seq, is_diff(k, v)) != TQ_OK || n_rows < 0 || max_len < 0) return 0;
   if (n_rows > 0x7fffffffLL / n_heads) return 0;
   // (max_len 0, the call's "table's capacity": room for any split)
-  const int n_split = max_len ? prefill_splits(n_rows, n_seq, n_heads / v->n_kv_heads, k->n_kv_heads, max_len) : kMaxSplit;
+  Share share = {true, kMaxSplit};
+  const int maps = k->n_kv_heads / v->n_kv_heads;
+  if (max_len) share = prefill_share(n_rows, n_seq, n_heads / v->n_kv_heads, k->n_kv_heads, maps, max_len);
   size_t row_off = 0;
-  return prefill_layout(k, v, n_heads, n_rows, prefill_line(n_rows, n_seq, n_heads / v->n_kv_heads, k->n_kv_heads), n_split,
-                        &row_off).total;
+  return prefill_layout(k, v, n_heads, n_rows, share.line, share.n_split, &row_off).total;
 }
 
 tq_status tq_paged4_decode(const tq_paged4 *k, const tq_paged4 *v, const int32_t *block_table, int max_pages,

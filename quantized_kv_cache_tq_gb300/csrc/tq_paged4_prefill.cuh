@@ -64,7 +64,7 @@ constexpr int HK = BN / 2;                    // keys of a softmax thread
 constexpr int ITEM_COST = 4;                      // key tiles' worth of time that an item costs besides its keys (8 us)
 constexpr int NT = 768;
 constexpr int W_UNPACK = 16, W_MMA = 20, W_NEXT = 21;      // first warps of the roles after the softmax
-constexpr int REG_SOFTMAX = 88, REG_UNPACK = 96, REG_MMA = 32;    // of 80 at the launch: 4 x 88 + 96 + 32 = 6 x 80
+constexpr int REG_SOFTMAX = 96, REG_UNPACK = 64, REG_MMA = 32;    // of 80 at the launch: 4 x 96 + 64 + 32 = 6 x 80
 
 template <int DK, int DV>
 struct Cfg {
@@ -131,6 +131,15 @@ __device__ __forceinline__ bool elect() {
   return p != 0;
 }
 
+__device__ __forceinline__ void sts1(uint32_t at, float x) {
+  asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(x) : "memory");
+}
+__device__ __forceinline__ float lds1(uint32_t at) {
+  float x;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(at) : "memory");
+  return x;
+}
+
 __device__ __forceinline__ uint32_t bits(__half2 h) { return *reinterpret_cast<const uint32_t *>(&h); }
 __device__ __forceinline__ __half2 as_half2(uint32_t u) { return *reinterpret_cast<const __half2 *>(&u); }
 
@@ -157,6 +166,12 @@ __device__ __forceinline__ Tile tile_of(const AttnArgs &a, const few::SeqWork &w
 }
 __device__ __forceinline__ int tiles_of(const AttnArgs &a, const few::SeqWork &w) {
   return static_cast<int>((static_cast<long long>(w.rows) * a.group + 2 * BM - 1) / (2 * BM));
+}
+
+// A piece, read anew (what only begin and end of its work need is not kept in registers through the loop).
+__device__ __forceinline__ Piece read_piece(const Piece *p) {
+  const volatile int *q = reinterpret_cast<const volatile int *>(p);
+  return {q[0], q[1], q[2], q[3], q[4], q[5], q[6], q[7], q[8]};
 }
 
 // Row tiles of a piece that have rows.
@@ -429,7 +444,7 @@ __global__ void __launch_bounds__(pre::NT, 1) prefill_kernel(const AttnArgs a) {
       }
     }
   } else if (warp >= W_UNPACK) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REG_UNPACK));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_UNPACK));
     // ===================== unpack: one key of the tile per thread =====================
     const int key = tid - 32 * W_UNPACK;
     const int mask = (1 << a.page_shift) - 1;
@@ -571,24 +586,29 @@ __global__ void __launch_bounds__(pre::NT, 1) prefill_kernel(const AttnArgs a) {
     const int X = warp >> 3, half = (warp >> 2) & 1;                    // tile A, B; keys 0-63, 64-127
     const int row = tid & (BM - 1);
     const uint32_t lane_off = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-    const uint32_t ts = tmem + lane_off + TS + HK * half, tp = tmem + lane_off + TP + 64 * X + (HK / 2) * half;
-    const uint32_t to = tmem + lane_off + TO + 128 * X;
+    const uint32_t ts = tmem + lane_off + TS + HK * half, tp = ts + TP - TS + 64 * X - (HK / 2) * half;
+    const uint32_t to = ts + TO - TS + 128 * X - HK * half;
     const int pair = 1 + 4 * X + (warp & 3);                            // named barrier of the rows' two warps
     bool ok = true;
     int base = 0;
     for (int i = 0;; ++i) {
-      const Piece pc = s_piece[i & 1];
-      if (pc.n_t < 0) break;
-      const int n_t = pc.n_t;
+      const int n_t = s_piece[i & 1].n_t;
+      if (n_t < 0) break;
+      bool here, row_ok;
+      int lim;                                // keys that the row sees, from the piece's first one on
+      float fx = 1.f;                         // x = fx s_t (score), fx > 0
+      {
+      const Piece pc = read_piece(&s_piece[i & 1]);
       const few::SeqWork sw = few::seq_work<1>(a, pc.seq, false);
       const Tile tl = tile_of(a, sw, pc.tile);
       const int hv = pc.kh / maps, map = pc.kh - hv * maps;
       const int r = tl.r0 + X * BM + row;     // row of the sequence
-      const bool here = X == 0 || tl.rows_all - tl.r0 > BM, row_ok = r < tl.rows_all;
+      here = X == 0 || tl.rows_all - tl.r0 > BM;
+      row_ok = r < tl.rows_all;
       const int qi = row_ok ? r / G : 0, head = hv * G + (row_ok ? r - qi * G : 0);
       const int64_t out_row = static_cast<int64_t>(sw.row0) + qi;
+      lim = (!row_ok ? 0 : a.causal ? max(0, sw.len - sw.rows + qi + 1) : sw.len) - pc.t_lo * BN;
       // ---- Q: half of the row's dims per thread
-      float fx = 1.f;                         // x = fx s_t (score), fx > 0
       if (here) {
         constexpr int NC = DK / 16;           // 8-element chunks of a thread
         const uint16_t *src = static_cast<const uint16_t *>(a.q) + out_row * a.q_stride +
@@ -648,15 +668,17 @@ __global__ void __launch_bounds__(pre::NT, 1) prefill_kernel(const AttnArgs a) {
         }
         tc::named_sync(pair, 64);             // the exchange is free for the maxima
       }
+      }
       tc::fence_async_smem();
       tc::named_sync(BAR_Q, 32 * (W_UNPACK + 1));
 
       float R = -INFINITY, l = 0.f;
-      float *ex = reinterpret_cast<float *>(smem + C::SROW) + X * 4 * BM;               // [J & 1][half][row]
-      const int lim = !row_ok ? 0 : a.causal ? max(0, sw.len - sw.rows + qi + 1) : sw.len;
+      const uint32_t ex = sbase + C::SROW + (X * 4 * BM + row) * 4;                     // [J & 1][half][row]
       const float2 fx2 = make_float2(fx, fx);
-      for (int j = 0; j < n_t; ++j) {
-        const int J = base + j;
+      int nvis = lim - HK * half;             // of the thread's keys of the tile, those that the row sees
+      const int J0 = base;
+      base += n_t;
+      for (int J = J0; J < base; ++J, nvis -= BN) {
         if (ok) {
           ok = wait_warp(&bars.s[X], J & 1);
           // the tile's scales.  (Not K's own barrier: K of tile J + 2 may be there already, and a slow warp would
@@ -664,7 +686,7 @@ __global__ void __launch_bounds__(pre::NT, 1) prefill_kernel(const AttnArgs a) {
           if (ok && here) ok = wait_warp(&bars.sc[J & 3], (J >> 2) & 1);
         }
         if (!here) {                          // no rows: the phases go on, no faster than with rows
-          if (ok && j > 0) ok = wait_warp(&bars.pv[X][(J - 1) & 1], ((J - 1) >> 1) & 1);
+          if (ok && J > J0) ok = wait_warp(&bars.pv[X][(J - 1) & 1], ((J - 1) >> 1) & 1);
           if (lane == 0) {
             tc::mbar_arrive(&bars.rd[X]);
             tc::mbar_arrive(&bars.p[X]);
@@ -686,10 +708,10 @@ __global__ void __launch_bounds__(pre::NT, 1) prefill_kernel(const AttnArgs a) {
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(&bars.rd[X]);
         }
-        const float4 *sc = reinterpret_cast<const float4 *>(smem + C::SSC + ((J & 3) * BN + HK * half) * 4);
+        const uint32_t sc = sbase + C::SSC + ((J & 3) * BN + HK * half) * 4;
 #pragma unroll
         for (int k = 0; k < HK / 4; ++k) {
-          const float4 s4 = sc[k];
+          const float4 s4 = few::lds4(sc + 16 * k);
           const float2 u = mul2(make_float2(y[4 * k], y[4 * k + 1]), make_float2(s4.x, s4.y));
           const float2 w = mul2(make_float2(y[4 * k + 2], y[4 * k + 3]), make_float2(s4.z, s4.w));
           y[4 * k] = u.x;
@@ -697,13 +719,12 @@ __global__ void __launch_bounds__(pre::NT, 1) prefill_kernel(const AttnArgs a) {
           y[4 * k + 2] = w.x;
           y[4 * k + 3] = w.y;
         }
-        const int nvis = lim - (pc.t_lo + j) * BN - HK * half;          // of the thread's keys, those that the row sees
         if (__any_sync(0xffffffffu, nvis < HK)) {
 #pragma unroll
           for (int k = 0; k < HK; ++k)
             if (k >= nvis) y[k] = -INFINITY;
         }
-        const float2 *tau = reinterpret_cast<const float2 *>(smem + C::STAU) + 4 * (J & 3) + 2 * half;
+        const float4 tau = few::lds4(sbase + C::STAU + (4 * (J & 3) + 2 * half) * 8);   // (tau, 2^-tau) of both 32 keys
         float top = -INFINITY;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
@@ -713,13 +734,13 @@ __global__ void __launch_bounds__(pre::NT, 1) prefill_kernel(const AttnArgs a) {
             m0 = max3(m0, y[32 * c + k], y[32 * c + k + 1]);
             m1 = max3(m1, y[32 * c + k + 2], y[32 * c + k + 3]);
           }
-          top = fmaxf(top, fmaf(fmaxf(m0, m1), fx, tau[c].x));
+          top = fmaxf(top, fmaf(fmaxf(m0, m1), fx, c ? tau.z : tau.x));
         }
         // (two places in turn: the other thread may still be reading the last tile's)
-        ex[(2 * (J & 1) + half) * BM + row] = top;
+        sts1(ex + (2 * (J & 1) + half) * BM * 4, top);
         tc::named_sync(pair, 64);
-        top = fmaxf(top, ex[(2 * (J & 1) + (half ^ 1)) * BM + row]);
-        if (j > 0) {                          // P and O stand still
+        top = fmaxf(top, lds1(ex + (2 * (J & 1) + (half ^ 1)) * BM * 4));
+        if (J > J0) {                         // P and O stand still
           ok = wait_warp(&bars.pv[X][(J - 1) & 1], ((J - 1) >> 1) & 1);
           if (!ok) continue;
           tc::fence_after_sync();
@@ -729,7 +750,7 @@ __global__ void __launch_bounds__(pre::NT, 1) prefill_kernel(const AttnArgs a) {
           const float f = raise ? exp2f(R - top) : 1.f;                 // 0 at the first raise
           if (raise) R = top;
           l *= f;
-          if (j > 0) {
+          if (J > J0) {
 #pragma unroll 1
             for (int c = half * (DV / 2); c < (half + 1) * (DV / 2); c += 8) {
               uint32_t o[8];
@@ -746,7 +767,7 @@ __global__ void __launch_bounds__(pre::NT, 1) prefill_kernel(const AttnArgs a) {
         const float Rs = R == -INFINITY ? 0.f : R;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          const float2 t2 = tau[c];
+          const float2 t2 = c ? make_float2(tau.z, tau.w) : make_float2(tau.x, tau.y);
           const float2 off = make_float2(t2.x - Rs, t2.x - Rs);
           float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
@@ -770,19 +791,23 @@ __global__ void __launch_bounds__(pre::NT, 1) prefill_kernel(const AttnArgs a) {
         if (lane == 0) tc::mbar_arrive(&bars.p[X]);
       }
       // the last product has to be done before O is read
-      if (ok && n_t > 0) {
-        ok = wait_warp(&bars.pv[X][(base + n_t - 1) & 1], ((base + n_t - 1) >> 1) & 1);
+      if (ok && base > J0) {
+        ok = wait_warp(&bars.pv[X][(base - 1) & 1], ((base - 1) >> 1) & 1);
         tc::fence_after_sync();
       }
-      base += n_t;
       if (!ok) s_fail = 1;
       // ===================== epilogue: columns in the order of the code words, half of them per thread =====================
       if (here) {
         tc::named_sync(pair, 64);                                       // the last exchange was read
-        ex[half * BM + row] = l;
+        sts1(ex + half * BM * 4, l);
         tc::named_sync(pair, 64);
-        l += ex[(half ^ 1) * BM + row];
+        l += lds1(ex + (half ^ 1) * BM * 4);
       }
+      const Piece pc = read_piece(&s_piece[i & 1]);
+      const few::SeqWork sw = few::seq_work<1>(a, pc.seq, false);
+      const int hv = pc.kh / maps, map = pc.kh - hv * maps, r = pc.tile * 2 * BM + X * BM + row;
+      const int qi = row_ok ? r / G : 0, head = hv * G + (row_ok ? r - qi * G : 0);
+      const int64_t out_row = static_cast<int64_t>(sw.row0) + qi;
       // 8 dims of the row: values times `inv` to the output, or as they are to the rows' partial results
       const bool rows_part = a.diff || a.n_split > 1;
       float *part = a.row_part + (((out_row * a.n_heads + head) * maps + map) * a.n_split +
@@ -826,7 +851,7 @@ __global__ void __launch_bounds__(pre::NT, 1) prefill_kernel(const AttnArgs a) {
 #pragma unroll 1
         for (int c = half * (DV / 2); c < (half + 1) * (DV / 2); c += 32) {
           uint32_t o[32];
-          if (n_t > 0) {
+          if (base > J0) {
             tc::tmem_ld32(to + c, o);
             tc::tmem_wait_ld();
           } else {

@@ -401,13 +401,14 @@ PRE = [  # dk, dv, kv heads, group, page, query rows, lens
     (256, 256, 1, 2, 32, [70], [130]),
     (128, 128, 8, 4, 16, [5, 5, 5], [600, 30, 5]),
     (128, 128, 1, 8, 16, [513], [2000]),
+    (64, 64, 2, 1, 32, [1, 200, 0, 0, 17, 300, 129, 128, 5], [1, 900, 10, 0, 17, 300, 200, 1025, 2]),
 ]
 
 
 @pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
-@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("causal,max_len", [(True, None), (False, None), (True, 1 << 20)])
 @pytest.mark.parametrize("dk,dv,hkv,group,page,nq,lens", PRE)
-def test_prefill(dk, dv, hkv, group, page, nq, lens, causal, dtype):
+def test_prefill(dk, dv, hkv, group, page, nq, lens, causal, max_len, dtype):
     import torch
     import quantized_kv_cache_tq_gb300 as tq
     b = Batch(31 + dk, lens, hkv, dk, dv, page)
@@ -417,7 +418,8 @@ def test_prefill(dk, dv, hkv, group, page, nq, lens, causal, dtype):
     q[start[-1]:] = float("nan")
     out = torch.full((rows, hkv * group, dv), 3.0, device="cuda", dtype=q.dtype)
     gs = torch.tensor(start, dtype=torch.int32, device="cuda")
-    tq.paged4_prefill(b.gk, b.gv, b.gt, b.gl, q, gs, causal=causal, out=out)
+    # (a long max_len has the work cut as one line over the SMs, a short one as CTAs per row tile)
+    tq.paged4_prefill(b.gk, b.gv, b.gt, b.gl, q, gs, causal=causal, max_len=max_len, out=out)
     ref, bound = P.attention(b.k, b.v, b.table, lens, _np(q), start, hkv * group, dk ** -0.5, causal)
     ref[start[-1]:], bound[start[-1]:] = 3.0, 0.0
     _check(out, ref, bound, dtype)
@@ -462,17 +464,18 @@ def test_prefill_rows_that_see_nothing_and_bad_row_ranges():
         assert tq._lib.tq_workspace_status(ws.data_ptr(), ws.numel(), stream) == tq._lib.TQ_ERR_DEVICE_CHECK
 
 
-def test_prefill_long_context_few_tiles():
+@pytest.mark.parametrize("max_len", [9000, 1 << 20])
+def test_prefill_long_context_few_tiles(max_len):
     # one tile of rows over a long context: its keys are shared by several CTAs
     import torch
     import quantized_kv_cache_tq_gb300 as tq
     b = Batch(43, [9000], 1, 128, 128, 64)
     q = b.query(100, 2, "bfloat16")
     gs = torch.tensor([0, 100], dtype=torch.int32, device="cuda")
-    out = tq.paged4_prefill(b.gk, b.gv, b.gt, b.gl, q, gs)
+    out = tq.paged4_prefill(b.gk, b.gv, b.gt, b.gl, q, gs, max_len=max_len)
     ref, bound = P.attention(b.k, b.v, b.table, [9000], _np(q), [0, 100], 2, 128 ** -0.5)
     _check(out, ref, bound, "bfloat16")
-    again = tq.paged4_prefill(b.gk, b.gv, b.gt, b.gl, q, gs)
+    again = tq.paged4_prefill(b.gk, b.gv, b.gt, b.gl, q, gs, max_len=max_len)
     assert torch.equal(out, again)
 
 
@@ -530,9 +533,10 @@ def test_diff_decode(dk, dv, hkv, group, page, norm):
         _check(out, ref, bound, dtype)
 
 
-@pytest.mark.parametrize("norm,causal,dtype", [(True, True, "bfloat16"), (False, True, "float16"), (True, False, "float16")])
+@pytest.mark.parametrize("norm,causal,dtype,max_len", [
+    (True, True, "bfloat16", None), (False, True, "float16", 1 << 20), (True, False, "float16", 64)])
 @pytest.mark.parametrize("dk,dv,hkv,group,page", DIFF)
-def test_diff_prefill(dk, dv, hkv, group, page, norm, causal, dtype):
+def test_diff_prefill(dk, dv, hkv, group, page, norm, causal, dtype, max_len):
     import torch
     import quantized_kv_cache_tq_gb300 as tq
     nq, lens = [70, 0, 5, 150], [70, 20, 300, 400]
@@ -545,7 +549,7 @@ def test_diff_prefill(dk, dv, hkv, group, page, norm, causal, dtype):
     out = torch.full((rows, heads, dv), 3.0, device="cuda", dtype=q.dtype)
     gs = torch.tensor(start, dtype=torch.int32, device="cuda")
     tq.paged4_diff_prefill(b.gk, b.gv, b.gt, b.gl, q, gs, lam, norm_weight=w, eps=1e-4, out_scale=0.8, causal=causal,
-                           out=out)
+                           max_len=max_len, out=out)
     ref, bound = P.attention(b.k, b.v, b.table, lens, _np(q), start, heads, dk ** -0.5, causal, lam=_np(lam),
                              norm_weight=_np(w) if norm else None, eps=1e-4, out_scale=0.8)
     ref[start[-1]:], bound[start[-1]:] = 3.0, 0.0
