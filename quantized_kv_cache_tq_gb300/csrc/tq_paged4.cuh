@@ -84,6 +84,7 @@ struct AttnArgs {
   int32_t page_shift;
   int32_t n_heads;           // output heads
   int32_t n_kv_heads;        // V heads
+  float inv_group;                 // 1 / group
   int32_t group;             // output heads per V head
   int32_t dk, dv;            // logical head dims
   int32_t wk, wv;            // stored widths

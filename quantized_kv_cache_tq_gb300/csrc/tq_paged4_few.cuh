@@ -972,6 +972,24 @@ __global__ void __launch_bounds__(FewCfg<DK, DV, NT, MAPS>::THREADS, FewCfg<DK, 
   }
 }
 
+// A launch that may begin while the one before it on the stream is still running (programmatic dependent launch); the
+// kernel waits itself before it reads what that writes.
+inline cudaError_t launch_beside(void (*kern)(AttnArgs), unsigned grid, unsigned threads, size_t smem, cudaStream_t s,
+                                 const AttnArgs &a) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a);
+  return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
 template <int DK, int DV, int NT, int MAPS>
 cudaError_t launch_few_t(const AttnArgs &a, cudaStream_t s) {
   using C = FewCfg<DK, DV, NT, MAPS>;
@@ -982,18 +1000,7 @@ cudaError_t launch_few_t(const AttnArgs &a, cudaStream_t s) {
   auto kern = few_kernel<DK, DV, NT, MAPS>;
   cudaError_t e = set_dynamic_smem(reinterpret_cast<const void *>(kern), C::SMEM);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(sm_count() * C::CTAS);
-  cfg.blockDim = dim3(C::THREADS);
-  cfg.dynamicSmemBytes = C::SMEM;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kern, a);
-  return e == cudaSuccess ? cudaGetLastError() : e;
+  return launch_beside(kern, sm_count() * C::CTAS, C::THREADS, C::SMEM, s, a);
 }
 
 }  // namespace p4

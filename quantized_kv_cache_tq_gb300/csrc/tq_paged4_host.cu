@@ -194,6 +194,7 @@ static tq_status attend(const Call &c) {
   a.n_heads = c.n_heads;
   a.n_kv_heads = c.v->n_kv_heads;
   a.group = group;
+  a.inv_group = 1.f / static_cast<float>(group);
   a.dk = c.k->head_dim;
   a.dv = c.v->head_dim;
   a.wk = wk;

@@ -15,7 +15,9 @@
 // the softmax threads have read it into registers, so the next product of scores
 // runs beside the rest of the softmax and does not wait for P V.  (With a buffer per
 // tile and P written over it, a tile's scores had to wait for its P V: 1200 us at
-// 2048 rows over 32768 cells, 8 KV heads, against NEW_FIG.)
+// 2048 rows over 32768 cells, 8 KV heads, against 1016 us in
+// that step.)  A softmax thread has its weights in registers before it waits for the
+// tile's last P V, so only their store stands between two products (807 -> 786 us).
 // The code of all roles has to stay small: with the products' loops unrolled for one
 // thread and a whole row's 128 keys per softmax thread, the product warp waited for
 // instructions (1390 us in that form).
@@ -81,7 +83,8 @@ struct Cfg {
   static constexpr uint32_t SSC = SKV + 2 * KV_BYTES;          // [j & 3][key] scale of a score
   static constexpr uint32_t STAU = SSC + 4 * BN * 4;           // [j & 3][32 keys] (tau, 2^-tau)
   static constexpr uint32_t SROW = STAU + 4 * 4 * 8;           // [tile][half][row] exchange between a row's threads
-  static constexpr uint32_t TOTAL = SROW + 2 * 2 * BM * 8;
+  static constexpr uint32_t SFX = SROW + 2 * 2 * BM * 8;       // [row] factor of a row's scores
+  static constexpr uint32_t TOTAL = SFX + 2 * BM * 4;
   static constexpr int SKS = KC / 2, PKS = BN / 16;            // k steps of S and of PV
 };
 
@@ -110,7 +113,10 @@ __device__ __forceinline__ void st8(uint32_t taddr, const uint32_t *r) {
 }
 
 // Bounded wait for phase `parity` of `bar` by a whole warp.  Without a suspend-time hint: with one, a warp that
-// found the phase open slept on past its end, on every step of the chain score - softmax - product (WAIT_FIG).
+// found the phase open slept on past its end, on every step of the chain score - softmax - product (2048 rows over 32768 cells: 1282 us with it, 1233 without).
+// SLEEP: with a pause between two tries, for the unpack warps, which have time and leave the others their issue slots
+// (811 -> 804 us).
+template <bool SLEEP = false>
 __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity) {
   const uint32_t at = tc::smem_u32(bar);
   for (int it = 0; it < (1 << 19); ++it) {
@@ -120,6 +126,7 @@ __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity) {
                  : "r"(at), "r"(parity)
                  : "memory");
     if (__all_sync(0xffffffffu, ok != 0)) return true;
+    if (SLEEP) __nanosleep(64);
   }
   return false;
 }
@@ -134,6 +141,9 @@ __device__ __forceinline__ bool elect() {
 __device__ __forceinline__ void sts1(uint32_t at, float x) {
   asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(x) : "memory");
 }
+__device__ __forceinline__ void sts4(uint32_t at, const uint32_t *x) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]) : "memory");
+}
 __device__ __forceinline__ float lds1(uint32_t at) {
   float x;
   asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(at) : "memory");
@@ -143,41 +153,75 @@ __device__ __forceinline__ float lds1(uint32_t at) {
 __device__ __forceinline__ uint32_t bits(__half2 h) { return *reinterpret_cast<const uint32_t *>(&h); }
 __device__ __forceinline__ __half2 as_half2(uint32_t u) { return *reinterpret_cast<const __half2 *>(&u); }
 
-// A piece of an item: key tiles t_lo .. t_lo + n_t - 1 of 256 rows of one sequence and K head.
+// A piece of an item: key tiles t_lo .. t_lo + n_t - 1 of 256 rows of one sequence and K head, with what every
+// role needs to know of the rows.
 struct Piece {
   int seq, tile, kh;        // tile: which 256 rows of the sequence
   int t_lo, n_t;            // n_t < 0: no more pieces
   int c0, n_con, slot;      // LINE: the CTAs that share the item, c0 .. c0 + n_con - 1; where this partial goes
   int slot0;                // ... and where that of c0 is
+  int row0, rem;            // row of the input and head of the group of the tile's first row
+  int left;                 // rows of the sequence from the tile's first one on
+  int lim0;                 // keys that the tile's first row's query sees (below 0: none)
+  int kv_hi;                // ... and its last row's
 };
 
-// Rows and key tiles of one 256-row tile.
+// 256-row tile `i` of a sequence of w.rows queries: its first row is head `rem` of query `q`.  Walked in order, so
+// that one division per sequence does.
 struct Tile {
-  int r0, rows_all, kv_hi, tiles;
+  int i, q, rem;
+  int rows_all, dq, dr;     // rows of the sequence; 256 rows are dq queries and dr heads
 };
-__device__ __forceinline__ Tile tile_of(const AttnArgs &a, const few::SeqWork &w, int tile) {
+__device__ __forceinline__ Tile first_tile(const AttnArgs &a, const few::SeqWork &w, int i) {
   Tile t;
+  t.i = i;
   t.rows_all = w.rows * a.group;
-  t.r0 = tile * 2 * BM;
-  const int last = min(t.rows_all, t.r0 + 2 * BM) - 1;
-  t.kv_hi = a.causal ? max(0, w.len - w.rows + last / a.group + 1) : w.len;
-  t.tiles = (t.kv_hi + BN - 1) / BN;
+  t.dq = 2 * BM / a.group;
+  t.dr = 2 * BM - t.dq * a.group;
+  t.q = i * 2 * BM / a.group;
+  t.rem = i * 2 * BM - t.q * a.group;
   return t;
 }
+__device__ __forceinline__ void next_tile(const AttnArgs &a, Tile &t) {
+  ++t.i;
+  t.q += t.dq;
+  t.rem += t.dr;
+  if (t.rem >= a.group) {
+    t.rem -= a.group;
+    ++t.q;
+  }
+}
+__device__ __forceinline__ int kv_hi_of(const AttnArgs &a, const few::SeqWork &w, const Tile &t) {
+  // (the query of row 255 is the one before the next tile's first row's, or its own)
+  int last = w.rows - 1;
+  if (t.rows_all - t.i * 2 * BM > 2 * BM) last = t.q + t.dq - (t.rem + t.dr == 0 ? 1 : 0) + (t.rem + t.dr > a.group ? 1 : 0);
+  return a.causal ? max(0, w.len - w.rows + last + 1) : w.len;
+}
+__device__ __forceinline__ int key_tiles(int kv_hi) { return (static_cast<uint32_t>(kv_hi) + BN - 1) / BN; }
 __device__ __forceinline__ int tiles_of(const AttnArgs &a, const few::SeqWork &w) {
-  return static_cast<int>((static_cast<long long>(w.rows) * a.group + 2 * BM - 1) / (2 * BM));
+  return (static_cast<uint32_t>(w.rows * a.group) + 2 * BM - 1) / (2 * BM);
+}
+__device__ __forceinline__ void rows_of_piece(const AttnArgs &a, const few::SeqWork &w, const Tile &t, Piece &p) {
+  p.tile = t.i;
+  p.row0 = w.row0 + t.q;
+  p.rem = t.rem;
+  p.left = t.rows_all - t.i * 2 * BM;
+  p.lim0 = a.causal ? w.len - w.rows + t.q + 1 : w.len;
+  p.kv_hi = kv_hi_of(a, w, t);
 }
 
 // A piece, read anew (what only begin and end of its work need is not kept in registers through the loop).
 __device__ __forceinline__ Piece read_piece(const Piece *p) {
   const volatile int *q = reinterpret_cast<const volatile int *>(p);
-  return {q[0], q[1], q[2], q[3], q[4], q[5], q[6], q[7], q[8]};
+  return {q[0], q[1], q[2], q[3], q[4], q[5], q[6], q[7], q[8], q[9], q[10], q[11], q[12], q[13]};
 }
 
-// Row tiles of a piece that have rows.
-__device__ __forceinline__ int row_tiles(const AttnArgs &a, const Piece &p) {
-  const few::SeqWork w = few::seq_work<1>(a, p.seq, false);
-  return w.rows * a.group - p.tile * 2 * BM > BM ? 2 : 1;
+// Row `r` (of 256) of a piece: its query's row of the input, its head within the group.
+__device__ __forceinline__ void query_of(const AttnArgs &a, int rem, int r, int &qi, int &head) {
+  // floor((x + 1/2) / G) in fp32 is exact: x < 2^22, and (x + 1/2) / G is at least 1 / 2G away from an integer
+  const int x = rem + r;
+  qi = static_cast<int>((static_cast<float>(x) + 0.5f) * a.inv_group);
+  head = x - qi * a.group;
 }
 
 // One CTA's walk along the line (one thread).
@@ -187,7 +231,7 @@ struct Walk {
   int seq, tile, kh;
 };
 __device__ inline Piece next_piece(const AttnArgs &a, Walk &w) {
-  Piece p = {0, 0, 0, 0, -1, 0, 1, 0, 0};
+  Piece p = {0, 0, 0, 0, -1, 0, 1, 0, 0, 0, 0, 0, 0, 0};
   const int k_heads = (a.diff ? 2 : 1) * a.n_kv_heads;
   while (w.cur < w.end) {
     const few::SeqWork sw = few::seq_work<1>(a, w.seq, false);
@@ -196,8 +240,8 @@ __device__ inline Piece next_piece(const AttnArgs &a, Walk &w) {
       w.tile = w.kh = 0;
       continue;
     }
-    const Tile t = tile_of(a, sw, w.tile);
-    const int per = t.tiles + ITEM_COST;
+    const Tile t = first_tile(a, sw, w.tile);
+    const int tiles = key_tiles(kv_hi_of(a, sw, t)), per = tiles + ITEM_COST;
     const int r = static_cast<int>(w.cur - w.pre);
     if (r >= per) {                           // the next item: heads first, then tiles
       w.pre += per;
@@ -211,17 +255,17 @@ __device__ inline Piece next_piece(const AttnArgs &a, Walk &w) {
     w.cur += stop - r;
     const int u0 = max(0, r - ITEM_COST), u1 = max(0, stop - ITEM_COST);
     // (an item without keys is its last empty unit's: its rows are zeros)
-    if (u1 <= u0 && !(t.tiles == 0 && stop == per)) continue;
+    if (u1 <= u0 && !(tiles == 0 && stop == per)) continue;
     p.seq = w.seq;
-    p.tile = w.tile;
+    rows_of_piece(a, sw, t, p);
     p.kh = w.kh;
     p.t_lo = u0;
     p.n_t = u1 - u0;
-    if (t.tiles > 0) {
+    if (tiles > 0) {
       const long long ia = w.pre + ITEM_COST;
       auto owner = [&](long long x) { return static_cast<int>(((x + 1) * w.n_work - 1) / w.total); };
       p.c0 = owner(ia);
-      p.n_con = owner(ia + t.tiles - 1) - p.c0 + 1;
+      p.n_con = owner(ia + tiles - 1) - p.c0 + 1;
       p.slot = w.share0 >= ia ? 0 : 1;
       p.slot0 = p.c0 * w.total / w.n_work >= ia ? 0 : 1;
     }
@@ -242,87 +286,10 @@ __global__ void __launch_bounds__(pre::NT, 1) prefill_kernel(const AttnArgs a) {
   __shared__ Walk s_walk;
   __shared__ uint32_t tmem_slot;
   __shared__ int s_fail, s_last;
-  __shared__ long long s_sum[NT / 32];
+  __shared__ long long s_sum[32];            // of warps (fewer than 32), or of 32 sequences
 
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int maps = a.diff ? 2 : 1, k_heads = maps * a.n_kv_heads, G = a.group;
-
-  // ---- the first piece
-  {
-    // in the split form heads fastest, row tiles slowest and from the last one down (under a causal mask the
-    // longest first)
-    const int want = LINE ? 0 : a.n_tiles - 1 - static_cast<int>(blockIdx.x) / k_heads / a.n_split;
-    if (tid == 0) {
-      s_fail = 0;
-      s_piece[0].n_t = s_piece[1].n_t = -1;
-      s_piece[0].seq = -1;
-    }
-    // Line (or row tiles) of the sequences s0 .. before `at`; a second pass finds the share's begin.
-    long long total = 0, begin = 0, end = 0, n_work = 0;
-    for (int pass = 0; pass < (LINE ? 2 : 1); ++pass) {
-      long long at = 0;
-      if (pass == 1) {
-        n_work = min(static_cast<long long>(gridDim.x), total);
-        if (blockIdx.x >= n_work) break;
-        begin = blockIdx.x * total / n_work;
-        end = (blockIdx.x + 1) * total / n_work;
-      }
-      for (int s0 = 0; s0 < a.n_seq; s0 += NT) {
-        const int s = s0 + tid;
-        long long v = 0;
-        if (s < a.n_seq) {
-          const few::SeqWork w = few::seq_work<1>(a, s, pass == 0 && blockIdx.x == 0);
-          const int n = tiles_of(a, w);
-          if (!LINE) v = n;
-          else
-            for (int i = 0; i < n; ++i) v += tile_of(a, w, i).tiles + ITEM_COST;
-          if (LINE) v *= k_heads;
-        }
-        long long x = v;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const long long y = __shfl_up_sync(0xffffffffu, x, o);
-          if (lane >= o) x += y;
-        }
-        __syncthreads();
-        if (lane == 31) s_sum[warp] = x;
-        __syncthreads();
-        long long all = 0;
-        for (int w = 0; w < NT / 32; ++w) {
-          if (w == warp) x += all;
-          all += s_sum[w];
-        }
-        x += at;
-        at += all;
-        if (!LINE && v > 0 && x - v <= want && want < x) {
-          const few::SeqWork w = few::seq_work<1>(a, s, false);
-          Piece p = {s, static_cast<int>(want - (x - v)), static_cast<int>(blockIdx.x) % k_heads, 0, 0, 0, 1, 0, 0};
-          const int tiles = tile_of(a, w, p.tile).tiles, split = static_cast<int>(blockIdx.x) / k_heads % a.n_split;
-          p.t_lo = static_cast<int>(static_cast<long long>(tiles) * split / a.n_split);
-          p.n_t = static_cast<int>(static_cast<long long>(tiles) * (split + 1) / a.n_split) - p.t_lo;
-          s_piece[0] = p;
-        }
-        if (LINE && pass == 1 && v > 0 && x - v <= begin && begin < x) {
-          const few::SeqWork w = few::seq_work<1>(a, s, false);
-          Walk k = {begin, end, x - v, begin, total, n_work, s, 0, 0};
-          for (;;) {                          // (begin < x: the loop ends at one of the sequence's tiles)
-            const long long t = static_cast<long long>(tile_of(a, w, k.tile).tiles + ITEM_COST) * k_heads;
-            if (begin < k.pre + t) break;
-            k.pre += t;
-            ++k.tile;
-          }
-          const int per = tile_of(a, w, k.tile).tiles + ITEM_COST;
-          k.kh = static_cast<int>((begin - k.pre) / per);
-          k.pre += static_cast<long long>(k.kh) * per;
-          s_piece[0] = next_piece(a, k);
-          s_walk = k;
-        }
-      }
-      if (pass == 0) total = at;
-    }
-    __syncthreads();
-  }
-  if (s_piece[0].n_t < 0) return;             // no work for this CTA
 
   if (warp == W_MMA) tc::tmem_alloc<512>(&tmem_slot);
   if (tid == NT - 1) {
@@ -348,10 +315,148 @@ __global__ void __launch_bounds__(pre::NT, 1) prefill_kernel(const AttnArgs a) {
                                  (key & 7) * 16) = make_uint4(0, 0, 0, 0);
   }
   tc::fence_async_smem();
+  // The launch may have begun beside the one before it (programmatic dependent launch).
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // ---- the first piece.  Up to 32 sequences each warp finds it alone, else the CTA together.
+  if (tid == 0) {
+    s_fail = 0;
+    s_piece[0].n_t = s_piece[1].n_t = -1;
+    s_piece[0].seq = -1;
+  }
+  __syncwarp();
+  {
+    // in the split form heads fastest, row tiles slowest and from the last one down (under a causal mask the
+    // longest first)
+    const int want = LINE ? 0 : a.n_tiles - 1 - static_cast<int>(blockIdx.x) / k_heads / a.n_split;
+    const bool alone = a.n_seq <= 32;
+    auto scan = [&](long long v) {            // over the warp, inclusive
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += y;
+      }
+      return v;
+    };
+    // the same over the CTA, behind `at`; moves `at` past all of it
+    auto scan_all = [&](long long v, long long &at) {
+      long long x = scan(v), all = 0;
+      __syncthreads();
+      if (lane == 31) s_sum[warp] = x;
+      __syncthreads();
+      for (int k = 0; k < NT / 32; ++k) {
+        if (k == warp) x += all;
+        all += s_sum[k];
+      }
+      x += at;
+      at += all;
+      return x;
+    };
+    if (!LINE) {
+      long long at = 0;
+      for (int s0 = 0; s0 < a.n_seq; s0 += NT) {
+        const int s = s0 + (alone ? lane : tid);
+        few::SeqWork w;
+        long long v = 0;
+        if (s < a.n_seq) {
+          w = few::seq_work<1>(a, s, blockIdx.x == 0);
+          v = tiles_of(a, w);
+        }
+        const long long x = alone ? scan(v) : scan_all(v, at);
+        if (v > 0 && x - v <= want && want < x && (warp == 0 || !alone)) {
+          Piece p = {s, 0, static_cast<int>(blockIdx.x) % k_heads, 0, 0, 0, 1, 0, 0, 0, 0, 0, 0, 0};
+          rows_of_piece(a, w, first_tile(a, w, static_cast<int>(want - (x - v))), p);
+          const int tiles = key_tiles(p.kv_hi), split = static_cast<int>(blockIdx.x) / k_heads % a.n_split;
+          p.t_lo = tiles * split / a.n_split;                // (below 2^24 tiles, 64 splits)
+          p.n_t = tiles * (split + 1) / a.n_split - p.t_lo;
+          s_piece[0] = p;
+        }
+      }
+    } else {
+      auto cost = [&](const few::SeqWork &w, const Tile &t) {
+        return static_cast<long long>(key_tiles(kv_hi_of(a, w, t)) + ITEM_COST) * k_heads;
+      };
+      long long begin = 0, end = 0, n_work = 0, total = 0;
+      auto share = [&]() {
+        n_work = min(static_cast<long long>(gridDim.x), total);
+        if (blockIdx.x >= n_work) return false;
+        begin = blockIdx.x * total / n_work;
+        end = (blockIdx.x + 1) * total / n_work;
+        return true;
+      };
+      if (alone) {                            // a warp per sequence, a lane per tile
+        for (int s = warp; s < a.n_seq; s += NT / 32) {
+          const few::SeqWork w = few::seq_work<1>(a, s, blockIdx.x == 0);
+          const int n = tiles_of(a, w);
+          long long v = 0;
+          for (int i = lane; i < n; i += 32) v += cost(w, first_tile(a, w, i));
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+          if (lane == 0) s_sum[s] = v;
+        }
+        __syncthreads();
+        const long long v = lane < a.n_seq ? s_sum[lane] : 0, x = scan(v);
+        total = __shfl_sync(0xffffffffu, x, 31);
+        if (share() && x - v <= begin && begin < x && warp == 0) {
+          s_walk.seq = lane;
+          s_walk.pre = x - v;
+        }
+      } else {                                // a thread per sequence; a second pass finds the share's begin
+        for (int pass = 0; pass < 2; ++pass) {
+          if (pass == 1 && !share()) break;
+          long long at = 0;
+          for (int s0 = 0; s0 < a.n_seq; s0 += NT) {
+            const int s = s0 + tid;
+            long long v = 0;
+            if (s < a.n_seq) {
+              const few::SeqWork w = few::seq_work<1>(a, s, pass == 0 && blockIdx.x == 0);
+              const int n = tiles_of(a, w);
+              for (Tile t = first_tile(a, w, 0); t.i < n; next_tile(a, t)) v += cost(w, t);
+            }
+            const long long x = scan_all(v, at);
+            if (pass == 1 && x - v <= begin && begin < x) {
+              s_walk.seq = s;
+              s_walk.pre = x - v;
+            }
+          }
+          total = at;
+        }
+        __syncthreads();
+      }
+      if (warp == 0 && blockIdx.x < n_work) {                // the tile and head where the share begins
+        __syncwarp();
+        Walk k = {begin, end, s_walk.pre, begin, total, n_work, s_walk.seq, 0, 0};
+        const few::SeqWork w = few::seq_work<1>(a, k.seq, false);
+        const int n = tiles_of(a, w);
+        for (int i0 = 0; i0 < n; i0 += 32) {
+          const long long c = i0 + lane < n ? cost(w, first_tile(a, w, i0 + lane)) : 0, x = scan(c) + k.pre;
+          const uint32_t hit = __ballot_sync(0xffffffffu, begin < x);
+          const int l = hit ? __ffs(hit) - 1 : 31;
+          k.pre = __shfl_sync(0xffffffffu, hit ? x - c : x, l);
+          if (hit) {
+            k.tile = i0 + l;
+            const long long per = __shfl_sync(0xffffffffu, c, l) / k_heads;
+            k.kh = static_cast<int>((begin - k.pre) / per);
+            k.pre += k.kh * per;
+            break;
+          }
+        }
+        __syncwarp();
+        if (lane == 0) {
+          s_piece[0] = next_piece(a, k);
+          s_walk = k;
+        }
+      }
+    }
+  }
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = tmem_slot;
+  if (s_piece[0].n_t < 0) {                   // no work for this CTA
+    if (warp == W_MMA) tc::tmem_dealloc<512>(tmem);
+    return;
+  }
   const uint32_t sbase = tc::smem_u32(smem);
   constexpr uint32_t TS = 0, TP = 128, TO = 256;        // TMEM columns: S, P of tile X at 128 + 64 X, O at 256 + 128 X
   // Barriers of the CTA: 0 all warps between two pieces; 1 .. 8 the two warps of 32 rows; 9 Q written (softmax
@@ -376,7 +481,7 @@ __global__ void __launch_bounds__(pre::NT, 1) prefill_kernel(const AttnArgs a) {
       for (int i = 0;; ++i) {
         const int n_t = s_piece[i & 1].n_t;
         if (n_t < 0) break;
-        const bool two = row_tiles(a, s_piece[i & 1]) == 2;
+        const bool two = s_piece[i & 1].left > BM;
         auto product = [&](int x, int j) {    // O += P V of row tile x, key tile j of the piece
           const int J = base + j;
           if (x == 0) ok = wait_warp(&bars.v[J & 1], (J >> 1) & 1);
@@ -454,55 +559,50 @@ __global__ void __launch_bounds__(pre::NT, 1) prefill_kernel(const AttnArgs a) {
       const Piece pc = s_piece[i & 1];
       if (pc.n_t < 0) break;
       const int n_t = pc.n_t, t_lo = pc.t_lo, kh = pc.kh, hv = kh / maps;
-      const int kv_hi = tile_of(a, few::seq_work<1>(a, pc.seq, false), pc.tile).kv_hi;
+      const int kv_hi = pc.kv_hi;
       const int32_t *table = a.block_table + static_cast<int64_t>(pc.seq) * a.max_pages;
       auto page_of = [&](int j) {
-        const int t = (t_lo + j) * BN + key;
-        return j < n_t && t < kv_hi ? __ldg(table + (t >> a.page_shift)) : -2;       // -2: no such key
+        const uint32_t t = static_cast<uint32_t>(t_lo + j) * BN + key;               // (up to 2^31 + 127)
+        return j < n_t && t < static_cast<uint32_t>(kv_hi) ? __ldg(table + (t >> a.page_shift)) : -2;   // no such key
       };
-      uint4 kraw[DK / 32], vraw[DV / 32];
+      constexpr int CK = DK / 32, CV = DV / 32;
+      constexpr uint32_t NONE = 0xffffffffu;
+      uint4 kraw[CK], vraw[CV];
       uint32_t ksm = 0, vsm = 0;              // (scale, offset) pairs
-      // row of the planes of this thread's key in tile j, or -1
-      auto row_of = [&](int j, int page) -> int64_t {
-        if (page < 0 || page >= a.n_pages) {
+      uint32_t kr, vr;                        // rows of the planes (below 2^32 by the caches' limits)
+      auto rows_of = [&](int j, int page) {
+        kr = vr = NONE;
+        if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(a.n_pages)) {
           if (page != -2) set_status(a.status, TQ_ERR_DEVICE_CHECK);                 // a zero row
-          return -1;
+          return;
         }
-        const int t = (t_lo + j) * BN + key;
-        return static_cast<int64_t>(page) * a.n_kv_heads * (mask + 1) + (t & mask);  // of V head 0
+        const uint32_t in = (static_cast<uint32_t>(t_lo + j) * BN + key) & mask, pg = static_cast<uint32_t>(page) * a.n_kv_heads;
+        kr = ((pg * maps + kh) << a.page_shift) + in;
+        vr = ((pg + hv) << a.page_shift) + in;
       };
-      auto load_k = [&](int64_t rw) {
-        ksm = 0;
+      auto load_k = [&]() {
+        ksm = kr != NONE ? __ldg(reinterpret_cast<const uint32_t *>(a.k_scales) + kr) : 0;
 #pragma unroll
-        for (int c = 0; c < DK / 32; ++c) kraw[c] = make_uint4(0, 0, 0, 0);
-        if (rw >= 0) {
-          // (row of K head kh: K planes have `maps` heads per V head)
-          const int64_t in = rw & mask, k = (rw - in) * maps + static_cast<int64_t>(kh) * (mask + 1) + in;
-          const uint4 *p = reinterpret_cast<const uint4 *>(a.k_codes + k * (DK / 2));
-          ksm = __ldg(reinterpret_cast<const uint32_t *>(a.k_scales) + k);
-#pragma unroll
-          for (int c = 0; c < DK / 32; ++c) kraw[c] = __ldg(p + c);
+        for (int c = 0; c < CK; ++c) {
+          kraw[c] = make_uint4(0, 0, 0, 0);
+          if (kr != NONE) kraw[c] = __ldg(reinterpret_cast<const uint4 *>(a.k_codes + static_cast<uint64_t>(kr) * (DK / 2)) + c);
         }
       };
-      auto load_v = [&](int64_t rw) {
-        vsm = 0;
+      auto load_v = [&]() {
+        vsm = vr != NONE ? __ldg(reinterpret_cast<const uint32_t *>(a.v_scales) + vr) : 0;
 #pragma unroll
-        for (int c = 0; c < DV / 32; ++c) vraw[c] = make_uint4(0, 0, 0, 0);
-        if (rw >= 0) {
-          const int64_t v = rw + static_cast<int64_t>(hv) * (mask + 1);
-          const uint4 *p = reinterpret_cast<const uint4 *>(a.v_codes + v * (DV / 2));
-          vsm = __ldg(reinterpret_cast<const uint32_t *>(a.v_scales) + v);
-#pragma unroll
-          for (int c = 0; c < DV / 32; ++c) vraw[c] = __ldg(p + c);
+        for (int c = 0; c < CV; ++c) {
+          vraw[c] = make_uint4(0, 0, 0, 0);
+          if (vr != NONE) vraw[c] = __ldg(reinterpret_cast<const uint4 *>(a.v_codes + static_cast<uint64_t>(vr) * (DV / 2)) + c);
         }
       };
-      int64_t rw = row_of(0, page_of(0));
-      load_k(rw);
-      load_v(rw);
+      rows_of(0, page_of(0));
+      load_k();
+      load_v();
       int page = page_of(1);
       for (int j = 0; j < n_t; ++j) {
         const int J = base + j, b = J & 1;
-        if (J >= 2) ok = wait_warp(&bars.kf[b], ((J - 2) >> 1) & 1);    // the K buffer's last users
+        if (J >= 2) ok = wait_warp<true>(&bars.kf[b], ((J - 2) >> 1) & 1);    // the K buffer's last users
         if (!ok) { s_fail = 1; break; }
         unsigned char *kd = smem + C::SKV + b * C::KV_BYTES + (key >> 3) * (C::KC * 128) + (key & 7) * 16;
         unsigned char *vd = smem + C::SKV + b * C::KV_BYTES + C::K_BYTES + (key >> 3) * (C::VC * 128) + (key & 7) * 16;
@@ -530,12 +630,12 @@ __global__ void __launch_bounds__(pre::NT, 1) prefill_kernel(const AttnArgs a) {
                          bits(__halves2half2(lo, __float2half_rn(0.f))), 0);
           reinterpret_cast<float *>(smem + C::SSC)[(J & 3) * BN + key] = sm.x;
 #pragma unroll
-          for (int c4 = 0; c4 < DK / 32; ++c4) {
-            const uint32_t w[4] = {kraw[c4].x & keep, kraw[c4].y & keep, kraw[c4].z & keep, kraw[c4].w & keep};
+          for (int i = 0; i < CK; ++i) {
+            const uint32_t w[4] = {kraw[i].x & keep, kraw[i].y & keep, kraw[i].z & keep, kraw[i].w & keep};
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               const uint32_t u = w[c] >> 8;
-              *reinterpret_cast<uint4 *>(kd + (4 * c4 + c) * 128) =
+              *reinterpret_cast<uint4 *>(kd + (4 * i + c) * 128) =
                   make_uint4(w[c] & 0x000f000fu, w[c] & 0x00f000f0u, u & 0x000f000fu, u & 0x00f000f0u);
             }
           }
@@ -546,17 +646,17 @@ __global__ void __launch_bounds__(pre::NT, 1) prefill_kernel(const AttnArgs a) {
           tc::mbar_arrive(&bars.sc[J & 3]);
           tc::mbar_arrive(&bars.k[b]);
         }
-        rw = row_of(j + 1, page);
-        load_k(rw);                           // on its way while the values are unpacked
+        rows_of(j + 1, page);
+        load_k();                             // on its way while the values are unpacked
         if (J >= 2)                           // the V buffer's last users
-          for (int x = 0; x < 2 && ok; ++x) ok = wait_warp(&bars.pv[x][b], ((J - 2) >> 1) & 1);
+          for (int x = 0; x < 2 && ok; ++x) ok = wait_warp<true>(&bars.pv[x][b], ((J - 2) >> 1) & 1);
         if (!ok) { s_fail = 1; break; }
         {
           const __half2 vs = __float2half2_rn(vsc.x * dn), vm = __float2half2_rn(vsc.y * dn);
           const __half2 k1024 = as_half2(0x64006400u), k16 = as_half2(0x2c002c00u), k64 = as_half2(0xd400d400u);
 #pragma unroll
-          for (int c4 = 0; c4 < DV / 32; ++c4) {
-            const uint32_t w[4] = {vraw[c4].x, vraw[c4].y, vraw[c4].z, vraw[c4].w};
+          for (int i = 0; i < CV; ++i) {
+            const uint32_t w[4] = {vraw[i].x, vraw[i].y, vraw[i].z, vraw[i].w};
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               const uint32_t u = w[c] >> 8;
@@ -565,13 +665,13 @@ __global__ void __launch_bounds__(pre::NT, 1) prefill_kernel(const AttnArgs a) {
               const __half2 c1 = __hfma2(as_half2((w[c] & 0x00f000f0u) | 0x64006400u), k16, k64);
               const __half2 c2 = __hsub2(as_half2((u & 0x000f000fu) | 0x64006400u), k1024);
               const __half2 c3 = __hfma2(as_half2((u & 0x00f000f0u) | 0x64006400u), k16, k64);
-              *reinterpret_cast<uint4 *>(vd + (4 * c4 + c) * 128) =
+              *reinterpret_cast<uint4 *>(vd + (4 * i + c) * 128) =
                   make_uint4(bits(__hfma2(c0, vs, vm)), bits(__hfma2(c1, vs, vm)), bits(__hfma2(c2, vs, vm)),
                              bits(__hfma2(c3, vs, vm)));
             }
           }
         }
-        load_v(rw);
+        load_v();
         page = page_of(j + 2);
         tc::fence_async_smem();
         __syncwarp();
@@ -596,82 +696,96 @@ __global__ void __launch_bounds__(pre::NT, 1) prefill_kernel(const AttnArgs a) {
       if (n_t < 0) break;
       bool here, row_ok;
       int lim;                                // keys that the row sees, from the piece's first one on
-      float fx = 1.f;                         // x = fx s_t (score), fx > 0
       {
-      const Piece pc = read_piece(&s_piece[i & 1]);
-      const few::SeqWork sw = few::seq_work<1>(a, pc.seq, false);
-      const Tile tl = tile_of(a, sw, pc.tile);
-      const int hv = pc.kh / maps, map = pc.kh - hv * maps;
-      const int r = tl.r0 + X * BM + row;     // row of the sequence
-      here = X == 0 || tl.rows_all - tl.r0 > BM;
-      row_ok = r < tl.rows_all;
-      const int qi = row_ok ? r / G : 0, head = hv * G + (row_ok ? r - qi * G : 0);
-      const int64_t out_row = static_cast<int64_t>(sw.row0) + qi;
-      lim = (!row_ok ? 0 : a.causal ? max(0, sw.len - sw.rows + qi + 1) : sw.len) - pc.t_lo * BN;
-      // ---- Q: half of the row's dims per thread
-      if (here) {
-        constexpr int NC = DK / 16;           // 8-element chunks of a thread
-        const uint16_t *src = static_cast<const uint16_t *>(a.q) + out_row * a.q_stride +
-                              static_cast<int64_t>(maps * head + map) * a.dk;
-        float2 *ex = reinterpret_cast<float2 *>(smem + C::SROW) + X * 2 * BM;           // [half][row]: (max, sum)
-        uint4 raw[NC];
-        float mx = 0.f, sum = 0.f;
+        const Piece pc = read_piece(&s_piece[i & 1]);
+        const int hv = pc.kh / maps, map = pc.kh - hv * maps;
+        here = X == 0 || pc.left > BM;
+        row_ok = X * BM + row < pc.left;
+        int qi, head;
+        query_of(a, pc.rem, row_ok ? X * BM + row : 0, qi, head);
+        lim = (!row_ok ? 0 : a.causal ? max(0, pc.lim0 + qi) : pc.lim0) - pc.t_lo * BN;
+        // ---- Q: a warp takes 16 rows, 8 beside each other, of which 4 lanes share one: a load touches 8 lines (with a
+        // row per lane 32; the first product then waited 6000 clocks for Q) and a store of 8 lanes 128 bytes
+        if (here) {
+          constexpr int NC = DK / 32;         // 8-element chunks of a lane and row
+          const int sub = lane >> 3, r0 = X * BM + 16 * (warp & 7) + (lane & 7);
+          uint4 raw[2][NC];
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          const int d = 8 * (half * NC + c);
-          raw[c] = make_uint4(0, 0, 0, 0);
-          if (row_ok && d < a.dk) raw[c] = __ldg(reinterpret_cast<const uint4 *>(src + d));
-        }
+          for (int t = 0; t < 2; ++t) {
+            const bool there = r0 + 8 * t < pc.left;
+            query_of(a, pc.rem, there ? r0 + 8 * t : 0, qi, head);
+            const uint16_t *src = static_cast<const uint16_t *>(a.q) + static_cast<int64_t>(pc.row0 + qi) * a.q_stride +
+                                  static_cast<int64_t>(maps * (head + hv * G) + map) * a.dk;
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          float v[8];
-          few::unpack8(raw[c], a.bf16, v);
+            for (int c = 0; c < NC; ++c) {
+              const int d = 8 * (sub + 4 * c);
+              raw[t][c] = there && d < a.dk ? __ldg(reinterpret_cast<const uint4 *>(src + d)) : make_uint4(0, 0, 0, 0);
+            }
+          }
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            mx = fmaxf(mx, fabsf(v[e]));
-            sum += v[e];
+          for (int t = 0; t < 2; ++t) {
+            float mx = 0.f;
+            float2 s2 = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+              float v[8];
+              few::unpack8(raw[t][c], a.bf16, v);
+#pragma unroll
+              for (int e = 0; e < 8; e += 2) {
+                mx = max3(mx, fabsf(v[e]), fabsf(v[e + 1]));
+                s2 = add2(s2, make_float2(v[e], v[e + 1]));
+              }
+            }
+            float sum = s2.x + s2.y;
+#pragma unroll
+            for (int o = 8; o < 32; o <<= 1) {
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+              sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            }
+            // largest entry in [2^e, 2^(e + 1)) -> [2^12, 2^13); the scale's sign goes into q, a scale of 0 makes it 0.
+            // (A row below 2^-100 keeps fewer bits; its scores are nothing to an exponent.)
+            const int e = mx > 0.f ? max(static_cast<int>(__float_as_uint(mx) >> 23) - 127, -100) : 0;
+            const float up = __uint_as_float(static_cast<uint32_t>(12 - e + 127) << 23) *
+                             (a.scale_log2 > 0.f ? 1.f : a.scale_log2 < 0.f ? -1.f : 0.f);
+            unsigned char *dst = smem + C::SQ + X * C::Q_BYTES + (2 * (warp & 7) + t) * 128 + (lane & 7) * 16;
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+              float v[8];
+              few::unpack8(raw[t][c], a.bf16, v);
+#pragma unroll
+              for (int k = 0; k < 8; k += 2) {
+                const float2 u = mul2(make_float2(v[k], v[k + 1]), make_float2(up, up * 0.0625f));
+                v[k] = u.x;
+                v[k + 1] = u.y;
+              }
+              // the order in which a code word unpacks: (0, 4), (1, 5), (2, 6), (3, 7)
+              *reinterpret_cast<uint4 *>(dst + (sub + 4 * c) * 2048) =
+                  make_uint4(few::half2_bits(v[0], v[4]), few::half2_bits(v[1], v[5]), few::half2_bits(v[2], v[6]),
+                             few::half2_bits(v[3], v[7]));
+            }
+            if (sub == 0) {
+              const float qs = sum * up * 0x1p-20f;
+              const __half h0 = __float2half_rn(qs);
+              const __half h1 = __float2half_rn(qs - __half2float(h0));
+              const __half h2 = __float2half_rn(qs - __half2float(h0) - __half2float(h1));
+              const __half z = __float2half_rn(0.f);
+              *reinterpret_cast<uint4 *>(dst + (DK / 8) * 2048) =
+                  make_uint4(bits(__halves2half2(h0, h1)), bits(__halves2half2(h2, h0)), bits(__halves2half2(h1, z)), 0);
+            } else if (sub == 1) {
+              *reinterpret_cast<uint4 *>(dst + (DK / 8 + 1) * 2048) = make_uint4(0, 0, 0, 0);
+            } else if (sub == 2) {
+              reinterpret_cast<float *>(smem + C::SFX)[r0 + 8 * t] =
+                  a.scale_log2 != 0.f
+                      ? fmaxf(fabsf(a.scale_log2) * 4096.f * __uint_as_float(static_cast<uint32_t>(e + 127) << 23), 1e-37f)
+                      : 1.f;
+            }
           }
         }
-        ex[half * BM + row] = make_float2(mx, sum);
-        tc::named_sync(pair, 64);
-        const float2 e0 = ex[row], e1 = ex[BM + row];
-        mx = fmaxf(e0.x, e1.x);
-        sum = e0.y + e1.y;
-        // largest entry in [2^e, 2^(e + 1)) -> [2^12, 2^13); the scale's sign goes into q, a scale of 0 makes it 0
-        const int e = mx > 0.f ? static_cast<int>(__float_as_uint(mx) >> 23) - 127 : 0;
-        const float s1 = __uint_as_float(static_cast<uint32_t>((12 - e) / 2 + 127) << 23);
-        const float s2 = __uint_as_float(static_cast<uint32_t>((12 - e) - (12 - e) / 2 + 127) << 23) *
-                         (a.scale_log2 > 0.f ? 1.f : a.scale_log2 < 0.f ? -1.f : 0.f);
-        if (a.scale_log2 != 0.f) fx = fmaxf(fabsf(a.scale_log2) * exp2f(static_cast<float>(12 + e)), 1e-37f);
-        unsigned char *dst = smem + C::SQ + X * C::Q_BYTES + (row >> 3) * 128 + (row & 7) * 16;
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          float v[8];
-          few::unpack8(raw[c], a.bf16, v);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) v[k] = v[k] * s1 * s2 * ((k & 1) ? 0.0625f : 1.f);
-          // the order in which a code word unpacks: (0, 4), (1, 5), (2, 6), (3, 7)
-          *reinterpret_cast<uint4 *>(dst + (half * NC + c) * 2048) =
-              make_uint4(few::half2_bits(v[0], v[4]), few::half2_bits(v[1], v[5]), few::half2_bits(v[2], v[6]),
-                         few::half2_bits(v[3], v[7]));
-        }
-        if (half == 0) {
-          const float qs = sum * s1 * s2 * 0x1p-20f;
-          const __half h0 = __float2half_rn(qs);
-          const __half h1 = __float2half_rn(qs - __half2float(h0));
-          const __half h2 = __float2half_rn(qs - __half2float(h0) - __half2float(h1));
-          const __half z = __float2half_rn(0.f);
-          *reinterpret_cast<uint4 *>(dst + (DK / 8) * 2048) =
-              make_uint4(bits(__halves2half2(h0, h1)), bits(__halves2half2(h2, h0)), bits(__halves2half2(h1, z)), 0);
-        } else {
-          *reinterpret_cast<uint4 *>(dst + (DK / 8 + 1) * 2048) = make_uint4(0, 0, 0, 0);
-        }
-        tc::named_sync(pair, 64);             // the exchange is free for the maxima
-      }
       }
       tc::fence_async_smem();
       tc::named_sync(BAR_Q, 32 * (W_UNPACK + 1));
 
+      const float fx = reinterpret_cast<const float *>(smem + C::SFX)[X * BM + row];    // x = fx s_t (score), fx > 0
       float R = -INFINITY, l = 0.f;
       const uint32_t ex = sbase + C::SROW + (X * 4 * BM + row) * 4;                     // [J & 1][half][row]
       const float2 fx2 = make_float2(fx, fx);
@@ -740,17 +854,31 @@ __global__ void __launch_bounds__(pre::NT, 1) prefill_kernel(const AttnArgs a) {
         sts1(ex + (2 * (J & 1) + half) * BM * 4, top);
         tc::named_sync(pair, 64);
         top = fmaxf(top, lds1(ex + (2 * (J & 1) + (half ^ 1)) * BM * 4));
-        if (J > J0) {                         // P and O stand still
+        const bool raise = top > R + RAISE, any = __any_sync(0xffffffffu, raise);
+        const float f = raise ? exp2f(R - top) : 1.f;                   // 0 at the first raise
+        if (raise) R = top;
+        l *= f;
+        const float Rs = R == -INFINITY ? 0.f : R;
+        uint32_t p[HK / 2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float2 t2 = c ? make_float2(tau.z, tau.w) : make_float2(tau.x, tau.y);
+          const float2 off = make_float2(t2.x - Rs, t2.x - Rs);
+          float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int q = 16 * c; q < 16 * c + 16; ++q) {
+            const float2 e = fma2(make_float2(y[2 * q], y[2 * q + 1]), fx2, off);
+            const float2 w = make_float2(tc::ex2(e.x), tc::ex2(e.y));                   // masked: 0
+            sum = add2(sum, w);
+            p[q] = few::half2_bits(w.x, w.y);
+          }
+          l = fmaf(sum.x + sum.y, t2.y, l);
+        }
+        if (J > J0) {                         // only now must P and O stand still
           ok = wait_warp(&bars.pv[X][(J - 1) & 1], ((J - 1) >> 1) & 1);
           if (!ok) continue;
           tc::fence_after_sync();
-        }
-        const bool raise = top > R + RAISE;
-        if (__any_sync(0xffffffffu, raise)) {
-          const float f = raise ? exp2f(R - top) : 1.f;                 // 0 at the first raise
-          if (raise) R = top;
-          l *= f;
-          if (J > J0) {
+          if (any) {
 #pragma unroll 1
             for (int c = half * (DV / 2); c < (half + 1) * (DV / 2); c += 8) {
               uint32_t o[8];
@@ -764,27 +892,8 @@ __global__ void __launch_bounds__(pre::NT, 1) prefill_kernel(const AttnArgs a) {
             }
           }
         }
-        const float Rs = R == -INFINITY ? 0.f : R;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const float2 t2 = c ? make_float2(tau.z, tau.w) : make_float2(tau.x, tau.y);
-          const float2 off = make_float2(t2.x - Rs, t2.x - Rs);
-          float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t p[8];
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              const int k = 32 * c + 16 * h + 2 * q;
-              const float2 e = fma2(make_float2(y[k], y[k + 1]), fx2, off);
-              const float2 w = make_float2(tc::ex2(e.x), tc::ex2(e.y));                 // masked: 0
-              sum = add2(sum, w);
-              p[q] = few::half2_bits(w.x, w.y);
-            }
-            st8(tp + 16 * c + 8 * h, p);
-          }
-          l = fmaf(sum.x + sum.y, t2.y, l);
-        }
+        for (int c = 0; c < 4; ++c) st8(tp + 8 * c, p + 8 * c);
         tc::tmem_wait_st();
         tc::fence_before_sync();
         __syncwarp();
@@ -804,37 +913,59 @@ __global__ void __launch_bounds__(pre::NT, 1) prefill_kernel(const AttnArgs a) {
         l += lds1(ex + (half ^ 1) * BM * 4);
       }
       const Piece pc = read_piece(&s_piece[i & 1]);
-      const few::SeqWork sw = few::seq_work<1>(a, pc.seq, false);
-      const int hv = pc.kh / maps, map = pc.kh - hv * maps, r = pc.tile * 2 * BM + X * BM + row;
-      const int qi = row_ok ? r / G : 0, head = hv * G + (row_ok ? r - qi * G : 0);
-      const int64_t out_row = static_cast<int64_t>(sw.row0) + qi;
-      // 8 dims of the row: values times `inv` to the output, or as they are to the rows' partial results
+      const int hv = pc.kh / maps, map = pc.kh - hv * maps;
       const bool rows_part = a.diff || a.n_split > 1;
-      float *part = a.row_part + (((out_row * a.n_heads + head) * maps + map) * a.n_split +
-                                  (LINE ? 0 : static_cast<int>(blockIdx.x) / k_heads % a.n_split)) * (DV + 4);
-      auto put = [&](int d, const float *v, float inv) {
-        if (!row_ok || d >= a.dv) return;
+      // where row r (of 256) puts its values: the output, or its partial results (R, l, -, -, values)
+      auto out_of = [&](int r) {
+        int qi, head;
+        query_of(a, pc.rem, r, qi, head);
+        return static_cast<int64_t>(pc.row0 + qi) * a.n_heads + hv * G + head;
+      };
+      auto part_at = [&](int64_t at) {
+        return a.row_part + ((at * maps + map) * a.n_split + (LINE ? 0 : static_cast<int>(blockIdx.x) / k_heads % a.n_split)) * (DV + 4);
+      };
+      // 64 bytes of each of the warp's rows (lane: row), values from dim d on, by way of shared memory (where Q was), so
+      // that a store touches 8 lines: 4 lanes share a row.  Swizzled, so that neither side has bank conflicts.
+      const uint32_t stage = sbase + C::SQ + X * C::Q_BYTES + (warp & 7) * 2048;
+      auto put64 = [&](const uint32_t *w, int d) {
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) sts4(stage + lane * 64 + ((c ^ (lane >> 1)) & 3) * 16, w + 4 * c);
+        __syncwarp();
+        const int c = lane & 3, dim = d + c * (rows_part ? 4 : 8);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const int rl = 8 * t + (lane >> 2), r = X * BM + 32 * (warp & 3) + rl;
+          const float4 u = few::lds4(stage + rl * 64 + ((c ^ (rl >> 1)) & 3) * 16);
+          if (r >= pc.left || dim >= a.dv) continue;
+          const int64_t to_row = out_of(r);
+          if (rows_part) *reinterpret_cast<float4 *>(part_at(to_row) + 4 + dim) = u;
+          else *reinterpret_cast<float4 *>(static_cast<uint16_t *>(a.out) + to_row * a.dv + dim) = u;
+        }
+      };
+      // 32 values of each row: times `inv` to the output, or as they are to the partial results
+      auto put32 = [&](int d, const float *v, float inv) {
+        uint32_t w[16];
         if (rows_part) {
-          *reinterpret_cast<float4 *>(part + 4 + d) = make_float4(v[0], v[1], v[2], v[3]);
-          *reinterpret_cast<float4 *>(part + 8 + d) = make_float4(v[4], v[5], v[6], v[7]);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(v[16 * h + e]);
+            put64(w, d + 16 * h);
+          }
           return;
         }
-        uint32_t w[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (a.bf16) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * e] * inv, v[2 * e + 1] * inv);
-            w[e] = *reinterpret_cast<const uint32_t *>(&h);
-          } else {
-            w[e] = few::half2_bits(v[2 * e] * inv, v[2 * e + 1] * inv);
-          }
+        for (int e = 0; e < 16; ++e) {
+          const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * e] * inv, v[2 * e + 1] * inv);
+          w[e] = a.bf16 ? *reinterpret_cast<const uint32_t *>(&h) : few::half2_bits(v[2 * e] * inv, v[2 * e + 1] * inv);
         }
-        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + (out_row * a.n_heads + head) * a.dv + d) =
-            make_uint4(w[0], w[1], w[2], w[3]);
+        put64(w, d);
       };
       // (R, l) of the row to its partial results; 1 / l for the output (nothing visible: zeros; NaN stays NaN)
       auto put_sums = [&](float m, float sum) {
-        if (rows_part && row_ok && half == 0) *reinterpret_cast<float4 *>(part) = make_float4(m, sum, 0.f, 0.f);
+        if (rows_part && row_ok && half == 0)
+          *reinterpret_cast<float4 *>(part_at(out_of(X * BM + row))) = make_float4(m, sum, 0.f, 0.f);
         return sum != 0.f ? 1.f / sum : 0.f;
       };
       const bool shared = LINE && pc.n_con > 1;
@@ -858,22 +989,20 @@ __global__ void __launch_bounds__(pre::NT, 1) prefill_kernel(const AttnArgs a) {
 #pragma unroll
             for (int k = 0; k < 32; ++k) o[k] = 0;
           }
+          float v[32];                        // dims c ..: the columns are in the order of the code words
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            float v[8];                                                  // dims c + 8 g ..
+          for (int k = 0; k < 32; k += 8)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              v[e] = __uint_as_float(o[8 * g + 2 * e]);
-              v[e + 4] = __uint_as_float(o[8 * g + 2 * e + 1]);
+              v[k + e] = __uint_as_float(o[k + 2 * e]);
+              v[k + e + 4] = __uint_as_float(o[k + 2 * e + 1]);
             }
-            const int d = c + 8 * g;
-            if (shared) {
-              float4 *q = reinterpret_cast<float4 *>(mine + 4 * BM) + (d / 4) * 2 * BM + at;
-              q[0] = make_float4(v[0], v[1], v[2], v[3]);
-              q[2 * BM] = make_float4(v[4], v[5], v[6], v[7]);
-            } else {
-              put(d, v, inv);
-            }
+          if (shared) {
+#pragma unroll
+            for (int k = 0; k < 32; k += 4)
+              reinterpret_cast<float4 *>(mine + 4 * BM)[((c + k) / 4) * 2 * BM + at] = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+          } else {
+            put32(c, v, inv);
           }
         }
         tc::fence_before_sync();
@@ -899,16 +1028,16 @@ __global__ void __launch_bounds__(pre::NT, 1) prefill_kernel(const AttnArgs a) {
           }
           inv = put_sums(M, sum);
 #pragma unroll 1
-          for (int d = half * (DV / 2); d < (half + 1) * (DV / 2); d += 16) {
-            float v[16];
+          for (int d = half * (DV / 2); d < (half + 1) * (DV / 2); d += 32) {
+            float v[32];
 #pragma unroll
-            for (int k = 0; k < 16; ++k) v[k] = 0.f;
+            for (int k = 0; k < 32; ++k) v[k] = 0.f;
             for (int c = 0; c < pc.n_con; ++c) {
               const float *q = part_of(c);
               const float rc = __ldcg(reinterpret_cast<const float2 *>(q) + at).x;
               const float w = rc == -INFINITY ? 0.f : exp2f(rc - M);
 #pragma unroll
-              for (int f = 0; f < 4; ++f) {
+              for (int f = 0; f < 8; ++f) {
                 const float4 u = __ldcg(reinterpret_cast<const float4 *>(q + 4 * BM) + (d / 4 + f) * 2 * BM + at);
                 v[4 * f] = fmaf(w, u.x, v[4 * f]);
                 v[4 * f + 1] = fmaf(w, u.y, v[4 * f + 1]);
@@ -916,8 +1045,7 @@ __global__ void __launch_bounds__(pre::NT, 1) prefill_kernel(const AttnArgs a) {
                 v[4 * f + 3] = fmaf(w, u.w, v[4 * f + 3]);
               }
             }
-            put(d, v, inv);
-            put(d + 8, v + 8, inv);
+            put32(d, v, inv);
           }
         }
       }
@@ -937,7 +1065,25 @@ __global__ void __launch_bounds__(256) prefill_merge_kernel(const AttnArgs a) {
   const int64_t id = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   const int64_t row = id / a.n_heads;
   const int head = static_cast<int>(id - row * a.n_heads);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (row >= a.n_rows) return;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int maps = a.diff ? 2 : 1;
+  constexpr int N = DV / 32;                  // values per lane: dims N lane ..
+  const bool in = N * lane < a.dv;
+  auto part_of = [&](int m, int k) {
+    return a.row_part + (((row * a.n_heads + head) * maps + m) * static_cast<int64_t>(a.n_split) + k) * (DV + 4);
+  };
+  auto load = [&](const float *p, float2 &rl, float2 *v) {
+    rl = __ldcg(reinterpret_cast<const float2 *>(p));
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i)
+      v[i] = in ? __ldcg(reinterpret_cast<const float2 *>(p + 4 + N * lane) + i) : make_float2(0.f, 0.f);
+  };
+  // first parts of both maps, on their way beside the search (a row of no sequence reads what is there, unused)
+  float2 rl[2], v[2][N / 2];
+  load(part_of(0, 0), rl[0], v[0]);
+  if (maps == 2) load(part_of(1, 0), rl[1], v[1]);
   // the row's sequence; rows of none stay as they are
   int lo = 0, hi = a.n_seq - 1;
   while (lo < hi) {
@@ -945,34 +1091,34 @@ __global__ void __launch_bounds__(256) prefill_merge_kernel(const AttnArgs a) {
     if (a.q_start[mid] <= row) lo = mid;
     else hi = mid - 1;
   }
-  const few::SeqWork sw = few::seq_work<1>(a, lo, false);
-  if (row < sw.row0 || row >= sw.row0 + sw.rows) return;
-  const int maps = a.diff ? 2 : 1;
-  constexpr int N = DV / 32;                  // values per lane: dims N lane ..
+  const int row_lo = a.q_start[lo], row_hi = a.q_start[lo + 1];
+  if (row_lo < 0 || row_hi > a.n_rows || row < row_lo || row >= row_hi) return;
   float y[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) y[i] = 0.f;
-  for (int m = 0; m < maps; ++m) {
-    const float *part = a.row_part + ((row * a.n_heads + head) * maps + m) * static_cast<int64_t>(a.n_split) * (DV + 4);
-    float M = -INFINITY;
-    for (int s = 0; s < a.n_split; ++s) M = fmaxf(M, __ldg(part + static_cast<int64_t>(s) * (DV + 4)));
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+    if (m == maps) break;
+    float M = rl[m].x;
+    for (int k = 1; k < a.n_split; ++k) M = fmaxf(M, __ldcg(part_of(m, k)));
     float l = 0.f, o[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) o[i] = 0.f;
-#pragma unroll 4
-    for (int s = 0; s < a.n_split; ++s) {
-      const float *p = part + static_cast<int64_t>(s) * (DV + 4);
-      const float2 rl = __ldg(reinterpret_cast<const float2 *>(p));
-      const float w = rl.x == -INFINITY ? 0.f : exp2f(rl.x - M);
-      l = fmaf(w, rl.y, l);
-      if (N * lane < a.dv) {
+    auto add = [&](const float2 &q, const float2 *u) {
+      const float w = q.x == -INFINITY ? 0.f : exp2f(q.x - M);
+      l = fmaf(w, q.y, l);
 #pragma unroll
-        for (int i = 0; i < N; i += 2) {
-          const float2 v = __ldg(reinterpret_cast<const float2 *>(p + 4 + N * lane + i));
-          o[i] = fmaf(w, v.x, o[i]);
-          o[i + 1] = fmaf(w, v.y, o[i + 1]);
-        }
+      for (int i = 0; i < N; i += 2) {
+        o[i] = fmaf(w, u[i / 2].x, o[i]);
+        o[i + 1] = fmaf(w, u[i / 2].y, o[i + 1]);
       }
+    };
+    add(rl[m], v[m]);
+#pragma unroll 4
+    for (int k = 1; k < a.n_split; ++k) {
+      float2 q, u[N / 2];
+      load(part_of(m, k), q, u);
+      add(q, u);
     }
     const float f = (l != 0.f ? 1.f / l : 0.f) * (m == 0 ? 1.f : -a.lam[head]);
 #pragma unroll
@@ -1004,11 +1150,9 @@ cudaError_t launch_prefill_t(const AttnArgs &a, cudaStream_t s) {
   cudaError_t e = set_dynamic_smem(reinterpret_cast<const void *>(kern), C::TOTAL);
   if (e != cudaSuccess) return e;
   const unsigned grid = a.line ? static_cast<unsigned>(sm_count()) : static_cast<unsigned>(a.n_tiles) * a.n_split * k_heads;
-  kern<<<grid, pre::NT, C::TOTAL, s>>>(a);
-  e = cudaGetLastError();
+  e = launch_beside(kern, grid, pre::NT, C::TOTAL, s, a);
   if (e != cudaSuccess || (a.n_split == 1 && !a.diff)) return e;
-  prefill_merge_kernel<DV><<<static_cast<unsigned>((a.n_rows * a.n_heads + 7) / 8), 256, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_beside(prefill_merge_kernel<DV>, static_cast<unsigned>((a.n_rows * a.n_heads + 7) / 8), 256, 0, s, a);
 }
 
 }  // namespace p4
