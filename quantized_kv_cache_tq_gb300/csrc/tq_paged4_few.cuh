@@ -220,6 +220,15 @@ struct SeqWork {
   long long items;    // (below 2^31, checked on the host)
 };
 
+// Arrival of a CTA whose threads have met at a barrier: what they wrote is visible to the CTAs that arrive later,
+// and what earlier ones wrote to this CTA behind its next barrier.  (Fences of all threads around a plain atomic take 0.4 to 0.6 us
+// more per call.)
+__device__ __forceinline__ int arrive_one(int32_t *counter) {
+  int r;
+  asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(r) : "l"(counter) : "memory");
+  return r;
+}
+
 template <int COLS>
 __device__ __forceinline__ SeqWork seq_work(const AttnArgs &a, int s, bool report) {
   SeqWork w;
@@ -806,13 +815,11 @@ __global__ void __launch_bounds__(FewCfg<DK, DV, NT, MAPS>::THREADS, FewCfg<DK, 
     bool finish = whole;
     if (!whole) {
       if (tid < NC) reinterpret_cast<float4 *>(mine)[tid] = *reinterpret_cast<float4 *>(wts + 4 * tid);
-      __threadfence();
       __syncthreads();
-      if (tid == 0) s_last = atomicAdd(a.counters + c0, 1) == n_con - 1;
+      if (tid == 0) s_last = arrive_one(a.counters + c0) == n_con - 1;
       __syncthreads();
       finish = s_last != 0;
       if (finish) {
-        __threadfence();
         if (tid == 0) a.counters[c0] = 0;
         // CTA c0's partial is in its slot 0 when the item's part begins its share, else in slot 1; the
         // others' parts begin their shares

@@ -1008,15 +1008,13 @@ __global__ void __launch_bounds__(pre::NT, 1) prefill_kernel(const AttnArgs a) {
         tc::fence_before_sync();
       }
       if (shared) {
-        __threadfence();
         tc::named_sync(BAR_SOFT, 32 * W_UNPACK);
         if (tid == 0) {
-          s_last = atomicAdd(a.counters + pc.c0, 1) == pc.n_con - 1;
+          s_last = few::arrive_one(a.counters + pc.c0) == pc.n_con - 1;
           if (s_last) a.counters[pc.c0] = 0;
         }
         tc::named_sync(BAR_SOFT, 32 * W_UNPACK);
         if (s_last && here) {
-          __threadfence();
           auto part_of = [&](int c) {
             return a.part + static_cast<int64_t>(2 * (pc.c0 + c) + (c == 0 ? pc.slot0 : 0)) * SLOT;
           };
