@@ -352,7 +352,8 @@ tq_status tq_f16_prompt_attn(const uint16_t *k, const uint16_t *v, int64_t n_cel
  * and int64 arrays 8-byte aligned; `max_pages` is the width of the block table
  * (row stride in entries), entry j of a sequence's row the page of its cells
  * j * page_size ..; entries beyond a sequence's length are never read.  Sequence
- * lengths and row counts are read on the device when the call runs.  A workspace
+ * lengths and row counts are read on the device when the call runs.  The attention
+ * calls take tables of max_pages * page_size up to 2^31 - 2^16 cells.  A workspace
  * of these calls is 256-byte aligned, zero-filled before its first use and left
  * ready by every call; calls of different shapes and kinds (decode, prefill,
  * differential) may share one, one after the other, but not with calls above
@@ -366,8 +367,8 @@ tq_status tq_f16_prompt_attn(const uint16_t *k, const uint16_t *v, int64_t n_cel
  *   scales  binary16 [n_pages][n_kv_heads][page_size][2]     (scale, offset)
  * A row stands for scale * code + offset (code 0 .. 15).  head_dim is a multiple
  * of 8, at most 256 (a dim that is not 64, 128 or 256 stores zero codes up to D);
- * page_size a power of two, 16 .. 1024; n_pages * n_kv_heads * page_size below 2^32.  Cell c of the cache is row
- * c % page_size of page c / page_size. */
+ * page_size a power of two, 16 .. 1024; n_pages * n_kv_heads * page_size below
+ * 2^32.  Cell c of the cache is row c % page_size of page c / page_size. */
 typedef struct tq_paged4 {
   int32_t n_kv_heads;
   int32_t head_dim;

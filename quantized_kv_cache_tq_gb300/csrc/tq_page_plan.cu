@@ -122,6 +122,7 @@ __global__ void __launch_bounds__(PT) plan_kernel(const PlanArgs a) {
   __shared__ Sums warp_sums[PT / 32];
   __shared__ int s_rows[PT], s_back[PT], s_more[PT], s_need[PT], s_old[PT];
   const int tid = threadIdx.x;
+  if (!ROWS) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the rows' launch may begin beside this one
   const long long count = *a.free_count;
   const bool one = a.n_seq <= PT;           // the only chunk: its sums are computed once
   Sums all = {0, 0, 0}, at = {0, 0, 0}, v = {0, 0, 0};
@@ -201,6 +202,7 @@ constexpr int ROWS_PER = 1024;
 __global__ void __launch_bounds__(256) rows_kernel(const PlanArgs a) {
   __shared__ int s_seq[2];
   const int r0 = static_cast<int>(static_cast<long long>(blockIdx.x) * ROWS_PER);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int total = a.q_start[a.n_seq];
   const int top = *a.new_free_count + a.page_start[a.n_seq];
   const int r1 = static_cast<int>(min(static_cast<long long>(r0) + ROWS_PER, static_cast<long long>(a.n_rows)));
@@ -233,8 +235,7 @@ cudaError_t launch_page_plan(const PlanArgs &a, cudaStream_t s) {
   plan_kernel<false><<<1, PT, 0, s>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  rows_kernel<<<static_cast<unsigned>((a.n_rows + ROWS_PER - 1) / ROWS_PER), 256, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_beside(rows_kernel, static_cast<unsigned>((a.n_rows + ROWS_PER - 1) / ROWS_PER), 256, 0, s, a);
 }
 
 }  // namespace p4

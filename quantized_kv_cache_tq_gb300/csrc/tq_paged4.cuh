@@ -107,5 +107,24 @@ cudaError_t launch_few(const AttnArgs &a, int columns, cudaStream_t s);
 bool prefill_supported(int wk, int wv);
 cudaError_t launch_prefill(const AttnArgs &a, cudaStream_t s);
 
+// A launch that may begin while the one before it on the stream is still running (programmatic dependent launch); the
+// kernel waits itself before it reads what that writes.
+template <typename Args>
+cudaError_t launch_beside(void (*kern)(Args), unsigned grid, unsigned threads, size_t smem, cudaStream_t s,
+                          const Args &a) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a);
+  return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
 }  // namespace p4
 }  // namespace tq

@@ -62,9 +62,6 @@
 namespace tq {
 namespace p4 {
 
-#ifndef FEW_NW
-#define FEW_NW 8
-#endif
 constexpr float RAISE = 12.f;         // growth of the maximum (log2) that rescales
 constexpr int UNIT = 64;              // keys per unit of work
 constexpr int TILE = 32;              // keys per warp tile
@@ -80,13 +77,13 @@ template <int DK, int DV, int NT, int MAPS>
 struct FewCfg {
   static constexpr int KS = DK / 16;                      // k steps of the scores
   static constexpr int MT = DV / 16;                      // m tiles of the values
-  static constexpr int NW = FEW_NW;                            // warps
+  static constexpr int NW = 8;                            // warps
   static constexpr int THREADS = NW * 32;
   static constexpr int KW = DK / 32;                      // words of a K row per lane
   static constexpr int COLS = MAPS == 2 ? 4 : 8 * NT;     // (row, head) columns per item
   static constexpr int NC = 8 * NT;                       // columns incl. maps
   // per SM: two where value accumulators and query fragments leave room in 128 registers a thread
-  static constexpr int CTAS = FEW_NW == 8 && NT * (4 * MT + 2 * KS * MAPS) <= (DK == 128 && MAPS == 2 ? 64 : 48) ? 2 : 1;
+  static constexpr int CTAS = NT * (4 * MT + 2 * KS * MAPS) <= (DK == 128 && MAPS == 2 ? 64 : 48) ? 2 : 1;
   // one stage: K rows [map][key], V rows [key], scale pairs [K maps, V][key]
   static constexpr int K_BYTES = TILE * DK / 2;
   static constexpr int V_BYTES = TILE * DV / 2;
@@ -221,8 +218,8 @@ struct SeqWork {
 };
 
 // Arrival of a CTA whose threads have met at a barrier: what they wrote is visible to the CTAs that arrive later,
-// and what earlier ones wrote to this CTA behind its next barrier.  (Fences of all threads around a plain atomic take 0.4 to 0.6 us
-// more per call.)
+// and what earlier ones wrote to this CTA behind its next barrier.  (Fences of all threads around a plain atomic
+// take 0.4 to 0.6 us more per call.)
 __device__ __forceinline__ int arrive_one(int32_t *counter) {
   int r;
   asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(r) : "l"(counter) : "memory");
@@ -558,7 +555,8 @@ __global__ void __launch_bounds__(FewCfg<DK, DV, NT, MAPS>::THREADS, FewCfg<DK, 
           }
         }
       // this lane's softmax columns are 2t and 2t + 1: their values sit in lanes g = 2t, 2t + 1
-      const float f = a.scale_log2 * exp2f(12.f + static_cast<float>(ex));          // 2^24 2^(ex - 12)
+      // (2^24 2^(ex - 12), as two factors: a small scale may come with queries near the end of their range)
+      const float f = a.scale_log2 * 4096.f * __uint_as_float(static_cast<uint32_t>(ex + 127) << 23);
       const float qs = a.scale_log2 * sum;
       fx[n] = make_float2(__shfl_sync(0xffffffffu, f, 8 * t), __shfl_sync(0xffffffffu, f, 8 * t + 4));
       qx[n] = make_float2(__shfl_sync(0xffffffffu, qs, 8 * t), __shfl_sync(0xffffffffu, qs, 8 * t + 4));
@@ -977,24 +975,6 @@ __global__ void __launch_bounds__(FewCfg<DK, DV, NT, MAPS>::THREADS, FewCfg<DK, 
       for (int64_t i = tid; i < n; i += C::THREADS) few::store2(a.out, at + 2 * i, 0.f, 0.f, a.bf16);
     }
   }
-}
-
-// A launch that may begin while the one before it on the stream is still running (programmatic dependent launch); the
-// kernel waits itself before it reads what that writes.
-inline cudaError_t launch_beside(void (*kern)(AttnArgs), unsigned grid, unsigned threads, size_t smem, cudaStream_t s,
-                                 const AttnArgs &a) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a);
-  return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
 template <int DK, int DV, int NT, int MAPS>

@@ -152,7 +152,8 @@ static tq_status attend(const Call &c) {
   const int64_t row = static_cast<int64_t>(c.diff ? 2 : 1) * c.n_heads * c.k->head_dim;
   if (c.q_stride < row || c.q_stride % 8) return TQ_ERR_INVALID_ARG;
   if (c.n_rows > 0x7fffffffLL / c.n_heads) return TQ_ERR_INVALID_ARG;
-  if (static_cast<int64_t>(c.max_pages) * c.k->page_size > 0x7fffffffLL) return TQ_ERR_INVALID_ARG;
+  // (the kernels count cells in 32 bits, up to the end of the last key tile)
+  if (static_cast<int64_t>(c.max_pages) * c.k->page_size > 0x7fff0000LL) return TQ_ERR_INVALID_ARG;
   if (c.n_seq == 0 || c.n_rows == 0) return TQ_OK;
   if (!al(c.block_table, 4) || !al(c.seq_len, 4) || (c.ragged && !al(c.q_start, 4)) || !al(c.q, 16) || !al(c.out, 16))
     return TQ_ERR_INVALID_ARG;

@@ -743,8 +743,8 @@ __global__ void __launch_bounds__(pre::NT, 1) prefill_kernel(const AttnArgs a) {
               sum += __shfl_xor_sync(0xffffffffu, sum, o);
             }
             // largest entry in [2^e, 2^(e + 1)) -> [2^12, 2^13); the scale's sign goes into q, a scale of 0 makes it 0.
-            // (A row below 2^-100 keeps fewer bits; its scores are nothing to an exponent.)
-            const int e = mx > 0.f ? max(static_cast<int>(__float_as_uint(mx) >> 23) - 127, -100) : 0;
+            // (A row whose entries all lie below 2^-114 keeps fewer bits.)
+            const int e = mx > 0.f ? max(static_cast<int>(__float_as_uint(mx) >> 23) - 127, -114) : 0;
             const float up = __uint_as_float(static_cast<uint32_t>(12 - e + 127) << 23) *
                              (a.scale_log2 > 0.f ? 1.f : a.scale_log2 < 0.f ? -1.f : 0.f);
             unsigned char *dst = smem + C::SQ + X * C::Q_BYTES + (2 * (warp & 7) + t) * 128 + (lane & 7) * 16;

@@ -508,6 +508,158 @@ def test_prefill_ranges(v_gain, q_gain, scale):
         _check(out, ref, bound, dtype)
 
 
+@pytest.mark.parametrize("n_seq,group,hkv,max_len", [(32, 4, 2, 600), (33, 5, 8, 4096), (40, 4, 2, 600), (40, 4, 8, 4096),
+                                                     (1600, 4, 1, 400), (1600, 4, 1, 16384)])
+def test_prefill_many_sequences(n_seq, group, hkv, max_len):
+    # up to 32 sequences a warp finds the work alone, beyond the CTA, beyond 768 in several steps; long max_len: one line
+    import torch
+    import quantized_kv_cache_tq_gb300 as tq
+    rng = np.random.default_rng(n_seq)
+    nq = [int(x) for x in rng.integers(0, 4 if n_seq > 100 else 90, n_seq)]
+    nq[-1] = 60
+    lens = [n + int(rng.integers(0, 40 if n_seq > 100 else 300)) for n in nq]
+    b = Batch(61, lens, hkv, 64, 64, 16)
+    start = np.cumsum([0] + nq)
+    q = b.query(int(start[-1]), hkv * group, "float16")
+    gs = torch.tensor(start, dtype=torch.int32, device="cuda")
+    out = tq.paged4_prefill(b.gk, b.gv, b.gt, b.gl, q, gs, max_len=max_len)
+    ref, bound = P.attention(b.k, b.v, b.table, lens, _np(q), start, hkv * group, 64 ** -0.5)
+    _check(out, ref, bound, "float16")
+
+
+@pytest.mark.parametrize("up", [118, -90])
+def test_scaled_queries_with_the_inverse_scale(up):
+    # a power of two moved from the queries to the scale changes nothing, near the ends of bfloat16's range too
+    import torch
+    import quantized_kv_cache_tq_gb300 as tq
+    b = Batch(59, [300, 90], 2, 128, 128, 16)
+    gs = torch.tensor([0, 140, 190], dtype=torch.int32, device="cuda")
+    q = b.query(190, 4, "bfloat16").clamp(-16, 16)
+    q = torch.where(q.abs() < 2.0 ** -16, torch.zeros_like(q), q)
+    big = q.double().mul(2.0 ** up).bfloat16()
+    assert torch.equal(big.double().mul(2.0 ** -up), q.double())
+    one = tq.paged4_prefill(b.gk, b.gv, b.gt, b.gl, q, gs, 0.125)
+    two = tq.paged4_prefill(b.gk, b.gv, b.gt, b.gl, big, gs, 0.125 * 2.0 ** -up)
+    assert torch.isfinite(one).all() and torch.equal(one, two)
+    one = tq.paged4_decode(b.gk, b.gv, b.gt, b.gl, q[:2], 0.125)
+    two = tq.paged4_decode(b.gk, b.gv, b.gt, b.gl, big[:2], 0.125 * 2.0 ** -up)
+    assert torch.isfinite(one).all() and torch.equal(one, two)
+
+
+def test_sequences_that_share_pages():
+    # a common prefix: its pages stand in several block tables; pages of 1024 cells
+    import torch
+    import quantized_kv_cache_tq_gb300 as tq
+    for page, lens in ((16, [200, 200, 131]), (1024, [2100, 2100, 1500])):
+        b = Batch(67, lens, 2, 128, 128, page)
+        shared = 128 // page if page < 128 else 1
+        b.table[1, :shared] = b.table[2, :shared] = b.table[0, :shared]
+        gt = torch.from_numpy(b.table).cuda()
+        q = b.query(3, 8, "bfloat16")
+        out = tq.paged4_decode(b.gk, b.gv, gt, b.gl, q)
+        ref, bound = P.attention(b.k, b.v, b.table, lens, _np(q), range(4), 8, 128 ** -0.5)
+        _check(out, ref, bound, "bfloat16")
+        start = [0, 33, 60, 80]
+        q = b.query(80, 8, "bfloat16")
+        out = tq.paged4_prefill(b.gk, b.gv, gt, b.gl, q, torch.tensor(start, dtype=torch.int32, device="cuda"))
+        ref, bound = P.attention(b.k, b.v, b.table, lens, _np(q), start, 8, 128 ** -0.5)
+        _check(out, ref, bound, "bfloat16")
+
+
+def test_prefill_lengths_beyond_the_table_are_cut():
+    import torch
+    import quantized_kv_cache_tq_gb300 as tq
+    b = Batch(71, [160, 160], 2, 128, 128, 16)
+    b.table = b.table[:, :10].copy()
+    gs = torch.tensor([0, 40, 70], dtype=torch.int32, device="cuda")
+    q = b.query(70, 4, "float16")
+    gl = torch.tensor([5000, -3], dtype=torch.int32, device="cuda")
+    ws = tq.workspace(tq.paged4_prefill_workspace(b.gk, b.gv, 4, 2, 70, 160))
+    out = tq.paged4_prefill(b.gk, b.gv, torch.from_numpy(b.table).cuda(), gl, q, gs, ws=ws)
+    ref, bound = P.attention(b.k, b.v, b.table, [160, 0], _np(q), [0, 40, 70], 4, 128 ** -0.5)
+    ref[40:], bound[40:] = 0.0, 0.0
+    _check(out, ref, bound, "float16")
+    assert (tq._lib.tq_workspace_status(ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream)
+            == tq._lib.TQ_ERR_DEVICE_CHECK)
+
+
+def test_calls_on_two_streams_at_once():
+    # each with a workspace of its own
+    import torch
+    import quantized_kv_cache_tq_gb300 as tq
+    b = Batch(73, [3000, 700, 90], 4, 128, 128, 16)
+    q, dq = b.query(400, 8, "bfloat16"), b.query(3, 8, "bfloat16")
+    gs = torch.tensor([0, 350, 380, 400], dtype=torch.int32, device="cuda")
+    want = tq.paged4_prefill(b.gk, b.gv, b.gt, b.gl, q, gs), tq.paged4_decode(b.gk, b.gv, b.gt, b.gl, dq)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    got = [[] for _ in streams]
+    wss = [tq.workspace(tq.paged4_prefill_workspace(b.gk, b.gv, 8, 3, 400, 3000)) for _ in streams]
+    torch.cuda.synchronize()
+    for _ in range(8):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                if i % 2:
+                    got[i].append(tq.paged4_decode(b.gk, b.gv, b.gt, b.gl, dq, ws=wss[i]))
+                else:
+                    got[i].append(tq.paged4_prefill(b.gk, b.gv, b.gt, b.gl, q, gs, max_len=3000, ws=wss[i]))
+    torch.cuda.synchronize()
+    for i in range(len(streams)):
+        assert all(torch.equal(o, got[i % 2][0]) for o in got[i])
+    assert torch.equal(got[1][0], want[1])
+    assert all(tq._lib.tq_workspace_status(w.data_ptr(), w.numel(), 0) == 0 for w in wss)
+
+
+@pytest.mark.parametrize("max_len", [700, 1 << 20])
+def test_prefill_graphs_share_a_workspace_with_decode(max_len):
+    # lengths and row ranges move between the replays; both forms of cutting the work
+    import torch
+    import quantized_kv_cache_tq_gb300 as tq
+    b = Batch(79, [600, 300], 2, 128, 128, 16)
+    d = Batch(83, [400, 257], 2, 64, 128, 32, maps=2)
+    q, dq, one = b.query(160, 8, "bfloat16"), d.query(160, 8, "float16"), b.query(2, 8, "bfloat16")
+    lam = torch.full((4,), 0.4, device="cuda")
+    gs = torch.tensor([0, 100, 160], dtype=torch.int32, device="cuda")
+    ws = tq.workspace(max(tq.paged4_prefill_workspace(b.gk, b.gv, 8, 2, 160, max_len),
+                          tq.paged4_prefill_workspace(d.gk, d.gv, 4, 2, 160, max_len),
+                          tq.paged4_decode_workspace(b.gk, b.gv, 8, 2)))
+    out, o1 = torch.zeros((160, 8, 128), device="cuda").bfloat16(), torch.zeros((2, 8, 128), device="cuda").bfloat16()
+    dout = torch.zeros((160, 4, 128), device="cuda").half()
+    calls = (lambda: tq.paged4_prefill(b.gk, b.gv, b.gt, b.gl, q, gs, max_len=max_len, out=out, ws=ws),
+             lambda: tq.paged4_diff_prefill(d.gk, d.gv, d.gt, d.gl, dq, gs, lam, max_len=max_len, out=dout, ws=ws),
+             lambda: tq.paged4_decode(b.gk, b.gv, b.gt, b.gl, one, out=o1, ws=ws))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for c in calls:
+            c()
+        side.synchronize()
+        graphs = [torch.cuda.CUDAGraph() for _ in calls]
+        for g, c in zip(graphs, calls):
+            with torch.cuda.graph(g, stream=side):
+                c()
+        for lens, dlens, start in (([600, 300], [400, 257], [0, 100, 160]), ([90, 17], [33, 257], [0, 90, 107]),
+                                   ([600, 0], [1, 100], [0, 1, 1])):
+            b.gl.copy_(torch.tensor(lens, dtype=torch.int32))
+            d.gl.copy_(torch.tensor(dlens, dtype=torch.int32))
+            gs.copy_(torch.tensor(start, dtype=torch.int32))
+            out.fill_(5.0)
+            dout.fill_(5.0)
+            for g in graphs + graphs[::-1]:
+                g.replay()
+            side.synchronize()
+            n = start[-1]
+            ref, bound = P.attention(b.k, b.v, b.table, lens, _np(q), start, 8, 128 ** -0.5)
+            _check(out[:n], np.nan_to_num(ref[:n]), bound[:n], "bfloat16")
+            ref, bound = P.attention(d.k, d.v, d.table, dlens, _np(dq), start, 4, 64 ** -0.5, lam=[0.4] * 4)
+            _check(dout[:n], np.nan_to_num(ref[:n]), bound[:n], "float16")
+            assert bool((out[n:] == 5.0).all()) and bool((dout[n:] == 5.0).all())
+            ref, bound = P.attention(b.k, b.v, b.table, lens, _np(one), range(3), 8, 128 ** -0.5)
+            ref[np.array(lens) == 0] = 0.0
+            _check(o1, ref, bound, "bfloat16")
+        assert tq._lib.tq_workspace_status(ws.data_ptr(), ws.numel(), side.cuda_stream) == 0
+
+
 # ---------------------------------------------------------------- differential
 
 DIFF = [(64, 64, 1, 1, 16), (64, 128, 2, 2, 32), (128, 128, 2, 4, 16), (128, 256, 1, 2, 16), (48, 96, 2, 3, 64),

@@ -225,3 +225,15 @@ def test_python_calls_refuse_before_the_library():
         tq.Paged4Cache.from_planes(c.codes, c.scales[:, :1], 128)
     with pytest.raises(tq.TQError):
         tq.Paged4Cache(2, 100, 16, 4, device="cpu")
+
+
+@pytest.mark.parametrize("kind", ["decode", "prefill", "diff_decode", "diff_prefill"])
+def test_attention_calls_refuse_tables_near_32_bits(kind):
+    # lengths are rounded up to tiles of keys in 32 bits: tables end 2^16 cells before
+    L = _lib()
+    kh = 4 if "diff" in kind else 2
+    k, v = _cache(L, h=kh, ps=1024), _cache(L, ps=1024)
+    assert _attend(L, kind, k=k, v=v, width=(1 << 21) - 1) == L.TQ_ERR_INVALID_ARG
+    assert _attend(L, kind, k=k, v=v, width=(1 << 21) - 63) == L.TQ_ERR_INVALID_ARG
+    # (at the limit the checks go on, to a workspace of no bytes)
+    assert _attend(L, kind, k=k, v=v, width=(1 << 21) - 64, ws_bytes=0) == L.TQ_ERR_WORKSPACE
