@@ -10,11 +10,10 @@
 //
 // - A warp streams its own 32-key tiles through a private ring of cp.async
 //   stages: it waits for its own copies only, and no CTA barrier stands in the
-//   loop.  (Bulk copies were measured too: the one-lane issue of four of them per
-//   tile takes more instructions than ten cp.async of the whole warp, 184 against
-//   the figure below.)  Rows are swizzled by 16-byte chunks (chunk_at), so that the
-//   copies, the 16-byte reads of K rows and the transposing matrix reads of V rows
-//   all spread over the banks.
+//   loop.  (Bulk copies were measured too: issuing four of them per tile from one
+//   lane takes more instructions than ten cp.async of the whole warp.)  Rows are
+//   swizzled by 16-byte chunks (chunk_at), so that the copies, the 16-byte reads of K
+//   rows and the transposing matrix reads of V rows all spread over the banks.
 // - Codes become operands with one AND: (w & 0x000f000f) read as two binary16
 //   values is the subnormal pair code 2^-24, (w & 0x00f000f0) is code 2^-20; the
 //   powers of two are exact and go into q (2^-4 on the second kind) and into the
@@ -34,8 +33,19 @@
 //   + sum p m would carry the rounding of w times the whole range of the row.  The
 //   sum taken is sum w (c - c0) + sum p (m + s c0) with c0 = clamp(-m / s, 0, 15)
 //   per row, the code that stands for 0: the rounding then meets the values
-//   themselves (binary16 output error over 32768 keys: 7.2e-4 without, 2.2e-4 with;
-//   the plain fp32 form has 2.1e-4, the output's own rounding).
+//   themselves.
+// - Binary16 outputs (FINE) take two steps more, since the above would cost them half
+//   as much again as their own rounding: what a weight's rounding leaves goes into a
+//   second product, and the value operand is code - 8 (see low_code).  Output error
+//   over 48000 keys, relative: 1.99e-4, that of the output's own rounding, against
+//   2.25e-4 with the second product alone and about 2.9e-4 with neither.  Time of 40
+//   ragged sequences 165 us, against 148 with the second product alone and 136 in
+//   bfloat16; of one sequence of 32768 keys 19.1, 18.1 and 17.3 us.
+// Measured (8 KV heads of 128, 4 query heads each): 40 ragged sequences of up to 32768
+// keys 135.5 us in bfloat16, 5.48 TB/s.  With all CTAs reading, two per SM, the memory
+// is what bounds it, and the pair of a CTA's SM ends up to 20 us later than the other.
+// One sequence of 900 keys 10.1 us, of one key 6.1: the launch, the lengths, the page,
+// the row, the merge are a chain of some eight trips to L2 or memory.
 //
 // Split of the work.  An item is a (sequence, V head, column chunk), its keys come
 // in units of 64.  Nothing about lengths is needed on the host: every CTA works its
@@ -44,7 +54,7 @@
 //   item, and a CTA has one piece.
 // - Else the items' units form one line that is cut into equal shares, one per CTA,
 //   however ragged the batch is.  Taking up an item costs a CTA about what SETUP
-//   units do (measured: 5 us, against 0.6 us per unit with all CTAs reading), so
+//   units do (measured: 4 to 5 us, against 0.5 us per unit with all CTAs reading), so
 //   every item begins with that many empty units: short sequences then do not pile
 //   up on one CTA (40 ragged sequences: the CTAs ended between 106 and 171 us
 //   without them).
@@ -145,6 +155,26 @@ __device__ __forceinline__ void mma16816(float *c, uint32_t a0, uint32_t a1, uin
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Codes in bits 0 .. 3 (low) or 4 .. 7 (high) of both 16-bit halves as binary16 pairs: code 2^-24, code 2^-20, or (FINE)
+// code - 8.  The tensor cores cut their sums off below 2^-24 of the largest term, always downwards, so a sum of codes
+// whose mean is later taken off again is short by some 10^-6 of that mean.
+template <bool FINE>
+__device__ __forceinline__ uint32_t low_code(uint32_t x) {
+  x &= 0x000f000fu;
+  if (!FINE) return x;
+  x |= 0x64006400u;                           // 1024 + code
+  const __half2 h = __hsub2(*reinterpret_cast<const __half2 *>(&x), __float2half2_rn(1032.f));
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+template <bool FINE>
+__device__ __forceinline__ uint32_t high_code(uint32_t x) {
+  x &= 0x00f000f0u;
+  if (!FINE) return x;
+  x |= 0x64006400u;                           // 1024 + 16 code
+  const __half2 h = __hfma2(*reinterpret_cast<const __half2 *>(&x), __float2half2_rn(0.0625f), __float2half2_rn(-72.f));
+  return *reinterpret_cast<const uint32_t *>(&h);
 }
 
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
@@ -300,7 +330,7 @@ __device__ __forceinline__ void scan_chunk(const AttnArgs &a, int s0, Scan *sums
 
 }  // namespace few
 
-template <int DK, int DV, int NT, int MAPS>
+template <int DK, int DV, int NT, int MAPS, bool FINE>
 __global__ void __launch_bounds__(FewCfg<DK, DV, NT, MAPS>::THREADS, FewCfg<DK, DV, NT, MAPS>::CTAS)
     few_kernel(const AttnArgs a) {
   using C = FewCfg<DK, DV, NT, MAPS>;
@@ -602,7 +632,7 @@ __global__ void __launch_bounds__(FewCfg<DK, DV, NT, MAPS>::THREADS, FewCfg<DK, 
         const float c0 = fminf(fmaxf(__fdividef(-v.y, v.x), 0.f), 15.f), vm = fmaf(v.x, c0, v.y);   // (0 / 0, NaN: 0)
         const float e = v.x != 0.f ? static_cast<float>(static_cast<int>(__float_as_uint(fabsf(v.x)) >> 23) - 127) : -24.f;
         sts4(prep + lane * 16, v.x, v.x, vm, vm);
-        sts2(prep + TILE * 16 + lane * 8, -c0, e);
+        sts2(prep + TILE * 16 + lane * 8, (FINE ? 8.f : 0.f) - c0, e);
         sts2(prep + TILE * 24 + lane * 8, k.x, k.y);
         if (MAPS == 2) {
           const float2 k1 = pair(MAPS - 1);
@@ -621,6 +651,7 @@ __global__ void __launch_bounds__(FewCfg<DK, DV, NT, MAPS>::THREADS, FewCfg<DK, 
         ksc[j] = lds2(prep + TILE * (MAPS == 2 ? 24 + 8 * (t >> 1) : 24) + (8 * j + g) * 8);
       }
       uint32_t pb[NT][2][2];                // weights as B fragments [half][keys 0-7, 8-15]
+      uint32_t pl[NT][2][2];                // and what their rounding left (FINE)
       float s[NT][2][4];
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
@@ -704,8 +735,15 @@ __global__ void __launch_bounds__(FewCfg<DK, DV, NT, MAPS>::THREADS, FewCfg<DK, 
             z[nn] = fma2(p, make_float2(vsc[j].z, vsc[j].w), z[nn]);
             const float2 w = mul2(p, make_float2(vsc[j].x, vsc[j].y));
             const __half2 h = __floats2half2_rn(w.x, w.y);
-            z[nn] = fma2(__half22float2(h), make_float2(vce[j].x, vce[j].x), z[nn]);
+            float2 r = __half22float2(h);
             pb[nn][j >> 1][j & 1] = transpose8(*reinterpret_cast<const uint32_t *>(&h));
+            if (FINE) {
+              const float2 left = sub2(w, r);
+              const __half2 lo = __floats2half2_rn(left.x, left.y);
+              r = add2(r, __half22float2(lo));
+              pl[nn][j >> 1][j & 1] = transpose8(*reinterpret_cast<const uint32_t *>(&lo));
+            }
+            z[nn] = fma2(r, make_float2(vce[j].x, vce[j].x), z[nn]);
           }
         }
       }
@@ -720,12 +758,16 @@ __global__ void __launch_bounds__(FewCfg<DK, DV, NT, MAPS>::THREADS, FewCfg<DK, 
           for (int e = 0; e < 2; ++e) {
             const uint32_t xa = vw[2 * e], xb = vw[2 * e + 1], ya = xa >> 8, yb = xb >> 8;
             const int mt = 2 * (2 * c2 + e);
+            const uint32_t x[8] = {low_code<FINE>(xa), high_code<FINE>(xa), low_code<FINE>(xb), high_code<FINE>(xb),
+                                   low_code<FINE>(ya), high_code<FINE>(ya), low_code<FINE>(yb), high_code<FINE>(yb)};
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-              mma16816(acc[n][mt], xa & 0x000f000fu, xa & 0x00f000f0u, xb & 0x000f000fu, xb & 0x00f000f0u,
-                       pb[n][hf][0], pb[n][hf][1]);
-              mma16816(acc[n][mt + 1], ya & 0x000f000fu, ya & 0x00f000f0u, yb & 0x000f000fu, yb & 0x00f000f0u,
-                       pb[n][hf][0], pb[n][hf][1]);
+              mma16816(acc[n][mt], x[0], x[1], x[2], x[3], pb[n][hf][0], pb[n][hf][1]);
+              mma16816(acc[n][mt + 1], x[4], x[5], x[6], x[7], pb[n][hf][0], pb[n][hf][1]);
+              if (FINE) {
+                mma16816(acc[n][mt], x[0], x[1], x[2], x[3], pl[n][hf][0], pl[n][hf][1]);
+                mma16816(acc[n][mt + 1], x[4], x[5], x[6], x[7], pl[n][hf][0], pl[n][hf][1]);
+              }
             }
           }
         }
@@ -917,8 +959,8 @@ __global__ void __launch_bounds__(FewCfg<DK, DV, NT, MAPS>::THREADS, FewCfg<DK, 
           for (int i = 0; i < 2; ++i) {
             const float ls = s_lz[col + i][0], zs = s_lz[col + i][1];
             const float inv = ls != 0.f ? 1.f / ls : 0.f;        // nothing visible: zeros (NaN stays NaN)
-            y[i][0] = ((i ? o4[k].y : o4[k].x) * 16777216.f + zs) * inv;
-            y[i][1] = ((i ? o4[k].w : o4[k].z) * 1048576.f + zs) * inv;
+            y[i][0] = ((i ? o4[k].y : o4[k].x) * (FINE ? 1.f : 16777216.f) + zs) * inv;
+            y[i][1] = ((i ? o4[k].w : o4[k].z) * (FINE ? 1.f : 1048576.f) + zs) * inv;
             if (MAPS == 2) {
               ex[(col + i) * DV + d] = y[i][0];
               ex[(col + i) * DV + d + 1] = y[i][1];
@@ -971,23 +1013,30 @@ __global__ void __launch_bounds__(FewCfg<DK, DV, NT, MAPS>::THREADS, FewCfg<DK, 
   for (int s = blockIdx.x; s < a.n_seq; s += gridDim.x) {
     const few::SeqWork w = few::seq_work<COLS>(a, s, false);
     if (w.len == 0) {
-      const int64_t n = static_cast<int64_t>(w.rows) * a.n_heads * a.dv / 2, at = static_cast<int64_t>(w.row0) * a.n_heads * a.dv;
+      const int64_t n = static_cast<int64_t>(w.rows) * a.n_heads * a.dv / 2;
+      const int64_t at = static_cast<int64_t>(w.row0) * a.n_heads * a.dv;
       for (int64_t i = tid; i < n; i += C::THREADS) few::store2(a.out, at + 2 * i, 0.f, 0.f, a.bf16);
     }
   }
 }
 
-template <int DK, int DV, int NT, int MAPS>
+template <int DK, int DV, int NT, int MAPS, bool FINE>
 cudaError_t launch_few_t(const AttnArgs &a, cudaStream_t s) {
   using C = FewCfg<DK, DV, NT, MAPS>;
   static_assert(C::SMEM <= 227 * 1024, "shared memory");
   // weights and sums of every CTA's partial and the teams' sums, at the merge
   static_assert(C::SMEM >= 2 * 152 * C::NC * 12 + C::THREADS * 16 || C::CTAS == 1, "merge");
   static_assert(MAPS == 1 || NT == 1, "differential: one tile of columns for both maps");
-  auto kern = few_kernel<DK, DV, NT, MAPS>;
+  auto kern = few_kernel<DK, DV, NT, MAPS, FINE>;
   cudaError_t e = set_dynamic_smem(reinterpret_cast<const void *>(kern), C::SMEM);
   if (e != cudaSuccess) return e;
   return launch_beside(kern, sm_count() * C::CTAS, C::THREADS, C::SMEM, s, a);
+}
+
+// (binary16 outputs keep the weights to 22 bits)
+template <int DK, int DV, int NT, int MAPS>
+cudaError_t launch_few_t(const AttnArgs &a, cudaStream_t s) {
+  return a.bf16 ? launch_few_t<DK, DV, NT, MAPS, false>(a, s) : launch_few_t<DK, DV, NT, MAPS, true>(a, s);
 }
 
 }  // namespace p4

@@ -388,6 +388,27 @@ def test_decode_repeats_bit_for_bit():
     assert all(torch.equal(o, outs[0]) for o in outs)
 
 
+@pytest.mark.parametrize("gain", [0.5, 1.0])
+def test_decode_error_in_binary16_is_the_outputs_own(gain):
+    # the weights' second parts and centred codes leave errors of some 2^-20, against 2^-12 of rounding the output:
+    # together at most 3% above the error of the exact result rounded (rms over 4 x 8 x 128 values)
+    import torch
+    import quantized_kv_cache_tq_gb300 as tq
+    b = Batch(97, [3000], 1, 128, 128, 16)
+    d = Batch(98, [3000], 1, 128, 128, 16, maps=2)
+    got, exact = [], []
+    for _ in range(4):
+        q = b.query(1, 8, "float16", gain)
+        got.append(_np(tq.paged4_decode(b.gk, b.gv, b.gt, b.gl, q)))
+        exact.append(P.attention(b.k, b.v, b.table, b.lens, _np(q), range(2), 8, 128 ** -0.5)[0])
+        q = d.query(1, 16, "float16", gain)
+        got.append(_np(tq.paged4_diff_decode(d.gk, d.gv, d.gt, d.gl, q, torch.zeros(8, device="cuda"))))
+        exact.append(P.attention(d.k, d.v, d.table, d.lens, _np(q), range(2), 8, 128 ** -0.5, lam=[0.0] * 8)[0])
+    got, exact = np.array(got), np.array(exact)
+    rms = lambda x: float(np.sqrt(np.mean(x * x)))  # noqa: E731
+    assert rms(got - exact) <= 1.03 * rms(exact.astype(np.float16) - exact)
+
+
 # ---------------------------------------------------------------- prefill
 
 PRE = [  # dk, dv, kv heads, group, page, query rows, lens
