@@ -17,7 +17,10 @@
 // rows and one chunk of sequences is done by the first kernel alone.
 //
 // Neither has bytes to speak of (12 per row): what counts is the length of the
-// chain of dependent loads, lengths -> sums -> page -> slot.
+// chain of dependent loads, lengths -> sums -> page -> slot.  Measured: a step of 48
+// sequences 4.2 us, of which an empty launch is about half; 700 admissions with 1.0 M
+// rows 10.1 us (12 MB written in 1.8 us at the memory's rate), 10.5 with the second
+// launch waiting for the first one's end.
 #include "tq_common.cuh"
 #include "tq_paged4.cuh"
 

@@ -80,9 +80,9 @@ static Layout few_layout(int wv) {
 // How the prompt kernel shares its work out: one line over the SMs, or n_split CTAs per item (256-row tile, K
 // head), whichever is estimated to end first.  In key tiles of one CTA (2 us): a CTA costs its key tiles + 4 for
 // set-up and epilogue, + 4 where rows' partial results are written and merged; a line costs its share, and 14 for
-// finding it and for the items cut at its ends.  Measured, line against split: 2048 rows over 32768 cells 847 /
-// 969 us, over 4096 cells 127 / 118 us, three differential chunks of up to 700 rows 97 / 111 us, five chunks of up
-// to 300 rows 54 / 38 us.
+// finding it and for the items cut at its ends.  Measured, line against split: 2048 rows over 32768 cells 818 /
+// 926 us, over 4096 cells 114 / 104 us, three differential chunks of up to 700 rows 90 / 104 us, 20 chunks of up to
+// 300 rows 90 / 83 us.
 constexpr int kMaxSplit = 16;
 struct Share {
   bool line;

@@ -14,15 +14,15 @@
 // and ONE score buffer (128) that the tiles use in turn: it is free again as soon as
 // the softmax threads have read it into registers, so the next product of scores
 // runs beside the rest of the softmax and does not wait for P V.  (With a buffer per
-// tile and P written over it, a tile's scores had to wait for its P V: 1200 us at
-// 2048 rows over 32768 cells, 8 KV heads, against 1016 us in
-// that step.)  A softmax thread has its weights in registers before it waits for the
-// tile's last P V, so only their store stands between two products (807 -> 786 us).
+// tile and P written over it, a tile's scores had to wait for its P V: 1200 us at 2048
+// rows over 32768 cells, 8 KV heads, against 1016 us in that step.)  A softmax thread
+// has its weights in registers before it waits for the tile's last P V, so only their
+// store stands between two products (807 -> 786 us).
 // The code of all roles has to stay small: with the products' loops unrolled for one
 // thread and a whole row's 128 keys per softmax thread, the product warp waited for
 // instructions (1390 us in that form).
 //
-// Numbers, so that 16-bit operands cost no accuracy beyond the output's own:
+// Numbers:
 // - Scores: K's operand is the code itself (a nibble masked in place reads as the
 //   binary16 subnormal code 2^-24 or 2^-20, exact), q is scaled by a power of two
 //   per row (exact for 16-bit inputs down to 2^-23 of the row's largest entry).  The
@@ -32,15 +32,28 @@
 //   |a_t| >= 2^19 is constant to 3e-5 and takes its offset alone.)
 // - Values: v_t 2^-tau rounded to binary16 (relative 2^-12 on average half), tau the
 //   largest exponent among 32 neighbouring keys; the weights p_t 2^tau are rounded
-//   to binary16 too.  Both roundings meet the values themselves.  R is a running
-//   maximum of x_t + tau, raised only when it would grow by more than 2^12 (which binary16 weights leave room
-//   for; with 2^8 the rescaling of O cost a tenth of the time).  Sums of
-//   weights stay in fp32.
+//   to binary16 too.  Both roundings meet the values themselves.  To bfloat16 outputs
+//   they are nothing; binary16 outputs have 2.9e-4 relative error at 2048 rows over
+//   32768 cells, against 2.1e-4 of rounding alone (a second product for what the
+//   rounding of P leaves would be half as much tensor work again).  R is a running
+//   maximum of x_t + tau, raised only when it would grow by more than 2^12 (which
+//   binary16 weights leave room for; with 2^8 the rescaling of O cost a tenth of the
+//   time).  Sums of weights stay in fp32.
+//
+// What bounds it (2048 rows over 32768 cells: 787 us, 1.35 PFLOP/s of 1.92): a pair of
+// row tiles takes 3300 clocks per key tile, of which the products need 2500 (their k
+// step for the offset included), the exponentials 2100 and the warps' instructions 1600
+// per scheduler; the rest is the chain scores - softmax - P V of the two tiles.  Part of
+// the exponentials by a polynomial was slower in every share (an eighth 794 us, a
+// quarter 831): the instructions weigh more.  Short calls are bound by the way to the
+// first product, 13000 clocks of 22000 for one key tile, mostly instructions fetched for
+// the first time: Q, lengths and output are read and written by whole lines and without
+// divisions for that (5 prompts of up to 300 rows 38.2 -> 31.8 us).
 //
 // Split of the work, two ways:
-// - LINE, where there are many (row tile, KV head) items: their key tiles, with ITEM_COST
-//   empty ones before each item, form one line that is cut into equal shares, one per
-//   SM, from the device's lengths.  A CTA's first and last item may be shared with
+// - LINE, where there are many (row tile, KV head) items: their key tiles, with
+//   ITEM_COST empty ones before each item, form one line that is cut into equal shares,
+//   one per SM, from the device's lengths.  A CTA's first and last item may be shared with
 //   others: partial results go to the workspace and the last CTA to arrive merges them,
 //   in the order of the CTAs.
 // - else (a short chunk behind a long context) each item's keys are cut into n_split
@@ -63,7 +76,7 @@ namespace pre {
 
 constexpr int BM = 128, BN = 128;             // rows of a tile, keys of a key tile
 constexpr int HK = BN / 2;                    // keys of a softmax thread
-constexpr int ITEM_COST = 4;                      // key tiles' worth of time that an item costs besides its keys (8 us)
+constexpr int ITEM_COST = 4;                  // key tiles' worth of time that an item costs besides its keys
 constexpr int NT = 768;
 constexpr int W_UNPACK = 16, W_MMA = 20, W_NEXT = 21;      // first warps of the roles after the softmax
 constexpr int REG_SOFTMAX = 96, REG_UNPACK = 64, REG_MMA = 32;    // of 80 at the launch: 4 x 96 + 64 + 32 = 6 x 80
@@ -113,7 +126,8 @@ __device__ __forceinline__ void st8(uint32_t taddr, const uint32_t *r) {
 }
 
 // Bounded wait for phase `parity` of `bar` by a whole warp.  Without a suspend-time hint: with one, a warp that
-// found the phase open slept on past its end, on every step of the chain score - softmax - product (2048 rows over 32768 cells: 1282 us with it, 1233 without).
+// found the phase open slept on past its end, on every step of the chain score - softmax - product (1282 us with it,
+// 1233 without, at 2048 rows over 32768 cells).
 // SLEEP: with a pause between two tries, for the unpack warps, which have time and leave the others their issue slots
 // (811 -> 804 us).
 template <bool SLEEP = false>
@@ -367,7 +381,7 @@ __global__ void __launch_bounds__(pre::NT, 1) prefill_kernel(const AttnArgs a) {
           Piece p = {s, 0, static_cast<int>(blockIdx.x) % k_heads, 0, 0, 0, 1, 0, 0, 0, 0, 0, 0, 0};
           rows_of_piece(a, w, first_tile(a, w, static_cast<int>(want - (x - v))), p);
           const int tiles = key_tiles(p.kv_hi), split = static_cast<int>(blockIdx.x) / k_heads % a.n_split;
-          p.t_lo = tiles * split / a.n_split;                // (below 2^24 tiles, 64 splits)
+          p.t_lo = tiles * split / a.n_split;                // (below 2^24 tiles, 16 splits)
           p.n_t = tiles * (split + 1) / a.n_split - p.t_lo;
           s_piece[0] = p;
         }
@@ -493,7 +507,8 @@ __global__ void __launch_bounds__(pre::NT, 1) prefill_kernel(const AttnArgs a) {
             if (x == 0 || two) {
 #pragma unroll
               for (int ks = 0; ks < C::PKS; ++ks)
-                mma_ta(tm + TO + 128 * x, tm + TP + 64 * x + 8 * ks, v + ((ks * 2 * C::VC * 128) >> 4), ID_PV, j > 0 || ks > 0);
+                mma_ta(tm + TO + 128 * x, tm + TP + 64 * x + 8 * ks, v + ((ks * 2 * C::VC * 128) >> 4), ID_PV,
+                       j > 0 || ks > 0);
             }
             tc::mma_commit(&bars.pv[x][J & 1]);
           }
@@ -517,7 +532,8 @@ __global__ void __launch_bounds__(pre::NT, 1) prefill_kernel(const AttnArgs a) {
                 if (x == 0 || two) {
 #pragma unroll
                   for (int ks = 0; ks < C::SKS; ++ks)
-                    tc::mma_f16(tm + TS, q0 + x * (C::Q_BYTES >> 4) + ((ks * 4096) >> 4), k + ((ks * 256) >> 4), ID_S, ks > 0);
+                    tc::mma_f16(tm + TS, q0 + x * (C::Q_BYTES >> 4) + ((ks * 4096) >> 4), k + ((ks * 256) >> 4), ID_S,
+                                ks > 0);
                 }
                 tc::mma_commit(&bars.s[x]);
                 tc::mma_commit(&bars.kf[J & 1]);
@@ -576,7 +592,8 @@ __global__ void __launch_bounds__(pre::NT, 1) prefill_kernel(const AttnArgs a) {
           if (page != -2) set_status(a.status, TQ_ERR_DEVICE_CHECK);                 // a zero row
           return;
         }
-        const uint32_t in = (static_cast<uint32_t>(t_lo + j) * BN + key) & mask, pg = static_cast<uint32_t>(page) * a.n_kv_heads;
+        const uint32_t in = (static_cast<uint32_t>(t_lo + j) * BN + key) & mask;
+        const uint32_t pg = static_cast<uint32_t>(page) * a.n_kv_heads;
         kr = ((pg * maps + kh) << a.page_shift) + in;
         vr = ((pg + hv) << a.page_shift) + in;
       };
@@ -585,7 +602,8 @@ __global__ void __launch_bounds__(pre::NT, 1) prefill_kernel(const AttnArgs a) {
 #pragma unroll
         for (int c = 0; c < CK; ++c) {
           kraw[c] = make_uint4(0, 0, 0, 0);
-          if (kr != NONE) kraw[c] = __ldg(reinterpret_cast<const uint4 *>(a.k_codes + static_cast<uint64_t>(kr) * (DK / 2)) + c);
+          if (kr != NONE)
+            kraw[c] = __ldg(reinterpret_cast<const uint4 *>(a.k_codes + static_cast<uint64_t>(kr) * (DK / 2)) + c);
         }
       };
       auto load_v = [&]() {
@@ -593,7 +611,8 @@ __global__ void __launch_bounds__(pre::NT, 1) prefill_kernel(const AttnArgs a) {
 #pragma unroll
         for (int c = 0; c < CV; ++c) {
           vraw[c] = make_uint4(0, 0, 0, 0);
-          if (vr != NONE) vraw[c] = __ldg(reinterpret_cast<const uint4 *>(a.v_codes + static_cast<uint64_t>(vr) * (DV / 2)) + c);
+          if (vr != NONE)
+            vraw[c] = __ldg(reinterpret_cast<const uint4 *>(a.v_codes + static_cast<uint64_t>(vr) * (DV / 2)) + c);
         }
       };
       rows_of(0, page_of(0));
@@ -922,7 +941,8 @@ __global__ void __launch_bounds__(pre::NT, 1) prefill_kernel(const AttnArgs a) {
         return static_cast<int64_t>(pc.row0 + qi) * a.n_heads + hv * G + head;
       };
       auto part_at = [&](int64_t at) {
-        return a.row_part + ((at * maps + map) * a.n_split + (LINE ? 0 : static_cast<int>(blockIdx.x) / k_heads % a.n_split)) * (DV + 4);
+        const int split = LINE ? 0 : static_cast<int>(blockIdx.x) / k_heads % a.n_split;
+        return a.row_part + ((at * maps + map) * a.n_split + split) * (DV + 4);
       };
       // 64 bytes of each of the warp's rows (lane: row), values from dim d on, by way of shared memory (where Q was), so
       // that a store touches 8 lines: 4 lanes share a row.  Swizzled, so that neither side has bank conflicts.
@@ -1000,7 +1020,8 @@ __global__ void __launch_bounds__(pre::NT, 1) prefill_kernel(const AttnArgs a) {
           if (shared) {
 #pragma unroll
             for (int k = 0; k < 32; k += 4)
-              reinterpret_cast<float4 *>(mine + 4 * BM)[((c + k) / 4) * 2 * BM + at] = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+              reinterpret_cast<float4 *>(mine + 4 * BM)[((c + k) / 4) * 2 * BM + at] =
+                  make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
           } else {
             put32(c, v, inv);
           }

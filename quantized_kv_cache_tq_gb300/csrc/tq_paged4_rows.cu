@@ -181,6 +181,11 @@ __device__ __forceinline__ Place place_of(const RowsArgs &a) {
   return p;
 }
 
+// the first of the thread's words of codes (the other is `lanes` further on)
+__device__ __forceinline__ int64_t codes_at(const Place &p) {
+  return static_cast<int64_t>(p.cell_row) * (2 * p.lanes) + p.e0 / 8;
+}
+
 template <int TYPE>
 __global__ void __launch_bounds__(RT, 6) set_rows_kernel(const RowsArgs a) {
   const Place p = place_of(a);
@@ -251,7 +256,7 @@ __global__ void __launch_bounds__(RT, 6) set_rows_kernel(const RowsArgs a) {
   }
   if (n < 2) w[1] = 0;                                     // zero codes beyond the row
   if (n < 1) w[0] = 0;
-  uint32_t *codes = reinterpret_cast<uint32_t *>(a.codes[p.which]) + static_cast<int64_t>(p.cell_row) * (2 * p.lanes) + p.e0 / 8;
+  uint32_t *codes = reinterpret_cast<uint32_t *>(a.codes[p.which]) + codes_at(p);
   codes[0] = w[0];
   codes[p.lanes] = w[1];
   if (p.e0 == 0)
@@ -263,7 +268,7 @@ template <int TYPE>
 __global__ void __launch_bounds__(RT) get_rows_kernel(const RowsArgs a) {
   const Place p = place_of(a);
   if (!p.ok || p.n == 0) return;
-  const uint32_t *codes = reinterpret_cast<const uint32_t *>(a.codes[p.which]) + static_cast<int64_t>(p.cell_row) * (2 * p.lanes) + p.e0 / 8;
+  const uint32_t *codes = reinterpret_cast<const uint32_t *>(a.codes[p.which]) + codes_at(p);
   const uint32_t sm = __ldcs(reinterpret_cast<const uint32_t *>(a.scales[p.which]) + p.cell_row);
   const uint32_t w[2] = {__ldcs(codes), __ldcs(codes + p.lanes)};
   const float s = __half2float(__ushort_as_half(static_cast<uint16_t>(sm)));
