@@ -353,8 +353,9 @@ tq_status tq_f16_prompt_attn(const uint16_t *k, const uint16_t *v, int64_t n_cel
  * (row stride in entries), entry j of a sequence's row the page of its cells
  * j * page_size ..; entries beyond a sequence's length are never read.  Sequence
  * lengths and row counts are read on the device when the call runs.  The attention
- * calls take tables of max_pages * page_size up to 2^31 - 2^16 cells.  A workspace
- * of these calls is 256-byte aligned, zero-filled before its first use and left
+ * calls take tables of max_pages * page_size up to 2^31 - 2^16 cells.  Outputs
+ * overlap no input, but where a call says so.  A workspace of these calls is
+ * 256-byte aligned, zero-filled before its first use and left
  * ready by every call; calls of different shapes and kinds (decode, prefill,
  * differential) may share one, one after the other, but not with calls above
  * this section and not by calls that run at the same time.  Its status word is

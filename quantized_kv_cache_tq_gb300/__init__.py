@@ -256,7 +256,7 @@ def _row_stride(t, shape, what: str) -> int:
     s0, s1, s2 = t.stride()
     if (s2 != 1 and shape[2] > 1) or (s1 != shape[2] and shape[1] > 1):
         raise ValueError(f"{what}: a row's heads have to be contiguous")
-    return s0 if shape[0] > 1 else max(s0, shape[1] * shape[2])
+    return s0 if shape[0] > 1 else shape[1] * shape[2]
 
 
 def _row_width(head_dim: int) -> int:
@@ -402,9 +402,11 @@ def paged4_prefill_workspace(kc: Paged4Cache, vc: Paged4Cache, n_heads: int, n_s
     return _lib.tq_paged4_prefill_workspace(kc.ref, vc.ref, n_heads, n_seq, n_rows, max_len)
 
 
-def _paged4_args(kc, vc, block_table, seq_len, q, maps, out, stream, *extra):
+def _paged4_args(kc, vc, block_table, seq_len, q, maps, out, ws, stream, *extra):
     """Checks shared by the attention calls -> (n_seq, max_pages, q type, q stride, output heads, out, stream)."""
     t = _row_type(q, "q", f32=False)
+    if ws is not None and (ws.element_size() != 1 or not ws.is_contiguous()):
+        raise ValueError("ws: a contiguous tensor of bytes is expected")
     if block_table.dim() != 2 or q.dim() != 3 or q.shape[1] % maps:
         raise ValueError("block_table: [n_seq][max_pages], q: [rows][heads][head_dim]")
     n_seq, max_pages = block_table.shape
@@ -418,7 +420,7 @@ def _paged4_args(kc, vc, block_table, seq_len, q, maps, out, stream, *extra):
     else:
         _ints(out, q.dtype, (rows, heads, vc.head_dim), "out")
     return n_seq, max_pages, t, stride, heads, out, _stream_here(stream, kc.index, vc.codes, block_table, seq_len, q,
-                                                                 out, *extra)
+                                                                 out, ws, *extra)
 
 
 def _diff_args(vc, heads, lam, norm_weight):
@@ -433,7 +435,7 @@ def paged4_decode(kc: Paged4Cache, vc: Paged4Cache, block_table, seq_len, q, sca
                   ws=None, stream=None):
     """One query row per sequence: q [n_seq][n_q_heads][Dk] (float16 or bfloat16, rows may be strided) over the
     seq_len[s] cells (device int32) of block_table[s] -> [n_seq][n_q_heads][Dv] of q's type."""
-    n_seq, max_pages, t, stride, heads, out, handle = _paged4_args(kc, vc, block_table, seq_len, q, 1, out, stream, ws)
+    n_seq, max_pages, t, stride, heads, out, handle = _paged4_args(kc, vc, block_table, seq_len, q, 1, out, ws, stream)
     _need(q.shape[0] == n_seq, "q: one row per sequence")
     scale = 1.0 / math.sqrt(kc.head_dim) if scale is None else scale
     if ws is None:
@@ -453,8 +455,8 @@ def paged4_prefill(kc: Paged4Cache, vc: Paged4Cache, block_table, seq_len, q, q_
     [n_rows][n_q_heads][Dk] are the last cells of sequence s.  max_rows and max_len (host): the most rows and cells
     of one sequence, where known; they only choose the kernel.  A workspace for the call is
     paged4_prefill_workspace(..., n_rows, max_len or the block table's capacity)."""
-    n_seq, max_pages, t, stride, heads, out, handle = _paged4_args(kc, vc, block_table, seq_len, q, 1, out, stream,
-                                                                   q_start, ws)
+    n_seq, max_pages, t, stride, heads, out, handle = _paged4_args(kc, vc, block_table, seq_len, q, 1, out, ws, stream,
+                                                                   q_start)
     _ints(q_start, _T.int32, (n_seq + 1,), "q_start")
     scale = 1.0 / math.sqrt(kc.head_dim) if scale is None else scale
     n_rows, max_len = q.shape[0], max_len or max_pages * kc.page_size
@@ -472,8 +474,8 @@ def paged4_diff_decode(kc: Paged4Cache, vc: Paged4Cache, block_table, seq_len, q
                        norm_weight=None, eps: float = 1e-5, out_scale: float = 1.0, out=None, ws=None, stream=None):
     """Differential attention, one query row per sequence: q [n_seq][2 n_heads][Dk], K with two heads per V head,
     lam (device float32 [n_heads]) the weights of the second map; optional RMS norm over each head's output."""
-    n_seq, max_pages, t, stride, heads, out, handle = _paged4_args(kc, vc, block_table, seq_len, q, 2, out, stream,
-                                                                   lam, norm_weight, ws)
+    n_seq, max_pages, t, stride, heads, out, handle = _paged4_args(kc, vc, block_table, seq_len, q, 2, out, ws, stream,
+                                                                   lam, norm_weight)
     _need(q.shape[0] == n_seq, "q: one row per sequence")
     lam_p, norm_p = _diff_args(vc, heads, lam, norm_weight)
     scale = 1.0 / math.sqrt(kc.head_dim) if scale is None else scale
@@ -493,8 +495,8 @@ def paged4_diff_prefill(kc: Paged4Cache, vc: Paged4Cache, block_table, seq_len, 
                         stream=None):
     """Differential attention of several query rows per sequence: rows as paged4_prefill, heads as
     paged4_diff_decode."""
-    n_seq, max_pages, t, stride, heads, out, handle = _paged4_args(kc, vc, block_table, seq_len, q, 2, out, stream,
-                                                                   q_start, lam, norm_weight, ws)
+    n_seq, max_pages, t, stride, heads, out, handle = _paged4_args(kc, vc, block_table, seq_len, q, 2, out, ws, stream,
+                                                                   q_start, lam, norm_weight)
     _ints(q_start, _T.int32, (n_seq + 1,), "q_start")
     lam_p, norm_p = _diff_args(vc, heads, lam, norm_weight)
     scale = 1.0 / math.sqrt(kc.head_dim) if scale is None else scale

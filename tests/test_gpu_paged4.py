@@ -325,6 +325,23 @@ def test_decode_strided_queries_and_given_out():
     assert tq._lib.tq_workspace_status(ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream) == 0
 
 
+def test_one_row_has_any_stride():
+    # the distance to a second row that is not there
+    import torch
+    import quantized_kv_cache_tq_gb300 as tq
+    b = Batch(89, [130], 2, 128, 128, 16)
+    q = b.query(1, 8, "float16")
+    odd = torch.zeros(4096, device="cuda", dtype=q.dtype).as_strided((1, 8, 128), (1027, 128, 1)).copy_(q)
+    assert torch.equal(tq.paged4_decode(b.gk, b.gv, b.gt, b.gl, odd), tq.paged4_decode(b.gk, b.gv, b.gt, b.gl, q))
+    slots = torch.tensor([3], device="cuda")
+    x = q[:, :2]
+    odd = odd[:, :2]
+    c = [tq.Paged4Cache(2, 128, 16, 1) for _ in range(4)]
+    tq.paged4_set_rows(c[0], c[1], odd, odd, slots)
+    tq.paged4_set_rows(c[2], c[3], x.contiguous(), x.contiguous(), slots)
+    assert torch.equal(c[0].codes, c[2].codes) and torch.equal(c[1].scales, c[3].scales) and bool(c[0].codes.any())
+
+
 def test_decode_bad_pages_and_lengths_are_reported():
     import torch
     import quantized_kv_cache_tq_gb300 as tq

@@ -223,6 +223,9 @@ def test_python_calls_refuse_before_the_library():
         tq.paged4_set_rows(c, c, q[:, :2], q[:, ::2], torch.zeros((1,), dtype=torch.int64))
     with pytest.raises(ValueError):
         tq.Paged4Cache.from_planes(c.codes, c.scales[:, :1], 128)
+    for ws in (torch.zeros(4096, dtype=torch.int32), torch.zeros(4096, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError, match="ws: "):
+            tq.paged4_decode(c, c, table, lens, q, ws=ws)
     with pytest.raises(tq.TQError):
         tq.Paged4Cache(2, 100, 16, 4, device="cpu")
 
