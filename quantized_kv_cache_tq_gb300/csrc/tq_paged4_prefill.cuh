@@ -36,11 +36,11 @@
 //   they are nothing; binary16 outputs have 2.9e-4 relative error at 2048 rows over
 //   32768 cells, against 2.1e-4 of rounding alone, and at worst (few thousand keys of
 //   like weight, values around 0) 3.5e-4 against 2.0e-4.  (Centred codes as the value
-//   operand, scales in the weights and offsets in an fp32 sum come to 2.5e-4, in
-//   1012 us instead of 787: two more numbers per key and row to load and multiply.)  R is a running
-//   maximum of x_t + tau, raised only when it would grow by more than 2^12 (which
-//   binary16 weights leave room for; with 2^8 the rescaling of O cost a tenth of the
-//   time).  Sums of weights stay in fp32.
+//   operand, scales in the weights and offsets in an fp32 sum come to 2.5e-4, in 1012 us
+//   instead of 787: two more numbers per key and row from shared memory.)  R is a
+//   running maximum of x_t + tau, raised only when it would grow by more than 2^12
+//   (which binary16 weights leave room for; with 2^8 the rescaling of O cost a tenth of
+//   the time).  Sums of weights stay in fp32.
 //
 // What bounds it (2048 rows over 32768 cells: 787 us, 1.35 PFLOP/s of 1.92): a pair of
 // row tiles takes 3300 clocks per key tile, of which the products need 2500 (their k
