@@ -169,10 +169,10 @@ __device__ __forceinline__ float lds1(uint32_t at) {
 __device__ __forceinline__ uint32_t bits(__half2 h) { return *reinterpret_cast<const uint32_t *>(&h); }
 __device__ __forceinline__ __half2 as_half2(uint32_t u) { return *reinterpret_cast<const __half2 *>(&u); }
 
-// A piece of an item: key tiles t_lo .. t_lo + n_t - 1 of 256 rows of one sequence and K head, with what every
+// A piece of an item: key tiles t_lo .. t_lo + n_t - 1 of 256 rows of one sequence and K head kh, with what every
 // role needs to know of the rows.
 struct Piece {
-  int seq, tile, kh;        // tile: which 256 rows of the sequence
+  int seq, kh;
   int t_lo, n_t;            // n_t < 0: no more pieces
   int c0, n_con, slot;      // LINE: the CTAs that share the item, c0 .. c0 + n_con - 1; where this partial goes
   int slot0;                // ... and where that of c0 is
@@ -218,7 +218,6 @@ __device__ __forceinline__ int tiles_of(const AttnArgs &a, const few::SeqWork &w
   return (static_cast<uint32_t>(w.rows * a.group) + 2 * BM - 1) / (2 * BM);
 }
 __device__ __forceinline__ void rows_of_piece(const AttnArgs &a, const few::SeqWork &w, const Tile &t, Piece &p) {
-  p.tile = t.i;
   p.row0 = w.row0 + t.q;
   p.rem = t.rem;
   p.left = t.rows_all - t.i * 2 * BM;
@@ -229,7 +228,7 @@ __device__ __forceinline__ void rows_of_piece(const AttnArgs &a, const few::SeqW
 // A piece, read anew (what only begin and end of its work need is not kept in registers through the loop).
 __device__ __forceinline__ Piece read_piece(const Piece *p) {
   const volatile int *q = reinterpret_cast<const volatile int *>(p);
-  return {q[0], q[1], q[2], q[3], q[4], q[5], q[6], q[7], q[8], q[9], q[10], q[11], q[12], q[13]};
+  return {q[0], q[1], q[2], q[3], q[4], q[5], q[6], q[7], q[8], q[9], q[10], q[11], q[12]};
 }
 
 // Row `r` (of 256) of a piece: its query's row of the input, its head within the group.
@@ -247,7 +246,7 @@ struct Walk {
   int seq, tile, kh;
 };
 __device__ inline Piece next_piece(const AttnArgs &a, Walk &w) {
-  Piece p = {0, 0, 0, 0, -1, 0, 1, 0, 0, 0, 0, 0, 0, 0};
+  Piece p = {0, 0, 0, -1, 0, 1, 0, 0, 0, 0, 0, 0, 0};
   const int k_heads = (a.diff ? 2 : 1) * a.n_kv_heads;
   while (w.cur < w.end) {
     const few::SeqWork sw = few::seq_work<1>(a, w.seq, false);
@@ -338,7 +337,6 @@ __global__ void __launch_bounds__(pre::NT, 1) prefill_kernel(const AttnArgs a) {
   if (tid == 0) {
     s_fail = 0;
     s_piece[0].n_t = s_piece[1].n_t = -1;
-    s_piece[0].seq = -1;
   }
   __syncwarp();
   {
@@ -380,7 +378,7 @@ __global__ void __launch_bounds__(pre::NT, 1) prefill_kernel(const AttnArgs a) {
         }
         const long long x = alone ? scan(v) : scan_all(v, at);
         if (v > 0 && x - v <= want && want < x && (warp == 0 || !alone)) {
-          Piece p = {s, 0, static_cast<int>(blockIdx.x) % k_heads, 0, 0, 0, 1, 0, 0, 0, 0, 0, 0, 0};
+          Piece p = {s, static_cast<int>(blockIdx.x) % k_heads, 0, 0, 0, 1, 0, 0, 0, 0, 0, 0, 0};
           rows_of_piece(a, w, first_tile(a, w, static_cast<int>(want - (x - v))), p);
           const int tiles = key_tiles(p.kv_hi), split = static_cast<int>(blockIdx.x) / k_heads % a.n_split;
           p.t_lo = tiles * split / a.n_split;                // (below 2^24 tiles, 16 splits)
