@@ -237,7 +237,7 @@ cudaError_t launch_page_plan(const PlanArgs &a, cudaStream_t s) {
   }
   plan_kernel<false><<<1, PT, 0, s>>>(a);
   cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || a.n_rows == 0) return e;        // a step in which sequences only shrink has no rows to fill
   return launch_beside(rows_kernel, static_cast<unsigned>((a.n_rows + ROWS_PER - 1) / ROWS_PER), 256, 0, s, a);
 }
 

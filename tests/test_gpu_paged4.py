@@ -247,6 +247,23 @@ def test_page_plan_without_sequences_or_rows():
     assert st == 0 and got[1].tolist() == [4, 3] and got[3].tolist() == [0]
 
 
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("n", [1024, 1025, 1500, 2100])
+def test_page_plan_of_many_sequences_that_only_shrink(n, in_place):
+    # no row to fill (n_rows 0), on both sides of what one chunk of sequences holds
+    import torch
+    import quantized_kv_cache_tq_gb300 as tq
+    rng = np.random.default_rng(n)
+    old, new, table, free, count, _ = _plan_case(rng, n, 16, 5, 1)
+    new = np.array([-int(rng.integers(0, o + 1)) if rng.random() < 0.7 else 0 for o in old], np.int32)
+    ref = P.page_plan(old, new, 16, table, free, count, 0)
+    assert ref[0] and ref[3] > count
+    got, st = _run_plan(tq, torch, old, new, 16, table, free, count, 0, in_place)
+    assert st == 0
+    for name, a, b in zip(("table", "free", "count", "len", "q_start", "page_start", "slots", "positions"), got, ref[1:]):
+        assert np.array_equal(a.cpu().numpy().reshape(-1), np.asarray(b).reshape(-1)), name
+
+
 # ---------------------------------------------------------------- decode
 
 @pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
