@@ -1,5 +1,5 @@
 /*
- * tq_testing.h -- a test hook of libtq, not part of the product API.
+ * tq_testing.h -- test hooks of libtq, not part of the product API.
  *
  * The decode kernels' split merge waits, a bounded number of times, for every
  * split's partial result ([HIP#28] "1. Graph-safe decode": a decode call must
@@ -27,6 +27,11 @@ tq_status tq_testing_decode_drop_split(const tq_cache *k, const tq_cache *v, con
                                        const tq_codebook *cbv, const float *q, int n_q_heads, int64_t kv_len,
                                        float scale, int algo, float *out, void *workspace, size_t workspace_bytes,
                                        int drop_split, tq_stream stream);
+
+/* Host only.  CTAs that the paged single-token kernel of these stored row widths is launched with on a device of `sms`
+ * SMs (0: no such kernel); columns: 8 or 16 query columns at a time.  An item that all of them share is merged in
+ * *merge_bytes of the *smem bytes of shared memory that a CTA has. */
+int tq_testing_paged4_few_grid(int k_width, int v_width, int columns, int diff, int sms, int *merge_bytes, int *smem);
 
 #ifdef __cplusplus
 }

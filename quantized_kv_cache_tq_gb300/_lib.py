@@ -119,7 +119,9 @@ _SIGS = {
     "tq_paged4_diff_prefill": (C.c_int, [C.POINTER(tq_paged4), C.POINTER(tq_paged4), _P, C.c_int, _P, _P, C.c_int, _P,
                                          C.c_int, C.c_int64, C.c_int64, C.c_int, C.c_int64, C.c_int64, _P, _P,
                                          C.c_float, C.c_float, C.c_float, C.c_int, _P, _P, C.c_size_t, _P]),
-    # test hook (include/tq_testing.h)
+    # test hooks (include/tq_testing.h)
+    "tq_testing_paged4_few_grid": (C.c_int, [C.c_int, C.c_int, C.c_int, C.c_int, C.c_int, C.POINTER(C.c_int),
+                                             C.POINTER(C.c_int)]),
     "tq_testing_decode_drop_split": (C.c_int, [C.POINTER(tq_cache), C.POINTER(tq_cache), C.POINTER(tq_codebook),
                                                C.POINTER(tq_codebook), _P, C.c_int, C.c_int64, C.c_float, C.c_int,
                                                _P, _P, C.c_size_t, C.c_int, _P]),

@@ -108,6 +108,13 @@ struct FewCfg {
   static constexpr int SMEM = RING > MERGE ? RING : MERGE;
   // a partial result: (R, l, z) of every column, then the value fragments
   static constexpr int PART = 4 * NC + NT * MT * 128;
+  // The grid: all CTAs that the SMs hold, as far as the merge of an item that every one of them shares finds room in
+  // shared memory (a weight and two sums per CTA and column, and the teams' sums).  At 152 SMs every shape has room.
+  static constexpr int merge_bytes(int ctas) { return ctas * NC * 12 + THREADS * 16; }
+  static constexpr int grid(int sms) {
+    const int fit = (SMEM - THREADS * 16) / (NC * 12);
+    return sms < (fit + CTAS - 1) / CTAS ? sms * CTAS : fit;
+  }
 };
 
 namespace few {
@@ -1024,13 +1031,12 @@ template <int DK, int DV, int NT, int MAPS, bool FINE>
 cudaError_t launch_few_t(const AttnArgs &a, cudaStream_t s) {
   using C = FewCfg<DK, DV, NT, MAPS>;
   static_assert(C::SMEM <= 227 * 1024, "shared memory");
-  // weights and sums of every CTA's partial and the teams' sums, at the merge
-  static_assert(C::SMEM >= 2 * 152 * C::NC * 12 + C::THREADS * 16 || C::CTAS == 1, "merge");
+  static_assert(C::merge_bytes(C::grid(1 << 20)) <= C::SMEM && C::grid(152) == 152 * C::CTAS, "merge");
   static_assert(MAPS == 1 || NT == 1, "differential: one tile of columns for both maps");
   auto kern = few_kernel<DK, DV, NT, MAPS, FINE>;
   cudaError_t e = set_dynamic_smem(reinterpret_cast<const void *>(kern), C::SMEM);
   if (e != cudaSuccess) return e;
-  return launch_beside(kern, sm_count() * C::CTAS, C::THREADS, C::SMEM, s, a);
+  return launch_beside(kern, C::grid(sm_count()), C::THREADS, C::SMEM, s, a);
 }
 
 // (binary16 outputs keep the weights to 22 bits)

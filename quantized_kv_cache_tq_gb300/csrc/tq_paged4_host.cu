@@ -4,6 +4,8 @@
 #include <string.h>
 
 #include "tq_paged4.cuh"
+#include "tq_paged4_few.cuh"
+#include "tq_testing.h"
 
 namespace tq {
 namespace p4 {
@@ -379,6 +381,25 @@ tq_status tq_paged4_diff_prefill(const tq_paged4 *k, const tq_paged4 *v, const i
             n_rows, max_rows, max_len, max_pages, n_seq, q_type, n_heads, causal, scale, eps, out_scale, true, true,
             stream};
   return attend(c);
+}
+
+int tq_testing_paged4_few_grid(int k_width, int v_width, int columns, int diff, int sms, int *merge_bytes, int *smem) {
+  auto of = [&](auto cfg) {
+    using C = decltype(cfg);
+    *merge_bytes = C::merge_bytes(C::grid(sms));
+    *smem = C::SMEM;
+    return C::grid(sms);
+  };
+  if (sms <= 0 || !merge_bytes || !smem || !few_supported(k_width, v_width, diff != 0)) return 0;
+  if (diff) {
+    if (k_width == 64) return v_width == 64 ? of(FewCfg<64, 64, 1, 2>()) : of(FewCfg<64, 128, 1, 2>());
+    return v_width == 128 ? of(FewCfg<128, 128, 1, 2>()) : of(FewCfg<128, 256, 1, 2>());
+  }
+  const bool one = columns <= 8;
+  if (k_width == 64) return one ? of(FewCfg<64, 64, 1, 1>()) : of(FewCfg<64, 64, 2, 1>());
+  if (k_width == 128) return one ? of(FewCfg<128, 128, 1, 1>()) : of(FewCfg<128, 128, 2, 1>());
+  if (v_width == 128) return one ? of(FewCfg<256, 128, 1, 1>()) : of(FewCfg<256, 128, 2, 1>());
+  return one ? of(FewCfg<256, 256, 1, 1>()) : of(FewCfg<256, 256, 2, 1>());
 }
 
 }  // extern "C"

@@ -203,6 +203,20 @@ def test_workspace_sizes_refuse():
     assert L.tq_paged4_prefill_workspace(k, v, 4, 2, 100, -1) == 0
 
 
+@pytest.mark.parametrize("wk,wv,diff", [(64, 64, 0), (128, 128, 0), (256, 128, 0), (256, 256, 0), (64, 64, 1), (64, 128, 1),
+                                        (128, 128, 1), (128, 256, 1)])
+@pytest.mark.parametrize("columns", [8, 16])
+def test_every_cta_of_a_launch_has_room_in_the_merge(wk, wv, diff, columns):
+    # one item shared by the whole grid, on devices of any number of SMs
+    import ctypes
+    L = _lib()
+    merge, smem = ctypes.c_int(), ctypes.c_int()
+    for sms in (1, 2, 108, 152, 153, 200, 304, 511, 1000, 20000):
+        ctas = L.lib.tq_testing_paged4_few_grid(wk, wv, columns, diff, sms, merge, smem)
+        assert 0 < ctas <= 2 * sms and merge.value <= smem.value <= 227 * 1024
+        assert sms > 152 or ctas in (sms, 2 * sms)               # every SM is used
+
+
 def test_python_calls_refuse_before_the_library():
     # tensors on the CPU: every check that needs no device comes first
     import torch
