@@ -355,12 +355,15 @@ tq_status tq_f16_prompt_attn(const uint16_t *k, const uint16_t *v, int64_t n_cel
  * lengths and row counts are read on the device when the call runs.  The attention
  * calls take tables of max_pages * page_size up to 2^31 - 2^16 cells.  Outputs
  * overlap no input, but where a call says so.  A workspace of these calls is
- * 256-byte aligned, zero-filled before its first use and left
- * ready by every call; calls of different shapes and kinds (decode, prefill,
- * differential) may share one, one after the other, but not with calls above
- * this section and not by calls that run at the same time.  Its status word is
- * read by tq_workspace_status.
+ * 256-byte aligned; its first TQ_PAGED4_WORKSPACE_HEAD bytes are zero before its
+ * first use, the others may hold anything, and every call leaves it ready; calls
+ * of different shapes and kinds (decode, prefill, differential) may share one, one
+ * after the other, but not with calls above this section and not by calls that run
+ * at the same time.  Its status word is read by tq_workspace_status.
  * ------------------------------------------------------------------------ */
+
+/* Bytes at the front of a workspace of the calls of this section that are zero before its first use. */
+#define TQ_PAGED4_WORKSPACE_HEAD 4096
 
 /* One paged 4-bit cache (K or V).  With D = head_dim rounded up to 64, 128 or 256:
  *   codes   uint8    [n_pages][n_kv_heads][page_size][D / 2]

@@ -402,6 +402,13 @@ def paged4_prefill_workspace(kc: Paged4Cache, vc: Paged4Cache, n_heads: int, n_s
     return _lib.tq_paged4_prefill_workspace(kc.ref, vc.ref, n_heads, n_seq, n_rows, max_len)
 
 
+def _paged4_ws(nbytes: int, device):
+    """A workspace for one call: what has to be zero is, the partial results' room is left as it comes."""
+    ws = _T.empty(max(nbytes, _lib.PAGED4_WORKSPACE_HEAD), dtype=_T.uint8, device=device)
+    ws[:_lib.PAGED4_WORKSPACE_HEAD].zero_()
+    return ws
+
+
 def _paged4_args(kc, vc, block_table, seq_len, q, maps, out, ws, stream, *extra):
     """Checks shared by the attention calls -> (n_seq, max_pages, q type, q stride, output heads, out, stream)."""
     t = _row_type(q, "q", f32=False)
@@ -439,7 +446,7 @@ def paged4_decode(kc: Paged4Cache, vc: Paged4Cache, block_table, seq_len, q, sca
     _need(q.shape[0] == n_seq, "q: one row per sequence")
     scale = 1.0 / math.sqrt(kc.head_dim) if scale is None else scale
     if ws is None:
-        ws = _made_on(stream, lambda: workspace(paged4_decode_workspace(kc, vc, heads, n_seq), q.device))
+        ws = _made_on(stream, lambda: _paged4_ws(paged4_decode_workspace(kc, vc, heads, n_seq), q.device))
     st = _lib.tq_paged4_decode(kc.ref, vc.ref, block_table.data_ptr(), max_pages, seq_len.data_ptr(), n_seq,
                                q.data_ptr(), t, stride, heads, scale, out.data_ptr(), ws.data_ptr(), ws.numel(),
                                handle)
@@ -461,7 +468,7 @@ def paged4_prefill(kc: Paged4Cache, vc: Paged4Cache, block_table, seq_len, q, q_
     scale = 1.0 / math.sqrt(kc.head_dim) if scale is None else scale
     n_rows, max_len = q.shape[0], max_len or max_pages * kc.page_size
     if ws is None:
-        ws = _made_on(stream, lambda: workspace(paged4_prefill_workspace(kc, vc, heads, n_seq, n_rows, max_len), q.device))
+        ws = _made_on(stream, lambda: _paged4_ws(paged4_prefill_workspace(kc, vc, heads, n_seq, n_rows, max_len), q.device))
     st = _lib.tq_paged4_prefill(kc.ref, vc.ref, block_table.data_ptr(), max_pages, seq_len.data_ptr(),
                                 q_start.data_ptr(), n_seq, q.data_ptr(), t, stride, n_rows, heads, max_rows, max_len,
                                 scale, int(causal), out.data_ptr(), ws.data_ptr(), ws.numel(), handle)
@@ -480,7 +487,7 @@ def paged4_diff_decode(kc: Paged4Cache, vc: Paged4Cache, block_table, seq_len, q
     lam_p, norm_p = _diff_args(vc, heads, lam, norm_weight)
     scale = 1.0 / math.sqrt(kc.head_dim) if scale is None else scale
     if ws is None:
-        ws = _made_on(stream, lambda: workspace(paged4_decode_workspace(kc, vc, heads, n_seq), q.device))
+        ws = _made_on(stream, lambda: _paged4_ws(paged4_decode_workspace(kc, vc, heads, n_seq), q.device))
     st = _lib.tq_paged4_diff_decode(kc.ref, vc.ref, block_table.data_ptr(), max_pages, seq_len.data_ptr(), n_seq,
                                     q.data_ptr(), t, stride, heads, lam_p, norm_p, eps, out_scale, scale,
                                     out.data_ptr(), ws.data_ptr(), ws.numel(), handle)
@@ -502,7 +509,7 @@ def paged4_diff_prefill(kc: Paged4Cache, vc: Paged4Cache, block_table, seq_len, 
     scale = 1.0 / math.sqrt(kc.head_dim) if scale is None else scale
     n_rows, max_len = q.shape[0], max_len or max_pages * kc.page_size
     if ws is None:
-        ws = _made_on(stream, lambda: workspace(paged4_prefill_workspace(kc, vc, heads, n_seq, n_rows, max_len), q.device))
+        ws = _made_on(stream, lambda: _paged4_ws(paged4_prefill_workspace(kc, vc, heads, n_seq, n_rows, max_len), q.device))
     st = _lib.tq_paged4_diff_prefill(kc.ref, vc.ref, block_table.data_ptr(), max_pages, seq_len.data_ptr(),
                                      q_start.data_ptr(), n_seq, q.data_ptr(), t, stride, n_rows, heads, max_rows,
                                      max_len, lam_p, norm_p, eps, out_scale, scale, int(causal), out.data_ptr(),

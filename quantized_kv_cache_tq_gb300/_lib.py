@@ -36,6 +36,10 @@ class tq_cache(C.Structure):
                 ("qs", C.c_void_p), ("signs", C.c_void_p)]
 
 
+# bytes of a paged call's workspace that are zero before its first use (TQ_PAGED4_WORKSPACE_HEAD)
+PAGED4_WORKSPACE_HEAD = 4096
+
+
 class tq_paged4(C.Structure):
     _fields_ = [("n_kv_heads", C.c_int32), ("head_dim", C.c_int32), ("page_size", C.c_int32),
                 ("n_pages", C.c_int32), ("codes", C.c_void_p), ("scales", C.c_void_p)]

@@ -99,6 +99,10 @@ struct AttnArgs {
   int32_t n_tiles;           // prompt kernel: upper bound of row tiles over all sequences
 };
 
+// CTAs of a launch whose CTAs share items, `per_sm` on each SM: each has an arrival counter in the workspace's head.
+constexpr int kMaxCtas = 960;
+inline int max_ctas(int per_sm) { return sm_count() * per_sm < kMaxCtas ? sm_count() * per_sm : kMaxCtas; }
+
 // Few-row kernel: 8 or 16 query columns at a time, keys split evenly over the grid.
 bool few_supported(int wk, int wv, bool diff);
 cudaError_t launch_few(const AttnArgs &a, int columns, cudaStream_t s);

@@ -112,7 +112,7 @@ struct FewCfg {
   // shared memory (a weight and two sums per CTA and column, and the teams' sums).  At 152 SMs every shape has room.
   static constexpr int merge_bytes(int ctas) { return ctas * NC * 12 + THREADS * 16; }
   static constexpr int grid(int sms) {
-    const int fit = (SMEM - THREADS * 16) / (NC * 12);
+    const int room = (SMEM - THREADS * 16) / (NC * 12), fit = room < kMaxCtas ? room : kMaxCtas;
     return sms < (fit + CTAS - 1) / CTAS ? sms * CTAS : fit;
   }
 };

@@ -63,18 +63,20 @@ bool few_supported(int wk, int wv, bool diff) {
   return (wk == wv) || (wk == 256 && wv == 128);
 }
 
-// Workspace: status word, arrival counters of the few-row kernel (one per CTA, in a place that does not
-// depend on the shape, so that calls of different shapes can share it), partials of either kernel.
-constexpr size_t kCountersOff = 256;
+// Workspace: status word, arrival counters (one per CTA of either kernel, in a place that does not depend on the shape,
+// so that calls of different shapes can share it), partials of either kernel.  Partials are written before they are read:
+// only the head in front of them has to be zero before the first use.
+constexpr size_t kCountersOff = 256, kHead = TQ_PAGED4_WORKSPACE_HEAD;
+static_assert(kCountersOff + sizeof(int32_t) * kMaxCtas <= kHead, "counters");
 struct Layout {
   size_t part_off, total;
 };
 
 static Layout few_layout(int wv) {
   Layout L;
-  const size_t ctas = 2 * static_cast<size_t>(sm_count());         // at most two per SM
+  const size_t ctas = static_cast<size_t>(max_ctas(2));            // at most two per SM
   const size_t columns = 16, tiles = 2;                            // the larger of the two column widths
-  L.part_off = kCountersOff + up(sizeof(int32_t) * ctas, 256);
+  L.part_off = kHead;
   L.total = L.part_off + sizeof(float) * 2 * ctas * (4 * columns + tiles * (wv / 16) * 128);
   return L;
 }

@@ -1168,7 +1168,7 @@ cudaError_t launch_prefill_t(const AttnArgs &a, cudaStream_t s) {
   auto kern = a.line ? prefill_kernel<DK, DV, true> : prefill_kernel<DK, DV, false>;
   cudaError_t e = set_dynamic_smem(reinterpret_cast<const void *>(kern), C::TOTAL);
   if (e != cudaSuccess) return e;
-  const unsigned grid = a.line ? static_cast<unsigned>(sm_count()) : static_cast<unsigned>(a.n_tiles) * a.n_split * k_heads;
+  const unsigned grid = a.line ? static_cast<unsigned>(max_ctas(1)) : static_cast<unsigned>(a.n_tiles) * a.n_split * k_heads;
   e = launch_beside(kern, grid, pre::NT, C::TOTAL, s, a);
   if (e != cudaSuccess || (a.n_split == 1 && !a.diff)) return e;
   return launch_beside(prefill_merge_kernel<DV>, static_cast<unsigned>((a.n_rows * a.n_heads + 7) / 8), 256, 0, s, a);

@@ -413,6 +413,30 @@ def test_decode_graph_follows_lengths_and_shares_a_workspace():
             _check(dout, ref, bound, "float16")
 
 
+def test_a_workspace_is_zero_in_its_head_only():
+    # NaN everywhere else before the first use; all four calls, in both ways of cutting a prompt's work
+    import torch
+    import quantized_kv_cache_tq_gb300 as tq
+    b = Batch(101, [1500, 300, 0, 64], 2, 128, 128, 16)
+    d = Batch(103, [1500, 300, 0, 64], 2, 64, 128, 16, maps=2)
+    gs = torch.tensor([0, 140, 150, 150, 170], dtype=torch.int32, device="cuda")
+    q, dq, lam = b.query(170, 8, "float16"), d.query(170, 8, "float16"), torch.full((4,), 0.3, device="cuda")
+
+    def calls(ws):
+        for max_len in (1500, 1 << 18):
+            yield tq.paged4_prefill(b.gk, b.gv, b.gt, b.gl, q, gs, max_len=max_len, ws=ws())
+            yield tq.paged4_diff_prefill(d.gk, d.gv, d.gt, d.gl, dq, gs, lam, max_len=max_len, ws=ws())
+        yield tq.paged4_decode(b.gk, b.gv, b.gt, b.gl, q[:4], ws=ws())
+        yield tq.paged4_diff_decode(d.gk, d.gv, d.gt, d.gl, dq[:4], lam, ws=ws())
+
+    def dirty():
+        ws = torch.full((128 << 20,), 0xff, dtype=torch.uint8, device="cuda")
+        ws[:tq._lib.PAGED4_WORKSPACE_HEAD] = 0
+        return ws
+    for got, want in zip(calls(dirty), calls(lambda: tq.workspace(128 << 20))):
+        assert bool(torch.isfinite(got).all()) and torch.equal(got, want)
+
+
 def test_decode_repeats_bit_for_bit():
     import torch
     import quantized_kv_cache_tq_gb300 as tq

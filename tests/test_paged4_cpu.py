@@ -217,6 +217,17 @@ def test_every_cta_of_a_launch_has_room_in_the_merge(wk, wv, diff, columns):
         assert sms > 152 or ctas in (sms, 2 * sms)               # every SM is used
 
 
+def test_a_calls_own_workspace_is_cleared_no_further_than_it_has_to(monkeypatch):
+    import torch
+    import quantized_kv_cache_tq_gb300 as tq
+    head = _lib().PAGED4_WORKSPACE_HEAD
+    names = tq._t()
+    monkeypatch.setattr(names, "empty", lambda n, **kw: torch.full((n,), 7, **kw))
+    ws = tq._paged4_ws(5 * head, "cpu")
+    assert ws.numel() == 5 * head and not ws[:head].any() and bool((ws[head:] == 7).all())
+    assert not tq._paged4_ws(0, "cpu").any()
+
+
 def test_python_calls_refuse_before_the_library():
     # tensors on the CPU: every check that needs no device comes first
     import torch
