@@ -469,7 +469,10 @@ tq_status tq_paged4_decode(const tq_paged4 *k, const tq_paged4 *v, const int32_t
                            tq_stream stream);
 
 /* Bytes of workspace of the prefill calls (plain and differential) for at most
- * n_rows query rows of n_seq sequences of at most max_len cells; 0 if refused. */
+ * n_rows query rows of at most n_seq sequences of at most max_len cells; 0 if
+ * refused.  It depends on n_rows only (n_seq and max_len are checked) and never
+ * shrinks as n_rows grows: a workspace for the largest step serves every smaller
+ * one, with any max_rows and max_len. */
 size_t tq_paged4_prefill_workspace(const tq_paged4 *k, const tq_paged4 *v, int n_heads, int n_seq, int64_t n_rows,
                                    int64_t max_len);
 
@@ -489,7 +492,7 @@ size_t tq_paged4_prefill_workspace(const tq_paged4 *k, const tq_paged4 *v, int n
  * max_len  host: the longest sequence, as far as the caller knows (0: the table's
  *          capacity).  It only chooses how many CTAs share a row's keys.
  * Other arguments, results and errors as tq_paged4_decode; the workspace is what
- * tq_paged4_prefill_workspace gives for the same n_rows, n_seq and max_len. */
+ * tq_paged4_prefill_workspace gives for n_rows or more. */
 tq_status tq_paged4_prefill(const tq_paged4 *k, const tq_paged4 *v, const int32_t *block_table, int max_pages,
                             const int32_t *seq_len, const int32_t *q_start, int n_seq, const void *q, int q_type,
                             int64_t q_stride, int64_t n_rows, int n_q_heads, int64_t max_rows, int64_t max_len,

@@ -398,7 +398,8 @@ def paged4_decode_workspace(kc: Paged4Cache, vc: Paged4Cache, n_heads: int, n_se
 
 def paged4_prefill_workspace(kc: Paged4Cache, vc: Paged4Cache, n_heads: int, n_seq: int, n_rows: int,
                              max_len: int) -> int:
-    """Bytes of workspace of paged4_prefill and, where K has two heads per V head, paged4_diff_prefill."""
+    """Bytes of workspace of paged4_prefill and, where K has two heads per V head, paged4_diff_prefill: it serves every
+    call of at most n_rows rows."""
     return _lib.tq_paged4_prefill_workspace(kc.ref, vc.ref, n_heads, n_seq, n_rows, max_len)
 
 
@@ -460,8 +461,8 @@ def paged4_prefill(kc: Paged4Cache, vc: Paged4Cache, block_table, seq_len, q, q_
                    stream=None):
     """Several query rows per sequence: rows q_start[s] .. q_start[s + 1] - 1 (device int32 [n_seq + 1]) of q
     [n_rows][n_q_heads][Dk] are the last cells of sequence s.  max_rows and max_len (host): the most rows and cells
-    of one sequence, where known; they only choose the kernel.  A workspace for the call is
-    paged4_prefill_workspace(..., n_rows, max_len or the block table's capacity)."""
+    of one sequence, where known; they only choose the kernel.  A workspace for the call is what
+    paged4_prefill_workspace gives for at least as many rows."""
     n_seq, max_pages, t, stride, heads, out, handle = _paged4_args(kc, vc, block_table, seq_len, q, 1, out, ws, stream,
                                                                    q_start)
     _ints(q_start, _T.int32, (n_seq + 1,), "q_start")

@@ -87,7 +87,10 @@ static Layout few_layout(int wv) {
 // finding it and for the items cut at its ends.  Measured, line against split: 2048 rows over 32768 cells 818 /
 // 926 us, over 4096 cells 114 / 104 us, three differential chunks of up to 700 rows 90 / 104 us, 20 chunks of up to
 // 300 rows 90 / 83 us.
+// Of the splits only those are taken whose rows' partial results fit in the room of a line's (row_room; no shape is
+// known where the estimate would choose another): a workspace for some rows then serves every call of fewer.
 constexpr int kMaxSplit = 16;
+static int64_t row_room() { return 2 * 256 * static_cast<int64_t>(max_ctas(1)); }     // (two partials of 256 rows per CTA)
 struct Share {
   bool line;
   int n_split;
@@ -99,7 +102,7 @@ static Share prefill_share(int64_t n_rows, int n_seq, int group, int k_heads, in
   if (items < k_heads) items = k_heads;
   Share best = {true, 1};
   int64_t least = (items * (tiles + 4) + sms - 1) / sms + 14;
-  for (int c = 1; c <= kMaxSplit && (c == 1 || tiles / c >= 4); ++c) {
+  for (int c = 1; c <= kMaxSplit && (c == 1 || (tiles / c >= 4 && n_rows * group * k_heads * c <= row_room())); ++c) {
     const int64_t cost = (items * c + sms - 1) / sms * ((tiles + c - 1) / c + 4 + (c > 1 || maps > 1 ? 4 : 0));
     if (cost < least) {
       best = {false, c};
@@ -115,16 +118,21 @@ static bool takes_prefill(const tq_paged4 *k, const tq_paged4 *v, int64_t rows_p
   return prefill_supported(row_width(k->head_dim), row_width(v->head_dim)) && rows_per_seq * group > 16;
 }
 
-// row_off: where the rows' partial results begin (behind the shared items' partials in the line form).
-static Layout prefill_layout(const tq_paged4 *k, const tq_paged4 *v, int n_heads, int64_t n_rows, bool line, int n_split,
+// row_off: where the rows' partial results begin.  The size only grows with n_rows, and depends neither on how the work
+// is shared out nor on sequences and lengths, so that a workspace serves every smaller call: it has room for a line's
+// shared items or for a split's rows, and behind it for the rows of two maps.
+static Layout prefill_layout(const tq_paged4 *k, const tq_paged4 *v, int n_heads, int64_t n_rows, int n_split,
                              size_t *row_off) {
   const int wv = row_width(v->head_dim), maps = k->n_kv_heads / v->n_kv_heads;
   Layout L = few_layout(wv);
   *row_off = L.part_off;
-  if (!prefill_supported(row_width(k->head_dim), wv)) return L;
-  if (line) *row_off += up(sizeof(float) * 2 * sm_count() * 256 * (wv + 2), 256);       // two partials per CTA
-  size_t end = *row_off;
-  if (n_split > 1 || maps > 1) end += static_cast<size_t>(n_rows) * n_heads * maps * n_split * (wv + 4) * sizeof(float);
+  if (!takes_prefill(k, v, n_rows, n_heads / v->n_kv_heads)) return L;
+  const size_t row = sizeof(float) * (wv + 4), room = static_cast<size_t>(row_room()) * row;
+  size_t end = L.part_off + room;
+  if (maps > 1) {
+    if (n_split == 1) *row_off = end;         // (differential rows leave partial results in the line form too)
+    end += static_cast<size_t>(n_rows) * n_heads * maps * row;
+  }
   if (end > L.total) L.total = end;
   return L;
 }
@@ -163,7 +171,7 @@ static tq_status attend(const Call &c) {
     return TQ_ERR_INVALID_ARG;
   const int wk = row_width(c.k->head_dim), wv = row_width(c.v->head_dim);
   const int group = c.n_heads / c.v->n_kv_heads;
-  const int64_t rows = c.ragged ? (c.max_rows ? c.max_rows : c.n_rows) : 1;
+  const int64_t rows = !c.ragged ? 1 : c.max_rows && c.max_rows < c.n_rows ? c.max_rows : c.n_rows;
   const bool prompt = c.ragged && takes_prefill(c.k, c.v, rows, group);
   Share share = {false, 1};
   if (prompt)
@@ -172,7 +180,7 @@ static tq_status attend(const Call &c) {
   const bool line = share.line;
   const int n_split = share.n_split;
   size_t row_off = 0;
-  const Layout L = prompt ? prefill_layout(c.k, c.v, c.n_heads, c.n_rows, line, n_split, &row_off) : few_layout(wv);
+  const Layout L = prompt ? prefill_layout(c.k, c.v, c.n_heads, c.n_rows, n_split, &row_off) : few_layout(wv);
   if (!al(c.workspace, 256) || c.workspace_bytes < L.total) return TQ_ERR_WORKSPACE;
   AttnArgs a;
   memset(&a, 0, sizeof(a));
@@ -335,12 +343,8 @@ size_t tq_paged4_prefill_workspace(const tq_paged4 *k, const tq_paged4 *v, int n
                                    int64_t max_len) {
   if (heads_ok(k, v, n_heads, n_seq, is_diff(k, v)) != TQ_OK || n_rows < 0 || max_len < 0) return 0;
   if (n_rows > 0x7fffffffLL / n_heads) return 0;
-  // (max_len 0, the call's "table's capacity": room for any split)
-  Share share = {true, kMaxSplit};
-  const int maps = k->n_kv_heads / v->n_kv_heads;
-  if (max_len) share = prefill_share(n_rows, n_seq, n_heads / v->n_kv_heads, k->n_kv_heads, maps, max_len);
   size_t row_off = 0;
-  return prefill_layout(k, v, n_heads, n_rows, share.line, share.n_split, &row_off).total;
+  return prefill_layout(k, v, n_heads, n_rows, 1, &row_off).total;
 }
 
 tq_status tq_paged4_decode(const tq_paged4 *k, const tq_paged4 *v, const int32_t *block_table, int max_pages,

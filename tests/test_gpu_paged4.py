@@ -437,6 +437,34 @@ def test_a_workspace_is_zero_in_its_head_only():
         assert bool(torch.isfinite(got).all()) and torch.equal(got, want)
 
 
+@pytest.mark.parametrize("maps", [1, 2])
+def test_the_largest_steps_workspace_serves_smaller_steps(maps):
+    # sized once for the most rows; steps of fewer rows take other ways of cutting the work, with other room for partials
+    import torch
+    import quantized_kv_cache_tq_gb300 as tq
+    lens = [1100, 900, 640, 700]
+    b = Batch(107, lens, 8, 64, 128 if maps == 2 else 64, 16, maps=maps)
+    heads, lam = 32, torch.full((32,), 0.3, device="cuda")
+    ws = tq.workspace(tq.paged4_prefill_workspace(b.gk, b.gv, heads, 4, 2048 // maps, 4096))
+    for nq, max_len in (([600 // maps, 700 // maps, 640 // maps, 108 // maps], 1100), ([700, 0, 0, 0], 4096),
+                        ([512, 0, 0, 0], 4096), ([128, 5, 1, 60], 4096), ([64, 0, 0, 0], 1100), ([9, 1, 1, 1], 0),
+                        ([1, 0, 1, 1], 1100)):
+        start = np.cumsum([0] + nq)
+        q = b.query(int(start[-1]), maps * heads, "bfloat16")
+        gs = torch.tensor(start, dtype=torch.int32, device="cuda")
+        if maps == 2:
+            out = tq.paged4_diff_prefill(b.gk, b.gv, b.gt, b.gl, q, gs, lam, max_len=max_len or None, ws=ws)
+        else:
+            out = tq.paged4_prefill(b.gk, b.gv, b.gt, b.gl, q, gs, max_len=max_len or None, ws=ws)
+        pick = np.sort(b.rng.permutation(int(start[-1]))[:40])
+        for s in range(4):                                         # some rows of each sequence, one by one
+            for r in pick[(pick >= start[s]) & (pick < start[s + 1])]:
+                n = lens[s] - int(start[s + 1] - 1 - r)
+                ref, bound = P.attention(b.k, b.v, b.table[s:s + 1], [n], _np(q[r:r + 1]), [0, 1], heads, 64 ** -0.5,
+                                         lam=[0.3] * heads if maps == 2 else None)
+                _check(out[r:r + 1], ref, bound, "bfloat16")
+
+
 def test_decode_repeats_bit_for_bit():
     import torch
     import quantized_kv_cache_tq_gb300 as tq

@@ -228,6 +228,36 @@ def test_a_calls_own_workspace_is_cleared_no_further_than_it_has_to(monkeypatch)
     assert not tq._paged4_ws(0, "cpu").any()
 
 
+@pytest.mark.parametrize("kind", ["prefill", "diff_prefill"])
+@pytest.mark.parametrize("dk,dv,hkv,group", [(128, 128, 8, 4), (64, 64, 2, 1), (64, 128, 4, 2), (128, 128, 1, 16), (256, 256, 2, 2)])
+def test_a_prefill_workspace_serves_every_smaller_call(kind, dk, dv, hkv, group):
+    # (256, 256) and, in one map, (64, 128): forms that the call or the prompt kernel does not take
+    L = _lib()
+    maps = 2 if kind == "diff_prefill" else 1
+    k, v, heads = _cache(L, h=maps * hkv, d=dk), _cache(L, h=hkv, d=dv), hkv * group
+    size = lambda rows, n_seq, max_len: L.tq_paged4_prefill_workspace(k, v, heads, n_seq, rows, max_len)  # noqa: E731
+    steps = [0, 1, 2, 3, 4, 5, 8, 16, 17, 30, 40, 64, 100, 128, 200, 300, 512, 700, 920, 1016, 1024, 1500, 2048]
+    most = size(2048, 8, 32768)
+    if (dk, dv, maps) in ((64, 128, 1), (256, 256, 2)):
+        assert most == 0
+        return
+    last = 0
+    for rows in steps:
+        got = {size(rows, n_seq, max_len) for n_seq in (1, 3, 8) for max_len in (0, 64, 1000, 4096, 8192, 32768)}
+        assert last <= min(got) and max(got) <= most, rows
+        last = max(got)
+    # what a call asks for is its own rows' size, whatever the hints (the few-row kernel's, if they choose that)
+    for rows in (1, 9, 64, 920):
+        need = size(rows, 3, 64)
+        for max_rows in (0, 1, 40, 5000):
+            for max_len in (0, 64, 4096, 100000):
+                a = dict(k=k, v=v, rows=rows, heads=heads, stride=maps * heads * dk, max_rows=max_rows, max_len=max_len)
+                few = L.tq_paged4_decode_workspace(k, v, heads, 3)
+                assert _attend(L, kind, **a, ws_bytes=min(need, few) - 1) == L.TQ_ERR_WORKSPACE
+                if max_rows == 0 or max_rows >= rows:
+                    assert _attend(L, kind, **a, ws_bytes=need - 1) == L.TQ_ERR_WORKSPACE
+
+
 def test_python_calls_refuse_before_the_library():
     # tensors on the CPU: every check that needs no device comes first
     import torch
