@@ -41,6 +41,14 @@
 //   running maximum of x_t + tau, raised only when it would grow by more than 2^12
 //   (which binary16 weights leave room for; with 2^8 the rescaling of O cost a tenth of
 //   the time).  Sums of weights stay in fp32.
+// - Where the largest values of the 32 keys are more than 2^SPREAD apart, each key has
+//   its own tau instead.  (A shared one rounds a key's values in steps set by another
+//   key, which a row may give no weight or, as a later row's, not see at all: by 0.5%
+//   at 2^-14 of the largest, and to nothing at 2^-24.  Up to 2^SPREAD it costs 2^-15 of
+//   the key's largest value: 15 times the rounding of a subnormal scale.)  The softmax
+//   threads then add a key's tau to its score and sum the weights by 2^-tau each: 776 us
+//   without such rows, 794 with one in every fiftieth page of 64 cells, 1231 with some
+//   among every 32 keys.
 //
 // What bounds it (2048 rows over 32768 cells: 787 us, 1.35 PFLOP/s of 1.92): a pair of
 // row tiles takes 3300 clocks per key tile, of which the products need 2500 (their k
@@ -81,6 +89,7 @@ constexpr int HK = BN / 2;                    // keys of a softmax thread
 constexpr int ITEM_COST = 4;                  // key tiles' worth of time that an item costs besides its keys
 constexpr int NT = 768;
 constexpr int W_UNPACK = 16, W_MMA = 20, W_NEXT = 21;      // first warps of the roles after the softmax
+constexpr int SPREAD = 6;                     // exponents that 32 keys' values may be apart and still share one
 constexpr int REG_SOFTMAX = 96, REG_UNPACK = 64, REG_MMA = 32;    // of 80 at the launch: 4 x 96 + 64 + 32 = 6 x 80
 
 template <int DK, int DV>
@@ -96,10 +105,11 @@ struct Cfg {
   static constexpr uint32_t KV_BYTES = K_BYTES + V_BYTES;
   // (K of a tile may be written as soon as its buffer's scores are done, their softmax still running: four of these)
   static constexpr uint32_t SSC = SKV + 2 * KV_BYTES;          // [j & 3][key] scale of a score
-  static constexpr uint32_t STAU = SSC + 4 * BN * 4;           // [j & 3][32 keys] (tau, 2^-tau)
+  static constexpr uint32_t STAU = SSC + 4 * BN * 4;           // [j & 3][32 keys] (tau, 2^-tau), or (-, 0): one per key
   static constexpr uint32_t SROW = STAU + 4 * 4 * 8;           // [tile][half][row] exchange between a row's threads
   static constexpr uint32_t SFX = SROW + 2 * 2 * BM * 8;       // [row] factor of a row's scores
-  static constexpr uint32_t TOTAL = SFX + 2 * BM * 4;
+  static constexpr uint32_t SKTAU = SFX + 2 * BM * 4;          // [j & 3][key] (tau, 2^-tau) of each key
+  static constexpr uint32_t TOTAL = SKTAU + 4 * BN * 8;
   static constexpr int SKS = KC / 2, PKS = BN / 16;            // k steps of S and of PV
 };
 
@@ -625,14 +635,18 @@ __global__ void __launch_bounds__(pre::NT, 1) prefill_kernel(const AttnArgs a) {
         if (!ok) { s_fail = 1; break; }
         unsigned char *kd = smem + C::SKV + b * C::KV_BYTES + (key >> 3) * (C::KC * 128) + (key & 7) * 16;
         unsigned char *vd = smem + C::SKV + b * C::KV_BYTES + C::K_BYTES + (key >> 3) * (C::VC * 128) + (key & 7) * 16;
-        // exponent of the 32 keys' values (with K: the softmax needs it)
+        // exponent of the 32 keys' values (with K: the softmax needs it), or of the key's own where they are far apart
         const float2 vsc = __half22float2(as_half2(vsm));
         const float top = fmaxf(fabsf(vsc.y), fabsf(fmaf(15.f, vsc.x, vsc.y)));
-        int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
-        e = min(30, max(-30, __reduce_max_sync(0xffffffffu, e)));
+        const int own = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+        const int most = __reduce_max_sync(0xffffffffu, own);
+        const bool apart = __any_sync(0xffffffffu, top > 0.f && most - own > SPREAD);
+        const int e = min(30, max(-30, apart ? own : most));
         const float dn = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);            // 2^-tau
+        reinterpret_cast<float2 *>(smem + C::SKTAU)[(J & 3) * BN + key] = make_float2(static_cast<float>(e), dn);
         if (lane == 0)
-          reinterpret_cast<float2 *>(smem + C::STAU)[(J & 3) * 4 + (warp - W_UNPACK)] = make_float2(static_cast<float>(e), dn);
+          reinterpret_cast<float2 *>(smem + C::STAU)[(J & 3) * 4 + (warp - W_UNPACK)] =
+              make_float2(static_cast<float>(e), apart ? 0.f : dn);
         {
           float2 sm = __half22float2(as_half2(ksm));
           float off = __fdividef(sm.y, sm.x);
@@ -857,7 +871,20 @@ __global__ void __launch_bounds__(pre::NT, 1) prefill_kernel(const AttnArgs a) {
           for (int k = 0; k < HK; ++k)
             if (k >= nvis) y[k] = -INFINITY;
         }
-        const float4 tau = few::lds4(sbase + C::STAU + (4 * (J & 3) + 2 * half) * 8);   // (tau, 2^-tau) of both 32 keys
+        float4 tau = few::lds4(sbase + C::STAU + (4 * (J & 3) + 2 * half) * 8);   // (tau, 2^-tau) of both 32 keys
+        const uint32_t key_tau = sbase + C::SKTAU + ((J & 3) * BN + HK * half) * 8;
+        const bool apart = tau.y == 0.f || tau.w == 0.f;
+        if (apart) {                          // each key's tau goes into its score, whose factor it has to stand
+          float un;
+          asm("rcp.approx.f32 %0, %1;" : "=f"(un) : "f"(fx));
+#pragma unroll
+          for (int k = 0; k < HK; k += 2) {
+            const float4 t4 = few::lds4(key_tau + 8 * k);
+            y[k] = fmaf(t4.x, un, y[k]);
+            y[k + 1] = fmaf(t4.z, un, y[k + 1]);
+          }
+          tau = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
         float top = -INFINITY;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
@@ -878,6 +905,16 @@ __global__ void __launch_bounds__(pre::NT, 1) prefill_kernel(const AttnArgs a) {
         if (raise) R = top;
         l *= f;
         const float Rs = R == -INFINITY ? 0.f : R;
+        if (apart) {                          // the sum of weights key by key (tau's factor of 0 leaves them out below)
+          float sum = 0.f;
+#pragma unroll
+          for (int k = 0; k < HK; k += 2) {
+            const float4 t4 = few::lds4(key_tau + 8 * k);
+            sum = fmaf(tc::ex2(fmaf(y[k], fx, -Rs)), t4.y, sum);
+            sum = fmaf(tc::ex2(fmaf(y[k + 1], fx, -Rs)), t4.w, sum);
+          }
+          l += sum;
+        }
         uint32_t p[HK / 2];
 #pragma unroll
         for (int c = 0; c < 2; ++c) {

@@ -615,6 +615,72 @@ def test_prefill_ranges(v_gain, q_gain, scale):
         _check(out, ref, bound, dtype)
 
 
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+@pytest.mark.parametrize("max_len", [96, 1 << 20])
+@pytest.mark.parametrize("where", ["future", "light", "bad page"])
+def test_prefill_small_values_beside_large_ones(dtype, max_len, where):
+    # one key has all the weight and small values; among its neighbours stands a row of values up to 2^35 times as large,
+    # which no row sees before it (causal), or which has no weight; or rows of zeros (a page outside the cache)
+    import torch
+    import quantized_kv_cache_tq_gb300 as tq
+    b = Batch(109, [96], 1, 128, 128, 16)
+    q = torch.full((40, 2, 128), 0.125, dtype=getattr(torch, dtype), device="cuda")
+    gs = torch.tensor([0, 40], dtype=torch.int32, device="cuda")
+    low, half = (-10, 2.0 ** -11) if dtype == "float16" else (-24, 2.0 ** -8)
+    at = lambda t: (b.table[0][t // 16], 0, t % 16)  # noqa: E731
+    for far in (0, 5, 6, 7, 8, 11, 14, 17, 21) + (() if dtype == "float16" else (24, 30, 35)):
+        for t in range(96):
+            b.k.scales[at(t)] = (2.0 ** -7, 8.0 if t == 50 else -8.0)
+            b.v.scales[at(t)] = (2.0 ** low, 2.0 ** low)           # values 2^low (1 .. 16)
+        big = 60 if where == "future" else 40
+        b.v.scales[at(big)] = (2.0 ** (low + far), 2.0 ** (low + far))
+        table = b.gt.clone()
+        if where == "bad page":
+            table[0, 2] = -1                                       # keys 32 .. 47, the large row's among them
+        out = tq.paged4_prefill(_upload(b.k), _upload(b.v), table, b.gl, q, gs, 1.0, max_len=max_len)
+        heavy = P.values(P.unpack(b.v.codes[at(50)], 128), b.v.scales[at(50)][0], b.v.scales[at(50)][1])
+        # (rows of a zero page have the score 0, 2^-178 of the weight); the weight's, the value's and the output's rounding
+        tol = (2 * 2.0 ** -11 + half) * (1 + 2.0 ** -6) * heavy
+        assert np.all(np.abs(_np(out) - heavy) <= tol), (far, float(np.max(np.abs(_np(out) - heavy) / heavy)))
+
+
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+@pytest.mark.parametrize("causal,max_len,maps", [(True, 300, 1), (False, 1 << 20, 1), (True, 1 << 20, 2)])
+def test_prefill_value_scales_far_apart(dtype, causal, max_len, maps):
+    # value rows of scales spread over 2^20 within every 32 keys, weights over e^16: all values positive, so that the
+    # result carries no more than its terms' relative errors
+    import torch
+    import quantized_kv_cache_tq_gb300 as tq
+    n, rows, low, half = 300, 140, *((-12, 2.0 ** -11) if dtype == "float16" else (-24, 2.0 ** -8))
+    b = Batch(113, [n], 1, 64, 128 if maps == 2 else 64, 16, maps=maps)
+    at = lambda t: (b.table[0][t // 16], slice(None), t % 16)  # noqa: E731
+    for t in range(n):
+        e = low + (0 if t % 32 == 5 else 20 if t % 32 == 21 else int(b.rng.integers(0, 21)))
+        b.v.scales[at(t)] = (2.0 ** e, 2.0 ** e)                   # values 2^e (1 .. 16)
+        b.k.scales[at(t)] = np.stack([np.zeros(maps), b.rng.uniform(-1, 1, maps)], -1)
+    q = torch.full((rows, 2 * maps, 64), 0.125, dtype=getattr(torch, dtype), device="cuda")
+    gs, gk, gv = torch.tensor([0, rows], dtype=torch.int32, device="cuda"), _upload(b.k), _upload(b.v)
+    if maps == 2:
+        # without a second map's share the result is the first map's
+        lam = torch.zeros(2, device="cuda")
+        out = tq.paged4_diff_prefill(gk, gv, b.gt, b.gl, q, gs, lam, 1.0, causal=causal, max_len=max_len)
+    else:
+        out = tq.paged4_prefill(gk, gv, b.gt, b.gl, q, gs, 1.0, causal=causal, max_len=max_len)
+    v, k = b.v.rows(b.table[0], n, 0)[0], b.k.rows(b.table[0], n, 0)[0]
+    x = k @ np.full(64, 0.125)
+    assert np.ptp(x) > 14
+    top = np.exp2(np.floor(np.log2(v.max(-1))))
+    got = _np(out)
+    for i in range(rows):
+        m = n - rows + i + 1 if causal else n
+        p = np.exp(x[:m] - x[:m].max())
+        p /= p.sum()
+        ref = p @ v[:m]
+        # weight, value and output, fp32 scores and sums; weights below 2^-14 of the largest term's in steps of 2^-24
+        tol = ref * (2 * 2.0 ** -11 + half) * (1 + 2.0 ** -6) + ref * 2.0 ** -16 + m * 2.0 ** -24 * (p * top[:m]).max()
+        assert np.all(np.abs(got[i] - ref) <= tol), (i, float(np.max(np.abs(got[i] - ref) / tol)))
+
+
 @pytest.mark.parametrize("n_seq,group,hkv,max_len", [(32, 4, 2, 600), (33, 5, 8, 4096), (40, 4, 2, 600), (40, 4, 8, 4096),
                                                      (1600, 4, 1, 400), (1600, 4, 1, 16384)])
 def test_prefill_many_sequences(n_seq, group, hkv, max_len):
