@@ -98,6 +98,41 @@ def softmax_map(q, k, v, sc, ends, scale, score_error=0.0):
     return out, bound
 
 
+def rms_limit(kc: Cache, vc: Cache, table, length, q, n_heads, scale, dtype, causal=True, lam=None):
+    """-> (exact output [rows][n_heads][Dv] of one sequence's last rows, rms that its error stays below).
+
+    The prompt kernel rounds every weight and every value to binary16 and the output to ``dtype``.  A rounding of half a
+    step h moves a number x by at most h |x|, evenly spread, so by h |x| / sqrt(3) rms; the terms' errors are
+    independent, and a term p v carries two: 2 (h p v)^2 / 3 each, added to the square of what rounding the exact output
+    itself leaves."""
+    maps, group = (1, n_heads // vc.n_kv_heads) if lam is None else (2, n_heads // vc.n_kv_heads)
+    n, h = q.shape[0], 2.0 ** -11
+    out = np.zeros((n, n_heads, vc.head_dim))
+    var = np.zeros_like(out)
+    ends = length - n + 1 + np.arange(n) if causal else np.full(n, length)
+    for head in range(n_heads):
+        hv = head // group
+        v = vc.rows(table, length, hv)[0]
+        for m in range(maps):
+            x = scale * q[:, maps * head + m] @ kc.rows(table, length, maps * hv + m)[0].T
+            x[np.arange(length)[None] >= ends[:, None]] = -np.inf
+            p = np.exp(x - x.max(-1, keepdims=True))
+            p /= p.sum(-1, keepdims=True)
+            f = 1.0 if m == 0 else -lam[head]
+            out[:, head] += f * (p @ v)
+            var[:, head] += 2 * h * h / 3 * f * f * ((p * p) @ (v * v))
+    own = round_to(out, dtype) - out
+    return out, float(np.sqrt(np.mean(own * own) + np.mean(var)))
+
+
+def round_to(x, dtype):
+    """float64 values rounded to binary16 or bfloat16 (ties to even), normal numbers."""
+    if dtype == "float16":
+        return x.astype(np.float16).astype(np.float64)
+    m, e = np.frexp(x)
+    return np.ldexp(np.rint(m * 256), e - 8)
+
+
 def attention(kc: Cache, vc: Cache, tables, lens, q, q_start, n_heads, scale, causal=True, lam=None,
               norm_weight=None, eps=0.0, out_scale=1.0):
     """Every attention call: (out, bound) [rows][n_heads][Dv]; rows outside q_start stay NaN.  lam: differential."""

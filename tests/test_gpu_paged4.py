@@ -571,6 +571,28 @@ def test_prefill_rows_that_see_nothing_and_bad_row_ranges():
         assert tq._lib.tq_workspace_status(ws.data_ptr(), ws.numel(), stream) == tq._lib.TQ_ERR_DEVICE_CHECK
 
 
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+@pytest.mark.parametrize("causal,max_len", [(True, 1500), (True, 1 << 20), (False, 1500)])
+@pytest.mark.parametrize("dk,dv,maps", [(128, 128, 1), (64, 64, 1), (64, 128, 2), (128, 128, 2)])
+def test_prefill_error_is_that_of_its_roundings(dk, dv, maps, causal, max_len, dtype):
+    import torch
+    import quantized_kv_cache_tq_gb300 as tq
+    n, rows, heads = 1500, 150, 2
+    b = Batch(127 + dk, [n], 1, dk, dv, 16, maps=maps)
+    gs = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
+    q = b.query(rows, maps * heads, dtype)
+    args = (b.gk, b.gv, b.gt, b.gl, q, gs)
+    if maps == 2:
+        lam = torch.tensor([0.25, 0.75], device="cuda")
+        out = tq.paged4_diff_prefill(*args, lam, causal=causal, max_len=max_len)
+    else:
+        out = tq.paged4_prefill(*args, causal=causal, max_len=max_len)
+    exact, limit = P.rms_limit(b.k, b.v, b.table[0], n, _np(q), heads, dk ** -0.5, dtype, causal,
+                               lam=[0.25, 0.75] if maps == 2 else None)
+    err = _np(out) - exact
+    assert float(np.sqrt(np.mean(err * err))) <= limit
+
+
 @pytest.mark.parametrize("max_len", [9000, 1 << 20])
 def test_prefill_long_context_few_tiles(max_len):
     # one tile of rows over a long context: its keys are shared by several CTAs

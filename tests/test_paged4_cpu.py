@@ -79,6 +79,32 @@ def test_differential_by_two_maps():
     assert np.allclose(normed[0, 0], 0.5 * w * out[0, 0] / np.sqrt((out[0, 0] ** 2).mean() + 1e-3), rtol=1e-12)
 
 
+@pytest.mark.parametrize("dtype,bits,within", [("float16", 11, True), ("bfloat16", 11, True), ("float16", 10, False),
+                                               ("float16", 9, False), ("bfloat16", 7, False)])
+def test_rms_limit_holds_for_binary16_operands_and_for_no_fewer_bits(dtype, bits, within):
+    # the prompt kernel's roundings in numpy, with weights and values of `bits` significant bits
+    rng = np.random.default_rng(4)
+    n, rows = 800, 60
+    kc, vc = P.Cache(1, 64, 16, 50), P.Cache(1, 64, 16, 50)
+    kc.set_rows(rng.standard_normal((n, 1, 64)), range(n))
+    vc.set_rows(rng.standard_normal((n, 1, 64)) + 0.3, range(n))
+    q = rng.standard_normal((rows, 2, 64))
+    exact, limit = P.rms_limit(kc, vc, np.arange(50), n, q, 2, 0.125, dtype)
+    assert np.allclose(exact, P.attention(kc, vc, [np.arange(50)], [n], q, [0, rows], 2, 0.125)[0], rtol=1e-12)
+
+    def cut(x):
+        m, e = np.frexp(x)
+        return np.ldexp(np.rint(m * 2.0 ** bits), e - bits)
+    k, v = kc.rows(np.arange(50), n, 0)[0], cut(vc.rows(np.arange(50), n, 0)[0])
+    got = np.zeros_like(exact)
+    for i in range(rows):
+        for h in range(2):
+            p = np.exp(0.125 * (k[:n - rows + i + 1] @ q[i, h]))
+            got[i, h] = cut(p) @ v[:len(p)] / p.sum()
+    err = P.round_to(got, dtype) - exact
+    assert (np.sqrt(np.mean(err * err)) <= limit) == within
+
+
 def test_plan_by_hand():
     # pages of 4: s0 5 -> 9 cells (takes one page), s1 8 -> 0 (returns two), s2 0 -> 1 (takes one)
     table = [[10, 11, 0], [12, 13, 0], [0, 0, 0]]
