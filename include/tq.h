@@ -504,8 +504,9 @@ tq_status tq_paged4_prefill(const tq_paged4 *k, const tq_paged4 *v, const int32_
  *   o   = a_0 - lambda[h] * a_1
  *   out[s][h] = out_scale * o                                     without norm_weight,
  *   out[s][h] = out_scale * norm_weight * o / sqrt(mean(o^2) + eps)   with it,
- * hv = h / (n_heads / v->n_kv_heads); the mean is over the head's values.  K has
- * two heads for each V head (2 hv and 2 hv + 1), q two for each output head.
+ * hv = h / (n_heads / v->n_kv_heads); the mean is over the head's values (o = 0
+ * gives zeros, with eps = 0 too).  K has two heads for each V head (2 hv and
+ * 2 hv + 1), q two for each output head.
  * lambda      device f32 [n_heads]: the learned weights of the second map
  * norm_weight device f32 [v->head_dim] or NULL
  * q           [n_seq] rows of [2 n_heads][k->head_dim]

@@ -111,6 +111,14 @@ cudaError_t launch_few(const AttnArgs &a, int columns, cudaStream_t s);
 bool prefill_supported(int wk, int wv);
 cudaError_t launch_prefill(const AttnArgs &a, cudaStream_t s);
 
+// out_scale / sqrt(mean(o^2) + eps) of a differential row with the sum of squares `ss`, out_scale without a norm.  A row of
+// zeros (no cell, or values that are 0) stays one where eps is 0.
+__device__ __forceinline__ float diff_factor(const AttnArgs &a, float ss) {
+  if (!a.norm_weight) return a.out_scale;
+  const float mean = ss / static_cast<float>(a.dv) + a.eps;
+  return mean != 0.f ? rsqrtf(mean) * a.out_scale : 0.f;
+}
+
 // A launch that may begin while the one before it on the stream is still running (programmatic dependent launch); the
 // kernel waits itself before it reads what that writes.
 template <typename Args>

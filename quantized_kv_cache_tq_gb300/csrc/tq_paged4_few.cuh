@@ -1000,7 +1000,7 @@ __global__ void __launch_bounds__(FewCfg<DK, DV, NT, MAPS>::THREADS, FewCfg<DK, 
               ss = fmaf(x, x, ss);
             }
           ss = warp_sum(ss);
-          const float r = a.norm_weight ? rsqrtf(ss / static_cast<float>(a.dv) + a.eps) * a.out_scale : a.out_scale;
+          const float r = diff_factor(a, ss);
 #pragma unroll
           for (int i = 0; i < DV / 64; ++i) {
             const int d = 64 * i + 2 * lane;

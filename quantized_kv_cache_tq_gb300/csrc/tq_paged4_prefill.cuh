@@ -1185,7 +1185,7 @@ __global__ void __launch_bounds__(256) prefill_merge_kernel(const AttnArgs a) {
 #pragma unroll
     for (int i = 0; i < N; ++i) ss = fmaf(y[i], y[i], ss);
     ss = warp_sum(ss);
-    const float r = a.norm_weight ? rsqrtf(ss / static_cast<float>(a.dv) + a.eps) * a.out_scale : a.out_scale;
+    const float r = diff_factor(a, ss);
 #pragma unroll
     for (int i = 0; i < N; ++i)
       y[i] *= r * (a.norm_weight && N * lane + i < a.dv ? a.norm_weight[N * lane + i] : 1.f);

@@ -903,6 +903,29 @@ def test_diff_prefill(dk, dv, hkv, group, page, norm, causal, dtype, max_len):
     _check(out, ref, bound, dtype)
 
 
+@pytest.mark.parametrize("max_rows,max_len", [(0, 64), (1, 64), (0, 1 << 20)])
+def test_diff_rows_without_values_are_zeros_without_eps(max_rows, max_len):
+    # rows that see no cell, sequences without cells, and value rows of zeros, normalised with eps = 0
+    import torch
+    import quantized_kv_cache_tq_gb300 as tq
+    nq, lens = [50, 20, 40], [30, 0, 40]
+    b = Batch(131, lens, 2, 64, 128, 16, maps=2)
+    page = [b.table[2][t // 16] for t in range(40)]
+    for t in range(40):
+        b.v.scales[page[t], :, t % 16] = 0.0                       # the third sequence's values
+    gv = _upload(b.v)
+    start = np.cumsum([0] + nq)
+    q, lam, w = b.query(110, 8, "float16"), torch.full((4,), 0.4, device="cuda"), torch.ones(128, device="cuda")
+    gs = torch.tensor(start, dtype=torch.int32, device="cuda")
+    out = tq.paged4_diff_prefill(b.gk, gv, b.gt, b.gl, q, gs, lam, norm_weight=w, eps=0.0, max_rows=max_rows, max_len=max_len)
+    assert not out[:20].any() and not out[50:].any() and bool(torch.isfinite(out).all())
+    ref, bound = P.attention(b.k, b.v, b.table[:1], [30], _np(q[20:50]), [0, 30], 4, 64 ** -0.5, lam=[0.4] * 4,
+                             norm_weight=np.ones(128))
+    _check(out[20:50], ref, bound, "float16")
+    one = tq.paged4_diff_decode(b.gk, gv, b.gt, b.gl, q[:3], lam, norm_weight=w, eps=0.0)
+    assert not one[1:].any() and bool(torch.isfinite(one).all()) and bool(one[0].any())
+
+
 # ---------------------------------------------------------------- together, as a server uses them
 
 def test_serving_steps_in_one_captured_graph():
