@@ -460,6 +460,8 @@ size_t tq_paged4_decode_workspace(const tq_paged4 *k, const tq_paged4 *v, int n_
  *             [n_q_heads][k->head_dim] contiguous; 16-byte aligned, q_stride a
  *             multiple of 8
  * out         device, q_type [n_seq][n_q_heads][v->head_dim], 16-byte aligned
+ * Scores scale * q . k are fp32 numbers; beyond 2^24 in magnitude, where they no
+ * longer tell keys one apart, results are not defined (in all attention calls).
  * Stored row widths (K, V): (64, 64), (128, 128), (256, 128), (256, 256).
  * Errors: TQ_ERR_INVALID_ARG, TQ_ERR_UNSUPPORTED (widths, q_type),
  * TQ_ERR_WORKSPACE, TQ_ERR_CUDA. */

@@ -722,6 +722,30 @@ def test_prefill_many_sequences(n_seq, group, hkv, max_len):
     _check(out, ref, bound, "float16")
 
 
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+@pytest.mark.parametrize("up", [4, 12, 15])
+def test_scores_up_to_2_24(up, dtype):
+    # keys whose scores are 2^(up + 2) and more apart, the largest 2^(up + 8.6): all weight is on the best key
+    import torch
+    import quantized_kv_cache_tq_gb300 as tq
+    b = Batch(137, [100], 1, 64, 64, 16)
+    order = b.rng.permutation(100)
+    for t in range(100):
+        b.k.scales[b.table[0][t // 16], 0, t % 16] = (0.0, 0.5 * float(order[t]) - 2.0)
+    q = torch.full((100, 1, 64), 8.0, dtype=getattr(torch, dtype), device="cuda")
+    scale = 2.0 ** up / 64
+    gk, gs = _upload(b.k), torch.tensor([0, 100], dtype=torch.int32, device="cuda")
+    best = [int(np.argmax(order[:t + 1])) for t in range(100)]
+    v = b.v.rows(b.table[0], 100, 0)[0][best][:, None]
+    # a weight, a value and the output rounded (the other keys' weights are below e^-64)
+    tol = (2 * 2.0 ** -11 + (2.0 ** -11 if dtype == "float16" else 2.0 ** -8)) * (1 + 2.0 ** -6) * np.abs(v) + 2.0 ** -20
+    for max_len in (100, 1 << 20):
+        out = tq.paged4_prefill(gk, b.gv, b.gt, b.gl, q, gs, scale, max_len=max_len)
+        assert np.all(np.abs(_np(out) - v) <= tol)
+    one = tq.paged4_decode(gk, b.gv, b.gt, b.gl, q[:1], scale)
+    assert np.all(np.abs(_np(one)[0] - v[-1]) <= tol[-1])
+
+
 @pytest.mark.parametrize("up", [118, -90])
 def test_scaled_queries_with_the_inverse_scale(up):
     # a power of two moved from the queries to the scale changes nothing, near the ends of bfloat16's range too
