@@ -493,6 +493,11 @@ size_t tq_paged4_prefill_workspace(const tq_paged4 *k, const tq_paged4 *v, int n
  *          known).  It only chooses the kernel.
  * max_len  host: the longest sequence, as far as the caller knows (0: the table's
  *          capacity).  It only chooses how many CTAs share a row's keys.
+ * Weights and values are rounded to binary16 as the products' operands (sums are
+ * fp32): binary16 results carry that next to their own rounding -- error 2.9e-4 rms
+ * where the exact result rounded has 2.1e-4, at most some 3.5e-4 -- and bfloat16
+ * results only their own.  (tq_paged4_decode, and this call with up to 16 rows times
+ * query heads per KV head, keep binary16 weights to 22 bits and values exact.)
  * Other arguments, results and errors as tq_paged4_decode; the workspace is what
  * tq_paged4_prefill_workspace gives for n_rows or more. */
 tq_status tq_paged4_prefill(const tq_paged4 *k, const tq_paged4 *v, const int32_t *block_table, int max_pages,

@@ -37,7 +37,7 @@
 //   32768 cells, against 2.1e-4 of rounding alone, and at worst (few thousand keys of
 //   like weight, values around 0) 3.5e-4 against 2.0e-4.  (Centred codes as the value
 //   operand, scales in the weights and offsets in an fp32 sum come to 2.5e-4, in 1012 us
-//   instead of 787: two more numbers per key and row from shared memory.)  R is a
+//   instead of 787 at that step: two more numbers per key and row from shared memory.)  R is a
 //   running maximum of x_t + tau, raised only when it would grow by more than 2^12
 //   (which binary16 weights leave room for; with 2^8 the rescaling of O cost a tenth of
 //   the time).  Sums of weights stay in fp32.
@@ -50,15 +50,16 @@
 //   without such rows, 794 with one in every fiftieth page of 64 cells, 1231 with some
 //   among every 32 keys.
 //
-// What bounds it (2048 rows over 32768 cells: 787 us, 1.35 PFLOP/s of 1.92): a pair of
-// row tiles takes 3300 clocks per key tile, of which the products need 2500 (their k
-// step for the offset included), the exponentials 2100 and the warps' instructions 1600
-// per scheduler; the rest is the chain scores - softmax - P V of the two tiles.  Part of
-// the exponentials by a polynomial was slower in every share (an eighth 794 us, a
-// quarter 831): the instructions weigh more.  Short calls are bound by the way to the
-// first product, 13000 clocks of 22000 for one key tile, mostly instructions fetched for
-// the first time: Q, lengths and output are read and written by whole lines and without
-// divisions for that (5 prompts of up to 300 rows 38.2 -> 31.8 us).
+// What bounds it (2048 rows over 32768 cells: 775 us, 1.38 PFLOP/s of 1.92): a pair of
+// row tiles takes 3640 clocks per key tile, set-up of items included, of which the tensor
+// pipe is busy 2400 (the k step for the offset included), the schedulers issue in 2500
+// and the exponentials take 1050; the rest is the chain scores - softmax - P V of the two
+// tiles.  Part of the exponentials by a polynomial was slower in every share (an eighth
+// 794 us, a quarter 831, against 787 then): the instructions weigh more.  Short calls are
+// bound by the way to the first product, 13000 clocks of 22000 for one key tile, mostly
+// instructions fetched for the first time: Q, lengths and output are read and written by
+// whole lines and without divisions for that (5 prompts of up to 300 rows 38.2 -> 31.8 us;
+// 31.4 now).
 //
 // Split of the work, two ways:
 // - LINE, where there are many (row tile, KV head) items: their key tiles, with
