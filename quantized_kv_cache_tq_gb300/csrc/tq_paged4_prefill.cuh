@@ -27,9 +27,11 @@
 //   binary16 subnormal code 2^-24 or 2^-20, exact), q is scaled by a power of two
 //   per row (exact for 16-bit inputs down to 2^-23 of the row's largest entry).  The
 //   offset's term rides along as one more k step: with a_t = m_t / s_t in two
-//   binary16 parts and sum(q) in three, the product is s_t-free, so the softmax
-//   multiplies a score by one number per key, s_t, in fp32.  (A row with
-//   |a_t| >= 2^19 is constant to 3e-5 and takes its offset alone.)
+//   binary16 parts and sum(q) in three for the first of them and two for the second,
+//   the product is s_t-free, so the softmax multiplies a score by one number per key,
+//   s_t, in fp32.  Parts and powers of two leave errors of 2^-22 of a_t and of some
+//   2^-21 of q's largest entry.  (A row with |a_t| >= 2^23 is constant to 2e-6 and
+//   takes its offset alone.)
 // - Values: v_t 2^-tau rounded to binary16 (relative 2^-12 on average half), tau the
 //   largest exponent among 32 neighbouring keys; the weights p_t 2^tau are rounded
 //   to binary16 too.  Both roundings meet the values themselves.  To bfloat16 outputs
@@ -652,13 +654,14 @@ __global__ void __launch_bounds__(pre::NT, 1) prefill_kernel(const AttnArgs a) {
           float2 sm = __half22float2(as_half2(ksm));
           float off = __fdividef(sm.y, sm.x);
           uint32_t keep = 0xffffffffu;
-          if (!(fabsf(off) < 0x1p19f)) {      // (a scale of 0 too) constant row: its offset alone
+          if (!(fabsf(off) < 0x1p23f)) {      // (a scale of 0 too) constant row: its offset alone
             keep = 0;
             off = sm.y > 0.f ? 0x1p16f : sm.y < 0.f ? -0x1p16f : 0.f;
             sm.x = sm.y != 0.f ? fabsf(sm.y) * 0x1p-16f : 1.f;
           }
-          const __half hi = __float2half_rn(off * 0.0625f);
-          const __half lo = __float2half_rn(off * 0.0625f - __half2float(hi));
+          // off 2^-8 = hi + lo 2^-8: times sum(q) 2^-16 and, for lo, 2^-24, of which each has its own parts
+          const __half hi = __float2half_rn(off * 0x1p-8f);
+          const __half lo = __float2half_rn(off - __half2float(hi) * 0x1p8f);
           *reinterpret_cast<uint4 *>(kd + (DK / 8) * 128) =
               make_uint4(bits(__halves2half2(hi, hi)), bits(__halves2half2(hi, lo)),
                          bits(__halves2half2(lo, __float2half_rn(0.f))), 0);
@@ -798,13 +801,15 @@ __global__ void __launch_bounds__(pre::NT, 1) prefill_kernel(const AttnArgs a) {
                              few::half2_bits(v[3], v[7]));
             }
             if (sub == 0) {
-              const float qs = sum * up * 0x1p-20f;
+              const float qs = sum * up * 0x1p-16f, ql = qs * 0x1p-8f;
               const __half h0 = __float2half_rn(qs);
               const __half h1 = __float2half_rn(qs - __half2float(h0));
               const __half h2 = __float2half_rn(qs - __half2float(h0) - __half2float(h1));
+              const __half l0 = __float2half_rn(ql);
+              const __half l1 = __float2half_rn(ql - __half2float(l0));
               const __half z = __float2half_rn(0.f);
               *reinterpret_cast<uint4 *>(dst + (DK / 8) * 2048) =
-                  make_uint4(bits(__halves2half2(h0, h1)), bits(__halves2half2(h2, h0)), bits(__halves2half2(h1, z)), 0);
+                  make_uint4(bits(__halves2half2(h0, h1)), bits(__halves2half2(h2, l0)), bits(__halves2half2(l1, z)), 0);
             } else if (sub == 1) {
               *reinterpret_cast<uint4 *>(dst + (DK / 8 + 1) * 2048) = make_uint4(0, 0, 0, 0);
             } else if (sub == 2) {

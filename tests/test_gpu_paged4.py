@@ -638,6 +638,32 @@ def test_prefill_ranges(v_gain, q_gain, scale):
 
 
 @pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+@pytest.mark.parametrize("s,m", [(0.5, -4.0), (2.0 ** -10, 1000.0), (2.0 ** -10, 1024.0), (2.0 ** -12, -600.0),
+                                 (2.0 ** -3, 65504.0), (2.0 ** -14, 500.0), (2.0 ** -24, 0.25)])
+def test_scores_of_key_rows_that_are_nearly_constant(s, m, dtype):
+    # offsets of up to 2^23 steps, and queries whose entries add up to 0: only the codes tell the keys apart
+    import torch
+    import quantized_kv_cache_tq_gb300 as tq
+    b = Batch(139, [400], 1, 64, 64, 16)
+    b.k.scales[:] = np.nan
+    for t in range(400):
+        b.k.scales[b.table[0][t // 16], 0, t % 16] = (s, m)
+    gk, gs = _upload(b.k), torch.tensor([0, 150], dtype=torch.int32, device="cuda")
+    q = np.ones((150, 2, 64))
+    for row in q.reshape(-1, 64):
+        row[b.rng.permutation(64)[:32]] = -1
+    q = torch.from_numpy(q).to(getattr(torch, dtype)).cuda()
+    scale = 2 / (37 * s)                                           # scores of some +-2: sums of +-codes have 37 rms
+    for max_len in (400, 1 << 20):
+        out = tq.paged4_prefill(gk, b.gv, b.gt, b.gl, q, gs, scale, max_len=max_len)
+        exact, limit = P.rms_limit(b.k, b.v, b.table[0], 400, _np(q), 2, scale, dtype)
+        err = _np(out) - exact
+        assert float(np.sqrt(np.mean(err * err))) <= limit
+    one = tq.paged4_decode(gk, b.gv, b.gt, b.gl, q[-1:], scale)
+    assert float(np.sqrt(np.mean((_np(one) - exact[-1:]) ** 2))) <= limit
+
+
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
 @pytest.mark.parametrize("max_len", [96, 1 << 20])
 @pytest.mark.parametrize("where", ["future", "light", "bad page"])
 def test_prefill_small_values_beside_large_ones(dtype, max_len, where):
