@@ -243,6 +243,14 @@ def test_every_cta_of_a_launch_has_room_in_the_merge(wk, wv, diff, columns):
         assert sms > 152 or ctas in (sms, 2 * sms)               # every SM is used
 
 
+def test_the_workspace_head_is_the_headers():
+    import os
+    import re
+    import quantized_kv_cache_tq_gb300 as tq
+    text = open(os.path.join(os.path.dirname(os.path.dirname(tq.__file__)), "include", "tq.h")).read()
+    assert int(re.search(r"#define TQ_PAGED4_WORKSPACE_HEAD (\d+)", text).group(1)) == _lib().PAGED4_WORKSPACE_HEAD
+
+
 def test_a_calls_own_workspace_is_cleared_no_further_than_it_has_to(monkeypatch):
     import torch
     import quantized_kv_cache_tq_gb300 as tq
