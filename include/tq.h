@@ -535,6 +535,159 @@ tq_status tq_paged4_diff_prefill(const tq_paged4 *k, const tq_paged4 *v, const i
                                  float out_scale, float scale, int causal, void *out, void *workspace,
                                  size_t workspace_bytes, tq_stream stream);
 
+/* ------------------------------------------------------------------------
+ * Rotary positions, and the int8 cache's writer, reader and single-token
+ * attention.  tq_int8_prompt_attn attends int8 rows that are in the cache already;
+ * the calls of this section put them there, positions included, and decode from
+ * them.  Slots and positions are what tq_page_plan gives.  The pages cited above
+ * have no counterpart: this is an addition of this library.  Conventions as in the
+ * section before; calls take rows of TQ_F32, TQ_F16 or TQ_BF16 elements, row r at
+ * element r * stride, its heads contiguous, strides multiples of 8 elements and at
+ * least a row.
+ * ------------------------------------------------------------------------ */
+
+/* Which elements of a head turn together, as pair j of rot_dim / 2:
+ * HALF: j and j + rot_dim / 2; INTERLEAVED: 2 j and 2 j + 1. */
+typedef enum { TQ_ROPE_HALF = 0, TQ_ROPE_INTERLEAVED = 1 } tq_rope_layout;
+
+/* Frequencies f_j (radians per position) of pair j, with f0_j = base^(-2 j / rot_dim):
+ *   PLAIN      f0_j
+ *   LINEAR     f0_j / factor
+ *   BASE       those of the base  base * factor^(rot_dim / (rot_dim - 2))   (rot_dim > 2)
+ *   ROTATIONS  w f0_j + (1 - w) f0_j / factor,  w = clamp((n_j - beta_slow) / (beta_fast - beta_slow), 0, 1),
+ *              n_j = original_len f0_j / (2 pi): how often the pair turns within original_len
+ *   PAIRS      the same with w = 1 - clamp((j - lo) / (hi - lo), 0, 1): by the pair's number between
+ *              lo = max(floor(j_fast), 0) and hi = max(min(ceil(j_slow), rot_dim - 1), lo), j_b the number (not a
+ *              whole one) of the pair that turns beta_b times within original_len (where lo = hi, hi is 0.001 more)
+ * ROTATIONS and PAIRS are the two usual forms of interpolation by parts (Peng et al., "YaRN: Efficient Context
+ * Window Extension of Large Language Models", 2023). */
+typedef enum {
+  TQ_ROPE_PLAIN = 0, TQ_ROPE_LINEAR = 1, TQ_ROPE_BASE = 2, TQ_ROPE_ROTATIONS = 3, TQ_ROPE_PAIRS = 4
+} tq_rope_kind;
+
+typedef struct tq_rope_scaling {
+  int32_t kind;            /* tq_rope_kind */
+  double factor;           /* > 0; not read by PLAIN */
+  double original_len;     /* > 0      } ROTATIONS and */
+  double beta_fast;        /* > beta_slow } PAIRS      */
+  double beta_slow;        /* > 0      } only          */
+} tq_rope_scaling;
+
+/* A rotation.  turns[j] is pair j's frequency in 2^-64 of a turn per position, so that position p times it,
+ * modulo 2^64, is the angle, reduced exactly however far the position. */
+typedef struct tq_rope {
+  int32_t rot_dim;         /* even: the first rot_dim elements of a head turn, the others pass */
+  int32_t layout;          /* tq_rope_layout */
+  float magnitude;         /* factor on the elements that turn (1: none) */
+  const uint64_t *turns;   /* device [rot_dim / 2] */
+} tq_rope;
+
+/* Host only.  The f_j of a scaling (NULL: PLAIN) in freqs [rot_dim / 2], and in *magnitude its usual factor: PAIRS
+ * with factor > 1 gives 0.1 ln(factor) + 1, everything else 1.  rot_dim: even, 2 .. 256; base > 0 (PAIRS:
+ * > 1).  Errors: TQ_ERR_INVALID_ARG. */
+tq_status tq_rope_frequencies(int rot_dim, double base, const tq_rope_scaling *scaling, double *freqs,
+                              float *magnitude);
+
+/* Host only.  turns[j] of n finite frequencies (any sign and size): freqs[j] / (2 pi) modulo 1, in 2^-64.
+ * Errors: TQ_ERR_INVALID_ARG. */
+tq_status tq_rope_turns(const double *freqs, int n, uint64_t *turns);
+
+/* One tensor of head rows of a call. */
+typedef struct tq_head_rows {
+  const void *src;          /* device */
+  int64_t src_stride;       /* elements between rows */
+  void *dst;                /* device; may be src, with the same stride */
+  int64_t dst_stride;
+  const float *norm_weight; /* device f32 [head_dim], or NULL: no norm */
+  int32_t n_heads;
+} tq_head_rows;
+
+/* Rotary positions of query and key rows, one launch.  For every row with a position p >= 0 and every head x:
+ *   y = x                                             without norm_weight,
+ *   y_i = norm_weight_i x_i / sqrt(mean(x^2) + eps)   with it (the mean over the head; a head of zeros stays one);
+ *   pair (a, b) of y turns by t_j = p f_j:  a' = g (a cos t_j - b sin t_j),  b' = g (a sin t_j + b cos t_j)
+ * with g = rope->magnitude; elements from rot_dim on are y.  fp32, rounded once to `type`.  inverse: by -t_j --
+ * the gradient of the rotation, given that of its result, and for g = 1 the way back (norms are refused there).
+ * q, k      either may be NULL
+ * head_dim  multiple of 8, 8 .. 256, at least rope->rot_dim
+ * type      TQ_F32, TQ_F16 or TQ_BF16, of both tensors
+ * positions device int32 [n_rows]; -1: the row of dst is left as it was; another negative one is, too, and stores
+ *           TQ_ERR_DEVICE_CHECK in *dev_status (device int32 or NULL)
+ * A dst overlaps no src but its own, and that as a whole.
+ * Errors: TQ_ERR_INVALID_ARG, TQ_ERR_CUDA. */
+tq_status tq_rope_rows(const tq_rope *rope, const tq_head_rows *q, const tq_head_rows *k, int head_dim, int type,
+                       float eps, int inverse, const int32_t *positions, int64_t n_rows, int32_t *dev_status,
+                       tq_stream stream);
+
+/* One int8 cache (K or V), in the planes that tq_int8_prompt_attn reads:
+ *   rows   int8     [n_cells][n_kv_heads][head_dim]
+ *   scales binary16 [n_cells][n_kv_heads]
+ * head_dim: multiple of 16, 16 .. 256; n_cells * n_kv_heads below 2^32; planes 16-byte aligned.  A row stands for
+ * scale * code. */
+typedef struct tq_int8 {
+  int32_t n_kv_heads;
+  int32_t head_dim;
+  int64_t n_cells;
+  void *rows;              /* device */
+  void *scales;            /* device */
+} tq_int8;
+
+/* Quantise-on-write of K and V rows, one launch.  Row r of every KV head goes to cell slots[r]:
+ *   scale = binary16(max |x| / 127),  code_i = clamp(rint(x_i / scale), -127, 127), 0 where scale = 0
+ * (ties to even, fp32).  A NaN counts as 0, magnitudes beyond 127 * 65504 as that.
+ * k_src  device, src_type [n_rows] rows of [k->n_kv_heads][k->head_dim] (v alike); 16-byte aligned
+ * slots  device int64 [n_rows], distinct; -1 skips the row; another slot outside the cache skips it too and
+ *        stores TQ_ERR_DEVICE_CHECK in *dev_status (device int32 or NULL)
+ * Errors: TQ_ERR_INVALID_ARG, TQ_ERR_CUDA. */
+tq_status tq_int8_set_rows(const tq_int8 *k, const tq_int8 *v, const void *k_src, int64_t k_stride,
+                           const void *v_src, int64_t v_stride, int src_type, const int64_t *slots, int64_t n_rows,
+                           int32_t *dev_status, tq_stream stream);
+
+/* The values that the cells of `slots` stand for, scale * code in fp32 rounded once to dst_type; a row whose slot
+ * is -1 (or outside the cache, with the same report) is left as it was.  Errors: TQ_ERR_INVALID_ARG, TQ_ERR_CUDA. */
+tq_status tq_int8_get_rows(const tq_int8 *k, const tq_int8 *v, void *k_dst, int64_t k_stride, void *v_dst,
+                           int64_t v_stride, int dst_type, const int64_t *slots, int64_t n_rows,
+                           int32_t *dev_status, tq_stream stream);
+
+/* What a step does between its projections and its attention, in one launch: tq_rope_rows of the queries, and
+ * tq_int8_set_rows of the keys, turned as tq_rope_rows turns them but not rounded before they are quantised, and of
+ * the values as they are.  A row is written to the cache where its slot is one and its position is not negative;
+ * a query row where its position is not negative.
+ * q       may be NULL; head_dim is k->head_dim
+ * k_rows  src, src_stride and norm_weight are read; n_heads is k->n_kv_heads; dst is NULL
+ * Other arguments, results and errors as in those calls. */
+tq_status tq_int8_rope_set_rows(const tq_int8 *k, const tq_int8 *v, const tq_rope *rope, const tq_head_rows *q,
+                                const tq_head_rows *k_rows, const void *v_src, int64_t v_stride, int type, float eps,
+                                const int32_t *positions, const int64_t *slots, int64_t n_rows, int32_t *dev_status,
+                                tq_stream stream);
+
+/* Bytes of workspace of tq_int8_decode for these caches, n_q_heads query heads and n_seq sequences; 0 if they are
+ * refused.  It depends neither on lengths nor on the number of sequences.  The workspace is one of the section
+ * before: it may be shared with that section's calls, one after the other. */
+size_t tq_int8_decode_workspace(const tq_int8 *k, const tq_int8 *v, int n_q_heads, int n_seq);
+
+/* Single-query decode of a batch over int8 cells:
+ *   out[s][h] = softmax_{t < seq_len[s]}(scale * q[s][h] . k_t) v_t
+ * with k_t, v_t the values of cell  block_table[s][t / page_size] * page_size + t % page_size  and query head h
+ * reading KV head h / (n_q_heads / n_kv_heads).  Pages of one cell are lists of cells, as tq_int8_prompt_attn's
+ * cell_of_pos.
+ * page_size   a power of two, 1 .. 65536
+ * seq_len     device int32 [n_seq] (0: a zero output; beyond max_pages * page_size or below 0: cut to that range,
+ *             and TQ_ERR_DEVICE_CHECK is stored in the workspace's status word)
+ * block_table device int32 [n_seq][max_pages]; entries beyond a sequence's length are not read; a page that does not
+ *             lie in the cache as a whole reads as zero rows and stores TQ_ERR_DEVICE_CHECK
+ * q           device, q_type (TQ_F16 or TQ_BF16): row s at element s * q_stride, [n_q_heads][k->head_dim]
+ *             contiguous; 16-byte aligned, q_stride a multiple of 8
+ * out         device, q_type [n_seq][n_q_heads][v->head_dim], 16-byte aligned
+ * Widths, the head dims rounded up to 64, 128 or 256 (K, V): (64, 64), (128, 128), (256, 128), (256, 256).  Weights
+ * of binary16 results are kept to 22 bits, of bfloat16 results to 11; values are exact and sums fp32.
+ * Scores beyond 2^24 in magnitude: results are not defined.
+ * Errors: TQ_ERR_INVALID_ARG, TQ_ERR_UNSUPPORTED (widths, q_type), TQ_ERR_WORKSPACE, TQ_ERR_CUDA. */
+tq_status tq_int8_decode(const tq_int8 *k, const tq_int8 *v, int page_size, const int32_t *block_table, int max_pages,
+                         const int32_t *seq_len, int n_seq, const void *q, int q_type, int64_t q_stride,
+                         int n_q_heads, float scale, void *out, void *workspace, size_t workspace_bytes,
+                         tq_stream stream);
+
 /* Host only.  64-bit FNV-1a hash of n_bytes host bytes (offset basis
  * 0xcbf29ce484222325, prime 0x100000001b3), so that two builds' outputs can be
  * compared bit for bit from one printed number ([QSA#1821] "Measured": each

@@ -11,7 +11,8 @@ import math
 
 from . import _lib
 from ._lib import (TQ_BF16, TQ_DECODE_AUTO, TQ_DECODE_LUT, TQ_DECODE_MMA, TQ_F16, TQ_F32,
-                   TQ_TURBO2, TQ_TURBO3, TQ_TURBO4, TQError, tq_cache, tq_codebook, tq_paged4)
+                   TQ_TURBO2, TQ_TURBO3, TQ_TURBO4, TQError, tq_cache, tq_codebook, tq_head_rows, tq_int8,
+                   tq_paged4, tq_rope)
 
 QS_BYTES = {2: 32, 3: 32, 4: 64}
 
@@ -280,7 +281,7 @@ class Paged4Cache:
             _ints(self.codes, torch.uint8, (*shape, _row_width(head_dim) // 2), "codes")
             _ints(self.scales, torch.float16, (*shape, 2), "scales")
             _need(self.codes.device == self.scales.device, "tensors are on different devices")
-        self.device = self.codes.device
+        self.device, self.plane = self.codes.device, self.codes
         self.index = self.codes.get_device()
         self.c = tq_paged4(n_kv_heads, head_dim, page_size, n_pages, self.codes.data_ptr(), self.scales.data_ptr())
         self.ref = C.byref(self.c)
@@ -427,7 +428,7 @@ def _paged4_args(kc, vc, block_table, seq_len, q, maps, out, ws, stream, *extra)
         out = _made_on(stream, lambda: _T.empty((rows, heads, vc.head_dim), dtype=q.dtype, device=q.device))
     else:
         _ints(out, q.dtype, (rows, heads, vc.head_dim), "out")
-    return n_seq, max_pages, t, stride, heads, out, _stream_here(stream, kc.index, vc.codes, block_table, seq_len, q,
+    return n_seq, max_pages, t, stride, heads, out, _stream_here(stream, kc.index, vc.plane, block_table, seq_len, q,
                                                                  out, ws, *extra)
 
 
@@ -517,4 +518,211 @@ def paged4_diff_prefill(kc: Paged4Cache, vc: Paged4Cache, block_table, seq_len, 
                                      ws.data_ptr(), ws.numel(), handle)
     if st:
         _lib.check("tq_paged4_diff_prefill", st)
+    return out
+
+
+# ---- rotary positions and the int8 cache (include/tq.h, "Rotary positions, and the int8 cache's ...")
+
+_LAYOUTS = {"half": _lib.TQ_ROPE_HALF, "interleaved": _lib.TQ_ROPE_INTERLEAVED}
+_KINDS = {"plain": _lib.TQ_ROPE_PLAIN, "linear": _lib.TQ_ROPE_LINEAR, "base": _lib.TQ_ROPE_BASE,
+          "rotations": _lib.TQ_ROPE_ROTATIONS, "pairs": _lib.TQ_ROPE_PAIRS}
+
+
+class Rope:
+    """A rotation of the first rot_dim elements of a head (tq_rope), its frequencies on the device.
+
+    ``scaling``: "plain", "linear", "base", "rotations" or "pairs" (tq_rope_frequencies), with ``factor`` and, for the
+    last two, ``original_len``, ``beta_fast`` and ``beta_slow``.  ``frequencies`` (radians per position, rot_dim / 2 of
+    them) takes the place of all these.  ``magnitude``: factor on what turns (None: the scaling's own)."""
+
+    def __init__(self, rot_dim: int, base: float = 10000.0, layout: str = "half", scaling: str = "plain",
+                 factor: float = 1.0, original_len: float = 0.0, beta_fast: float = 32.0, beta_slow: float = 1.0,
+                 frequencies=None, magnitude: float | None = None, device="cuda"):
+        torch = _torch()
+        _need(layout in _LAYOUTS, f"layout: one of {', '.join(_LAYOUTS)}")
+        _need(scaling in _KINDS, f"scaling: one of {', '.join(_KINDS)}")
+        if frequencies is None:
+            s = _lib.tq_rope_scaling(_KINDS[scaling], factor, original_len, beta_fast, beta_slow)
+            frequencies, own = _lib.tq_rope_frequencies(rot_dim, base, s)
+        else:
+            own = 1.0
+            _need(rot_dim > 0 and rot_dim % 2 == 0 and len(frequencies) == rot_dim // 2,
+                  "frequencies: rot_dim / 2 of them")
+        self.rot_dim, self.layout, self.frequencies = rot_dim, layout, [float(x) for x in frequencies]
+        self.magnitude = own if magnitude is None else magnitude
+        turns = [t - (1 << 64) if t >> 63 else t for t in _lib.tq_rope_turns(self.frequencies)]
+        self.turns = torch.tensor(turns, dtype=torch.int64, device=device)      # (unsigned numbers, held as int64)
+        self.device, self.index = self.turns.device, self.turns.get_device()
+        self.c = tq_rope(rot_dim, _LAYOUTS[layout], self.magnitude, self.turns.data_ptr())
+        self.ref = C.byref(self.c)
+
+
+def _head_rows(t, shape, out, norm, what: str):
+    """tq_head_rows of rows t (and their output), and the type of both."""
+    code = _row_type(t, what)
+    norm_p = None
+    if norm is not None:
+        _ints(norm, _T.float32, (shape[2],), what + "_norm")
+        norm_p = norm.data_ptr()
+    stride = _row_stride(t, shape, what)
+    if out is None:
+        return tq_head_rows(t.data_ptr(), stride, None, 0, norm_p, shape[1]), code
+    _need(out.dtype is t.dtype, f"{what}_out has another type than {what}")
+    return tq_head_rows(t.data_ptr(), stride, out.data_ptr(), _row_stride(out, shape, what + "_out"), norm_p,
+                        shape[1]), code
+
+
+def _zeros_like_rows(stream, t):
+    return _made_on(stream, lambda: _t().zeros(t.shape, dtype=t.dtype, device=t.device))
+
+
+def _status(dev_status):
+    if dev_status is None:
+        return None
+    _ints(dev_status, _t().int32, (1,), "dev_status")
+    return dev_status.data_ptr()
+
+
+def rope_rows(rope: Rope, positions, q, k=None, q_norm=None, k_norm=None, eps: float = 1e-6, inverse: bool = False,
+              q_out=None, k_out=None, dev_status=None, stream=None):
+    """Rotary positions (device int32 [n]) of rows q [n][n_q_heads][head_dim] and, if given, k, each head RMS-normed
+    before where q_norm / k_norm (float32 [head_dim]) are given.  Rows may be strided, and q_out may be q (in place).
+    Rows whose position is -1 stay as they were (new outputs: zeros).  ``inverse`` turns the other way: the gradient.
+    -> q_out, or (q_out, k_out) with k."""
+    _need(q.dim() == 3 and (k is None or k.dim() == 3), "rows: [n][heads][head_dim]")
+    n, _, d = q.shape
+    _ints(positions, _t().int32, (n,), "positions")
+    q_out = _zeros_like_rows(stream, q) if q_out is None else q_out
+    qr, code = _head_rows(q, (n, q.shape[1], d), q_out, q_norm, "q")
+    kr = None
+    if k is not None:
+        _need(k.dtype is q.dtype, "q and k have different types")
+        k_out = _zeros_like_rows(stream, k) if k_out is None else k_out
+        kr = _head_rows(k, (n, k.shape[1], d), k_out, k_norm, "k")[0]
+    else:
+        _need(k_norm is None and k_out is None, "k_norm and k_out go with k")
+    status = _status(dev_status)
+    handle = _stream_here(stream, rope.index, positions, q, k, q_out, k_out, q_norm, k_norm, dev_status)
+    st = _lib.tq_rope_rows(rope.ref, qr, kr, d, code, eps, inverse, positions.data_ptr(), n, status, handle)
+    if st:
+        _lib.check("tq_rope_rows", st)
+    return q_out if k is None else (q_out, k_out)
+
+
+class Int8Cache:
+    """Planes of one int8 cache (K or V): rows int8 [n_cells][n_kv_heads][head_dim] and scales float16
+    [n_cells][n_kv_heads], those of int8_prompt_attn."""
+
+    def __init__(self, n_kv_heads: int, head_dim: int, n_cells: int, device="cuda", _planes=None):
+        torch = _torch()
+        _need(n_kv_heads > 0 and n_cells > 0 and 0 < head_dim <= 256 and head_dim % 16 == 0 and
+              n_kv_heads <= 65536 and n_cells * n_kv_heads < 1 << 32,
+              "int8 cache: head_dim a multiple of 16 up to 256, n_cells * n_kv_heads below 2^32")
+        self.n_kv_heads, self.head_dim, self.n_cells = n_kv_heads, head_dim, n_cells
+        if _planes is None:
+            self.rows = torch.zeros((n_cells, n_kv_heads, head_dim), dtype=torch.int8, device=device)
+            self.scales = torch.zeros((n_cells, n_kv_heads), dtype=torch.float16, device=device)
+        else:
+            self.rows, self.scales = _planes
+            _ints(self.rows, torch.int8, (n_cells, n_kv_heads, head_dim), "rows")
+            _ints(self.scales, torch.float16, (n_cells, n_kv_heads), "scales")
+            _need(self.rows.device == self.scales.device, "tensors are on different devices")
+        self.device, self.plane, self.index = self.rows.device, self.rows, self.rows.get_device()
+        self.c = tq_int8(n_kv_heads, head_dim, n_cells, self.rows.data_ptr(), self.scales.data_ptr())
+        self.ref = C.byref(self.c)
+
+    @classmethod
+    def from_planes(cls, rows, scales):
+        """A cache over planes that exist already."""
+        n_cells, heads, dim = rows.shape
+        return cls(heads, dim, n_cells, _planes=(rows, scales))
+
+
+def int8_set_rows(kc: Int8Cache, vc: Int8Cache, k_src, v_src, slots, dev_status=None, stream=None):
+    """Quantise rows k_src, v_src [n][n_kv_heads][head_dim] (rows may be strided) into cells ``slots`` (device int64
+    [n]; -1: not stored)."""
+    n = slots.shape[0]
+    t = _row_type(k_src, "k_src")
+    _need(v_src.dtype is k_src.dtype, "k_src and v_src have different types")
+    status = _rows_status(slots, n, dev_status)
+    ks = _row_stride(k_src, (n, kc.n_kv_heads, kc.head_dim), "k_src")
+    vs = _row_stride(v_src, (n, vc.n_kv_heads, vc.head_dim), "v_src")
+    stream = _stream_here(stream, kc.index, vc.rows, k_src, v_src, slots, dev_status)
+    st = _lib.tq_int8_set_rows(kc.ref, vc.ref, k_src.data_ptr(), ks, v_src.data_ptr(), vs, t, slots.data_ptr(), n,
+                               status, stream)
+    if st:
+        _lib.check("tq_int8_set_rows", st)
+
+
+def int8_get_rows(kc: Int8Cache, vc: Int8Cache, slots, dtype=None, k_out=None, v_out=None, dev_status=None,
+                  stream=None):
+    """The values that cells ``slots`` stand for: (k, v) [n][n_kv_heads][head_dim] of ``dtype`` (default: that of a given
+    output, else float16).  Rows whose slot is -1 stay as they were (new outputs: zeros)."""
+    n = slots.shape[0]
+    given = k_out if k_out is not None else v_out
+    dtype = dtype or (_t().float16 if given is None else given.dtype)
+    make = lambda c: _made_on(stream, lambda: _t().zeros((n, c.n_kv_heads, c.head_dim), dtype=dtype,  # noqa: E731
+                                                         device=slots.device))
+    k_out = make(kc) if k_out is None else k_out
+    v_out = make(vc) if v_out is None else v_out
+    t = _row_type(k_out, "k_out")
+    _need(v_out.dtype is k_out.dtype and dtype is k_out.dtype, "k_out, v_out and dtype differ")
+    status = _rows_status(slots, n, dev_status)
+    ks = _row_stride(k_out, (n, kc.n_kv_heads, kc.head_dim), "k_out")
+    vs = _row_stride(v_out, (n, vc.n_kv_heads, vc.head_dim), "v_out")
+    stream = _stream_here(stream, kc.index, vc.rows, k_out, v_out, slots, dev_status)
+    st = _lib.tq_int8_get_rows(kc.ref, vc.ref, k_out.data_ptr(), ks, v_out.data_ptr(), vs, t, slots.data_ptr(), n,
+                               status, stream)
+    if st:
+        _lib.check("tq_int8_get_rows", st)
+    return k_out, v_out
+
+
+def int8_rope_set_rows(kc: Int8Cache, vc: Int8Cache, rope: Rope, positions, q, k_src, v_src, slots, q_norm=None,
+                       k_norm=None, eps: float = 1e-6, q_out=None, dev_status=None, stream=None):
+    """A step's rows in one launch: q [n][n_q_heads][head_dim] (or None) as rope_rows, k_src and v_src as
+    int8_set_rows, the keys normed and turned before.  Rows without a position or a slot (-1) are not stored.
+    -> q_out (None without q); it may be q."""
+    n = slots.shape[0]
+    t = _row_type(k_src, "k_src")
+    _need(v_src.dtype is k_src.dtype and (q is None or q.dtype is k_src.dtype), "q, k_src and v_src have different types")
+    status = _rows_status(slots, n, dev_status)
+    _ints(positions, _T.int32, (n,), "positions")
+    qr = None
+    if q is not None:
+        _need(q.dim() == 3, "q: [n][heads][head_dim]")
+        q_out = _zeros_like_rows(stream, q) if q_out is None else q_out
+        qr = _head_rows(q, (n, q.shape[1], kc.head_dim), q_out, q_norm, "q")[0]
+    else:
+        _need(q_norm is None and q_out is None, "q_norm and q_out go with q")
+    kr = _head_rows(k_src, (n, kc.n_kv_heads, kc.head_dim), None, k_norm, "k_src")[0]
+    vs = _row_stride(v_src, (n, vc.n_kv_heads, vc.head_dim), "v_src")
+    handle = _stream_here(stream, kc.index, vc.rows, rope.turns, positions, q, k_src, v_src, slots, q_out, q_norm,
+                          k_norm, dev_status)
+    st = _lib.tq_int8_rope_set_rows(kc.ref, vc.ref, rope.ref, qr, kr, v_src.data_ptr(), vs, t, eps,
+                                    positions.data_ptr(), slots.data_ptr(), n, status, handle)
+    if st:
+        _lib.check("tq_int8_rope_set_rows", st)
+    return q_out
+
+
+def int8_decode_workspace(kc: Int8Cache, vc: Int8Cache, n_heads: int, n_seq: int) -> int:
+    """Bytes of workspace of int8_decode."""
+    return _lib.tq_int8_decode_workspace(kc.ref, vc.ref, n_heads, n_seq)
+
+
+def int8_decode(kc: Int8Cache, vc: Int8Cache, block_table, seq_len, q, scale: float | None = None, page_size: int = 1,
+                out=None, ws=None, stream=None):
+    """One query row per sequence: q [n_seq][n_q_heads][Dk] (float16 or bfloat16, rows may be strided) over the
+    seq_len[s] cells (device int32) that block_table[s] names, in pages of page_size cells (1: a list of cells)
+    -> [n_seq][n_q_heads][Dv] of q's type."""
+    n_seq, max_pages, t, stride, heads, out, handle = _paged4_args(kc, vc, block_table, seq_len, q, 1, out, ws, stream)
+    _need(q.shape[0] == n_seq, "q: one row per sequence")
+    scale = 1.0 / math.sqrt(kc.head_dim) if scale is None else scale
+    if ws is None:
+        ws = _made_on(stream, lambda: _paged4_ws(int8_decode_workspace(kc, vc, heads, n_seq), q.device))
+    st = _lib.tq_int8_decode(kc.ref, vc.ref, page_size, block_table.data_ptr(), max_pages, seq_len.data_ptr(), n_seq,
+                             q.data_ptr(), t, stride, heads, scale, out.data_ptr(), ws.data_ptr(), ws.numel(), handle)
+    if st:
+        _lib.check("tq_int8_decode", st)
     return out

@@ -45,6 +45,29 @@ class tq_paged4(C.Structure):
                 ("n_pages", C.c_int32), ("codes", C.c_void_p), ("scales", C.c_void_p)]
 
 
+TQ_ROPE_HALF, TQ_ROPE_INTERLEAVED = 0, 1
+TQ_ROPE_PLAIN, TQ_ROPE_LINEAR, TQ_ROPE_BASE, TQ_ROPE_ROTATIONS, TQ_ROPE_PAIRS = 0, 1, 2, 3, 4
+
+
+class tq_rope_scaling(C.Structure):
+    _fields_ = [("kind", C.c_int32), ("factor", C.c_double), ("original_len", C.c_double), ("beta_fast", C.c_double),
+                ("beta_slow", C.c_double)]
+
+
+class tq_rope(C.Structure):
+    _fields_ = [("rot_dim", C.c_int32), ("layout", C.c_int32), ("magnitude", C.c_float), ("turns", C.c_void_p)]
+
+
+class tq_head_rows(C.Structure):
+    _fields_ = [("src", C.c_void_p), ("src_stride", C.c_int64), ("dst", C.c_void_p), ("dst_stride", C.c_int64),
+                ("norm_weight", C.c_void_p), ("n_heads", C.c_int32)]
+
+
+class tq_int8(C.Structure):
+    _fields_ = [("n_kv_heads", C.c_int32), ("head_dim", C.c_int32), ("n_cells", C.c_int64), ("rows", C.c_void_p),
+                ("scales", C.c_void_p)]
+
+
 class TQError(RuntimeError):
     def __init__(self, fn: str, status: int):
         self.status = status
@@ -123,6 +146,21 @@ _SIGS = {
     "tq_paged4_diff_prefill": (C.c_int, [C.POINTER(tq_paged4), C.POINTER(tq_paged4), _P, C.c_int, _P, _P, C.c_int, _P,
                                          C.c_int, C.c_int64, C.c_int64, C.c_int, C.c_int64, C.c_int64, _P, _P,
                                          C.c_float, C.c_float, C.c_float, C.c_int, _P, _P, C.c_size_t, _P]),
+    "tq_rope_frequencies": (C.c_int, [C.c_int, C.c_double, C.POINTER(tq_rope_scaling), C.POINTER(C.c_double),
+                                      C.POINTER(C.c_float)]),
+    "tq_rope_turns": (C.c_int, [C.POINTER(C.c_double), C.c_int, C.POINTER(C.c_uint64)]),
+    "tq_rope_rows": (C.c_int, [C.POINTER(tq_rope), C.POINTER(tq_head_rows), C.POINTER(tq_head_rows), C.c_int, C.c_int,
+                               C.c_float, C.c_int, _P, C.c_int64, _P, _P]),
+    "tq_int8_set_rows": (C.c_int, [C.POINTER(tq_int8), C.POINTER(tq_int8), _P, C.c_int64, _P, C.c_int64, C.c_int, _P,
+                                   C.c_int64, _P, _P]),
+    "tq_int8_get_rows": (C.c_int, [C.POINTER(tq_int8), C.POINTER(tq_int8), _P, C.c_int64, _P, C.c_int64, C.c_int, _P,
+                                   C.c_int64, _P, _P]),
+    "tq_int8_rope_set_rows": (C.c_int, [C.POINTER(tq_int8), C.POINTER(tq_int8), C.POINTER(tq_rope),
+                                        C.POINTER(tq_head_rows), C.POINTER(tq_head_rows), _P, C.c_int64, C.c_int,
+                                        C.c_float, _P, _P, C.c_int64, _P, _P]),
+    "tq_int8_decode_workspace": (C.c_size_t, [C.POINTER(tq_int8), C.POINTER(tq_int8), C.c_int, C.c_int]),
+    "tq_int8_decode": (C.c_int, [C.POINTER(tq_int8), C.POINTER(tq_int8), C.c_int, _P, C.c_int, _P, C.c_int, _P, C.c_int,
+                                 C.c_int64, C.c_int, C.c_float, _P, _P, C.c_size_t, _P]),
     # test hooks (include/tq_testing.h)
     "tq_testing_paged4_few_grid": (C.c_int, [C.c_int, C.c_int, C.c_int, C.c_int, C.c_int, C.POINTER(C.c_int),
                                              C.POINTER(C.c_int)]),
@@ -298,3 +336,27 @@ tq_paged4_prefill_workspace = lib.tq_paged4_prefill_workspace
 tq_paged4_prefill = lib.tq_paged4_prefill
 tq_paged4_diff_decode = lib.tq_paged4_diff_decode
 tq_paged4_diff_prefill = lib.tq_paged4_diff_prefill
+
+
+def tq_rope_frequencies(rot_dim: int, base: float, scaling: tq_rope_scaling | None = None):
+    """-> (frequencies [rot_dim / 2], magnitude)"""
+    f, m = (C.c_double * max(rot_dim // 2, 1))(), C.c_float()
+    check("tq_rope_frequencies", lib.tq_rope_frequencies(rot_dim, base, None if scaling is None else C.byref(scaling), f,
+                                                         C.byref(m)))
+    return list(f), m.value
+
+
+def tq_rope_turns(freqs):
+    n = len(freqs)
+    t = (C.c_uint64 * max(n, 1))()
+    check("tq_rope_turns", lib.tq_rope_turns((C.c_double * max(n, 1))(*[float(x) for x in freqs]), n, t))
+    return list(t)[:n]
+
+
+# (caches, rotations and head rows as references, everything else passed through)
+tq_rope_rows = lib.tq_rope_rows
+tq_int8_set_rows = lib.tq_int8_set_rows
+tq_int8_get_rows = lib.tq_int8_get_rows
+tq_int8_rope_set_rows = lib.tq_int8_rope_set_rows
+tq_int8_decode_workspace = lib.tq_int8_decode_workspace
+tq_int8_decode = lib.tq_int8_decode
