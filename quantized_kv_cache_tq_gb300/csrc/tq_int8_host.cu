@@ -331,6 +331,7 @@ tq_status tq_int8_decode(const tq_int8 *k, const tq_int8 *v, int page_size, cons
   a.wv = wv;
   a.bf16 = q_type == TQ_BF16;
   a.causal = 1;
+  a.n_rows_cache = k->n_cells * k->n_kv_heads;
   a.scale_log2 = scale * 1.4426950408889634f;
   return mapped(i8::launch_decode(a, static_cast<cudaStream_t>(stream)));
 }

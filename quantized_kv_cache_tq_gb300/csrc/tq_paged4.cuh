@@ -97,6 +97,7 @@ struct AttnArgs {
   int32_t line;              // prompt kernel: one line of work over the SMs (else n_split CTAs per item)
   int32_t n_split;           // prompt kernel: key-range splits per tile
   int32_t n_tiles;           // prompt kernel: upper bound of row tiles over all sequences
+  int64_t n_rows_cache;      // int8 kernel: rows of a cache plane (cells times KV heads)
 };
 
 // CTAs of a launch whose CTAs share items, `per_sm` on each SM: each has an arrival counter in the workspace's head.
