@@ -662,8 +662,8 @@ tq_status tq_int8_rope_set_rows(const tq_int8 *k, const tq_int8 *v, const tq_rop
                                 tq_stream stream);
 
 /* Bytes of workspace of tq_int8_decode for these caches, n_q_heads query heads and n_seq sequences; 0 if they are
- * refused.  It depends neither on lengths nor on the number of sequences.  The workspace is one of the section
- * before: it may be shared with that section's calls, one after the other. */
+ * refused.  It depends neither on shapes, lengths nor the number of sequences.  The workspace is one of the section
+ * before: it may be shared with that section's calls, one after the other, and is large enough for its decode calls. */
 size_t tq_int8_decode_workspace(const tq_int8 *k, const tq_int8 *v, int n_q_heads, int n_seq);
 
 /* Single-query decode of a batch over int8 cells:

@@ -5,14 +5,20 @@
 // Columns are the query heads of a KV head, eight per tensor-core tile.  The work is reading the cache once, so
 // everything is arranged around the loads:
 //
-// - A warp streams its own 16-key tiles through a private ring of cp.async stages: it waits for its own copies only,
-//   and no CTA barrier stands in the loop.  Each lane looks up one key's cell, so that pages of any size, single cells
-//   among them, cost the same; the copying lanes get the row numbers by shuffles.  Rows are swizzled by 16-byte chunks
-//   so that copies and both kinds of reads spread over the banks.
+// - A warp streams its own tiles of 32 keys (16 where rows are wide) through a private ring of cp.async stages: it waits
+//   for its own copies only, and no CTA barrier stands in the loop.  Each lane looks up one key's cell, so that pages of
+//   any size, single cells among them, serve; where a tile lies in one page its rows lie at even distances, else the
+//   copying lanes get the row numbers by shuffles.  Rows are swizzled by 16-byte chunks so that copies and both kinds of
+//   reads spread over the banks.
 // - Codes become binary16 operands exactly: (w & 0x00ff00ff) ^ 0x64806480 is the pair 1024 + (code + 128), and 1152 is
-//   taken off (three instructions for two codes).  Scores want pairs within a row: the words of a K row serve as they
-//   are, the head dim's order being free as long as q has the same.  The value operand wants pairs of neighbouring
-//   keys: two PRMT lay two rows' words side by side.
+//   taken off (two instructions for two codes, one more for the odd bytes).  Scores want pairs within a row: the words
+//   of a K row serve as they are, the head dim's order being free as long as q has the same.  The value operand wants
+//   pairs of neighbouring keys: a transposing ldmatrix over 16-bit units (two codes) delivers them so.
+//   (Codes + 128 as binary16 subnormals, 128 sum(q) and 128 sum(p) taken off at the end, save the subtractions and no
+//   time: they run on a pipe that is free.  They cost precision where a heavy key's values are near 0.)
+// - One CTA of eight warps per SM, with registers for two score tiles at a time in four chains of products: with two
+//   CTAs of 16-key tiles an SM the per-tile work (455 against 315 instructions per 16 keys) and the wait for products
+//   kept memory idle, and the CTAs of a pair ended up to 50 us apart (40 ragged sequences: 218 against 190 us).
 // - Scores: q is scaled by a power of two per column, so that its binary16 form is exact for binary16 and bfloat16
 //   inputs down to 2^-23 of the column's largest entry.
 // - The value weights p_t s^V_t are rounded to binary16: R is a running maximum of x_t + exponent(s^V_t), so the
@@ -20,10 +26,16 @@
 //   would grow by more than 2^12.  Binary16 outputs (FINE) take what that rounding left in a second product, since it
 //   would cost them nearly as much again as their own rounding.
 //
-// Split of the work as in the paged 4-bit kernel (tq_paged4_few.cuh): an item is a (sequence, KV head, column chunk),
-// its keys come in units of 64; few items of like length are cut into even pieces, else all units form one line that is
-// cut into equal shares.  CTAs that share an item leave partial results, the last to arrive merges them in the order of
-// the CTAs.
+// Split of the work.  A CTA's warps take one, two or four KV heads (1 << hs) of the same cells side by side, so that what
+// it reads of a cell lies together (40 ragged sequences 217 -> 190 us, single scattered cells 362 -> 262 us against one
+// head at a time); the warps left take every so many-th tile.  An item is a (sequence, group of heads,
+// column chunk), its keys come in units of 64.  Nothing about lengths is needed on the host: every CTA works its share
+// out from the device's lengths.
+// - Few items of like length: each is cut into as many pieces as there are CTAs per item, and a CTA has one piece.
+// - Else the items' units form one line that is cut into equal shares, one per CTA, however ragged the batch is; taking
+//   up an item counts as SET units.
+// An item that several CTAs share leaves partial results (R, sum, values) in the workspace, a CTA's first and last item
+// at most, and the last CTA to arrive merges them in the order of the CTAs, so that a repeated call gives the same bits.
 #pragma once
 
 #include <math.h>
@@ -38,11 +50,19 @@ namespace i8 {
 
 using p4::AttnArgs;
 using p4::RAISE;
-using p4::UNIT;
 
-constexpr int TILE = 16;              // keys per warp tile
+constexpr int UNIT = 64;              // keys per unit of work
 constexpr int MIN_PIECE = 2;          // units of a piece at least: one tile for each of eight warps
-constexpr int SET = p4::SETUP;         // units of work that an item costs besides its keys
+constexpr int SET = 6;                // units' worth of work that an item costs besides its keys
+// Heads side by side, two choices.  A share of few units has little to gain, and more heads a CTA means fewer CTAs per
+// head's keys (a sequence of 700 cells over 16-cell pages 8.5 us with one head at a time, 9.2 with two).  And the CTA
+// that merges an item reads all its partial results (a sequence of 32768 cells 21.2 us with 19 of one head, 24.4 with 40
+// of two).
+constexpr int LONG = 8;               // units of a share at least
+constexpr int MERGED = 72;            // partial results of a head, times heads, at most
+
+// Heads side by side whose partial results a CTA has room for in the workspace: 4 Ki values of fragments.
+constexpr int part_heads(int wv, int nt) { return 512 / (wv * nt) < 4 ? 512 / (wv * nt) : 4; }
 
 template <int WK, int WV, int NT, bool FINE>
 struct Cfg {
@@ -51,62 +71,129 @@ struct Cfg {
   static constexpr int NW = 8;
   static constexpr int THREADS = NW * 32;
   static constexpr int NC = 8 * NT;                       // columns
-  static constexpr int CTAS = NT * (4 * MT + 2 * KS) <= 48 ? 2 : 1;     // per SM, by the registers
-  // one stage: K rows, V rows, per key (K scale's word, V scale's word, selector of the half, -)
+  static constexpr int TILE = WK + WV <= 256 ? 32 : 16;   // keys per warp tile
+  static constexpr int HALVES = TILE / 16;
+  // one stage: K rows, V rows, the words of the K and V scales, the halves of these that count
   static constexpr int K_BYTES = TILE * WK, V_BYTES = TILE * WV;
   static constexpr int SC = K_BYTES + V_BYTES;
-  static constexpr int STAGE = SC + TILE * 16;
+  static constexpr int STAGE = (SC + TILE * 12 + 127) / 128 * 128;
+  static constexpr int PREP = TILE * 16;                  // a warp's unpacked scales of one tile
   static constexpr int MERGE = NW * NT * MT * 512 + NW * NC * 8 + NC * 8;       // CTA merge, in the same place
-  static constexpr int BUDGET = (CTAS == 2 ? 111 : 222) * 1024;
-  static constexpr int FIT = BUDGET / (NW * STAGE);
+  static constexpr int FIT = (222 * 1024 / NW - PREP) / STAGE;
   static constexpr int STAGES = FIT > 4 ? 4 : FIT;
-  static constexpr int RING = NW * STAGES * STAGE;
+  static constexpr int RING = NW * (STAGES * STAGE + PREP);
   static constexpr int SMEM = RING > MERGE ? RING : MERGE;
-  static constexpr int PART = 2 * NC + NT * MT * 128;     // a partial result: (R, l) of every column, then fragments
-  // the grid: all CTAs that the SMs hold, as far as the merge of an item that every one of them shares finds room
-  static constexpr int merge_bytes(int ctas) { return ctas * NC * 8 + THREADS * 16; }
+  static constexpr int PART = 2 * NC + NT * MT * 128;     // a head's partial result: (R, l) of every column, then fragments
+  static constexpr int HEADS = part_heads(WV, NT);        // heads side by side at most
+  // A merge: (weight, sum) of every CTA and column, and the fragments of one CTA at least.  The grid: one CTA per SM, as
+  // far as the merge of an item that every one of them shares finds room.
+  static constexpr int merge_bytes(int ctas) { return ctas * NC * 8 + NT * MT * 512; }
   static constexpr int grid(int sms) {
-    const int room = (SMEM - THREADS * 16) / (NC * 8), fit = room < p4::kMaxCtas ? room : p4::kMaxCtas;
-    return sms < (fit + CTAS - 1) / CTAS ? sms * CTAS : fit;
+    const int room = (SMEM - NT * MT * 512) / (NC * 8), fit = room < p4::kMaxCtas ? room : p4::kMaxCtas;
+    return sms < fit ? sms : fit;
   }
   static_assert(STAGES >= 2 && STAGE % 128 == 0, "stages");
+  static_assert(HEADS * PART <= 4096 + 128, "partial results");
+  static_assert(2 * MERGED * NC * 8 + HEADS * NT * MT * 512 <= SMEM, "merge of heads side by side");
 };
 
 // Byte offset of 16-byte chunk c of row r.  K: one lane quad reads four chunks of a row, eight lanes those of rows r and
-// r + 1, which the turn of odd rows by four chunks puts on eight different places.  V: eight lanes read two neighbouring
-// chunks of rows 0, 2, 4 and 6 (rows of 64 bytes: half chunks, two rows a line).
+// r + 1, which the turn of odd rows by four chunks puts on eight different places.  V: a matrix read takes one chunk of
+// eight rows.
 template <int W>
 __device__ __forceinline__ uint32_t k_chunk(int r, int c) {
   return W == 64 ? r * 64 + c * 16 : r * W + ((c ^ ((r & 1) << 2)) * 16);
 }
 template <int W>
 __device__ __forceinline__ uint32_t v_chunk(int r, int c) {
-  return W == 64 ? (r >> 1) * 128 + (((((r & 1) << 2) + c) ^ (r & 6)) * 16) : r * W + ((c ^ (r & 6)) * 16);
+  return W == 64 ? (r >> 1) * 128 + (((((r & 1) << 2) + c) ^ ((r >> 1) & 3)) * 16) : r * W + ((c ^ (r & 7)) * 16);
 }
+// The turn's share of copy i in a V chunk's place: its rows are 32 / (W / 16) i and on.
+template <int W>
+__device__ __forceinline__ constexpr uint32_t v_turn(int i) { return W == 64 ? 0u : ((i * (512 / W)) & 7) * 16u; }
 
-// Codes in bytes 0 and 2 (even) or 1 and 3 (odd) of a word as a pair of binary16 numbers.
-__device__ __forceinline__ uint32_t codes_at(uint32_t w) {
+// Codes in bytes 0 and 2 of a word as a pair of binary16 numbers (of w >> 8: those in bytes 1 and 3).
+__device__ __forceinline__ uint32_t codes_of(uint32_t w) {
   const uint32_t x = (w & 0x00ff00ffu) ^ 0x64806480u;                     // 1024 + 128 + code
   const __half2 h = __hsub2(*reinterpret_cast<const __half2 *>(&x), __float2half2_rn(1152.f));
   return *reinterpret_cast<const uint32_t *>(&h);
 }
-__device__ __forceinline__ uint32_t even_codes(uint32_t w) { return codes_at(w); }
-__device__ __forceinline__ uint32_t odd_codes(uint32_t w) { return codes_at(w >> 8); }
+
+__device__ __forceinline__ const uint8_t *ahead(const uint8_t *p, uint32_t step, int i) {
+  uint64_t r;
+  asm("mad.wide.u32 %0, %1, %2, %3;" : "=l"(r) : "r"(step), "r"(i), "l"(reinterpret_cast<uint64_t>(p)));
+  return reinterpret_cast<const uint8_t *>(r);
+}
 
 __device__ __forceinline__ float scale_of(uint32_t word, uint32_t sel) {
   return __half2float(__ushort_as_half(static_cast<uint16_t>(prmt_b32(word, 0u, sel))));
 }
 
+// a / b (b > 0, a >= 0): of numbers below 2^32, as nearly all are, in 32 bits
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  if ((static_cast<uint64_t>(a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
+// A sequence's length as the call takes it.
+__device__ __forceinline__ int length_of(const AttnArgs &a, int s, bool report) {
+  const long long cap = static_cast<long long>(a.max_pages) << a.page_shift;
+  const int len = a.seq_len[s];
+  if (len >= 0 && len <= cap) return len;
+  if (report) set_status(a.status, TQ_ERR_DEVICE_CHECK);
+  return len < 0 ? 0 : static_cast<int>(cap);
+}
+
+// What lies before this thread's sequence s0 + tid on a line where every sequence with cells takes its units and SET
+// more: `units` of them, and `seqs` such sequences.  Moves `at` past all sequences of the block.
+struct Line {
+  long long units;
+  int seqs, longest;
+};
+template <int NW>
+__device__ __forceinline__ void scan_lengths(const AttnArgs &a, int s0, Line *sums, bool report, Line &at, Line &before,
+                                             int &own) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  own = s0 + tid < a.n_seq ? (length_of(a, s0 + tid, report) + UNIT - 1) / UNIT : 0;
+  Line x = {own > 0 ? own + SET : 0, own > 0 ? 1 : 0, own};
+  const Line v = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long u = __shfl_up_sync(0xffffffffu, x.units, o);
+    const int n = __shfl_up_sync(0xffffffffu, x.seqs, o);
+    if (lane >= o) {
+      x.units += u;
+      x.seqs += n;
+    }
+  }
+  x.longest = __reduce_max_sync(0xffffffffu, own);
+  __syncthreads();
+  if (lane == 31) sums[warp] = x;
+  __syncthreads();
+  Line all = {0, 0, 0};
+#pragma unroll
+  for (int w = 0; w < NW; ++w) {
+    if (w == warp) {
+      x.units += all.units;
+      x.seqs += all.seqs;
+    }
+    all.units += sums[w].units;
+    all.seqs += sums[w].seqs;
+    all.longest = max(all.longest, sums[w].longest);
+  }
+  before = {at.units + x.units - v.units, at.seqs + x.seqs - v.seqs, 0};
+  at = {at.units + all.units, at.seqs + all.seqs, max(at.longest, all.longest)};
+}
+
 template <int WK, int WV, int NT, bool FINE>
-__global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, Cfg<WK, WV, NT, FINE>::CTAS)
+__global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, 1)
     decode_kernel(const AttnArgs a) {
   using C = Cfg<WK, WV, NT, FINE>;
   using namespace p4::few;
-  constexpr int NW = C::NW, MT = C::MT, NC = C::NC;
+  constexpr int NW = C::NW, MT = C::MT, NC = C::NC, TILE = C::TILE;
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ Scan s_scan[NW];
-  __shared__ int s_longest[NW];
-  __shared__ float s_l[NC];
+  __shared__ Line s_scan[NW];
+  __shared__ float s_l[NW * NC];
   __shared__ long long s_pre;
   __shared__ int s_seq, s_last;
 
@@ -115,39 +202,67 @@ __global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, Cfg<WK, WV, NT
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");     // nothing that earlier launches write is read before this
 
-  // ---- this CTA's share of the work: a piece of an item, or the line's units [cur, end)
-  Scan sum = {0, 0};
-  long long lo = 0, hi = 0, first = 0;
-  int longest = 0;
-  for (int s0 = 0; s0 < a.n_seq; s0 += C::THREADS)
-    scan_chunk<NC, NW>(a, s0, s_scan, blockIdx.x == 0, sum, lo, hi, first, longest);
-  longest = __reduce_max_sync(0xffffffffu, longest);
-  if (lane == 0) s_longest[warp] = longest;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < NW; ++w) longest = max(longest, s_longest[w]);
-  const long long total = sum.line;
-  const int pieces = sum.item > 0 && sum.item <= gridDim.x ? gridDim.x / static_cast<int>(sum.item) : 0;   // per item
+  // ---- the work, as a line of units
+  Line sum = {0, 0, 0}, before = {0, 0, 0};
+  int own = 0;
+  for (int s0 = 0; s0 < a.n_seq; s0 += C::THREADS) scan_lengths<NW>(a, s0, s_scan, blockIdx.x == 0, sum, before, own);
+  const int chunks = (a.group + NC - 1) / NC, grid = gridDim.x;
+  const long long line1 = sum.units * chunks;             // (of one KV head)
+  // Heads side by side: as many as the KV heads divide into, while the CTAs' shares stay LONG and whoever merges the
+  // longest sequence's item has at most MERGED partial results to read (one from each CTA's share, and one more at
+  // either end).
+  int hs = 0;
+  while ((2 << hs) <= C::HEADS && a.n_kv_heads % (2 << hs) == 0) {
+    const long long n = a.n_kv_heads >> (hs + 1), line = n * line1;
+    if (line < static_cast<long long>(LONG) * grid ||
+        static_cast<long long>(sum.longest) * grid > ((MERGED >> (hs + 1)) - 2) * line)
+      break;
+    ++hs;
+  }
+  const int per_seq = (a.n_kv_heads >> hs) * chunks;      // items of a sequence
+  const long long total = sum.units * per_seq, items = static_cast<long long>(sum.seqs) * per_seq;
+  const int pieces = items > 0 && items <= grid ? grid / static_cast<int>(items) : 0;   // per item
   // (a line costs a CTA the taking up of a second item, which the even pieces may then take longer)
-  const bool even = pieces > 0 && static_cast<long long>(max(MIN_PIECE, (longest + pieces - 1) / pieces) - SET) *
-                                          static_cast<long long>(gridDim.x) <= total;
-  const long long n_work = even ? pieces * sum.item : min(static_cast<long long>(gridDim.x), total);
-  const bool works = blockIdx.x < n_work;
+  const int least = max(1, MIN_PIECE >> hs);              // units of a piece: one tile for each warp
+  const bool even = pieces > 0 && static_cast<long long>(max(least, (sum.longest + pieces - 1) / pieces) - SET) * grid <= total;
+  const int n_work = static_cast<int>(even ? pieces * items : min(static_cast<long long>(grid), total));     // shares
+  // piece o of the line: where it begins, and which one unit x belongs to
+  auto start_of = [&](int o) { return quotient(o * total, n_work); };
+  auto piece_of = [&](long long x) { return static_cast<int>(quotient((x + 1) * n_work - 1, total)); };
+
+  // ---- the warp's ring, and the lane's places in its rows
+  const int head_of = warp & ((1 << hs) - 1), tile0 = warp >> hs, tiles_by = NW >> hs;
+  const uint32_t ring = tc::smem_u32(smem) + warp * (C::STAGES * C::STAGE + C::PREP), prep = ring + C::STAGES * C::STAGE;
+  const uint32_t kc_at = k_chunk<WK>(lane / C::KCH, lane % C::KCH), vc_at = C::K_BYTES + v_chunk<WV>(lane / C::VCH, lane % C::VCH);
+  const uint32_t k_size = (lane % C::KCH) * 16 < a.dk ? 16 : 0, v_size = (lane % C::VCH) * 16 < a.dv ? 16 : 0;
+  uint32_t k_at[C::KS / 4];                     // reads: K row g, chunks t + 4 j
+#pragma unroll
+  for (int j = 0; j < C::KS / 4; ++j) k_at[j] = k_chunk<WK>(g, t + 4 * j);
+  uint32_t v_at[MT / 2];                        // matrices of keys 0-7 / 8-15 and chunks 2 j, 2 j + 1
+#pragma unroll
+  for (int j = 0; j < MT / 2; ++j) v_at[j] = C::K_BYTES + v_chunk<WV>(lane & 15, 2 * j + (lane >> 4));
+  const int page_mask = (1 << a.page_shift) - 1;
+  const uint8_t *k_base = a.k_codes + (k_size ? 16 * (lane % C::KCH) : 0), *v_base = a.v_codes + (v_size ? 16 * (lane % C::VCH) : 0);
+  // (the last scale of a plane with an odd number of them is half a word)
+  const uint32_t last_row = static_cast<uint32_t>(a.n_rows_cache - 1);
+
+  // ---- this CTA's piece: of an item (even), or the line's units [cur, end)
+  const int piece = blockIdx.x;
   long long cur = 0, end = 0, pre = 0;
   int seq = 0;
-  if (works) {
-    cur = even ? blockIdx.x / pieces : blockIdx.x * total / n_work;        // (even: an item)
-    end = even ? cur + 1 : (blockIdx.x + 1) * total / n_work;
-    Scan at = {0, 0};
+  if (piece < n_work) {
+    cur = even ? piece / pieces : start_of(piece);
+    end = even ? cur + 1 : start_of(piece + 1);
+    Line at = {0, 0, 0};
     for (int s0 = 0; s0 < a.n_seq; s0 += C::THREADS) {
-      // (a batch of one chunk still has its sums in registers)
-      if (a.n_seq > C::THREADS) scan_chunk<NC, NW>(a, s0, s_scan, false, at, lo, hi, first, longest);
-      const int s = s0 + tid;
-      if (s < a.n_seq && hi > lo) {
-        const SeqWork w = seq_work<NC>(a, s, false);
-        if (even ? first <= cur && cur < first + w.items : lo <= cur && cur < hi) {
-          s_seq = s;
-          s_pre = even ? first : lo;
+      // (a batch of one block still has its sums in registers)
+      if (a.n_seq > C::THREADS) scan_lengths<NW>(a, s0, s_scan, false, at, before, own);
+      if (own > 0) {
+        const long long first = even ? static_cast<long long>(before.seqs) * per_seq : before.units * per_seq;
+        const long long n = even ? per_seq : static_cast<long long>(own + SET) * per_seq;
+        if (first <= cur && cur < first + n) {
+          s_seq = s0 + tid;
+          s_pre = first;
         }
       }
     }
@@ -157,55 +272,41 @@ __global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, Cfg<WK, WV, NT
   }
   const long long share0 = cur;
 
-  // ---- the warp's ring, and the lane's places in its rows
-  const uint32_t ring = tc::smem_u32(smem) + warp * (C::STAGES * C::STAGE);
-  const uint32_t kc_at = k_chunk<WK>(lane / C::KCH, lane % C::KCH), vc_at = C::K_BYTES + v_chunk<WV>(lane / C::VCH, lane % C::VCH);
-  const uint32_t k_size = (lane % C::KCH) * 16 < a.dk ? 16 : 0, v_size = (lane % C::VCH) * 16 < a.dv ? 16 : 0;
-  uint32_t k_at[C::KS / 4];                     // reads: K row g, chunks t + 4 j
-#pragma unroll
-  for (int j = 0; j < C::KS / 4; ++j) k_at[j] = k_chunk<WK>(g, t + 4 * j);
-  const uint32_t v_at = C::K_BYTES + (WV == 64 ? v_chunk<WV>(2 * t, g >> 1) + 8 * (g & 1) : v_chunk<WV>(2 * t, g));
-  const int page_mask = (1 << a.page_shift) - 1;
-  const uint8_t *k_base = a.k_codes + (k_size ? 16 * (lane % C::KCH) : 0), *v_base = a.v_codes + (v_size ? 16 * (lane % C::VCH) : 0);
-  const uint16_t *scales = lane < TILE ? a.k_scales : a.v_scales;
-  // (the last scale of a plane with an odd number of them is half a word)
-  const uint32_t last_row = static_cast<uint32_t>(a.n_rows_cache - 1);
-
   while (cur < end) {
     // ---- one segment: units u0 .. u1 - 1 of an item, which CTAs c0 .. c0 + n_con - 1 share
-    const SeqWork w = seq_work<NC>(a, seq, false);
-    long long item, ia = 0;               // ia: the line's unit that is the item's first one
-    int u0, u1, c0, n_con;
+    const int len = length_of(a, seq, false), units = (len + UNIT - 1) / UNIT;
+    long long ia = 0;                     // the line's unit that is the item's first one
+    int item, u0, u1, c0, n_con;
     if (even) {
-      item = cur - pre;
-      const int n = max(1, min(pieces, static_cast<int>(w.units) / MIN_PIECE)), i = blockIdx.x % pieces;
+      item = static_cast<int>(cur - pre);
+      const int n = max(1, min(pieces, units / least)), i = piece % pieces;
       if (i >= n) break;
-      u0 = static_cast<int>(i * w.units / n);
-      u1 = static_cast<int>((i + 1) * w.units / n);
-      c0 = blockIdx.x - i;
+      u0 = static_cast<int>(static_cast<long long>(i) * units / n);
+      u1 = static_cast<int>(static_cast<long long>(i + 1) * units / n);
+      c0 = piece - i;
       n_con = n;
       cur = end;
     } else {
-      const long long per = w.units + SET;
-      if (w.units == 0 || cur - pre >= per * w.items) {
-        if (w.units > 0) pre += per * w.items;
+      const int per = units + SET;
+      if (units == 0 || cur - pre >= static_cast<long long>(per) * per_seq) {
+        if (units > 0) pre += static_cast<long long>(per) * per_seq;
         ++seq;
         continue;
       }
-      item = (cur - pre) / per;
-      const int r = static_cast<int>((cur - pre) - item * per), stop = static_cast<int>(min(per, r + (end - cur)));
+      item = static_cast<int>(quotient(cur - pre, per));
+      const int r = static_cast<int>((cur - pre) - static_cast<long long>(item) * per);
+      const int stop = static_cast<int>(min(static_cast<long long>(per), r + (end - cur)));
       cur += stop - r;
       u0 = max(0, r - SET);
       u1 = max(0, stop - SET);
       if (u1 <= u0) continue;
-      ia = pre + item * per + SET;
-      auto owner = [&](long long x) { return static_cast<int>(((x + 1) * n_work - 1) / total); };
-      c0 = owner(ia);
-      n_con = owner(ia + w.units - 1) - c0 + 1;
+      ia = pre + static_cast<long long>(item) * per + SET;
+      c0 = piece_of(ia);
+      n_con = piece_of(ia + units - 1) - c0 + 1;
     }
-    const int hv = static_cast<int>(item) / w.chunks, chunk = static_cast<int>(item) - hv * w.chunks;
+    const int h0 = (item / chunks) << hs, chunk = item % chunks, hv = h0 + head_of;
     const int c_base = chunk * NC, n_cols = min(NC, a.group - c_base);
-    const int k_begin = u0 * UNIT, k_end = min(w.len, u1 * UNIT);
+    const int k_begin = u0 * UNIT, k_end = min(len, u1 * UNIT);
     const int n_tiles = k_end > k_begin ? (k_end - k_begin + TILE - 1) / TILE : 0;
     const int32_t *table = a.block_table + static_cast<int64_t>(seq) * a.max_pages;
 
@@ -227,48 +328,81 @@ __global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, Cfg<WK, WV, NT
         }
     }
 
-    // ---- the warp's tile copies
-    auto page_of = [&](int tile) {                              // of the lane's key (both halves of a warp look up the same)
-      const int key = k_begin + tile * TILE + (lane & 15);
+    // ---- the warp's tile copies.  Numbers of rows fit 32 bits (checked on the host); all ones: no row, zeros.
+    const uint32_t kv_heads = a.n_kv_heads;
+    // Which half of its word a key's scale is: all the same for an even number of KV heads, else by the cell, whose
+    // number is even where the key's is, but for pages of one cell (odd_cells: noted with the copy).
+    const uint32_t half_sel = (hv ^ (kv_heads & lane)) & 1 ? 0x4432u : 0x4410u;
+    const bool odd_cells = (kv_heads & 1) && a.page_shift == 0;
+    auto page_of = [&](int tile) {                              // of the lane's key
+      const int key = k_begin + tile * TILE + (lane & (TILE - 1));
       return key < k_end ? __ldg(table + (key >> a.page_shift)) : -1;
     };
+    auto scales_in = [&](uint32_t row, bool ok, uint32_t st) {
+      if (TILE < 32 && lane >= TILE) return;
+      const uint32_t n = !ok ? 0 : row == last_row && !(row & 1) ? 2 : 4;
+      cp4(st + C::SC + lane * 4, a.k_scales + (row & ~1u), n);
+      cp4(st + C::SC + (TILE + lane) * 4, a.v_scales + (row & ~1u), n);
+      if (odd_cells)
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(st + C::SC + (2 * TILE + lane) * 4), "r"(row & 1 ? 0x4432u : 0x4410u) : "memory");
+    };
     auto issue = [&](int tile, int page, uint32_t st) {
-      const int key = k_begin + tile * TILE + (lane & 15);
+      const int key = k_begin + tile * TILE + (lane & (TILE - 1));
       const bool in = key < k_end, ok = in && static_cast<unsigned>(page) < static_cast<unsigned>(a.n_pages);
-      if (in && !ok) set_status(a.status, TQ_ERR_DEVICE_CHECK);
-      // (numbers of rows fit 32 bits, checked on the host; all ones: no row, zeros)
-      const uint32_t row = ok ? ((static_cast<uint32_t>(page) << a.page_shift) + (key & page_mask)) *
-                                        static_cast<uint32_t>(a.n_kv_heads) + hv
-                              : 0xffffffffu;
-      cp4(st + C::SC + (lane & 15) * 16 + (lane < TILE ? 0 : 4), scales + (ok ? row & ~1u : 0u),
-          !ok ? 0 : row == last_row && !(row & 1) ? 2 : 4);
-      if (lane < TILE)
-        asm volatile("st.shared.u32 [%0], %1;" ::"r"(st + C::SC + lane * 16 + 8), "r"(row & 1 ? 0x4432u : 0x4410u) : "memory");
+      const uint32_t row = ((static_cast<uint32_t>(page) << a.page_shift) + (key & page_mask)) * kv_heads + hv;
+      if (__all_sync(0xffffffffu, ok)) {
+        scales_in(row, true, st);
+        if (a.page_shift >= (TILE == 32 ? 5 : 4)) {             // a tile lies in one page, its rows at even distances
+          const uint32_t row0 = __shfl_sync(0xffffffffu, row, 0);
+          const uint8_t *ks = k_base + static_cast<uint64_t>(row0 + (lane / C::KCH) * kv_heads) * a.dk;
+          const uint8_t *vs = v_base + static_cast<uint64_t>(row0 + (lane / C::VCH) * kv_heads) * a.dv;
+          const uint32_t k_step = (32 / C::KCH) * kv_heads * a.dk, v_step = (32 / C::VCH) * kv_heads * a.dv;
 #pragma unroll
-      for (int i = 0; i < C::KCH / 2; ++i) {
-        const uint32_t r = __shfl_sync(0xffffffffu, row, i * (32 / C::KCH) + lane / C::KCH);
-        cp16(st + kc_at + i * 512, k_base + (r == 0xffffffffu ? 0 : static_cast<uint64_t>(r) * a.dk),
-             r == 0xffffffffu ? 0 : k_size);
-      }
+          for (int i = 0; i < TILE * C::KCH / 32; ++i) cp16(st + kc_at + i * 512, ahead(ks, k_step, i), k_size);
 #pragma unroll
-      for (int i = 0; i < C::VCH / 2; ++i) {
-        const uint32_t r = __shfl_sync(0xffffffffu, row, i * (32 / C::VCH) + lane / C::VCH);
-        // (the turn's share of i: rows of a copy lie 32 / VCH apart)
-        const uint32_t turn = WV == 64 ? 0u : ((i * (32 / C::VCH)) & 6) * 16u;
-        cp16(st + ((vc_at + i * 512) ^ turn), v_base + (r == 0xffffffffu ? 0 : static_cast<uint64_t>(r) * a.dv),
-             r == 0xffffffffu ? 0 : v_size);
+          for (int i = 0; i < TILE * C::VCH / 32; ++i) cp16(st + (vc_at ^ v_turn<WV>(i)) + i * 512, ahead(vs, v_step, i), v_size);
+        } else {
+#pragma unroll
+          for (int i = 0; i < TILE * C::KCH / 32; ++i) {
+            const uint32_t r = __shfl_sync(0xffffffffu, row, i * (32 / C::KCH) + lane / C::KCH);
+            cp16(st + kc_at + i * 512, k_base + static_cast<uint64_t>(r) * a.dk, k_size);
+          }
+#pragma unroll
+          for (int i = 0; i < TILE * C::VCH / 32; ++i) {
+            const uint32_t r = __shfl_sync(0xffffffffu, row, i * (32 / C::VCH) + lane / C::VCH);
+            cp16(st + (vc_at ^ v_turn<WV>(i)) + i * 512, v_base + static_cast<uint64_t>(r) * a.dv, v_size);
+          }
+        }
+      } else {                            // the last tile, or a page outside the cache: zeros for what is not there
+        if (in && !ok) set_status(a.status, TQ_ERR_DEVICE_CHECK);
+        scales_in(ok ? row : 0, ok, st);
+        const uint32_t mine = ok ? row : 0xffffffffu;
+#pragma unroll
+        for (int i = 0; i < TILE * C::KCH / 32; ++i) {
+          const uint32_t r = __shfl_sync(0xffffffffu, mine, i * (32 / C::KCH) + lane / C::KCH);
+          cp16(st + kc_at + i * 512, k_base + (r == 0xffffffffu ? 0 : static_cast<uint64_t>(r) * a.dk),
+               r == 0xffffffffu ? 0 : k_size);
+        }
+#pragma unroll
+        for (int i = 0; i < TILE * C::VCH / 32; ++i) {
+          const uint32_t r = __shfl_sync(0xffffffffu, mine, i * (32 / C::VCH) + lane / C::VCH);
+          cp16(st + (vc_at ^ v_turn<WV>(i)) + i * 512, v_base + (r == 0xffffffffu ? 0 : static_cast<uint64_t>(r) * a.dv),
+               r == 0xffffffffu ? 0 : v_size);
+        }
       }
     };
-    uint32_t st = ring, st_fill = ring;           // the stage read, and the one filled, next
+    uint32_t st = ring, st_fill = ring;           // the stage read next, and the one filled: the one read last
     auto next_stage = [&](uint32_t x) { return x == ring + (C::STAGES - 1) * C::STAGE ? ring : x + C::STAGE; };
+    int page[C::STAGES];                          // of the first tiles, looked up at once
+#pragma unroll
+    for (int i = 0; i < C::STAGES; ++i) page[i] = page_of(tile0 + i * tiles_by);
 #pragma unroll
     for (int i = 0; i < C::STAGES - 1; ++i) {
-      const int tile = warp + i * NW;
-      if (tile < n_tiles) issue(tile, page_of(tile), st_fill);
+      if (tile0 + i * tiles_by < n_tiles) issue(tile0 + i * tiles_by, page[i], st_fill);
       st_fill = next_stage(st_fill);
       tc::cp_async_commit();
     }
-    int page_next = page_of(warp + (C::STAGES - 1) * NW);
+    int page_next = page[C::STAGES - 1];
 
     // ---- query fragments
     uint32_t qf[NT][C::KS][2];
@@ -303,74 +437,111 @@ __global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, Cfg<WK, WV, NT
     }
 
     float acc[NT][MT][4];
-    float2 R[NT], Rs[NT], l[NT];              // of columns 2t, 2t + 1; Rs: R, or 0 as long as there is none
+    // of columns 2t, 2t + 1; Ru: R + RAISE; Rs: R, or 0 as long as there is none
+    float2 R[NT], Ru[NT], Rs[NT], l[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
       for (int i = 0; i < MT; ++i)
 #pragma unroll
         for (int c = 0; c < 4; ++c) acc[n][i][c] = 0.f;
-      R[n] = make_float2(-INFINITY, -INFINITY);
+      R[n] = Ru[n] = make_float2(-INFINITY, -INFINITY);
       Rs[n] = l[n] = make_float2(0.f, 0.f);
     }
 
-    for (int tile = warp; tile < n_tiles; tile += NW, st = next_stage(st)) {
+    for (int tile = tile0; tile < n_tiles; tile += tiles_by, st = next_stage(st)) {
       const int key0 = k_begin + tile * TILE;
       cp_wait<C::STAGES - 2>();
       __syncwarp();               // everybody's copies of this tile are there; the slot filled next was read
       {
-        const int nt = tile + (C::STAGES - 1) * NW;
+        const int nt = tile + (C::STAGES - 1) * tiles_by;
         if (nt < n_tiles) issue(nt, page_next, st_fill);
-        st_fill = next_stage(st_fill);
+        st_fill = st;
         tc::cp_async_commit();
-        page_next = page_of(nt + NW);
+        page_next = page_of(nt + tiles_by);
       }
 
-      // scores of keys g and g + 8, columns 2t and 2t + 1
-      float s[NT][4];
+      // the lane's key: its scales ready for use (V's exponent is an integer in the low bits of 2^23; 0's counts as -24)
+      if (TILE == 32 || lane < TILE) {
+        uint32_t u[2], sel = half_sel;
+        lds<1>(u, st + C::SC + lane * 4);
+        lds<1>(u + 1, st + C::SC + (TILE + lane) * 4);
+        if (odd_cells) lds<1>(&sel, st + C::SC + (2 * TILE + lane) * 4);
+        const float x = scale_of(u[1], sel);
+        sts4(prep + lane * 16, scale_of(u[0], sel), x,
+             fmaxf(__uint_as_float((__float_as_uint(fabsf(x)) >> 23) | 0x4b000000u) - 8388735.f, -24.f), 0.f);
+      }
+      __syncwarp();
+      // scores of keys g + 8 j, columns 2t and 2t + 1
+      constexpr int H = C::HALVES;
+      float s[NT][H][4];
+      {
+        float s2[NT][H][4];                 // (of every other step, so that no product waits for the one before)
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) s[n][c] = 0.f;
+          for (int hf = 0; hf < H; ++hf)
 #pragma unroll
-      for (int j = 0; j < C::KS / 4; ++j) {
-        uint32_t w0[4], w1[4];
-        lds<4>(w0, st + k_at[j]);
-        lds<4>(w1, st + k_at[j] + 8 * WK);
+            for (int c = 0; c < 4; ++c) s[n][hf][c] = s2[n][hf][c] = 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t x0 = even_codes(w0[i]), x1 = even_codes(w1[i]), x2 = odd_codes(w0[i]), x3 = odd_codes(w1[i]);
+        for (int j = 0; j < C::KS / 4; ++j) {
+          uint32_t w0[H][4], w1[H][4];
 #pragma unroll
-          for (int n = 0; n < NT; ++n) mma16816(s[n], x0, x1, x2, x3, qf[n][4 * j + i][0], qf[n][4 * j + i][1]);
+          for (int hf = 0; hf < H; ++hf) {
+            lds<4>(w0[hf], st + k_at[j] + hf * 16 * WK);
+            lds<4>(w1[hf], st + k_at[j] + (hf * 16 + 8) * WK);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int hf = 0; hf < H; ++hf) {
+              const uint32_t x0 = codes_of(w0[hf][i]), x1 = codes_of(w1[hf][i]);
+              const uint32_t x2 = codes_of(w0[hf][i] >> 8), x3 = codes_of(w1[hf][i] >> 8);
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+                mma16816((i & 1 ? s2 : s)[n][hf], x0, x1, x2, x3, qf[n][4 * j + i][0], qf[n][4 * j + i][1]);
+            }
         }
-      }
-      float ks[2], vs[2], ve[2];
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        uint32_t u[4];
-        lds<4>(u, st + C::SC + (g + 8 * r) * 16);
-        ks[r] = scale_of(u[0], u[2]);
-        vs[r] = scale_of(u[1], u[2]);
-        ve[r] = vs[r] != 0.f ? static_cast<float>(static_cast<int>(__float_as_uint(fabsf(vs[r])) >> 23) - 127) : -24.f;
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int hf = 0; hf < H; ++hf)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) s[n][hf][c] += s2[n][hf][c];
       }
-      uint32_t pb[NT][2], pl[NT][2];        // weights as B fragments [keys 0-7, 8-15], and what their rounding left
+      float4 sc[2 * H];                     // of keys g + 8 j: the scales, V's exponent
+#pragma unroll
+      for (int j = 0; j < 2 * H; ++j) sc[j] = lds4(prep + (g + 8 * j) * 16);
+      uint32_t pb[NT][2 * H], pl[NT][2 * H];      // weights as B fragments [keys 8 j ..], and what their rounding left
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        float2 x[2];
+        float2 x[2 * H];
+        float mt[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          x[r] = mul2(mul2(make_float2(ks[r], ks[r]), make_float2(s[n][2 * r], s[n][2 * r + 1])), fx[n]);
-          if (key0 + 8 * r + g >= k_end) x[r] = make_float2(-INFINITY, -INFINITY);
+        for (int j = 0; j < 2 * H; ++j) {
+          const float2 sj = make_float2(s[n][j >> 1][2 * (j & 1)], s[n][j >> 1][2 * (j & 1) + 1]);
+          x[j] = mul2(mul2(make_float2(sc[j].x, sc[j].x), sj), fx[n]);
         }
-        const float mt[2] = {fmaxf(x[0].x + ve[0], x[1].x + ve[1]), fmaxf(x[0].y + ve[0], x[1].y + ve[1])};
-        const bool raise = mt[0] > R[n].x + RAISE || mt[1] > R[n].y + RAISE;
+        if (key0 + TILE > k_end) {
+#pragma unroll
+          for (int j = 0; j < 2 * H; ++j)
+            if (key0 + 8 * j + g >= k_end) x[j] = make_float2(-INFINITY, -INFINITY);
+        }
+#pragma unroll
+        for (int j = 0; j < 2 * H; j += 2) {
+          const float2 u = add2(x[j], make_float2(sc[j].z, sc[j].z)), w = add2(x[j + 1], make_float2(sc[j + 1].z, sc[j + 1].z));
+          mt[0] = max3(mt[0], u.x, w.x);
+          mt[1] = max3(mt[1], u.y, w.y);
+        }
+        const bool raise = mt[0] > Ru[n].x || mt[1] > Ru[n].y;
         if (__any_sync(0xffffffffu, raise)) {
-          auto lift = [&](float m, float &r, float &rs, float &lo, int i) {
+          auto lift = [&](float m, float &r, float &ru, float &rs, float &lo, int i) {
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            if (m > r + RAISE) {
+            if (m > ru) {
               const float f = exp2f(r - m);             // 0 at the first raise
               r = rs = m;
+              ru = m + RAISE;
               lo *= f;
 #pragma unroll
               for (int k = 0; k < MT; ++k) {
@@ -379,53 +550,45 @@ __global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, Cfg<WK, WV, NT
               }
             }
           };
-          lift(mt[0], R[n].x, Rs[n].x, l[n].x, 0);
-          lift(mt[1], R[n].y, Rs[n].y, l[n].y, 1);
+          lift(mt[0], R[n].x, Ru[n].x, Rs[n].x, l[n].x, 0);
+          lift(mt[1], R[n].y, Ru[n].y, Rs[n].y, l[n].y, 1);
         }
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const float2 d = sub2(x[r], Rs[n]);
+        for (int j = 0; j < 2 * H; ++j) {
+          const float2 d = sub2(x[j], Rs[n]);
           const float2 p = make_float2(tc::ex2(d.x), tc::ex2(d.y));
           l[n] = add2(l[n], p);
-          const float2 wv = mul2(p, make_float2(vs[r], vs[r]));
+          const float2 wv = mul2(p, make_float2(sc[j].y, sc[j].y));
           const __half2 h = __floats2half2_rn(wv.x, wv.y);
-          pb[n][r] = transpose8(*reinterpret_cast<const uint32_t *>(&h));
+          pb[n][j] = transpose8(*reinterpret_cast<const uint32_t *>(&h));
           if (FINE) {
             const float2 left = sub2(wv, __half22float2(h));
-            pl[n][r] = transpose8(half2_bits(left.x, left.y));
+            pl[n][j] = transpose8(half2_bits(left.x, left.y));
           }
         }
       }
-      // values: m tile 2 i + e of a lane's word i holds dims 4 i + 2 e of its piece (rows g) and + 1 (rows g + 8)
-      constexpr int VW = WV == 64 ? 2 : 4, VJ = WV == 256 ? 2 : 1;         // words of a piece, pieces
+      // values: m tile c holds dims 16 c + 2 g (rows g) and + 1 (rows g + 8)
 #pragma unroll
-      for (int j = 0; j < VJ; ++j) {
-        uint32_t w0[4], w1[4], w2[4], w3[4];      // keys 2t, 2t + 1, 2t + 8, 2t + 9
-        const uint32_t at = st + v_at + j * 128;
-        const uint32_t at1 = WV == 64 ? st + (v_at ^ 64u) : at + WV;
-        lds<VW>(w0, at);
-        lds<VW>(w1, at1);
-        lds<VW>(w2, at + 8 * WV);
-        lds<VW>(w3, at1 + 8 * WV);
+      for (int hf = 0; hf < H; ++hf)
 #pragma unroll
-        for (int i = 0; i < VW; ++i)
+        for (int c = 0; c < MT; c += 2) {
+          uint32_t vw[4];                   // (chunk c: keys 0-7, 8-15), (chunk c + 1: the same)
+          ldsm4t(vw, st + v_at[c / 2] + hf * 16 * WV);
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const uint32_t sel = e ? 0x7632u : 0x5410u;
-            const uint32_t ya = prmt_b32(w0[i], w1[i], sel), yb = prmt_b32(w2[i], w3[i], sel);
-            const uint32_t x0 = even_codes(ya), x1 = odd_codes(ya), x2 = even_codes(yb), x3 = odd_codes(yb);
-            const int m = (j * VW + i) * 2 + e;
+            const uint32_t x0 = codes_of(vw[2 * e]), x1 = codes_of(vw[2 * e] >> 8);
+            const uint32_t x2 = codes_of(vw[2 * e + 1]), x3 = codes_of(vw[2 * e + 1] >> 8);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-              mma16816(acc[n][m], x0, x1, x2, x3, pb[n][0], pb[n][1]);
-              if (FINE) mma16816(acc[n][m], x0, x1, x2, x3, pl[n][0], pl[n][1]);
+              mma16816(acc[n][c + e], x0, x1, x2, x3, pb[n][2 * hf], pb[n][2 * hf + 1]);
+              if (FINE) mma16816(acc[n][c + e], x0, x1, x2, x3, pl[n][2 * hf], pl[n][2 * hf + 1]);
             }
           }
-      }
+        }
     }
     cp_wait<0>();
 
-    // ---- the CTA's warps together: fragments [warp][n][mt][lane] and (R, l) [warp][column]
+    // ---- a head's warps together: fragments [warp][n][mt][lane] and (R, l) [warp][column]
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -435,8 +598,7 @@ __global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, Cfg<WK, WV, NT
       }
     __syncthreads();                        // the ring is no longer read
     float4 *frag = reinterpret_cast<float4 *>(smem);
-    float2 *stat = reinterpret_cast<float2 *>(smem + NW * NT * MT * 512);      // [warp][column]: (R, l), then a weight
-    float2 *own = stat + NW * NC;                                              // [column]: the CTA's
+    float2 *stat = reinterpret_cast<float2 *>(smem + NW * NT * MT * 512);      // [warp][column]: (R, l), then (weight, l)
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -449,140 +611,142 @@ __global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, Cfg<WK, WV, NT
       }
     }
     __syncthreads();
-    if (tid < NC) {
-      float M = -INFINITY, ls = 0.f;
-      for (int x = 0; x < NW; ++x) M = fmaxf(M, stat[x * NC + tid].x);
-      for (int x = 0; x < NW; ++x) {
-        float2 *p = stat + x * NC + tid;
-        const float f = p->x == -INFINITY ? 0.f : exp2f(p->x - M);
-        ls += f * p->y;
-        p->x = f;                           // the warp's weight
-      }
-      own[tid] = make_float2(M, ls);
-      s_l[tid] = ls;
-    }
-    __syncthreads();
 
-    // Fragments with columns that exist: of each (tile, m tile), lanes (g, t) with 1, 2 or 4 of the t.  A thread takes
-    // PER of them, or several threads one.
+    // Fragments with columns that exist: of each (head, tile, m tile), lanes (g, t) with 1, 2 or 4 of the t.
+    const int heads = 1 << hs;
     const int tsh = n_cols > 4 ? 2 : n_cols > 2 ? 1 : 0;
-    const int n_frag = NT * MT * (8 << tsh);
+    constexpr int FSH = NT * MT == 4 ? 5 : NT * MT == 8 ? 6 : NT * MT == 16 ? 7 : 8;
+    const int fsh = FSH + tsh, n_frag = 1 << fsh, all_frag = n_frag << hs;
+    static_assert(NT * MT * 8 == 1 << FSH, "fragments");
     auto frag_at = [&](int v) { return (v >> (3 + tsh)) * 32 + ((v >> tsh) & 7) * 4 + (v & ((1 << tsh) - 1)); };
     auto col_of = [&](int f) { return 8 * (f / (MT * 32)) + 2 * (f & 3); };
-    constexpr int PER = (NT * MT * 32 + C::THREADS - 1) / C::THREADS;
     auto add = [](float4 &o, float w0, float w1, const float4 &p) {
       o.x = fmaf(w0, p.x, o.x);
       o.y = fmaf(w1, p.y, o.y);
       o.z = fmaf(w0, p.z, o.z);
       o.w = fmaf(w1, p.w, o.w);
     };
-    const bool whole = n_con == 1;
-    float *mine = a.part + static_cast<int64_t>(2 * blockIdx.x + (even || share0 >= ia ? 0 : 1)) * C::PART;
-    float4 o4[PER];
+    // fragment f of head h0 + h: dims d, d + 1 of columns col, col + 1
+    auto put = [&](int h, int f, const float4 &o) {
+      const int mt = (f / 32) % MT, fl = f & 31, col = col_of(f);
+      const int d = 16 * mt + 2 * (fl >> 2);
+      if (d >= a.dv) return;
 #pragma unroll
-    for (int k = 0; k < PER; ++k) {
-      const int v = tid + k * C::THREADS;
-      o4[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (v < n_frag) {
-        const int f = frag_at(v), col = col_of(f);
-#pragma unroll
-        for (int x = 0; x < NW; ++x)
-          add(o4[k], stat[x * NC + col].x, stat[x * NC + col + 1].x, frag[x * (NT * MT * 32) + f]);
-        if (!whole) reinterpret_cast<float4 *>(mine + 2 * NC)[v] = o4[k];
+      for (int i = 0; i < 2; ++i) {
+        if (col + i >= n_cols) continue;
+        const float ls = s_l[h * NC + col + i], inv = ls != 0.f ? 1.f / ls : 0.f;
+        const int64_t at = (static_cast<int64_t>(seq) * a.n_heads + (h0 + h) * a.group + c_base + col + i) * a.dv + d;
+        store2(a.out, at, (i ? o.y : o.x) * inv, (i ? o.w : o.z) * inv, a.bf16);
       }
+    };
+    const bool whole = n_con == 1;
+    float *mine = a.part + static_cast<int64_t>(2 * piece + (even || share0 >= ia ? 0 : 1)) * C::HEADS * C::PART;
+    if (tid < heads * NC) {
+      const int h = tid / NC, col = tid - h * NC;
+      float M = -INFINITY, ls = 0.f;
+      float2 rl[NW];
+#pragma unroll
+      for (int x = 0; x < NW; ++x) {
+        rl[x] = x < tiles_by ? stat[(h + (x << hs)) * NC + col] : make_float2(-INFINITY, 0.f);
+        M = fmaxf(M, rl[x].x);
+      }
+#pragma unroll
+      for (int x = 0; x < NW; ++x) {
+        const float f = rl[x].x == -INFINITY ? 0.f : exp2f(rl[x].x - M);
+        ls += f * rl[x].y;
+        if (x < tiles_by) stat[(h + (x << hs)) * NC + col].x = f;           // the warp's weight
+      }
+      s_l[tid] = ls;
+      if (!whole) reinterpret_cast<float2 *>(mine + h * C::PART)[col] = make_float2(M, ls);
     }
-    bool finish = whole;
+    __syncthreads();
+    for (int v = tid; v < all_frag; v += C::THREADS) {
+      const int h = v >> fsh, u = v & (n_frag - 1), f = frag_at(u), col = col_of(f);
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < NW; ++k)
+        if (k < tiles_by) {
+          const int x = h + (k << hs);
+          add(o, stat[x * NC + col].x, stat[x * NC + col + 1].x, frag[x * (NT * MT * 32) + f]);
+        }
+      if (whole) put(h, f, o);
+      else reinterpret_cast<float4 *>(mine + h * C::PART + 2 * NC)[u] = o;
+    }
     if (!whole) {
-      if (tid < NC) reinterpret_cast<float2 *>(mine)[tid] = own[tid];
       __syncthreads();
       if (tid == 0) s_last = arrive_one(a.counters + c0) == n_con - 1;
       __syncthreads();
-      finish = s_last != 0;
-      if (finish) {
+      if (s_last) {
         if (tid == 0) a.counters[c0] = 0;
         // CTA c0's partial is in its slot 0 when the item's part begins its share, else in slot 1; the others' parts
         // begin their shares
-        const int slot0 = even || c0 * total / n_work >= ia ? 0 : 1;
-        auto part_of = [&](int c) { return a.part + static_cast<int64_t>(2 * (c0 + c) + (c == 0 ? slot0 : 0)) * C::PART; };
-        // with few fragments, `teams` threads share one, each taking every teams-th partial
-        const int teams = n_frag < C::THREADS ? C::THREADS / n_frag : 1, team = n_frag < C::THREADS ? tid / n_frag : 0;
-        const int v0 = n_frag < C::THREADS ? tid - team * n_frag : tid;
-        constexpr int B = C::CTAS == 2 ? 16 : 24;                // loads in flight per thread
-        float4 p[B];
-        auto fetch = [&](int c, int v) {
-#pragma unroll
-          for (int i = 0; i < B; ++i) {
-            p[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (c + i * teams < n_con && v < n_frag)
-              p[i] = __ldcg(reinterpret_cast<const float4 *>(part_of(c + i * teams) + 2 * NC) + v);
-          }
+        const int slot0 = even || start_of(c0) >= ia ? 0 : 1;
+        auto part_of = [&](int c, int h) {
+          return a.part + (static_cast<int64_t>(2 * (c0 + c) + (c == 0 ? slot0 : 0)) * C::HEADS + h) * C::PART;
         };
-        fetch(team, v0);                                         // on its way while the weights are worked out
-        float *cw = reinterpret_cast<float *>(smem);             // [CTA][column]: weight of its partial
-        float *cl = cw + n_con * NC;
-        for (int col = warp; col < NC; col += NW) {
-          float M = -INFINITY, ls = 0.f;
-#pragma unroll 2
-          for (int c = lane; c < n_con; c += 32) {
-            const float2 r = __ldcg(reinterpret_cast<const float2 *>(part_of(c)) + col);
-            cw[c * NC + col] = r.x;
-            cl[c * NC + col] = r.y;
-            M = fmaxf(M, r.x);
+        // shared memory: [CTA][head, column] weights and sums, then the fragments of as many CTAs as there is room for
+        const int hc = NC << hs;
+        float *cw = reinterpret_cast<float *>(smem), *cl = cw + n_con * hc;
+        float4 *buf = reinterpret_cast<float4 *>(cl + n_con * hc);
+        const int room = (C::SMEM - n_con * hc * 8) / (all_frag * 16);
+        auto fetch = [&](int c1) {                               // of CTAs c1 and on
+          const int n = min(room, n_con - c1) * all_frag;
+          for (int i = tid; i < n; i += C::THREADS) {
+            const int c = i / all_frag, v = i - c * all_frag;
+            cp16(tc::smem_u32(buf + i), part_of(c1 + c, v >> fsh) + 2 * NC + 4 * (v & (n_frag - 1)));
           }
-          M = warp_max(M);
-          for (int c = lane; c < n_con; c += 32) {
-            const float r = cw[c * NC + col];
-            const float f = r == -INFINITY ? 0.f : exp2f(r - M);
-            cw[c * NC + col] = f;
-            ls = fmaf(f, cl[c * NC + col], ls);
-          }
-          ls = warp_sum(ls);
-          if (lane == 0) s_l[col] = ls;
+          tc::cp_async_commit();
+        };
+        fetch(0);                                                // on its way while the weights are worked out
+        for (int i = tid; i < n_con * hc; i += C::THREADS) {
+          const int c = i / hc, col = i % hc;
+          const float2 r = __ldcg(reinterpret_cast<const float2 *>(part_of(c, col / NC)) + col % NC);
+          cw[i] = r.x;
+          cl[i] = r.y;
         }
         __syncthreads();
-        float4 *red = reinterpret_cast<float4 *>(cl + n_con * NC);
+        for (int col = tid >> 3; col < hc; col += C::THREADS / 8) {      // eight threads a column
+          float M = -INFINITY, ls = 0.f;
+          for (int c = tid & 7; c < n_con; c += 8) M = fmaxf(M, cw[c * hc + col]);
 #pragma unroll
-        for (int k = 0; k < PER; ++k) {
-          const int v = v0 + k * C::THREADS, col = col_of(frag_at(v < n_frag ? v : 0));
-          if (k > 0) fetch(team, v);
-          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int c = team; c < n_con; c += B * teams) {
-            if (c > team) fetch(c, v);
-#pragma unroll
-            for (int i = 0; i < B; ++i)
-              if (c + i * teams < n_con) {
-                const float2 w2 = *reinterpret_cast<const float2 *>(cw + (c + i * teams) * NC + col);
-                add(o, w2.x, w2.y, p[i]);
-              }
+          for (int o = 1; o < 8; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+          for (int c = tid & 7; c < n_con; c += 8) {
+            const float r = cw[c * hc + col];
+            const float f = r == -INFINITY ? 0.f : exp2f(r - M);
+            cw[c * hc + col] = f;
+            ls = fmaf(f, cl[c * hc + col], ls);
           }
-          o4[k] = o;
+#pragma unroll
+          for (int o = 1; o < 8; o <<= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
+          if ((tid & 7) == 0) s_l[col] = ls;
         }
-        if (teams > 1) {
-          if (team > 0 && team < teams) red[(team - 1) * n_frag + v0] = o4[0];
+        constexpr int MOST = (C::HEADS * NT * MT * 32 + C::THREADS - 1) / C::THREADS;     // fragments of a thread
+        float4 o[MOST];
+#pragma unroll
+        for (int k = 0; k < MOST; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c1 = 0; c1 < n_con; c1 += room) {
+          cp_wait<0>();
           __syncthreads();
-          if (team == 0)
-            for (int x = 1; x < teams; ++x) add(o4[0], 1.f, 1.f, red[(x - 1) * n_frag + v0]);
-        }
-      }
-    }
-    if (finish) {
-      // fragment f = (n, mt, lane): dims d, d + 1 of columns col, col + 1
 #pragma unroll
-      for (int k = 0; k < PER; ++k) {
-        const int v = tid + k * C::THREADS;
-        if (v < n_frag) {
-          const int f = frag_at(v), mt = (f / 32) % MT, fl = f & 31, col = col_of(f);
-          constexpr int VW = WV == 64 ? 2 : 4;
-          const int d = 128 * (mt / (2 * VW)) + 4 * VW * (fl >> 2) + 2 * (mt % (2 * VW));
-          if (d < a.dv) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              if (col + i >= n_cols) continue;
-              const float ls = s_l[col + i], inv = ls != 0.f ? 1.f / ls : 0.f;
-              const int64_t at = (static_cast<int64_t>(seq) * a.n_heads + hv * a.group + c_base + col + i) * a.dv + d;
-              store2(a.out, at, (i ? o4[k].y : o4[k].x) * inv, (i ? o4[k].w : o4[k].z) * inv, a.bf16);
+          for (int k = 0; k < MOST; ++k) {
+            const int v = tid + k * C::THREADS;
+            if (v >= all_frag) break;
+            const int col = (v >> fsh) * NC + col_of(frag_at(v & (n_frag - 1)));
+#pragma unroll 8
+            for (int c = c1; c < min(n_con, c1 + room); ++c) {
+              const float2 w2 = *reinterpret_cast<const float2 *>(cw + c * hc + col);
+              add(o[k], w2.x, w2.y, buf[(c - c1) * all_frag + v]);
             }
           }
+          if (c1 + room < n_con) {
+            __syncthreads();
+            fetch(c1 + room);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < MOST; ++k) {
+          const int v = tid + k * C::THREADS;
+          if (v < all_frag) put(v >> fsh, frag_at(v & (n_frag - 1)), o[k]);
         }
       }
     }
@@ -591,7 +755,7 @@ __global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, Cfg<WK, WV, NT
 
   // sequences without cells: their rows are zeros
   for (int s = blockIdx.x; s < a.n_seq; s += gridDim.x) {
-    if (seq_work<NC>(a, s, false).len == 0) {
+    if (length_of(a, s, false) == 0) {
       const int64_t n = static_cast<int64_t>(a.n_heads) * a.dv / 2, at = s * 2 * n;
       for (int64_t i = tid; i < n; i += C::THREADS) store2(a.out, at + 2 * i, 0.f, 0.f, a.bf16);
     }
@@ -602,7 +766,7 @@ template <int WK, int WV, int NT, bool FINE>
 cudaError_t launch_t(const AttnArgs &a, cudaStream_t s) {
   using C = Cfg<WK, WV, NT, FINE>;
   static_assert(C::SMEM <= 227 * 1024, "shared memory");
-  static_assert(C::merge_bytes(C::grid(1 << 20)) <= C::SMEM && C::grid(152) == 152 * C::CTAS, "merge");
+  static_assert(C::merge_bytes(C::grid(1 << 20)) <= C::SMEM && C::grid(152) == 152, "merge");
   auto kern = decode_kernel<WK, WV, NT, FINE>;
   cudaError_t e = set_dynamic_smem(reinterpret_cast<const void *>(kern), C::SMEM);
   if (e != cudaSuccess) return e;

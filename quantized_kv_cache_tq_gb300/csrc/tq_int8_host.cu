@@ -273,14 +273,14 @@ static tq_status decode_shape(const tq_int8 *k, const tq_int8 *v, int n_q_heads,
 }
 
 // Workspace: laid out as the paged calls' (status word, arrival counters, partial results), so that one serves both.
+// Two partial results per CTA, each of at most 4096 values and (maximum, sum) of 8 columns a head (tq_int8_decode.cuh).
 constexpr size_t kCountersOff = 256;
-static size_t decode_bytes(int wv) {
-  const size_t ctas = static_cast<size_t>(p4::max_ctas(2)), columns = 16, tiles = 2;
-  return TQ_PAGED4_WORKSPACE_HEAD + sizeof(float) * 2 * ctas * (4 * columns + tiles * (wv / 16) * 128);
+static size_t decode_bytes() {
+  return TQ_PAGED4_WORKSPACE_HEAD + sizeof(float) * 2 * static_cast<size_t>(p4::max_ctas(2)) * (4096 + 128);
 }
 
 size_t tq_int8_decode_workspace(const tq_int8 *k, const tq_int8 *v, int n_q_heads, int n_seq) {
-  return decode_shape(k, v, n_q_heads, n_seq) == TQ_OK ? decode_bytes(p4::row_width(v->head_dim)) : 0;
+  return decode_shape(k, v, n_q_heads, n_seq) == TQ_OK ? decode_bytes() : 0;
 }
 
 tq_status tq_int8_decode(const tq_int8 *k, const tq_int8 *v, int page_size, const int32_t *block_table, int max_pages,
@@ -300,7 +300,7 @@ tq_status tq_int8_decode(const tq_int8 *k, const tq_int8 *v, int page_size, cons
   if (n_seq == 0) return TQ_OK;
   if (!al(block_table, 4) || !al(seq_len, 4) || !al(q, 16) || !al(out, 16)) return TQ_ERR_INVALID_ARG;
   const int wk = p4::row_width(k->head_dim), wv = p4::row_width(v->head_dim);
-  if (!al(workspace, 256) || workspace_bytes < decode_bytes(wv)) return TQ_ERR_WORKSPACE;
+  if (!al(workspace, 256) || workspace_bytes < decode_bytes()) return TQ_ERR_WORKSPACE;
   p4::AttnArgs a;
   memset(&a, 0, sizeof(a));
   a.k_codes = static_cast<const uint8_t *>(k->rows);
