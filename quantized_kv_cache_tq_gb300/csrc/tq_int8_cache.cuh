@@ -41,6 +41,8 @@ struct StepArgs {
   float gain;                 // factor on what turns
   float sign;                 // -1: the other way round
   float eps;
+  int32_t groups[3];          // CTAs side by side for a part's heads, and heads of each (set at the launch)
+  int32_t heads_per;
 };
 cudaError_t launch_step_rows(int type, const StepArgs &a, cudaStream_t s);
 cudaError_t launch_get_rows(int type, const p4::RowsArgs &a, cudaStream_t s);
