@@ -557,19 +557,27 @@ class Rope:
         self.ref = C.byref(self.c)
 
 
-def _head_rows(t, shape, out, norm, what: str):
-    """tq_head_rows of rows t (and their output), and the type of both."""
-    code = _row_type(t, what)
+def _rows_stride(t, heads: int, dim: int, what: str) -> int:
+    """_row_stride of rows whose shape is checked already."""
+    return heads * dim if t.is_contiguous() else _row_stride(t, t.shape, what)
+
+
+def _head_rows(t, heads: int, dim: int, out, norm, what: str):
+    """tq_head_rows of rows t [n][heads][dim] and of their output."""
+    stride = _rows_stride(t, heads, dim, what)
     norm_p = None
     if norm is not None:
-        _ints(norm, _T.float32, (shape[2],), what + "_norm")
+        _ints(norm, _T.float32, (dim,), what + "_norm")
         norm_p = norm.data_ptr()
-    stride = _row_stride(t, shape, what)
     if out is None:
-        return tq_head_rows(t.data_ptr(), stride, None, 0, norm_p, shape[1]), code
-    _need(out.dtype is t.dtype, f"{what}_out has another type than {what}")
-    return tq_head_rows(t.data_ptr(), stride, out.data_ptr(), _row_stride(out, shape, what + "_out"), norm_p,
-                        shape[1]), code
+        return tq_head_rows(t.data_ptr(), stride, None, 0, norm_p, heads)
+    if out is t:
+        at = t.data_ptr()
+        return tq_head_rows(at, stride, at, stride, norm_p, heads)
+    if out.dtype is not t.dtype or out.shape != t.shape:
+        raise ValueError(f"{what}_out: type and shape of {what} are expected")
+    return tq_head_rows(t.data_ptr(), stride, out.data_ptr(), _rows_stride(out, heads, dim, what + "_out"), norm_p,
+                        heads)
 
 
 def _zeros_like_rows(stream, t):
@@ -589,19 +597,23 @@ def rope_rows(rope: Rope, positions, q, k=None, q_norm=None, k_norm=None, eps: f
     before where q_norm / k_norm (float32 [head_dim]) are given.  Rows may be strided, and q_out may be q (in place).
     Rows whose position is -1 stay as they were (new outputs: zeros).  ``inverse`` turns the other way: the gradient.
     -> q_out, or (q_out, k_out) with k."""
-    _need(q.dim() == 3 and (k is None or k.dim() == 3), "rows: [n][heads][head_dim]")
-    n, _, d = q.shape
-    _ints(positions, _t().int32, (n,), "positions")
-    q_out = _zeros_like_rows(stream, q) if q_out is None else q_out
-    qr, code = _head_rows(q, (n, q.shape[1], d), q_out, q_norm, "q")
-    kr = None
+    if q.dim() != 3:
+        raise ValueError("q: [n][heads][head_dim]")
+    code = _row_type(q, "q")
+    n, heads, d = q.shape
+    _ints(positions, _T.int32, (n,), "positions")
+    if q_out is None:
+        q_out = _zeros_like_rows(stream, q)
+    qr, kr = _head_rows(q, heads, d, q_out, q_norm, "q"), None
     if k is not None:
-        _need(k.dtype is q.dtype, "q and k have different types")
-        k_out = _zeros_like_rows(stream, k) if k_out is None else k_out
-        kr = _head_rows(k, (n, k.shape[1], d), k_out, k_norm, "k")[0]
-    else:
-        _need(k_norm is None and k_out is None, "k_norm and k_out go with k")
-    status = _status(dev_status)
+        if k.dim() != 3 or k.shape[0] != n or k.shape[2] != d or k.dtype is not q.dtype:
+            raise ValueError("k: [n][heads][head_dim] as q, of its type")
+        if k_out is None:
+            k_out = _zeros_like_rows(stream, k)
+        kr = _head_rows(k, k.shape[1], d, k_out, k_norm, "k")
+    elif k_norm is not None or k_out is not None:
+        raise ValueError("k_norm and k_out go with k")
+    status = None if dev_status is None else _status(dev_status)
     handle = _stream_here(stream, rope.index, positions, q, k, q_out, k_out, q_norm, k_norm, dev_status)
     st = _lib.tq_rope_rows(rope.ref, qr, kr, d, code, eps, inverse, positions.data_ptr(), n, status, handle)
     if st:
@@ -683,19 +695,24 @@ def int8_rope_set_rows(kc: Int8Cache, vc: Int8Cache, rope: Rope, positions, q, k
     """A step's rows in one launch: q [n][n_q_heads][head_dim] (or None) as rope_rows, k_src and v_src as
     int8_set_rows, the keys normed and turned before.  Rows without a position or a slot (-1) are not stored.
     -> q_out (None without q); it may be q."""
-    n = slots.shape[0]
+    n, d = slots.shape[0], kc.head_dim
     t = _row_type(k_src, "k_src")
-    _need(v_src.dtype is k_src.dtype and (q is None or q.dtype is k_src.dtype), "q, k_src and v_src have different types")
+    if v_src.dtype is not k_src.dtype or (q is not None and q.dtype is not k_src.dtype):
+        raise ValueError("q, k_src and v_src have different types")
     status = _rows_status(slots, n, dev_status)
     _ints(positions, _T.int32, (n,), "positions")
     qr = None
     if q is not None:
-        _need(q.dim() == 3, "q: [n][heads][head_dim]")
-        q_out = _zeros_like_rows(stream, q) if q_out is None else q_out
-        qr = _head_rows(q, (n, q.shape[1], kc.head_dim), q_out, q_norm, "q")[0]
-    else:
-        _need(q_norm is None and q_out is None, "q_norm and q_out go with q")
-    kr = _head_rows(k_src, (n, kc.n_kv_heads, kc.head_dim), None, k_norm, "k_src")[0]
+        if q.dim() != 3 or q.shape[0] != n or q.shape[2] != d:
+            raise ValueError("q: [n][heads][head_dim] is expected, head_dim as the keys'")
+        if q_out is None:
+            q_out = _zeros_like_rows(stream, q)
+        qr = _head_rows(q, q.shape[1], d, q_out, q_norm, "q")
+    elif q_norm is not None or q_out is not None:
+        raise ValueError("q_norm and q_out go with q")
+    if k_src.shape != (n, kc.n_kv_heads, d):
+        raise ValueError(f"k_src: shape {(n, kc.n_kv_heads, d)} is expected, not {tuple(k_src.shape)}")
+    kr = _head_rows(k_src, kc.n_kv_heads, d, None, k_norm, "k_src")
     vs = _row_stride(v_src, (n, vc.n_kv_heads, vc.head_dim), "v_src")
     handle = _stream_here(stream, kc.index, vc.rows, rope.turns, positions, q, k_src, v_src, slots, q_out, q_norm,
                           k_norm, dev_status)

@@ -28,6 +28,14 @@ struct Part {
 
 constexpr int Q = 0, K = 1, V = 2;
 
+// Work as a line of units (a head of a tile of rows), tensor after tensor, `per` for each CTA and one more for the first
+// `more` of them.
+struct Units {
+  int64_t part[3];
+  int64_t per;
+  int32_t more;
+};
+
 struct StepArgs {
   Part part[3];
   const uint64_t *turns;      // [rot / 2], 2^-64 of a turn per position
@@ -41,8 +49,7 @@ struct StepArgs {
   float gain;                 // factor on what turns
   float sign;                 // -1: the other way round
   float eps;
-  int32_t groups[3];          // CTAs side by side for a part's heads, and heads of each (set at the launch)
-  int32_t heads_per;
+  Units units;                // (set at the launch)
 };
 cudaError_t launch_step_rows(int type, const StepArgs &a, cudaStream_t s);
 cudaError_t launch_get_rows(int type, const p4::RowsArgs &a, cudaStream_t s);

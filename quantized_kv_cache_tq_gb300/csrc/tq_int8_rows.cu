@@ -16,8 +16,11 @@
 //   a turn, of which the upper 32 bits below the whole turns are kept.  Sine and cosine
 //   are then polynomials on an eighth of a turn either way (turn_sincos), eight per
 //   thread, used for all heads that the thread goes through.
-// - A thread goes through 1 to 8 heads of its row, the next one's elements on their way
-//   while it works; which, the launch chooses by how many CTAs there are (heads_per).
+// - A unit of work is one head of the 8 to 32 rows that a CTA takes side by side.  All units of a tensor, tile after
+//   tile, and of one tensor after the other form a line, of which each CTA takes an equal share (one unit, in short
+//   calls): no CTA is left over for a last wave, and what a row needs -- position, slot, angles -- is worked out once
+//   for the heads that follow.  Each thread copies its elements of the next units to a ring of its own in shared memory
+//   (cp.async) while it works: registers hold one unit, and nobody waits for anybody else.
 #include <math.h>
 
 #include "tq_common.cuh"
@@ -27,20 +30,13 @@ namespace tq {
 namespace i8 {
 namespace {
 
-constexpr int RT = 256;             // threads of a CTA
-#ifndef NB0
-#define NB0 4
-#endif
-#ifndef NB1
-#define NB1 4
-#endif
-#ifndef MAXH
-#define MAXH 8
-#endif
-#ifndef ENOUGH
-#define ENOUGH 8
-#endif
-constexpr int kEnough = ENOUGH;
+constexpr int RT = 128;             // threads of a CTA
+constexpr int kStages = 3;          // units of a thread's ring
+// CTAs per SM: what the registers allow.  Rotations run best with 95 of them: six CTAs instead of five (rope of 20001
+// rows 71 instead of 65 us) leave the loads of positions and angles one after the other, four (67 us) too few of them
+// on their way.  More stages than three read no faster and hinder the writes (71 us with four).
+constexpr int kGet = 16;
+constexpr int ctas_of(int rot) { return rot == 0 ? 8 : rot == 3 ? 4 : 5; }
 constexpr float kTop = 127.f * 65504.f;
 
 enum Rot { kNone = 0, kHalf = 1, kInterleaved = 2, kHalfAny = 3 };
@@ -50,16 +46,19 @@ template <int TYPE>
 struct Raw {
   uint4 u[TYPE == TQ_F32 ? 2 : 1];
 };
+
+// (nothing there: zeros.  Eights of 32-bit elements are copied in two halves of a sector, which meet in L1.)
 template <int TYPE>
-__device__ __forceinline__ void load8(const void *src, int64_t at, Raw<TYPE> &r) {
-  if (TYPE == TQ_F32) {
-    const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const float *>(src) + at);
-    r.u[0] = __ldcs(p);
-    r.u[TYPE == TQ_F32 ? 1 : 0] = __ldcs(p + 1);
-  } else {
-    r.u[0] = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(src) + at));
-  }
+__device__ __forceinline__ void cp16(uint4 *to, const void *from, bool there) {
+  const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(to)), n = there ? 16 : 0;
+  if (TYPE == TQ_F32)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(at), "l"(from), "r"(n) : "memory");
+  else
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at), "l"(from), "r"(n) : "memory");
 }
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 template <int TYPE>
 __device__ __forceinline__ void unpack8(const Raw<TYPE> &w, float2 *x) {
   if (TYPE == TQ_F32) {
@@ -130,9 +129,13 @@ __device__ __forceinline__ float top3(float a, float b, float c) {
 __device__ __forceinline__ void codes16(const float2 *x, float s, uint32_t *w) {
   float2 c[8];
   if (s >= 0x1p-14f) {
-    // the correctly rounded quotient from the correctly rounded reciprocal: q0 = x r, q = q0 + r (x - q0 s) (Markstein,
-    // "Computation of elementary functions on the IBM RISC System/6000 processor", 1990); at most 127 (1 + 2^-11)
-    const float r = __frcp_rn(s);
+    // The correctly rounded quotient from the correctly rounded reciprocal: q0 = x r, q = q0 + r (x - q0 s) (Markstein,
+    // "Computation of elementary functions on the IBM RISC System/6000 processor", 1990); it is at most 127 (1 + 2^-11).
+    // One Newton step rounds the reciprocal of an 11-bit number correctly: none lies nearer than 2^-36 of itself to the
+    // middle of two floats.
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+    r = fmaf(fmaf(-s, r, 1.f), r, r);
     const float2 r2 = make_float2(r, r), s2 = make_float2(-s, -s);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -152,302 +155,390 @@ __device__ __forceinline__ void codes16(const float2 *x, float s, uint32_t *w) {
                     prmt_b32(__float_as_uint(c[2 * i + 1].x), __float_as_uint(c[2 * i + 1].y), 0x0040u), 0x5410u);
 }
 
+// a / b of numbers below 2^32, as nearly all are, in 32 bits
+__device__ __forceinline__ int64_t quotient(int64_t a, int b) {
+  return static_cast<uint64_t>(a) >> 32 ? a / b : static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+}
+
+// log2 of the lanes of a row
+__host__ __device__ constexpr int lane_shift(int head_dim) { return head_dim <= 64 ? 2 : head_dim <= 128 ? 3 : 4; }
+
+// The launch may begin beside the one before it (p4::launch_beside); nothing is read or written before that has ended.
+__device__ __forceinline__ void after_earlier_launches() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// A CTA's share of `n` units, `more` of which are left over for the first CTAs.
+struct Share {
+  int64_t at, end;
+};
+__device__ __forceinline__ Share share_of(const Units &u) {
+  const int64_t b = blockIdx.x, at = b * u.per + min(b, static_cast<int64_t>(u.more));
+  return {at, at + u.per + (b < u.more)};
+}
+
 template <int TYPE, int ROT>
-__global__ void __launch_bounds__(RT, ROT == kNone ? NB0 : ROT == kHalfAny ? 2 : NB1) step_rows_kernel(const StepArgs a) {
-  // ---- which tensor, which heads, which row
-  int w = Q, group = blockIdx.y;
-  while (group >= a.groups[w]) group -= a.groups[w++];
-  const Part &p = a.part[w];
-  const int d = p.head_dim, sh = d <= 64 ? 2 : d <= 128 ? 3 : 4, lanes = 1 << sh;      // lanes of a row
-  const int l = threadIdx.x & (lanes - 1);
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * (RT >> sh) + (threadIdx.x >> sh);
-  int pos = -1;
-  bool ok = row < a.n_rows;
-  int64_t slot = 0;
-  if (ok) {
-    pos = ROT == kNone ? 0 : __ldg(a.positions + row);
-    if (p.cells) slot = __ldg(a.slots + row);
-    const bool cell_ok = !p.cells || static_cast<uint64_t>(slot) < static_cast<uint64_t>(a.n_cells);
-    if (l == 0 && (pos < -1 || (!cell_ok && slot != -1))) set_status(a.status, TQ_ERR_DEVICE_CHECK);
-    ok = pos >= 0 && cell_ok;
-  }
-  const bool turns = ROT != kNone && p.turns;
+__global__ void __launch_bounds__(RT, ctas_of(ROT)) step_rows_kernel(const StepArgs a) {
+  constexpr int S = kStages, W = TYPE == TQ_F32 ? 2 : 1;        // stages; 16-byte words of an eight
+  __shared__ uint4 ring[S][2 * W][RT];            // each thread's own
+  after_earlier_launches();
+  for (Share u = share_of(a.units); u.at < u.end;) {
+    // ---- units of one tensor: from head `head` of the rows of tile `tile` on
+    int w = Q;
+    int64_t unit = u.at;
+    while (unit >= a.units.part[w]) unit -= a.units.part[w++];
+    int left = static_cast<int>(min(min(u.end - u.at, a.units.part[w] - unit), int64_t{1 << 30}));
+    u.at += left;
+    const Part &p = a.part[w];
+    const int d = p.head_dim, sh = lane_shift(d), lanes = 1 << sh;
+    const int l = threadIdx.x & (lanes - 1);
+    const int64_t tile = quotient(unit, p.n_heads);
+    uint32_t row = static_cast<uint32_t>(tile) * (RT >> sh) + (threadIdx.x >> sh);      // (there are less than 2^31)
+    const uint32_t n_rows = static_cast<uint32_t>(a.n_rows);
+    int head = static_cast<int>(unit - tile * p.n_heads);
+    const bool turns = ROT != kNone && p.turns;
 
-  // ---- the lane's two eights
-  const int h = a.rot / 2;
-  int c0 = l, c1 = l + lanes;
-  if (ROT == kHalf && turns) {        // eights j and j + h / 8 turn together, the ones that pass are paired as they come
-    const int n = h / 8;
-    c0 = l < n ? l : n + l;
-    c1 = l < n ? n + l : lanes + l;
-  }
-  const int n_in = ok ? (8 * c0 < d) + (8 * c1 < d) : 0;                               // (c0 < c1)
-
-  // ---- angles: half, of pairs 8 c0 ..; interleaved, of pairs 4 c0 .. and 4 c1 ..; half_any, of each element
-  constexpr int NA = ROT == kNone ? 1 : ROT == kHalfAny ? 16 : 8;
-  float ca[NA], sa[NA];
-  bool turned[2] = {false, false};                                                     // whether an eight turns at all
-  if (turns && ok) {
-#pragma unroll
-    for (int i = 0; i < NA; ++i) {
-      const int e = 8 * (NA == 16 && i >= 8 ? c1 : c0) + (i & 7);                      // (half_any: the element)
-      const int j = ROT == kHalf ? 8 * c0 + i : ROT == kInterleaved ? 4 * (i < 4 ? c0 : c1) + (i & 3) : e < h ? e : e - h;
-      if (ROT == kInterleaved || ROT == kHalfAny) turned[NA == 16 ? i / 8 : i / 4] |= ROT == kHalfAny ? e < a.rot : j < h;
-      else turned[0] = turned[1] = 8 * c0 < h;
-      ca[i] = 1.f;
-      sa[i] = 0.f;
-      if (j < h) {
-        const uint64_t t = __ldg(a.turns + j);
-        const uint32_t u = static_cast<uint32_t>(pos);
-        turn_sincos(u * static_cast<uint32_t>(t >> 32) + __umulhi(u, static_cast<uint32_t>(t)), sa[i], ca[i]);
-        sa[i] *= a.sign * a.gain;
-        ca[i] *= a.gain;
-      }
+    // ---- the lane's two eights
+    const int h = a.rot / 2;
+    int c0 = l, c1 = l + lanes;
+    if (ROT == kHalf && turns) {      // eights j and j + h / 8 turn together, the ones that pass are paired as they come
+      const int n = h / 8;
+      c0 = l < n ? l : n + l;
+      c1 = l < n ? n + l : lanes + l;
     }
-  }
+    const int n_row = (8 * c0 < d) + (8 * c1 < d);                                     // (c0 < c1)
 
-  // ---- head after head
-  int head = group * a.heads_per;
-  const int heads = min(p.n_heads, head + a.heads_per);
-  int64_t at = row * p.src_stride + static_cast<int64_t>(head) * d;
-  Raw<TYPE> next[2];
-  next[0] = next[1] = Raw<TYPE>{};
-  auto fetch = [&]() {
-    if (n_in >= 1) load8<TYPE>(p.src, at + 8 * c0, next[0]);
-    if (n_in >= 2) load8<TYPE>(p.src, at + 8 * c1, next[1]);
-  };
-  fetch();
-  for (; head < heads; ++head) {
-    float2 x[8];                      // elements 8 c0 .. and 8 c1 ..
-    unpack8<TYPE>(next[0], x);
-    unpack8<TYPE>(next[1], x + 4);
-    float y[ROT == kHalfAny ? 16 : 1];        // half_any: the partners
-    if (ROT == kHalfAny && turns) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int e = 8 * (i < 8 ? c0 : c1) + (i & 7);
-        y[ROT == kHalfAny ? i : 0] = ok && e < a.rot ? load1<TYPE>(p.src, at + (e < h ? e + h : e - h)) : 0.f;
+    int pos_next = -1;
+    int64_t slot_next = -1;
+    auto look_up = [&](uint32_t r) {   // a row's position and cell, asked for ahead of time
+      if (r < n_rows) {
+        pos_next = ROT == kNone ? 0 : __ldg(a.positions + r);
+        slot_next = p.cells ? __ldg(a.slots + r) : 0;
+      } else {
+        pos_next = -1;
+        slot_next = -1;
       }
-      __syncwarp();                   // rows that turn in place: everything is read before something is written
-    }
-    at += d;
-    if (head + 1 < heads) fetch();
-    if (p.norm) {
-      float2 s2 = make_float2(0.f, 0.f);
+    };
+    look_up(row);
+
+    // ---- copies of the next units' elements, on their way while this one is worked on
+    constexpr int size = TYPE == TQ_F32 ? 4 : 2;
+    auto row_at = [&](uint32_t r, int hd) {
+      return static_cast<const char *>(p.src) + (r * p.src_stride + static_cast<int64_t>(hd) * d + 8 * c0) * size;
+    };
+    const char *from = row_at(row, head);
+    uint32_t from_row = row;
+    int from_left = left, from_head = head, fill = 0;
+    auto fetch = [&]() {
+      if (from_left > 0) {
+        const bool there = from_row < n_rows;
+        const char *q0 = there && n_row >= 1 ? from : static_cast<const char *>(p.src);
+        const char *q1 = there && n_row >= 2 ? from + 8 * (c1 - c0) * size : static_cast<const char *>(p.src);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s2 = fma2(x[i], x[i], s2);
-      float ss = s2.x + s2.y;
-      for (int o = 1; o < lanes; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      const float mean = ss / static_cast<float>(d) + a.eps, r = mean != 0.f ? rsqrtf(mean) : 0.f;
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-        if (k < n_in) {
-          const float4 *n4 = reinterpret_cast<const float4 *>(p.norm + 8 * (k ? c1 : c0));
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float4 n = __ldg(n4 + i);
-            x[4 * k + 2 * i] = mul2(x[4 * k + 2 * i], make_float2(n.x * r, n.y * r));
-            x[4 * k + 2 * i + 1] = mul2(x[4 * k + 2 * i + 1], make_float2(n.z * r, n.w * r));
-          }
+        for (int i = 0; i < W; ++i) {
+          cp16<TYPE>(&ring[fill][i][threadIdx.x], q0 + 16 * i, there && n_row >= 1);
+          cp16<TYPE>(&ring[fill][W + i][threadIdx.x], q1 + 16 * i, there && n_row >= 2);
         }
+        --from_left;
+        from += d * size;
+        if (++from_head == p.n_heads) {
+          from_head = 0;
+          from_row += RT >> sh;
+          from = row_at(from_row, 0);
+        }
+        fill = fill == S - 1 ? 0 : fill + 1;
+      }
+      cp_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) fetch();
+
+    constexpr int NA = ROT == kNone ? 1 : ROT == kHalfAny ? 16 : 8;
+    float ca[NA], sa[NA];
+    bool turned[2], ok = false;                                                        // whether an eight turns at all
+    uint32_t cell_row = 0;            // (rows of a plane are less than 2^32)
+    int n_in = 0, stage = 0;
+    auto take_up = [&]() {            // the row: its position, its cell, its angles
+      // half: of pairs 8 c0 ..; interleaved: of pairs 4 c0 .. and 4 c1 ..; half_any: of each element
+      auto pair_of = [&](int i) {
+        const int e = 8 * (NA == 16 && i >= 8 ? c1 : c0) + (i & 7);                    // (half_any: the element)
+        return ROT == kHalf ? 8 * c0 + i : ROT == kInterleaved ? 4 * (i < 4 ? c0 : c1) + (i & 3) : e < h ? e : e - h;
+      };
+      uint64_t t[NA];
+      if (turns)
+#pragma unroll
+        for (int i = 0; i < NA; ++i) t[i] = pair_of(i) < h ? __ldg(a.turns + pair_of(i)) : 0;
+      const int pos = pos_next;
+      const int64_t slot = slot_next;
+      look_up(row + (RT >> sh));
+      const bool cell_ok = !p.cells || static_cast<uint64_t>(slot) < static_cast<uint64_t>(a.n_cells);
+      if (l == 0 && (pos < -1 || (!cell_ok && slot != -1))) set_status(a.status, TQ_ERR_DEVICE_CHECK);
+      ok = pos >= 0 && cell_ok;
+      cell_row = static_cast<uint32_t>(slot) * p.n_heads + head;
+      n_in = ok ? n_row : 0;
+      turned[0] = turned[1] = false;
+      if (turns && ok) {
+#pragma unroll
+        for (int i = 0; i < NA; ++i) {
+          // (a pair beyond the last one: frequency 0, no element asks for it)
+          const uint32_t q = static_cast<uint32_t>(pos);
+          turn_sincos(q * static_cast<uint32_t>(t[i] >> 32) + __umulhi(q, static_cast<uint32_t>(t[i])), sa[i], ca[i]);
+          sa[i] *= a.sign * a.gain;
+          ca[i] *= a.gain;
+        }
+        turned[0] = ROT == kHalfAny ? 8 * c0 < a.rot : pair_of(0) < h;
+        turned[1] = ROT == kHalf ? turned[0] : ROT == kHalfAny ? 8 * c1 < a.rot : pair_of(4 % NA) < h;
+      }
+    };
+
+    // ---- unit after unit
+    for (bool fresh = true; left > 0; --left) {
+      if (head == p.n_heads) {
+        head = 0;
+        row += RT >> sh;
+        fresh = true;
+      }
+      if (fresh) take_up();
+      fresh = false;
+      const int this_head = head++;
+      cp_wait<S - 2>();
+      Raw<TYPE> r0, r1;
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        r0.u[i] = ring[stage][i][threadIdx.x];
+        r1.u[i] = ring[stage][W + i][threadIdx.x];
+      }
+      stage = stage == S - 1 ? 0 : stage + 1;
+      fetch();
+      float2 x[8];                      // elements 8 c0 .. and 8 c1 ..
+      unpack8<TYPE>(r0, x);
+      unpack8<TYPE>(r1, x + 4);
+      float y[ROT == kHalfAny ? 16 : 1];        // half_any: the partners
       if (ROT == kHalfAny && turns) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const int e = 8 * (i < 8 ? c0 : c1) + (i & 7);
-          if (ok && e < a.rot) y[ROT == kHalfAny ? i : 0] *= r * __ldg(p.norm + (e < h ? e + h : e - h));
+          y[ROT == kHalfAny ? i : 0] = ok && e < a.rot ? load1<TYPE>(p.src, row * p.src_stride + this_head * d + (e < h ? e + h : e - h)) : 0.f;
         }
+        __syncwarp();                   // rows that turn in place: everything is read before something is written
       }
-    }
-    if (ROT == kHalf && turned[0]) {
+      if (p.norm) {
+        float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 c = make_float2(ca[2 * i], ca[2 * i + 1]), s = make_float2(sa[2 * i], sa[2 * i + 1]);
-        const float2 u = x[i], v = x[4 + i];
-        x[i] = sub2(mul2(u, c), mul2(v, s));
-        x[4 + i] = fma2(u, s, mul2(v, c));
-      }
-    }
-    if (ROT == kInterleaved) {
+        for (int i = 0; i < 8; ++i) s2 = fma2(x[i], x[i], s2);
+        float ss = s2.x + s2.y;
+        for (int o = 1; o < lanes; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        const float mean = ss / static_cast<float>(d) + a.eps, r = mean != 0.f ? rsqrtf(mean) : 0.f;
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
-        if (turned[k]) {
-          const int n = h - 4 * (k ? c1 : c0);             // its pairs that turn
+        for (int k = 0; k < 2; ++k)
+          if (k < n_in) {
+            const float4 *n4 = reinterpret_cast<const float4 *>(p.norm + 8 * (k ? c1 : c0));
 #pragma unroll
-          for (int i = 4 * k; i < 4 * k + 4; ++i) {
-            const float2 u = x[i], v = make_float2(fmaf(-u.y, sa[i % NA], u.x * ca[i % NA]), fmaf(u.x, sa[i % NA], u.y * ca[i % NA]));
-            if (n >= 4 || (i & 3) < n) x[i] = v;
+            for (int i = 0; i < 2; ++i) {
+              const float4 n = __ldg(n4 + i);
+              x[4 * k + 2 * i] = mul2(x[4 * k + 2 * i], make_float2(n.x * r, n.y * r));
+              x[4 * k + 2 * i + 1] = mul2(x[4 * k + 2 * i + 1], make_float2(n.z * r, n.w * r));
+            }
+          }
+        if (ROT == kHalfAny && turns) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int e = 8 * (i < 8 ? c0 : c1) + (i & 7);
+            if (ok && e < a.rot) y[ROT == kHalfAny ? i : 0] *= r * __ldg(p.norm + (e < h ? e + h : e - h));
           }
         }
-    }
-    if (ROT == kHalfAny && turns) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int e = 8 * (i < 8 ? c0 : c1) + (i & 7), k = ROT == kHalfAny ? i : 0;
-        float &v = i & 1 ? x[i / 2].y : x[i / 2].x;
-        if (e < a.rot) v = e < h ? fmaf(-y[k], sa[k % NA], v * ca[k % NA]) : fmaf(y[k], sa[k % NA], v * ca[k % NA]);
       }
-    }
-    if (!p.cells) {
-      const int64_t to = row * p.dst_stride + static_cast<int64_t>(head) * d;
-      if (n_in >= 1) store8<TYPE>(p.dst, to + 8 * c0, x);
-      if (n_in >= 2) store8<TYPE>(p.dst, to + 8 * c1, x + 4);
-      continue;
-    }
-    // ---- int8 (elements beyond the row are zeros)
-    float top = top3(x[0].x, x[0].y, x[1].x);
-    top = top3(top, x[1].y, x[2].x);
-    top = top3(top, x[2].y, x[3].x);
-    top = top3(top, x[3].y, x[4].x);
-    top = top3(top, x[4].y, x[5].x);
-    top = top3(top, x[5].y, x[6].x);
-    top = top3(top, x[6].y, x[7].x);
-    top = top3(top, x[7].y, x[7].y);
-    if (!(top <= kTop)) {             // a stored value is finite: NaN counts as 0, larger magnitudes as the largest
-      top = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        x[i].x = x[i].x == x[i].x ? fminf(fmaxf(x[i].x, -kTop), kTop) : 0.f;
-        x[i].y = x[i].y == x[i].y ? fminf(fmaxf(x[i].y, -kTop), kTop) : 0.f;
-        top = fmaxf(top, fmaxf(fabsf(x[i].x), fabsf(x[i].y)));
-      }
-    }
-    for (int o = 1; o < lanes; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (n_in == 0) continue;
-    const __half hs = __float2half_rn(__fdiv_rn(top, 127.f));
-    const float s = __half2float(hs);
-    uint32_t cw[4] = {0, 0, 0, 0};
-    if (s > 0.f) codes16(x, s, cw);
-    const int64_t cell_row = slot * p.n_heads + head;
-    int8_t *to = p.cells + cell_row * d;
-    *reinterpret_cast<uint2 *>(to + 8 * c0) = make_uint2(cw[0], cw[1]);
-    if (n_in >= 2) *reinterpret_cast<uint2 *>(to + 8 * c1) = make_uint2(cw[2], cw[3]);
-    if (l == 0) p.scales[cell_row] = __half_as_ushort(hs);
-  }
-}
-
-template <int TYPE>
-__global__ void __launch_bounds__(RT, 4) get_rows_kernel(const p4::RowsArgs a, const int heads_per, const int k_groups) {
-  const int w = static_cast<int>(blockIdx.y) >= k_groups, group = blockIdx.y - (w ? k_groups : 0);
-  const int d = a.head_dim[w], sh = d <= 64 ? 2 : d <= 128 ? 3 : 4, lanes = 1 << sh, l = threadIdx.x & (lanes - 1);
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * (RT >> sh) + (threadIdx.x >> sh);
-  if (row >= a.n_rows) return;
-  const int64_t slot = __ldg(a.slots + row);
-  if (static_cast<uint64_t>(slot) >= static_cast<uint64_t>(a.n_cells)) {
-    if (slot != -1 && l == 0) set_status(a.status, TQ_ERR_DEVICE_CHECK);
-    return;
-  }
-  const int n_in = (8 * l < d) + (8 * (l + lanes) < d);
-  if (n_in == 0) return;
-  int head = group * heads_per;
-  const int heads = min(a.n_heads[w], head + heads_per);
-  int64_t cell_row = slot * a.n_heads[w] + head, to = row * a.stride[w] + static_cast<int64_t>(head) * d + 8 * l;
-  uint2 c[2], next[2];
-  uint16_t s_next = 0;
-  next[1] = make_uint2(0, 0);
-  auto fetch = [&]() {
-    const uint8_t *p = a.codes[w] + cell_row * d + 8 * l;
-    s_next = __ldcs(a.scales[w] + cell_row);
-    next[0] = __ldcs(reinterpret_cast<const uint2 *>(p));
-    if (n_in >= 2) next[1] = __ldcs(reinterpret_cast<const uint2 *>(p + 8 * lanes));
-  };
-  fetch();
-  for (; head < heads; ++head, to += d) {
-    c[0] = next[0];
-    c[1] = next[1];
-    const __half hs = __ushort_as_half(s_next);
-    ++cell_row;
-    if (head + 1 < heads) fetch();
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      if (k >= n_in) break;
-      const uint32_t u[2] = {c[k].x ^ 0x80808080u, c[k].y ^ 0x80808080u};              // code + 128
-      if (TYPE == TQ_F16) {
-        // 1024 + 128 + code as binary16, 1152 taken off; the product, rounded once, is that of fp32 rounded once
-        uint32_t r[4];
+      if (ROT == kHalf && turned[0]) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint32_t v = prmt_b32(u[i / 2], 0x64646464u, i & 1 ? 0x4342u : 0x4140u);
-          const __half2 y = __hmul2(__hsub2(*reinterpret_cast<const __half2 *>(&v), __float2half2_rn(1152.f)), __half2half2(hs));
-          r[i] = *reinterpret_cast<const uint32_t *>(&y);
+          const float2 c = make_float2(ca[2 * i], ca[2 * i + 1]), s = make_float2(sa[2 * i], sa[2 * i + 1]);
+          const float2 u = x[i], v = x[4 + i];
+          x[i] = sub2(mul2(u, c), mul2(v, s));
+          x[4 + i] = fma2(u, s, mul2(v, c));
         }
-        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.dst[w]) + to + 8 * lanes * k) = make_uint4(r[0], r[1], r[2], r[3]);
-      } else {
-        const float s = __half2float(hs);
-        float2 y[4];
+      }
+      if (ROT == kInterleaved) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {                      // a byte in the low bits of 2^23 is the float 2^23 + code + 128
-          const uint32_t v0 = prmt_b32(u[i / 2], 0x4b000000u, i & 1 ? 0x7442u : 0x7440u);
-          const uint32_t v1 = prmt_b32(u[i / 2], 0x4b000000u, i & 1 ? 0x7443u : 0x7441u);
-          y[i] = mul2(make_float2(s, s), add2(make_float2(__uint_as_float(v0), __uint_as_float(v1)),
-                                              make_float2(-8388736.f, -8388736.f)));
+        for (int k = 0; k < 2; ++k)
+          if (turned[k]) {
+            const int n = h - 4 * (k ? c1 : c0);             // its pairs that turn
+#pragma unroll
+            for (int i = 4 * k; i < 4 * k + 4; ++i) {
+              const float2 u = x[i], v = make_float2(fmaf(-u.y, sa[i % NA], u.x * ca[i % NA]), fmaf(u.x, sa[i % NA], u.y * ca[i % NA]));
+              if (n >= 4 || (i & 3) < n) x[i] = v;
+            }
+          }
+      }
+      if (ROT == kHalfAny && turns) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int e = 8 * (i < 8 ? c0 : c1) + (i & 7), k = ROT == kHalfAny ? i : 0;
+          float &v = i & 1 ? x[i / 2].y : x[i / 2].x;
+          if (e < a.rot) v = e < h ? fmaf(-y[k], sa[k % NA], v * ca[k % NA]) : fmaf(y[k], sa[k % NA], v * ca[k % NA]);
         }
-        store8<TYPE>(a.dst[w], to + 8 * lanes * k, y);
+      }
+      if (!p.cells) {
+        const int64_t to = row * p.dst_stride + static_cast<int64_t>(this_head) * d;
+        if (n_in >= 1) store8<TYPE>(p.dst, to + 8 * c0, x);
+        if (n_in >= 2) store8<TYPE>(p.dst, to + 8 * c1, x + 4);
+        continue;
+      }
+      // ---- int8 (elements beyond the row are zeros)
+      float top = top3(x[0].x, x[0].y, x[1].x);
+      top = top3(top, x[1].y, x[2].x);
+      top = top3(top, x[2].y, x[3].x);
+      top = top3(top, x[3].y, x[4].x);
+      top = top3(top, x[4].y, x[5].x);
+      top = top3(top, x[5].y, x[6].x);
+      top = top3(top, x[6].y, x[7].x);
+      top = top3(top, x[7].y, x[7].y);
+      if (!(top <= kTop)) {             // a stored value is finite: NaN counts as 0, larger magnitudes as the largest
+        top = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          x[i].x = x[i].x == x[i].x ? fminf(fmaxf(x[i].x, -kTop), kTop) : 0.f;
+          x[i].y = x[i].y == x[i].y ? fminf(fmaxf(x[i].y, -kTop), kTop) : 0.f;
+          top = fmaxf(top, fmaxf(fabsf(x[i].x), fabsf(x[i].y)));
+        }
+      }
+      for (int o = 1; o < lanes; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      if (n_in == 0) continue;
+      // (top / 127, rounded correctly, as the codes' quotients are)
+      const float q0 = top * (1.f / 127.f);
+      const __half hs = __float2half_rn(fmaf(fmaf(q0, -127.f, top), 1.f / 127.f, q0));
+      const float s = __half2float(hs);
+      uint32_t cw[4] = {0, 0, 0, 0};
+      if (s > 0.f) codes16(x, s, cw);
+      int8_t *to = p.cells + static_cast<uint64_t>(cell_row) * d;
+      *reinterpret_cast<uint2 *>(to + 8 * c0) = make_uint2(cw[0], cw[1]);
+      if (n_in >= 2) *reinterpret_cast<uint2 *>(to + 8 * c1) = make_uint2(cw[2], cw[3]);
+      if (l == 0) p.scales[cell_row] = __half_as_ushort(hs);
+      ++cell_row;
+    }
+    cp_wait<0>();                     // (the ring is filled anew)
+  }
+}
+
+struct GetArgs {
+  p4::RowsArgs rows;
+  Units units;
+};
+
+template <int TYPE>
+__global__ void __launch_bounds__(RT, kGet) get_rows_kernel(const GetArgs args) {
+  const p4::RowsArgs &a = args.rows;
+  after_earlier_launches();
+  for (Share u = share_of(args.units); u.at < u.end;) {
+    const int w = u.at >= args.units.part[0];
+    const int64_t unit = w ? u.at - args.units.part[0] : u.at;
+    const int d = a.head_dim[w], sh = lane_shift(d), lanes = 1 << sh, l = threadIdx.x & (lanes - 1);
+    const int64_t tile = quotient(unit, a.n_heads[w]), row = tile * (RT >> sh) + (threadIdx.x >> sh);
+    int head = static_cast<int>(unit - tile * a.n_heads[w]);
+    const int heads = static_cast<int>(min(static_cast<int64_t>(a.n_heads[w]), head + (u.end - u.at)));
+    u.at += heads - head;
+    if (row >= a.n_rows) continue;
+    const int64_t slot = __ldg(a.slots + row);
+    if (static_cast<uint64_t>(slot) >= static_cast<uint64_t>(a.n_cells)) {
+      if (slot != -1 && l == 0) set_status(a.status, TQ_ERR_DEVICE_CHECK);
+      continue;
+    }
+    const int n_in = (8 * l < d) + (8 * (l + lanes) < d);
+    if (n_in == 0) continue;
+    int64_t cell_row = slot * a.n_heads[w] + head, to = row * a.stride[w] + static_cast<int64_t>(head) * d + 8 * l;
+    uint2 c[2], next[2];
+    uint16_t s_next = 0;
+    next[1] = make_uint2(0, 0);
+    auto fetch = [&]() {
+      const uint8_t *p = a.codes[w] + cell_row * d + 8 * l;
+      s_next = __ldcs(a.scales[w] + cell_row);
+      next[0] = __ldcs(reinterpret_cast<const uint2 *>(p));
+      if (n_in >= 2) next[1] = __ldcs(reinterpret_cast<const uint2 *>(p + 8 * lanes));
+    };
+    fetch();
+    for (; head < heads; ++head, to += d) {
+      c[0] = next[0];
+      c[1] = next[1];
+      const __half hs = __ushort_as_half(s_next);
+      ++cell_row;
+      if (head + 1 < heads) fetch();
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        if (k >= n_in) break;
+        const uint32_t u[2] = {c[k].x ^ 0x80808080u, c[k].y ^ 0x80808080u};              // code + 128
+        if (TYPE == TQ_F16) {
+          // 1024 + 128 + code as binary16, 1152 taken off; the product, rounded once, is that of fp32 rounded once
+          uint32_t r[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t v = prmt_b32(u[i / 2], 0x64646464u, i & 1 ? 0x4342u : 0x4140u);
+            const __half2 y = __hmul2(__hsub2(*reinterpret_cast<const __half2 *>(&v), __float2half2_rn(1152.f)), __half2half2(hs));
+            r[i] = *reinterpret_cast<const uint32_t *>(&y);
+          }
+          *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.dst[w]) + to + 8 * lanes * k) = make_uint4(r[0], r[1], r[2], r[3]);
+        } else {
+          const float s = __half2float(hs);
+          float2 y[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {                      // a byte in the low bits of 2^23 is the float 2^23 + code + 128
+            const uint32_t v0 = prmt_b32(u[i / 2], 0x4b000000u, i & 1 ? 0x7442u : 0x7440u);
+            const uint32_t v1 = prmt_b32(u[i / 2], 0x4b000000u, i & 1 ? 0x7443u : 0x7441u);
+            y[i] = mul2(make_float2(s, s), add2(make_float2(__uint_as_float(v0), __uint_as_float(v1)),
+                                                make_float2(-8388736.f, -8388736.f)));
+          }
+          store8<TYPE>(a.dst[w], to + 8 * lanes * k, y);
+        }
       }
     }
   }
 }
 
-// Heads that a thread goes through: as many as leave enough CTAs for the SMs (and no more than 65535 in a grid's y).
-int heads_of(int64_t row_ctas, const int *n_heads, int parts, int *groups, int *total) {
-  for (int per = MAXH;; per /= 2) {
-    *total = 0;
-    for (int i = 0; i < parts; ++i) *total += groups[i] = (n_heads[i] + per - 1) / per;
-    if (per == 1 || row_ctas * *total >= kEnough * sm_count()) {
-      while (*total > 65535) {
-        per *= 2;
-        *total = 0;
-        for (int i = 0; i < parts; ++i) *total += groups[i] = (n_heads[i] + per - 1) / per;
-      }
-      return per;
-    }
+// The line of work of up to three tensors, cut for at most `ctas` CTAs; the CTAs that it takes.
+unsigned cut(Units &u, const int *n_heads, const int *head_dim, int parts, int64_t n_rows, int ctas) {
+  int64_t n = 0;
+  for (int i = 0; i < 3; ++i) {
+    const int rows = i < parts ? RT >> lane_shift(head_dim[i]) : 1;
+    u.part[i] = i < parts ? (n_rows + rows - 1) / rows * n_heads[i] : 0;
+    n += u.part[i];
   }
+  const int64_t grid = n < ctas ? n : ctas;
+  u.per = n / grid;
+  u.more = static_cast<int32_t>(n % grid);
+  return static_cast<unsigned>(grid);
 }
 
-int64_t row_ctas_of(int64_t n_rows, int head_dim) {
-  const int rows = RT / (p4::row_width(head_dim) / 16);
-  return (n_rows + rows - 1) / rows;
+template <int TYPE, int ROT>
+cudaError_t launch_step_t(StepArgs &a, cudaStream_t s) {
+  int n_heads[3], head_dim[3];
+  for (int i = 0; i < 3; ++i) {
+    n_heads[i] = a.part[i].n_heads;
+    head_dim[i] = a.part[i].head_dim;
+  }
+  const unsigned grid = cut(a.units, n_heads, head_dim, 3, a.n_rows, ctas_of(ROT) * sm_count());
+  return p4::launch_beside(step_rows_kernel<TYPE, ROT>, grid, RT, 0, s, a);
 }
 
 template <int TYPE>
-void launch_step(const StepArgs &a, dim3 grid, cudaStream_t s) {
-  if (!a.positions) step_rows_kernel<TYPE, kNone><<<grid, RT, 0, s>>>(a);
-  else if (a.layout == TQ_ROPE_INTERLEAVED) step_rows_kernel<TYPE, kInterleaved><<<grid, RT, 0, s>>>(a);
-  else if (a.rot % 16 == 0) step_rows_kernel<TYPE, kHalf><<<grid, RT, 0, s>>>(a);
-  else step_rows_kernel<TYPE, kHalfAny><<<grid, RT, 0, s>>>(a);
+cudaError_t launch_step(StepArgs &a, cudaStream_t s) {
+  if (!a.positions) return launch_step_t<TYPE, kNone>(a, s);
+  if (a.layout == TQ_ROPE_INTERLEAVED) return launch_step_t<TYPE, kInterleaved>(a, s);
+  return a.rot % 16 == 0 ? launch_step_t<TYPE, kHalf>(a, s) : launch_step_t<TYPE, kHalfAny>(a, s);
 }
 
 }  // namespace
 
 cudaError_t launch_step_rows(int type, const StepArgs &args, cudaStream_t s) {
   StepArgs a = args;
-  int n_heads[3], total = 0;
-  int64_t x = 0;
-  for (int i = 0; i < 3; ++i) {
-    n_heads[i] = a.part[i].n_heads;
-    const int64_t r = n_heads[i] ? row_ctas_of(a.n_rows, a.part[i].head_dim) : 0;
-    if (r > x) x = r;
-  }
-  a.heads_per = heads_of(x, n_heads, 3, a.groups, &total);
-  const dim3 grid(static_cast<unsigned>(x), static_cast<unsigned>(total));
-  switch (type) {
-    case TQ_F32: launch_step<TQ_F32>(a, grid, s); break;
-    case TQ_F16: launch_step<TQ_F16>(a, grid, s); break;
-    default: launch_step<TQ_BF16>(a, grid, s); break;
-  }
-  return cudaGetLastError();
+  return type == TQ_F32 ? launch_step<TQ_F32>(a, s) : type == TQ_F16 ? launch_step<TQ_F16>(a, s) : launch_step<TQ_BF16>(a, s);
 }
 
 cudaError_t launch_get_rows(int type, const p4::RowsArgs &a, cudaStream_t s) {
-  int groups[2], total = 0;
-  const int64_t k = row_ctas_of(a.n_rows, a.head_dim[0]), v = row_ctas_of(a.n_rows, a.head_dim[1]), x = k > v ? k : v;
-  const int per = heads_of(x, a.n_heads, 2, groups, &total);
-  const dim3 grid(static_cast<unsigned>(x), static_cast<unsigned>(total));
-  switch (type) {
-    case TQ_F32: get_rows_kernel<TQ_F32><<<grid, RT, 0, s>>>(a, per, groups[0]); break;
-    case TQ_F16: get_rows_kernel<TQ_F16><<<grid, RT, 0, s>>>(a, per, groups[0]); break;
-    default: get_rows_kernel<TQ_BF16><<<grid, RT, 0, s>>>(a, per, groups[0]); break;
-  }
-  return cudaGetLastError();
+  GetArgs g;
+  g.rows = a;
+  const unsigned grid = cut(g.units, a.n_heads, a.head_dim, 2, a.n_rows, kGet * sm_count());
+  return type == TQ_F32   ? p4::launch_beside(get_rows_kernel<TQ_F32>, grid, RT, 0, s, g)
+         : type == TQ_F16 ? p4::launch_beside(get_rows_kernel<TQ_F16>, grid, RT, 0, s, g)
+                          : p4::launch_beside(get_rows_kernel<TQ_BF16>, grid, RT, 0, s, g);
 }
 
 }  // namespace i8
