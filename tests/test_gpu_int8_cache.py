@@ -103,22 +103,38 @@ def test_rope_rows(dtype, layout, d, rot):
 
 
 @pytest.mark.parametrize("n", [1, 2, 33, 700, 5000])
-@pytest.mark.parametrize("hq,hk", [(1, 1), (7, 1), (32, 8), (9, 3), (16, 16)])
-def test_rope_rows_of_any_number(n, hq, hk):
+@pytest.mark.parametrize("hq,hk,d,rot,layout,dtype", [(1, 1, 64, 64, "half", "bfloat16"), (7, 1, 64, 64, "half", "bfloat16"),
+                                                      (32, 8, 128, 128, "half", "float16"), (9, 3, 80, 20, "half", "float16"),
+                                                      (16, 16, 48, 24, "interleaved", "bfloat16"),
+                                                      (5, 2, 256, 256, "half", "float32"), (6, 2, 40, 20, "half", "float32"),
+                                                      (8, 4, 128, 64, "interleaved", "float32")])
+def test_rope_rows_of_any_number(n, hq, hk, d, rot, layout, dtype):
     # every split of rows and heads over threads gives the same bits as a row and a head by themselves
     import torch
     import quantized_kv_cache_tq_gb300 as tq
     g = torch.Generator(device="cuda").manual_seed(n)
-    rope = tq.Rope(64, 500000.0, scaling="pairs", factor=8.0, original_len=8192.0)
-    q = torch.randn((n, hq, 64), generator=g, device="cuda").bfloat16()
-    k = torch.randn((n, hk, 64), generator=g, device="cuda").bfloat16()
+    rope = tq.Rope(rot, 500000.0, layout=layout, scaling="pairs", factor=8.0, original_len=8192.0)
+    q = torch.randn((n, hq, d), generator=g, device="cuda").to(getattr(torch, dtype))
+    k = torch.randn((n, hk, d), generator=g, device="cuda").to(q.dtype)
     pos = torch.randint(0, 1 << 20, (n,), generator=g, device="cuda", dtype=torch.int32)
-    a, b = tq.rope_rows(rope, pos, q, k)
-    _check_turned(a[:50], _np(q[:50]), pos[:50].cpu().numpy(), rope, "bfloat16")
-    for i in {0, n // 2, n - 1}:
+    if n > 5:
+        pos[n // 3::7] = -1
+    live = (pos >= 0).tolist()
+    a, b = tq.rope_rows(rope, pos, q, k, q_out=torch.full_like(q, 7.0), k_out=torch.full_like(k, 7.0))
+    at = [i for i in range(n) if live[i]]
+    at = sorted({at[(len(at) - 1) * i // 40] for i in range(41)})
+    for x, y in ((q, a), (k, b)):
+        _check_turned(y[at], _np(x[at]), pos[at].cpu().numpy(), rope, dtype)
+        assert bool((y[pos < 0] == 7).all()) and bool((y[pos >= 0] != 7).any(-1).all())
+    for i in at[::8]:
         for h in {0, hq - 1}:
             assert torch.equal(tq.rope_rows(rope, pos[i:i + 1], q[i:i + 1, h:h + 1].contiguous())[0, 0], a[i, h])
         assert torch.equal(tq.rope_rows(rope, pos[i:i + 1], k[i:i + 1])[0], b[i])
+    # in place, all at once
+    c, e = q.clone(), k.clone()
+    tq.rope_rows(rope, pos, c, e, q_out=c, k_out=e)
+    assert torch.equal(c[pos >= 0], a[pos >= 0]) and torch.equal(e[pos >= 0], b[pos >= 0])
+    assert torch.equal(c[pos < 0], q[pos < 0]) and torch.equal(e[pos < 0], k[pos < 0])
 
 
 @pytest.mark.parametrize("dtype", ["float32", "float16", "bfloat16"])
@@ -264,6 +280,48 @@ def test_set_and_get_rows(dtype, dk, dv):
     assert k2.dtype == torch.float16 and not k2[5].any() and v2.shape == (n, hv, dv)
 
 
+@pytest.mark.parametrize("n,hk,hv,dk,dv,dtype", [(5000, 8, 8, 128, 128, "float16"), (3001, 3, 1, 80, 256, "bfloat16"),
+                                                 (2500, 2, 5, 256, 16, "float32"), (12000, 1, 1, 64, 64, "float16")])
+def test_rows_of_large_calls(n, hk, hv, dk, dv, dtype):
+    # shares that begin and end anywhere, rows without cells among them
+    import torch
+    import quantized_kv_cache_tq_gb300 as tq
+    rng = np.random.default_rng(n)
+    cells = n + 100
+    xk, xv = _gpu(_rows(rng, n, hk, dk), dtype), _gpu(_rows(rng, n, hv, dv), dtype)
+    slots = rng.permutation(cells)[:n].astype(np.int64)
+    slots[::9] = -1
+    kc, vc = I.Cache(hk, dk, cells), I.Cache(hv, dv, cells)
+    kc.set_rows(_np(xk), slots)
+    vc.set_rows(_np(xv), slots)
+    gk, gv, gs = tq.Int8Cache(hk, dk, cells), tq.Int8Cache(hv, dv, cells), _gpu(slots)
+    tq.int8_set_rows(gk, gv, xk, xv, gs)
+    out = tq.int8_get_rows(gk, gv, gs, k_out=torch.full_like(xk, 5.0), v_out=torch.full_like(xv, 5.0))
+    for g, c, o in ((gk, kc, out[0]), (gv, vc, out[1])):
+        assert np.array_equal(g.rows.cpu().numpy(), c.rows)
+        assert np.array_equal(g.scales.cpu().numpy().view(np.int16), c.scales.view(np.int16))
+        want = torch.from_numpy(I.values(c.rows[slots], c.scales[slots]).astype(np.float32)).to(o.dtype)
+        want[slots < 0] = 5.0
+        assert torch.equal(o.cpu(), want)
+
+
+def test_every_scale():
+    # rows whose scale is each binary16 number from 2^-16 on: the codes' quotients are the correctly rounded ones
+    import torch
+    import quantized_kv_cache_tq_gb300 as tq
+    s = np.arange(0x0100, 0x7c00, dtype=np.uint16).view(np.float16).astype(np.float32)
+    rng = np.random.default_rng(1)
+    x = (rng.integers(-254, 255, (len(s), 1, 32)) / 2 + rng.choice([0, 2.0 ** -16, -2.0 ** -16], (len(s), 1, 32))) * s[:, None, None]
+    x = x.astype(np.float32)                                 # codes' borders, and just beside them
+    x[:, :, 3] = 127 * s[:, None]
+    c = I.Cache(1, 32, len(s))
+    c.set_rows(x, np.arange(len(s)))
+    g, h = tq.Int8Cache(1, 32, len(s)), tq.Int8Cache(1, 32, len(s))
+    tq.int8_set_rows(g, h, _gpu(x), _gpu(x), torch.arange(len(s), device="cuda"))
+    assert np.array_equal(g.scales.cpu().numpy().view(np.int16), c.scales.view(np.int16))
+    assert np.array_equal(g.rows.cpu().numpy(), c.rows)
+
+
 def test_rows_out_of_range_and_special_values():
     import torch
     import quantized_kv_cache_tq_gb300 as tq
@@ -371,6 +429,39 @@ def test_rope_set_rows(dtype, layout, dk, dv, rot, norm):
     assert torch.equal(z[pos >= 0], q_out[pos >= 0]) and torch.equal(z[pos < 0], q[pos < 0])
 
 
+@pytest.mark.parametrize("hq,hk,d,dv,rot,layout,dtype", [(32, 8, 128, 128, 128, "half", "bfloat16"),
+                                                         (9, 3, 80, 64, 20, "half", "float16"),
+                                                         (4, 1, 64, 256, 32, "interleaved", "float32")])
+def test_rope_set_rows_of_large_calls(hq, hk, d, dv, rot, layout, dtype):
+    # a large call's rows are those of single ones, bit for bit
+    import torch
+    import quantized_kv_cache_tq_gb300 as tq
+    g = torch.Generator(device="cuda").manual_seed(d)
+    n, cells = 3333, 4000
+    rope = tq.Rope(rot, layout=layout)
+    q, k, v = (torch.randn((n, h, e), generator=g, device="cuda").to(getattr(torch, dtype)) for h, e in ((hq, d), (hk, d), (hk, dv)))
+    norm = 1 + 0.1 * torch.randn((d,), generator=g, device="cuda")
+    pos = torch.randint(0, 100000, (n,), generator=g, device="cuda", dtype=torch.int32)
+    slots = torch.randperm(cells, generator=g, device="cuda")[:n]
+    pos[5::11], slots[7::13] = -1, -1
+    kc, vc = tq.Int8Cache(hk, d, cells), tq.Int8Cache(hk, dv, cells)
+    out = tq.int8_rope_set_rows(kc, vc, rope, pos, q, k, v, slots, q_norm=norm, k_norm=norm)
+    k1, v1 = tq.Int8Cache(hk, d, cells), tq.Int8Cache(hk, dv, cells)
+    alone = torch.zeros_like(q)
+    for i in range(0, n, 101):
+        one = slice(i, i + 7)
+        alone[one] = tq.int8_rope_set_rows(k1, v1, rope, pos[one], q[one], k[one], v[one], slots[one], q_norm=norm, k_norm=norm)
+        assert torch.equal(out[one], alone[one])
+        at = slots[one][(slots[one] >= 0) & (pos[one] >= 0)]
+        for x, y in ((kc, k1), (vc, v1)):
+            assert torch.equal(x.rows[at], y.rows[at]) and torch.equal(x.scales[at], y.scales[at])
+    live = (pos >= 0) & (slots >= 0)
+    held = torch.zeros(cells, dtype=torch.bool, device="cuda")
+    held[slots[live]] = True
+    assert bool(vc.rows[held].any(-1).any(-1).all()) and not vc.rows[~held].any() and not kc.rows[~held].any()
+    assert not out[pos < 0].any()
+
+
 def test_rope_set_rows_bad_slots_and_positions():
     import torch
     import quantized_kv_cache_tq_gb300 as tq
@@ -459,6 +550,34 @@ def test_decode_splits(n_seq, length):
     b = Batch(length, lens, 1, 64, 64, 16)
     q = b.query(2, "float16")
     b.check(tq.int8_decode(b.gk, b.gv, b.gt, b.gl, q, 0.125, page_size=16), q, 0.125, "float16")
+
+
+@pytest.mark.parametrize("dk,dv,hkv,group,page,dtype", [(128, 128, 8, 4, 32, "bfloat16"), (64, 64, 4, 8, 16, "float16"),
+                                                        (128, 128, 4, 12, 1, "float16"), (256, 256, 2, 3, 16, "bfloat16"),
+                                                        (192, 128, 6, 2, 8, "float16"), (80, 80, 8, 1, 64, "bfloat16")])
+def test_decode_of_batches_that_take_heads_side_by_side(dk, dv, hkv, group, page, dtype):
+    # enough work for several heads a CTA, items that many CTAs share, empty sequences among them
+    import quantized_kv_cache_tq_gb300 as tq
+    rng = np.random.default_rng(dk * group)
+    lens = [3000] + [int(x) for x in rng.integers(0, 3000, 30)] + [0, 1, 0, 64, 65] + [int(x) for x in rng.integers(1, 90, 8)]
+    if hkv * group < 10:
+        lens = lens + lens
+    b = Batch(dk, lens, hkv, dk, dv, page)
+    q = b.query(hkv * group, dtype)
+    out = tq.int8_decode(b.gk, b.gv, b.gt, b.gl, q, dk ** -0.5, page_size=page)
+    b.check(out, q, dk ** -0.5, dtype)
+
+
+@pytest.mark.parametrize("gain", [0.05, 1.0])
+def test_decode_error_in_binary16_is_the_outputs_own(gain):
+    # weights of 22 bits and exact values leave little but the rounding of the output: 2^-11 / sqrt(3) relative rms of
+    # numbers spread over a binade's half steps (at most), and a tenth for the fp32 sums
+    import quantized_kv_cache_tq_gb300 as tq
+    b = Batch(31, [20000], 2, 128, 128, 16)
+    q = b.query(8, "float16", gain)
+    out = _np(tq.int8_decode(b.gk, b.gv, b.gt, b.gl, q, 128 ** -0.5, page_size=16))
+    ref, _ = I.attention(b.k, b.v, b.table, b.lens, 16, _np(q), 128 ** -0.5, 22)
+    assert np.sqrt(((out - ref) ** 2).mean()) <= 1.1 * 2.0 ** -11 / 3 ** 0.5 * np.sqrt((ref ** 2).mean())
 
 
 @pytest.mark.parametrize("v_gain,k_gain,q_gain,scale", [(1e-6, 1.0, 1.0, 0.1), (2e4, 1.0, 1.0, 0.1), (1.0, 1.0, 1e3, 1e-4),
