@@ -11,7 +11,7 @@
 //   256), so that every access is of 8 or 16 bytes and neighbouring lanes share
 //   sectors.  Which two eights: in the half layout those that turn together, so that
 //   no element looks for its partner in another lane (half_any, where half of rot_dim
-//   is no multiple of 8: the partners are read a second time, element by element).
+//   is no multiple of 8: by way of shared memory).
 // - The angle is an integer product: the position times the pair's 64-bit fraction of
 //   a turn, of which the upper 32 bits below the whole turns are kept.  Sine and cosine
 //   are then polynomials on an eighth of a turn either way (turn_sincos), eight per
@@ -47,14 +47,18 @@ struct Raw {
   uint4 u[TYPE == TQ_F32 ? 2 : 1];
 };
 
-// (nothing there: zeros.  Eights of 32-bit elements are copied in two halves of a sector, which meet in L1.)
+// 16 bytes, or (n = 0) zeros.  Eights of 32-bit elements are copied in two halves of a sector, which meet in L1.
 template <int TYPE>
-__device__ __forceinline__ void cp16(uint4 *to, const void *from, bool there) {
-  const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(to)), n = there ? 16 : 0;
+__device__ __forceinline__ void cp16(uint32_t to, const void *from, uint32_t n) {
   if (TYPE == TQ_F32)
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(at), "l"(from), "r"(n) : "memory");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(n) : "memory");
   else
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at), "l"(from), "r"(n) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(n) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t at) {
+  uint4 u;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "r"(at) : "memory");
+  return u;
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -98,13 +102,6 @@ __device__ __forceinline__ void store8(void *dst, int64_t at, const float2 *x) {
     *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(dst) + at) = make_uint4(r[0], r[1], r[2], r[3]);
   }
 }
-template <int TYPE>
-__device__ __forceinline__ float load1(const void *p, int64_t i) {
-  if (TYPE == TQ_F32) return __ldcs(static_cast<const float *>(p) + i);
-  const uint16_t u = __ldcs(static_cast<const uint16_t *>(p) + i);
-  return TYPE == TQ_F16 ? __half2float(__ushort_as_half(u)) : __uint_as_float(static_cast<uint32_t>(u) << 16);
-}
-
 // sin and cos of a 32-bit fraction of a turn: the nearest quarter turn taken off exactly, then polynomials in the
 // angle t on [-pi/4, pi/4], fitted for the least largest error (sine 3.6e-9 relative, cosine 1e-10; what counts is the
 // rounding of t and of the sums, some 1e-7).
@@ -182,6 +179,7 @@ template <int TYPE, int ROT>
 __global__ void __launch_bounds__(RT, ctas_of(ROT)) step_rows_kernel(const StepArgs a) {
   constexpr int S = kStages, W = TYPE == TQ_F32 ? 2 : 1;        // stages; 16-byte words of an eight
   __shared__ uint4 ring[S][2 * W][RT];            // each thread's own
+  __shared__ float line[ROT == kHalfAny ? RT * 16 + 32 * 4 : 1];      // half_any: rows, where the partners are found
   after_earlier_launches();
   for (Share u = share_of(a.units); u.at < u.end;) {
     // ---- units of one tensor: from head `head` of the rows of tile `tile` on
@@ -223,31 +221,34 @@ __global__ void __launch_bounds__(RT, ctas_of(ROT)) step_rows_kernel(const StepA
     look_up(row);
 
     // ---- copies of the next units' elements, on their way while this one is worked on
+    // (rows behind the last one read that one again; eights behind the head dim are zeros)
     constexpr int size = TYPE == TQ_F32 ? 4 : 2;
     auto row_at = [&](uint32_t r, int hd) {
-      return static_cast<const char *>(p.src) + (r * p.src_stride + static_cast<int64_t>(hd) * d + 8 * c0) * size;
+      return static_cast<const char *>(p.src) +
+             (min(r, n_rows - 1) * p.src_stride + static_cast<int64_t>(hd) * d + (n_row >= 1 ? 8 * c0 : 0)) * size;
     };
     const char *from = row_at(row, head);
+    const int to_c1 = n_row >= 2 ? 8 * (c1 - c0) * size : 0, n_heads = p.n_heads;
+    const uint32_t size0 = n_row >= 1 ? 16 : 0, size1 = n_row >= 2 ? 16 : 0;
     uint32_t from_row = row;
-    int from_left = left, from_head = head, fill = 0;
+    int from_left = left, from_head = head;
+    const uint32_t ring_at = static_cast<uint32_t>(__cvta_generic_to_shared(&ring[0][0][threadIdx.x]));
+    constexpr uint32_t kStage = sizeof(ring[0]), kWord = sizeof(ring[0][0]);
+    uint32_t fill = ring_at;
     auto fetch = [&]() {
-      if (from_left > 0) {
-        const bool there = from_row < n_rows;
-        const char *q0 = there && n_row >= 1 ? from : static_cast<const char *>(p.src);
-        const char *q1 = there && n_row >= 2 ? from + 8 * (c1 - c0) * size : static_cast<const char *>(p.src);
+      if (--from_left >= 0) {
 #pragma unroll
         for (int i = 0; i < W; ++i) {
-          cp16<TYPE>(&ring[fill][i][threadIdx.x], q0 + 16 * i, there && n_row >= 1);
-          cp16<TYPE>(&ring[fill][W + i][threadIdx.x], q1 + 16 * i, there && n_row >= 2);
+          cp16<TYPE>(fill + i * kWord, from + 16 * i, size0);
+          cp16<TYPE>(fill + (W + i) * kWord, from + to_c1 + 16 * i, size1);
         }
-        --from_left;
         from += d * size;
-        if (++from_head == p.n_heads) {
+        if (++from_head == n_heads) {
           from_head = 0;
           from_row += RT >> sh;
           from = row_at(from_row, 0);
         }
-        fill = fill == S - 1 ? 0 : fill + 1;
+        fill = fill == ring_at + (S - 1) * kStage ? ring_at : fill + kStage;
       }
       cp_commit();
     };
@@ -258,7 +259,8 @@ __global__ void __launch_bounds__(RT, ctas_of(ROT)) step_rows_kernel(const StepA
     float ca[NA], sa[NA];
     bool turned[2], ok = false;                                                        // whether an eight turns at all
     uint32_t cell_row = 0;            // (rows of a plane are less than 2^32)
-    int n_in = 0, stage = 0;
+    int n_in = 0;
+    uint32_t stage = ring_at;
     auto take_up = [&]() {            // the row: its position, its cell, its angles
       // half: of pairs 8 c0 ..; interleaved: of pairs 4 c0 .. and 4 c1 ..; half_any: of each element
       auto pair_of = [&](int i) {
@@ -275,7 +277,7 @@ __global__ void __launch_bounds__(RT, ctas_of(ROT)) step_rows_kernel(const StepA
       const bool cell_ok = !p.cells || static_cast<uint64_t>(slot) < static_cast<uint64_t>(a.n_cells);
       if (l == 0 && (pos < -1 || (!cell_ok && slot != -1))) set_status(a.status, TQ_ERR_DEVICE_CHECK);
       ok = pos >= 0 && cell_ok;
-      cell_row = static_cast<uint32_t>(slot) * p.n_heads + head;
+      cell_row = static_cast<uint32_t>(slot) * n_heads + head;
       n_in = ok ? n_row : 0;
       turned[0] = turned[1] = false;
       if (turns && ok) {
@@ -294,7 +296,7 @@ __global__ void __launch_bounds__(RT, ctas_of(ROT)) step_rows_kernel(const StepA
 
     // ---- unit after unit
     for (bool fresh = true; left > 0; --left) {
-      if (head == p.n_heads) {
+      if (head == n_heads) {
         head = 0;
         row += RT >> sh;
         fresh = true;
@@ -306,23 +308,14 @@ __global__ void __launch_bounds__(RT, ctas_of(ROT)) step_rows_kernel(const StepA
       Raw<TYPE> r0, r1;
 #pragma unroll
       for (int i = 0; i < W; ++i) {
-        r0.u[i] = ring[stage][i][threadIdx.x];
-        r1.u[i] = ring[stage][W + i][threadIdx.x];
+        r0.u[i] = lds16(stage + i * kWord);
+        r1.u[i] = lds16(stage + (W + i) * kWord);
       }
-      stage = stage == S - 1 ? 0 : stage + 1;
+      stage = stage == ring_at + (S - 1) * kStage ? ring_at : stage + kStage;
       fetch();
       float2 x[8];                      // elements 8 c0 .. and 8 c1 ..
       unpack8<TYPE>(r0, x);
       unpack8<TYPE>(r1, x + 4);
-      float y[ROT == kHalfAny ? 16 : 1];        // half_any: the partners
-      if (ROT == kHalfAny && turns) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int e = 8 * (i < 8 ? c0 : c1) + (i & 7);
-          y[ROT == kHalfAny ? i : 0] = ok && e < a.rot ? load1<TYPE>(p.src, row * p.src_stride + this_head * d + (e < h ? e + h : e - h)) : 0.f;
-        }
-        __syncwarp();                   // rows that turn in place: everything is read before something is written
-      }
       if (p.norm) {
         float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll
@@ -341,13 +334,6 @@ __global__ void __launch_bounds__(RT, ctas_of(ROT)) step_rows_kernel(const StepA
               x[4 * k + 2 * i + 1] = mul2(x[4 * k + 2 * i + 1], make_float2(n.z * r, n.w * r));
             }
           }
-        if (ROT == kHalfAny && turns) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int e = 8 * (i < 8 ? c0 : c1) + (i & 7);
-            if (ok && e < a.rot) y[ROT == kHalfAny ? i : 0] *= r * __ldg(p.norm + (e < h ? e + h : e - h));
-          }
-        }
       }
       if (ROT == kHalf && turned[0]) {
 #pragma unroll
@@ -371,12 +357,22 @@ __global__ void __launch_bounds__(RT, ctas_of(ROT)) step_rows_kernel(const StepA
           }
       }
       if (ROT == kHalfAny && turns) {
+        float *mine = line + (threadIdx.x >> sh) * (16 * lanes + 4);
+        __syncwarp();                 // the unit before has been read
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int e = 8 * (i < 8 ? c0 : c1) + (i & 7), k = ROT == kHalfAny ? i : 0;
-          float &v = i & 1 ? x[i / 2].y : x[i / 2].x;
-          if (e < a.rot) v = e < h ? fmaf(-y[k], sa[k % NA], v * ca[k % NA]) : fmaf(y[k], sa[k % NA], v * ca[k % NA]);
-        }
+        for (int i = 0; i < 8; ++i) *reinterpret_cast<float2 *>(mine + 8 * (i < 4 ? c0 : c1) + 2 * (i & 3)) = x[i];
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          if (turned[k]) {
+#pragma unroll
+            for (int i = 8 * k; i < 8 * k + 8; ++i) {
+              const int e = 8 * (k ? c1 : c0) + (i & 7), m = i % NA;
+              float &v = i & 1 ? x[i / 2].y : x[i / 2].x;
+              if (e < h) v = fmaf(-mine[e + h], sa[m], v * ca[m]);
+              else if (e < a.rot) v = fmaf(mine[e - h], sa[m], v * ca[m]);
+            }
+          }
       }
       if (!p.cells) {
         const int64_t to = row * p.dst_stride + static_cast<int64_t>(this_head) * d;
