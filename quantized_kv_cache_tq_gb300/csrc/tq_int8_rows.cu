@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(RT, ctas_of(ROT)) step_rows_kernel(const StepA
     uint32_t row = static_cast<uint32_t>(tile) * (RT >> sh) + (threadIdx.x >> sh);      // (there are less than 2^31)
     const uint32_t n_rows = static_cast<uint32_t>(a.n_rows);
     int head = static_cast<int>(unit - tile * p.n_heads);
-    const bool turns = ROT != kNone && p.turns;
+    const bool turns = ROT != kNone && p.turns, stored = p.cells != nullptr;
 
     // ---- the lane's two eights
     const int h = a.rot / 2;
@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(RT, ctas_of(ROT)) step_rows_kernel(const StepA
     auto look_up = [&](uint32_t r) {   // a row's position and cell, asked for ahead of time
       if (r < n_rows) {
         pos_next = ROT == kNone ? 0 : __ldg(a.positions + r);
-        slot_next = p.cells ? __ldg(a.slots + r) : 0;
+        slot_next = stored ? __ldg(a.slots + r) : 0;
       } else {
         pos_next = -1;
         slot_next = -1;
@@ -258,7 +258,9 @@ __global__ void __launch_bounds__(RT, ctas_of(ROT)) step_rows_kernel(const StepA
     constexpr int NA = ROT == kNone ? 1 : ROT == kHalfAny ? 16 : 8;
     float ca[NA], sa[NA];
     bool turned[2], ok = false;                                                        // whether an eight turns at all
-    uint32_t cell_row = 0;            // (rows of a plane are less than 2^32)
+    char *to = nullptr;               // where the unit's first eight goes, and the row's scale
+    uint16_t *to_scale = nullptr;
+    const int to_next = stored ? d : d * size, to_second = (c1 - c0) * (stored ? 8 : 8 * size);
     int n_in = 0;
     uint32_t stage = ring_at;
     auto take_up = [&]() {            // the row: its position, its cell, its angles
@@ -274,10 +276,16 @@ __global__ void __launch_bounds__(RT, ctas_of(ROT)) step_rows_kernel(const StepA
       const int pos = pos_next;
       const int64_t slot = slot_next;
       look_up(row + (RT >> sh));
-      const bool cell_ok = !p.cells || static_cast<uint64_t>(slot) < static_cast<uint64_t>(a.n_cells);
+      const bool cell_ok = !stored || static_cast<uint64_t>(slot) < static_cast<uint64_t>(a.n_cells);
       if (l == 0 && (pos < -1 || (!cell_ok && slot != -1))) set_status(a.status, TQ_ERR_DEVICE_CHECK);
       ok = pos >= 0 && cell_ok;
-      cell_row = static_cast<uint32_t>(slot) * n_heads + head;
+      if (stored) {                   // (rows of a plane are less than 2^32)
+        const uint32_t cell_row = static_cast<uint32_t>(slot) * n_heads + head;
+        to = reinterpret_cast<char *>(p.cells) + static_cast<uint64_t>(cell_row) * d + 8 * c0;
+        to_scale = p.scales + cell_row;
+      } else {
+        to = static_cast<char *>(p.dst) + (row * p.dst_stride + static_cast<int64_t>(head) * d + 8 * c0) * size;
+      }
       n_in = ok ? n_row : 0;
       turned[0] = turned[1] = false;
       if (turns && ok) {
@@ -303,7 +311,7 @@ __global__ void __launch_bounds__(RT, ctas_of(ROT)) step_rows_kernel(const StepA
       }
       if (fresh) take_up();
       fresh = false;
-      const int this_head = head++;
+      ++head;
       cp_wait<S - 2>();
       Raw<TYPE> r0, r1;
 #pragma unroll
@@ -330,8 +338,8 @@ __global__ void __launch_bounds__(RT, ctas_of(ROT)) step_rows_kernel(const StepA
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               const float4 n = __ldg(n4 + i);
-              x[4 * k + 2 * i] = mul2(x[4 * k + 2 * i], make_float2(n.x * r, n.y * r));
-              x[4 * k + 2 * i + 1] = mul2(x[4 * k + 2 * i + 1], make_float2(n.z * r, n.w * r));
+              x[4 * k + 2 * i] = mul2(x[4 * k + 2 * i], mul2(make_float2(n.x, n.y), make_float2(r, r)));
+              x[4 * k + 2 * i + 1] = mul2(x[4 * k + 2 * i + 1], mul2(make_float2(n.z, n.w), make_float2(r, r)));
             }
           }
       }
@@ -374,10 +382,11 @@ __global__ void __launch_bounds__(RT, ctas_of(ROT)) step_rows_kernel(const StepA
             }
           }
       }
-      if (!p.cells) {
-        const int64_t to = row * p.dst_stride + static_cast<int64_t>(this_head) * d;
-        if (n_in >= 1) store8<TYPE>(p.dst, to + 8 * c0, x);
-        if (n_in >= 2) store8<TYPE>(p.dst, to + 8 * c1, x + 4);
+      char *const here = to;
+      to += to_next;
+      if (!stored) {
+        if (n_in >= 1) store8<TYPE>(here, 0, x);
+        if (n_in >= 2) store8<TYPE>(here + to_second, 0, x + 4);
         continue;
       }
       // ---- int8 (elements beyond the row are zeros)
@@ -406,11 +415,9 @@ __global__ void __launch_bounds__(RT, ctas_of(ROT)) step_rows_kernel(const StepA
       const float s = __half2float(hs);
       uint32_t cw[4] = {0, 0, 0, 0};
       if (s > 0.f) codes16(x, s, cw);
-      int8_t *to = p.cells + static_cast<uint64_t>(cell_row) * d;
-      *reinterpret_cast<uint2 *>(to + 8 * c0) = make_uint2(cw[0], cw[1]);
-      if (n_in >= 2) *reinterpret_cast<uint2 *>(to + 8 * c1) = make_uint2(cw[2], cw[3]);
-      if (l == 0) p.scales[cell_row] = __half_as_ushort(hs);
-      ++cell_row;
+      *reinterpret_cast<uint2 *>(here) = make_uint2(cw[0], cw[1]);
+      if (n_in >= 2) *reinterpret_cast<uint2 *>(here + to_second) = make_uint2(cw[2], cw[3]);
+      if (l == 0) *to_scale++ = __half_as_ushort(hs);
     }
     cp_wait<0>();                     // (the ring is filled anew)
   }
