@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(RT, ctas_of(ROT)) step_rows_kernel(const StepA
           // (a pair beyond the last one: frequency 0, no element asks for it)
           const uint32_t q = static_cast<uint32_t>(pos);
           turn_sincos(q * static_cast<uint32_t>(t[i] >> 32) + __umulhi(q, static_cast<uint32_t>(t[i])), sa[i], ca[i]);
-          sa[i] *= a.sign * a.gain;
+          sa[i] *= ROT == kHalfAny && 8 * (i < 8 ? c0 : c1) + (i & 7) < h ? -a.sign * a.gain : a.sign * a.gain;
           ca[i] *= a.gain;
         }
         turned[0] = ROT == kHalfAny ? 8 * c0 < a.rot : pair_of(0) < h;
@@ -377,8 +377,8 @@ __global__ void __launch_bounds__(RT, ctas_of(ROT)) step_rows_kernel(const StepA
             for (int i = 8 * k; i < 8 * k + 8; ++i) {
               const int e = 8 * (k ? c1 : c0) + (i & 7), m = i % NA;
               float &v = i & 1 ? x[i / 2].y : x[i / 2].x;
-              if (e < h) v = fmaf(-mine[e + h], sa[m], v * ca[m]);
-              else if (e < a.rot) v = fmaf(mine[e - h], sa[m], v * ca[m]);
+              const float r = fmaf(mine[e < h ? e + h : e - h], sa[m], v * ca[m]);     // (sa: -sin in the first half)
+              v = e < a.rot ? r : v;
             }
           }
       }
