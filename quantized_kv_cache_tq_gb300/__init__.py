@@ -557,27 +557,22 @@ class Rope:
         self.ref = C.byref(self.c)
 
 
-def _rows_stride(t, heads: int, dim: int, what: str) -> int:
-    """_row_stride of rows whose shape is checked already."""
-    return heads * dim if t.is_contiguous() else _row_stride(t, t.shape, what)
-
-
 def _head_rows(t, heads: int, dim: int, out, norm, what: str):
     """tq_head_rows of rows t [n][heads][dim] and of their output."""
-    stride = _rows_stride(t, heads, dim, what)
+    stride = heads * dim if t.is_contiguous() else _row_stride(t, t.shape, what)
     norm_p = None
     if norm is not None:
         _ints(norm, _T.float32, (dim,), what + "_norm")
         norm_p = norm.data_ptr()
+    at = t.data_ptr()
     if out is None:
-        return tq_head_rows(t.data_ptr(), stride, None, 0, norm_p, heads)
+        return tq_head_rows(at, stride, None, 0, norm_p, heads)
     if out is t:
-        at = t.data_ptr()
         return tq_head_rows(at, stride, at, stride, norm_p, heads)
     if out.dtype is not t.dtype or out.shape != t.shape:
         raise ValueError(f"{what}_out: type and shape of {what} are expected")
-    return tq_head_rows(t.data_ptr(), stride, out.data_ptr(), _rows_stride(out, heads, dim, what + "_out"), norm_p,
-                        heads)
+    return tq_head_rows(at, stride, out.data_ptr(),
+                        heads * dim if out.is_contiguous() else _row_stride(out, out.shape, what + "_out"), norm_p, heads)
 
 
 def _zeros_like_rows(stream, t):
@@ -585,8 +580,6 @@ def _zeros_like_rows(stream, t):
 
 
 def _status(dev_status):
-    if dev_status is None:
-        return None
     _ints(dev_status, _t().int32, (1,), "dev_status")
     return dev_status.data_ptr()
 
@@ -597,20 +590,21 @@ def rope_rows(rope: Rope, positions, q, k=None, q_norm=None, k_norm=None, eps: f
     before where q_norm / k_norm (float32 [head_dim]) are given.  Rows may be strided, and q_out may be q (in place).
     Rows whose position is -1 stay as they were (new outputs: zeros).  ``inverse`` turns the other way: the gradient.
     -> q_out, or (q_out, k_out) with k."""
-    if q.dim() != 3:
+    code, shape = _row_type(q, "q"), q.shape
+    if len(shape) != 3:
         raise ValueError("q: [n][heads][head_dim]")
-    code = _row_type(q, "q")
-    n, heads, d = q.shape
+    n, heads, d = shape
     _ints(positions, _T.int32, (n,), "positions")
     if q_out is None:
         q_out = _zeros_like_rows(stream, q)
     qr, kr = _head_rows(q, heads, d, q_out, q_norm, "q"), None
     if k is not None:
-        if k.dim() != 3 or k.shape[0] != n or k.shape[2] != d or k.dtype is not q.dtype:
+        shape = k.shape
+        if len(shape) != 3 or shape[0] != n or shape[2] != d or k.dtype is not q.dtype:
             raise ValueError("k: [n][heads][head_dim] as q, of its type")
         if k_out is None:
             k_out = _zeros_like_rows(stream, k)
-        kr = _head_rows(k, k.shape[1], d, k_out, k_norm, "k")
+        kr = _head_rows(k, shape[1], d, k_out, k_norm, "k")
     elif k_norm is not None or k_out is not None:
         raise ValueError("k_norm and k_out go with k")
     status = None if dev_status is None else _status(dev_status)
@@ -696,18 +690,19 @@ def int8_rope_set_rows(kc: Int8Cache, vc: Int8Cache, rope: Rope, positions, q, k
     int8_set_rows, the keys normed and turned before.  Rows without a position or a slot (-1) are not stored.
     -> q_out (None without q); it may be q."""
     n, d = slots.shape[0], kc.head_dim
-    t = _row_type(k_src, "k_src")
-    if v_src.dtype is not k_src.dtype or (q is not None and q.dtype is not k_src.dtype):
+    t, dtype = _row_type(k_src, "k_src"), k_src.dtype
+    if v_src.dtype is not dtype or (q is not None and q.dtype is not dtype):
         raise ValueError("q, k_src and v_src have different types")
     status = _rows_status(slots, n, dev_status)
     _ints(positions, _T.int32, (n,), "positions")
     qr = None
     if q is not None:
-        if q.dim() != 3 or q.shape[0] != n or q.shape[2] != d:
+        shape = q.shape
+        if len(shape) != 3 or shape[0] != n or shape[2] != d:
             raise ValueError("q: [n][heads][head_dim] is expected, head_dim as the keys'")
         if q_out is None:
             q_out = _zeros_like_rows(stream, q)
-        qr = _head_rows(q, q.shape[1], d, q_out, q_norm, "q")
+        qr = _head_rows(q, shape[1], d, q_out, q_norm, "q")
     elif q_norm is not None or q_out is not None:
         raise ValueError("q_norm and q_out go with q")
     if k_src.shape != (n, kc.n_kv_heads, d):

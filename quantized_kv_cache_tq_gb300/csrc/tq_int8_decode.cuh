@@ -16,8 +16,9 @@
 //   pairs of neighbouring keys: a transposing ldmatrix over 16-bit units (two codes) delivers them so.
 //   (Codes + 128 as binary16 subnormals, 128 sum(q) and 128 sum(p) taken off at the end, save the subtractions and no
 //   time: they run on a pipe that is free.  They cost precision where a heavy key's values are near 0.)
-// - One CTA of eight warps per SM, with registers for two score tiles at a time in four chains of products: with two
-//   CTAs of 16-key tiles an SM the per-tile work (455 against 315 instructions per 16 keys) and the wait for products
+// - The pages of the tile that is copied next are copied ahead as well, one ring turn before they are needed.
+// - One CTA of eight warps per SM (two where rows have 64 codes), with registers for two score tiles at a time in four
+//   chains of products: with two CTAs of 16-key tiles an SM the per-tile work (455 against 315 instructions per 16 keys) and the wait for products
 //   kept memory idle, and the CTAs of a pair ended up to 50 us apart (40 ragged sequences: 218 against 190 us).
 // - Scores: q is scaled by a power of two per column, so that its binary16 form is exact for binary16 and bfloat16
 //   inputs down to 2^-23 of the column's largest entry.
@@ -71,15 +72,18 @@ struct Cfg {
   static constexpr int NW = 8;
   static constexpr int THREADS = NW * 32;
   static constexpr int NC = 8 * NT;                       // columns
+  // CTAs per SM: two where registers and rings leave room (decode of 40 ragged sequences, heads of 64: 116 -> 108 us)
+  static constexpr int CTAS = WK == 64 && NT == 1 ? 2 : 1;
   static constexpr int TILE = WK + WV <= 256 ? 32 : 16;   // keys per warp tile
   static constexpr int HALVES = TILE / 16;
-  // one stage: K rows, V rows, the words of the K and V scales, the halves of these that count
+  // one stage: K rows, V rows, the words of the K and V scales, the halves of these that count, and the pages of the
+  // tile that is to be copied when this one is read
   static constexpr int K_BYTES = TILE * WK, V_BYTES = TILE * WV;
   static constexpr int SC = K_BYTES + V_BYTES;
-  static constexpr int STAGE = (SC + TILE * 12 + 127) / 128 * 128;
+  static constexpr int STAGE = (SC + TILE * 16 + 127) / 128 * 128;
   static constexpr int PREP = TILE * 16;                  // a warp's unpacked scales of one tile
   static constexpr int MERGE = NW * NT * MT * 512 + NW * NC * 8 + NC * 8;       // CTA merge, in the same place
-  static constexpr int FIT = (222 * 1024 / NW - PREP) / STAGE;
+  static constexpr int FIT = (222 * 1024 / CTAS / NW - PREP) / STAGE;
   static constexpr int STAGES = FIT > 4 ? 4 : FIT;
   static constexpr int RING = NW * (STAGES * STAGE + PREP);
   static constexpr int SMEM = RING > MERGE ? RING : MERGE;
@@ -90,7 +94,7 @@ struct Cfg {
   static constexpr int merge_bytes(int ctas) { return ctas * NC * 8 + NT * MT * 512; }
   static constexpr int grid(int sms) {
     const int room = (SMEM - NT * MT * 512) / (NC * 8), fit = room < p4::kMaxCtas ? room : p4::kMaxCtas;
-    return sms < fit ? sms : fit;
+    return sms < (fit + CTAS - 1) / CTAS ? sms * CTAS : fit;
   }
   static_assert(STAGES >= 2 && STAGE % 128 == 0, "stages");
   static_assert(HEADS * PART <= 4096 + 128, "partial results");
@@ -186,7 +190,7 @@ __device__ __forceinline__ void scan_lengths(const AttnArgs &a, int s0, Line *su
 }
 
 template <int WK, int WV, int NT, bool FINE>
-__global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, 1)
+__global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, Cfg<WK, WV, NT, FINE>::CTAS)
     decode_kernel(const AttnArgs a) {
   using C = Cfg<WK, WV, NT, FINE>;
   using namespace p4::few;
@@ -242,6 +246,7 @@ __global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, 1)
 #pragma unroll
   for (int j = 0; j < MT / 2; ++j) v_at[j] = C::K_BYTES + v_chunk<WV>(lane & 15, 2 * j + (lane >> 4));
   const int page_mask = (1 << a.page_shift) - 1;
+  const bool apart = TILE >> a.page_shift > 1;  // a tile lies in several pages
   const uint8_t *k_base = a.k_codes + (k_size ? 16 * (lane % C::KCH) : 0), *v_base = a.v_codes + (v_size ? 16 * (lane % C::VCH) : 0);
   // (the last scale of a plane with an odd number of them is half a word)
   const uint32_t last_row = static_cast<uint32_t>(a.n_rows_cache - 1);
@@ -348,11 +353,15 @@ __global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, 1)
     };
     auto issue = [&](int tile, int page, uint32_t st) {
       const int key = k_begin + tile * TILE + (lane & (TILE - 1));
+      const int ahead_key = key + (C::STAGES - 1) * tiles_by * TILE;
+      if (TILE == 32 || lane < TILE)
+        cp4(st + C::SC + (3 * TILE + lane) * 4, table + (ahead_key < k_end ? ahead_key >> a.page_shift : 0),
+            ahead_key < k_end ? 4 : 0);
       const bool in = key < k_end, ok = in && static_cast<unsigned>(page) < static_cast<unsigned>(a.n_pages);
       const uint32_t row = ((static_cast<uint32_t>(page) << a.page_shift) + (key & page_mask)) * kv_heads + hv;
       if (__all_sync(0xffffffffu, ok)) {
         scales_in(row, true, st);
-        if (a.page_shift >= (TILE == 32 ? 5 : 4)) {             // a tile lies in one page, its rows at even distances
+        if (!apart) {                                           // a tile lies in one page, its rows at even distances
           const uint32_t row0 = __shfl_sync(0xffffffffu, row, 0);
           const uint8_t *ks = k_base + static_cast<uint64_t>(row0 + (lane / C::KCH) * kv_heads) * a.dk;
           const uint8_t *vs = v_base + static_cast<uint64_t>(row0 + (lane / C::VCH) * kv_heads) * a.dv;
@@ -393,16 +402,15 @@ __global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, 1)
     };
     uint32_t st = ring, st_fill = ring;           // the stage read next, and the one filled: the one read last
     auto next_stage = [&](uint32_t x) { return x == ring + (C::STAGES - 1) * C::STAGE ? ring : x + C::STAGE; };
-    int page[C::STAGES];                          // of the first tiles, looked up at once
+    int page[C::STAGES - 1];                      // of the first tiles, looked up at once
 #pragma unroll
-    for (int i = 0; i < C::STAGES; ++i) page[i] = page_of(tile0 + i * tiles_by);
+    for (int i = 0; i < C::STAGES - 1; ++i) page[i] = page_of(tile0 + i * tiles_by);
 #pragma unroll
     for (int i = 0; i < C::STAGES - 1; ++i) {
       if (tile0 + i * tiles_by < n_tiles) issue(tile0 + i * tiles_by, page[i], st_fill);
       st_fill = next_stage(st_fill);
       tc::cp_async_commit();
     }
-    int page_next = page[C::STAGES - 1];
 
     // ---- query fragments
     uint32_t qf[NT][C::KS][2];
@@ -455,10 +463,16 @@ __global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, 1)
       __syncwarp();               // everybody's copies of this tile are there; the slot filled next was read
       {
         const int nt = tile + (C::STAGES - 1) * tiles_by;
-        if (nt < n_tiles) issue(nt, page_next, st_fill);
+        // Where a tile's rows lie apart, the warps of a cell's heads keep together, so that what they read of a cell is
+        // asked for at once (6 x 140000 single cells 321 -> 265 us; in larger pages the wait costs more than it gives).
+        if (hs > 0 && apart) asm volatile("bar.sync %0, %1;" ::"r"(1 + tile0), "r"(32 << hs) : "memory");
+        if (nt < n_tiles) {
+          uint32_t p;
+          lds<1>(&p, st + C::SC + (3 * TILE + (lane & (TILE - 1))) * 4);
+          issue(nt, static_cast<int>(p), st_fill);
+        }
         st_fill = st;
         tc::cp_async_commit();
-        page_next = page_of(nt + tiles_by);
       }
 
       // the lane's key: its scales ready for use (V's exponent is an integer in the low bits of 2^23; 0's counts as -24)
@@ -766,7 +780,7 @@ template <int WK, int WV, int NT, bool FINE>
 cudaError_t launch_t(const AttnArgs &a, cudaStream_t s) {
   using C = Cfg<WK, WV, NT, FINE>;
   static_assert(C::SMEM <= 227 * 1024, "shared memory");
-  static_assert(C::merge_bytes(C::grid(1 << 20)) <= C::SMEM && C::grid(152) == 152, "merge");
+  static_assert(C::merge_bytes(C::grid(1 << 20)) <= C::SMEM && C::grid(152) == 152 * C::CTAS, "merge");
   auto kern = decode_kernel<WK, WV, NT, FINE>;
   cudaError_t e = set_dynamic_smem(reinterpret_cast<const void *>(kern), C::SMEM);
   if (e != cudaSuccess) return e;
