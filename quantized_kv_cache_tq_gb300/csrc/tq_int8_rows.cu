@@ -178,6 +178,7 @@ __device__ __forceinline__ Share share_of(const Units &u) {
 template <int TYPE, int ROT>
 __global__ void __launch_bounds__(RT, ctas_of(ROT)) step_rows_kernel(const StepArgs a) {
   constexpr int S = kStages, W = TYPE == TQ_F32 ? 2 : 1;        // stages; 16-byte words of an eight
+  constexpr bool kFours = TYPE == TQ_F32 && ROT == kNone;
   __shared__ uint4 ring[S][2 * W][RT];            // each thread's own
   __shared__ float line[ROT == kHalfAny ? RT * 16 + 32 * 4 : 1];      // half_any: rows, where the partners are found
   after_earlier_launches();
@@ -205,7 +206,8 @@ __global__ void __launch_bounds__(RT, ctas_of(ROT)) step_rows_kernel(const StepA
       c0 = l < n ? l : n + l;
       c1 = l < n ? n + l : lanes + l;
     }
-    const int n_row = (8 * c0 < d) + (8 * c1 < d);                                     // (c0 < c1)
+    // (c0 < c1.  32-bit rows that nothing turns: four fours, l + k lanes, so that every access is of whole sectors.)
+    const int n_row = kFours ? max(0, (d - 4 * l + 4 * lanes - 1) >> (sh + 2)) : (8 * c0 < d) + (8 * c1 < d);
 
     int pos_next = -1;
     int64_t slot_next = -1;
@@ -225,7 +227,7 @@ __global__ void __launch_bounds__(RT, ctas_of(ROT)) step_rows_kernel(const StepA
     constexpr int size = TYPE == TQ_F32 ? 4 : 2;
     auto row_at = [&](uint32_t r, int hd) {
       return static_cast<const char *>(p.src) +
-             (min(r, n_rows - 1) * p.src_stride + static_cast<int64_t>(hd) * d + (n_row >= 1 ? 8 * c0 : 0)) * size;
+             (min(r, n_rows - 1) * p.src_stride + static_cast<int64_t>(hd) * d + (n_row >= 1 ? (kFours ? 4 * l : 8 * c0) : 0)) * size;
     };
     const char *from = row_at(row, head);
     const int to_c1 = n_row >= 2 ? 8 * (c1 - c0) * size : 0, n_heads = p.n_heads;
@@ -238,9 +240,9 @@ __global__ void __launch_bounds__(RT, ctas_of(ROT)) step_rows_kernel(const StepA
     auto fetch = [&]() {
       if (--from_left >= 0) {
 #pragma unroll
-        for (int i = 0; i < W; ++i) {
-          cp16<TYPE>(fill + i * kWord, from + 16 * i, size0);
-          cp16<TYPE>(fill + (W + i) * kWord, from + to_c1 + 16 * i, size1);
+        for (int i = 0; i < 2 * W; ++i) {
+          if (kFours) cp16<TQ_F16>(fill + i * kWord, i < n_row ? from + 16 * i * lanes : from, i < n_row ? 16 : 0);
+          else cp16<TYPE>(fill + i * kWord, from + (i < W ? 0 : to_c1) + 16 * (i % W), i < W ? size0 : size1);
         }
         from += d * size;
         if (++from_head == n_heads) {
@@ -281,7 +283,7 @@ __global__ void __launch_bounds__(RT, ctas_of(ROT)) step_rows_kernel(const StepA
       ok = pos >= 0 && cell_ok;
       if (stored) {                   // (rows of a plane are less than 2^32)
         const uint32_t cell_row = static_cast<uint32_t>(slot) * n_heads + head;
-        to = reinterpret_cast<char *>(p.cells) + static_cast<uint64_t>(cell_row) * d + 8 * c0;
+        to = reinterpret_cast<char *>(p.cells) + static_cast<uint64_t>(cell_row) * d + (kFours ? 4 * l : 8 * c0);
         to_scale = p.scales + cell_row;
       } else {
         to = static_cast<char *>(p.dst) + (row * p.dst_stride + static_cast<int64_t>(head) * d + 8 * c0) * size;
@@ -415,8 +417,14 @@ __global__ void __launch_bounds__(RT, ctas_of(ROT)) step_rows_kernel(const StepA
       const float s = __half2float(hs);
       uint32_t cw[4] = {0, 0, 0, 0};
       if (s > 0.f) codes16(x, s, cw);
-      *reinterpret_cast<uint2 *>(here) = make_uint2(cw[0], cw[1]);
-      if (n_in >= 2) *reinterpret_cast<uint2 *>(here + to_second) = make_uint2(cw[2], cw[3]);
+      if (kFours) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (k < n_in) *reinterpret_cast<uint32_t *>(here + k * 4 * lanes) = cw[k];
+      } else {
+        *reinterpret_cast<uint2 *>(here) = make_uint2(cw[0], cw[1]);
+        if (n_in >= 2) *reinterpret_cast<uint2 *>(here + to_second) = make_uint2(cw[2], cw[3]);
+      }
       if (l == 0) *to_scale++ = __half_as_ushort(hs);
     }
     cp_wait<0>();                     // (the ring is filled anew)
@@ -446,50 +454,61 @@ __global__ void __launch_bounds__(RT, kGet) get_rows_kernel(const GetArgs args) 
       if (slot != -1 && l == 0) set_status(a.status, TQ_ERR_DEVICE_CHECK);
       continue;
     }
-    const int n_in = (8 * l < d) + (8 * (l + lanes) < d);
-    if (n_in == 0) continue;
-    int64_t cell_row = slot * a.n_heads[w] + head, to = row * a.stride[w] + static_cast<int64_t>(head) * d + 8 * l;
-    uint2 c[2], next[2];
+    // A lane's codes: two eights, l and l + lanes; of 32-bit rows four fours, so that every access is of whole sectors.
+    constexpr int N = TYPE == TQ_F32 ? 4 : 2, E = 16 / N;
+    const int n_in = (d - E * l + E * lanes - 1) >> (sh + (N == 4 ? 2 : 3));
+    if (E * l >= d) continue;
+    int64_t cell_row = slot * a.n_heads[w] + head, to = row * a.stride[w] + static_cast<int64_t>(head) * d + E * l;
+    uint32_t next[4] = {0, 0, 0, 0};
     uint16_t s_next = 0;
-    next[1] = make_uint2(0, 0);
     auto fetch = [&]() {
-      const uint8_t *p = a.codes[w] + cell_row * d + 8 * l;
+      const uint8_t *p = a.codes[w] + cell_row * d + E * l;
       s_next = __ldcs(a.scales[w] + cell_row);
-      next[0] = __ldcs(reinterpret_cast<const uint2 *>(p));
-      if (n_in >= 2) next[1] = __ldcs(reinterpret_cast<const uint2 *>(p + 8 * lanes));
+#pragma unroll
+      for (int k = 0; k < N; ++k)
+        if (k < n_in) {
+          if (N == 4) {
+            next[k] = __ldcs(reinterpret_cast<const uint32_t *>(p + E * lanes * k));
+          } else {
+            const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(p + E * lanes * k));
+            next[2 * k % 4] = v.x;
+            next[(2 * k + 1) % 4] = v.y;
+          }
+        }
     };
     fetch();
     for (; head < heads; ++head, to += d) {
-      c[0] = next[0];
-      c[1] = next[1];
+      uint32_t u[4];                                         // code + 128
+#pragma unroll
+      for (int i = 0; i < 4; ++i) u[i] = next[i] ^ 0x80808080u;
       const __half hs = __ushort_as_half(s_next);
       ++cell_row;
       if (head + 1 < heads) fetch();
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
+      for (int k = 0; k < N; ++k) {
         if (k >= n_in) break;
-        const uint32_t u[2] = {c[k].x ^ 0x80808080u, c[k].y ^ 0x80808080u};              // code + 128
         if (TYPE == TQ_F16) {
           // 1024 + 128 + code as binary16, 1152 taken off; the product, rounded once, is that of fp32 rounded once
           uint32_t r[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const uint32_t v = prmt_b32(u[i / 2], 0x64646464u, i & 1 ? 0x4342u : 0x4140u);
+            const uint32_t v = prmt_b32(u[(2 * k + i / 2) % 4], 0x64646464u, i & 1 ? 0x4342u : 0x4140u);
             const __half2 y = __hmul2(__hsub2(*reinterpret_cast<const __half2 *>(&v), __float2half2_rn(1152.f)), __half2half2(hs));
             r[i] = *reinterpret_cast<const uint32_t *>(&y);
           }
-          *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.dst[w]) + to + 8 * lanes * k) = make_uint4(r[0], r[1], r[2], r[3]);
+          *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.dst[w]) + to + E * lanes * k) = make_uint4(r[0], r[1], r[2], r[3]);
         } else {
           const float s = __half2float(hs);
           float2 y[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {                      // a byte in the low bits of 2^23 is the float 2^23 + code + 128
-            const uint32_t v0 = prmt_b32(u[i / 2], 0x4b000000u, i & 1 ? 0x7442u : 0x7440u);
-            const uint32_t v1 = prmt_b32(u[i / 2], 0x4b000000u, i & 1 ? 0x7443u : 0x7441u);
-            y[i] = mul2(make_float2(s, s), add2(make_float2(__uint_as_float(v0), __uint_as_float(v1)),
+          for (int i = 0; i < E / 2; ++i) {                  // a byte in the low bits of 2^23 is the float 2^23 + code + 128
+            const uint32_t v = u[N == 4 ? k : (2 * k + i / 2) % 4];
+            y[i] = mul2(make_float2(s, s), add2(make_float2(__uint_as_float(prmt_b32(v, 0x4b000000u, i & 1 ? 0x7442u : 0x7440u)),
+                                                            __uint_as_float(prmt_b32(v, 0x4b000000u, i & 1 ? 0x7443u : 0x7441u))),
                                                 make_float2(-8388736.f, -8388736.f)));
           }
-          store8<TYPE>(a.dst[w], to + 8 * lanes * k, y);
+          if (TYPE == TQ_F32) *reinterpret_cast<float4 *>(static_cast<float *>(a.dst[w]) + to + E * lanes * k) = make_float4(y[0].x, y[0].y, y[1].x, y[1].y);
+          else store8<TYPE>(a.dst[w], to + E * lanes * k, y);
         }
       }
     }
