@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, Cfg<WK, WV, NT
   constexpr int NW = C::NW, MT = C::MT, NC = C::NC, TILE = C::TILE;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ Line s_scan[NW];
-  __shared__ float s_l[NW * NC];
+  __shared__ float s_inv[NW * NC];
   __shared__ long long s_pre;
   __shared__ int s_seq, s_last;
 
@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, Cfg<WK, WV, NT
 #pragma unroll
   for (int j = 0; j < MT / 2; ++j) v_at[j] = C::K_BYTES + v_chunk<WV>(lane & 15, 2 * j + (lane >> 4));
   const int page_mask = (1 << a.page_shift) - 1;
-  const bool apart = TILE >> a.page_shift > 1;  // a tile lies in several pages
+  const bool apart = TILE / 2 >> a.page_shift > 1;        // half a tile lies in several pages
   const uint8_t *k_base = a.k_codes + (k_size ? 16 * (lane % C::KCH) : 0), *v_base = a.v_codes + (v_size ? 16 * (lane % C::VCH) : 0);
   // (the last scale of a plane with an odd number of them is half a word)
   const uint32_t last_row = static_cast<uint32_t>(a.n_rows_cache - 1);
@@ -286,8 +286,9 @@ __global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, Cfg<WK, WV, NT
       item = static_cast<int>(cur - pre);
       const int n = max(1, min(pieces, units / least)), i = piece % pieces;
       if (i >= n) break;
-      u0 = static_cast<int>(static_cast<long long>(i) * units / n);
-      u1 = static_cast<int>(static_cast<long long>(i + 1) * units / n);
+      const int each = units / n, rest = units - each * n;    // (the first pieces take one unit of the rest each)
+      u0 = i * each + min(i, rest);
+      u1 = u0 + each + (i < rest ? 1 : 0);
       c0 = piece - i;
       n_con = n;
       cur = end;
@@ -309,7 +310,7 @@ __global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, Cfg<WK, WV, NT
       c0 = piece_of(ia);
       n_con = piece_of(ia + units - 1) - c0 + 1;
     }
-    const int h0 = (item / chunks) << hs, chunk = item % chunks, hv = h0 + head_of;
+    const int hg = chunks == 1 ? item : item / chunks, chunk = item - hg * chunks, h0 = hg << hs, hv = h0 + head_of;
     const int c_base = chunk * NC, n_cols = min(NC, a.group - c_base);
     const int k_begin = u0 * UNIT, k_end = min(len, u1 * UNIT);
     const int n_tiles = k_end > k_begin ? (k_end - k_begin + TILE - 1) / TILE : 0;
@@ -359,44 +360,36 @@ __global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, Cfg<WK, WV, NT
             ahead_key < k_end ? 4 : 0);
       const bool in = key < k_end, ok = in && static_cast<unsigned>(page) < static_cast<unsigned>(a.n_pages);
       const uint32_t row = ((static_cast<uint32_t>(page) << a.page_shift) + (key & page_mask)) * kv_heads + hv;
-      if (__all_sync(0xffffffffu, ok)) {
-        scales_in(row, true, st);
-        if (!apart) {                                           // a tile lies in one page, its rows at even distances
-          const uint32_t row0 = __shfl_sync(0xffffffffu, row, 0);
+      const uint32_t there = __ballot_sync(0xffffffffu, ok);
+      scales_in(ok ? row : 0, ok, st);
+      if (there == 0xffffffffu && !apart) {                     // half a tile lies in one page, its rows at even distances
+        const uint32_t k_step = (32 / C::KCH) * kv_heads * a.dk, v_step = (32 / C::VCH) * kv_heads * a.dv;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          constexpr int NK = TILE * C::KCH / 64, NV = TILE * C::VCH / 64;        // copies of half a tile
+          const uint32_t row0 = __shfl_sync(0xffffffffu, row, h * (TILE / 2));
           const uint8_t *ks = k_base + static_cast<uint64_t>(row0 + (lane / C::KCH) * kv_heads) * a.dk;
           const uint8_t *vs = v_base + static_cast<uint64_t>(row0 + (lane / C::VCH) * kv_heads) * a.dv;
-          const uint32_t k_step = (32 / C::KCH) * kv_heads * a.dk, v_step = (32 / C::VCH) * kv_heads * a.dv;
 #pragma unroll
-          for (int i = 0; i < TILE * C::KCH / 32; ++i) cp16(st + kc_at + i * 512, ahead(ks, k_step, i), k_size);
+          for (int i = 0; i < NK; ++i) cp16(st + kc_at + (h * NK + i) * 512, ahead(ks, k_step, i), k_size);
 #pragma unroll
-          for (int i = 0; i < TILE * C::VCH / 32; ++i) cp16(st + (vc_at ^ v_turn<WV>(i)) + i * 512, ahead(vs, v_step, i), v_size);
-        } else {
-#pragma unroll
-          for (int i = 0; i < TILE * C::KCH / 32; ++i) {
-            const uint32_t r = __shfl_sync(0xffffffffu, row, i * (32 / C::KCH) + lane / C::KCH);
-            cp16(st + kc_at + i * 512, k_base + static_cast<uint64_t>(r) * a.dk, k_size);
-          }
-#pragma unroll
-          for (int i = 0; i < TILE * C::VCH / 32; ++i) {
-            const uint32_t r = __shfl_sync(0xffffffffu, row, i * (32 / C::VCH) + lane / C::VCH);
-            cp16(st + (vc_at ^ v_turn<WV>(i)) + i * 512, v_base + static_cast<uint64_t>(r) * a.dv, v_size);
-          }
+          for (int i = 0; i < NV; ++i)
+            cp16(st + (vc_at ^ v_turn<WV>(h * NV + i)) + (h * NV + i) * 512, ahead(vs, v_step, i), v_size);
         }
-      } else {                            // the last tile, or a page outside the cache: zeros for what is not there
+      } else {                            // rows apart, the last tile, or a page outside the cache: zeros for what is not there
         if (in && !ok) set_status(a.status, TQ_ERR_DEVICE_CHECK);
-        scales_in(ok ? row : 0, ok, st);
-        const uint32_t mine = ok ? row : 0xffffffffu;
+        const uint32_t mine = ok ? row : 0;
 #pragma unroll
         for (int i = 0; i < TILE * C::KCH / 32; ++i) {
-          const uint32_t r = __shfl_sync(0xffffffffu, mine, i * (32 / C::KCH) + lane / C::KCH);
-          cp16(st + kc_at + i * 512, k_base + (r == 0xffffffffu ? 0 : static_cast<uint64_t>(r) * a.dk),
-               r == 0xffffffffu ? 0 : k_size);
+          const int k = i * (32 / C::KCH) + lane / C::KCH;
+          const uint32_t r = __shfl_sync(0xffffffffu, mine, k);
+          cp16(st + kc_at + i * 512, k_base + static_cast<uint64_t>(r) * a.dk, there >> k & 1 ? k_size : 0);
         }
 #pragma unroll
         for (int i = 0; i < TILE * C::VCH / 32; ++i) {
-          const uint32_t r = __shfl_sync(0xffffffffu, mine, i * (32 / C::VCH) + lane / C::VCH);
-          cp16(st + (vc_at ^ v_turn<WV>(i)) + i * 512, v_base + (r == 0xffffffffu ? 0 : static_cast<uint64_t>(r) * a.dv),
-               r == 0xffffffffu ? 0 : v_size);
+          const int k = i * (32 / C::VCH) + lane / C::VCH;
+          const uint32_t r = __shfl_sync(0xffffffffu, mine, k);
+          cp16(st + (vc_at ^ v_turn<WV>(i)) + i * 512, v_base + static_cast<uint64_t>(r) * a.dv, there >> k & 1 ? v_size : 0);
         }
       }
     };
@@ -405,9 +398,11 @@ __global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, Cfg<WK, WV, NT
     int page[C::STAGES - 1];                      // of the first tiles, looked up at once
 #pragma unroll
     for (int i = 0; i < C::STAGES - 1; ++i) page[i] = page_of(tile0 + i * tiles_by);
+#pragma unroll 1
+    for (int i = 0; i < C::STAGES - 1; ++i) {     // (not unrolled: instructions are fetched anew for every segment)
+      if (tile0 + i * tiles_by < n_tiles) issue(tile0 + i * tiles_by, page[0], st_fill);
 #pragma unroll
-    for (int i = 0; i < C::STAGES - 1; ++i) {
-      if (tile0 + i * tiles_by < n_tiles) issue(tile0 + i * tiles_by, page[i], st_fill);
+      for (int j = 1; j < C::STAGES - 1; ++j) page[j - 1] = page[j];
       st_fill = next_stage(st_fill);
       tc::cp_async_commit();
     }
@@ -427,17 +422,18 @@ __global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, Cfg<WK, WV, NT
       }
 #pragma unroll
       for (int o = 1; o < 4; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      // max in [2^ex, 2^(ex+1)) -> scaled to [2^12, 2^13), by two factors, so that each is a normal number
-      const int ex = mx > 0.f ? static_cast<int>(__float_as_uint(mx) >> 23) - 127 : 0;
-      const float s1 = __uint_as_float(static_cast<uint32_t>((12 - ex) / 2 + 127) << 23);
-      const float s2 = __uint_as_float(static_cast<uint32_t>((12 - ex) - (12 - ex) / 2 + 127) << 23);
+      // max in [2^ex, 2^(ex+1)) -> scaled to [2^12, 2^13) (below 2^-114 to less, exactly as well)
+      const int ex = mx > 0x1p-114f ? static_cast<int>(__float_as_uint(mx) >> 23) - 127 : -114;
+      const float up = __uint_as_float(static_cast<uint32_t>(12 - ex + 127) << 23);
 #pragma unroll
       for (int j = 0; j < C::KS / 4; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float *x = v[j] + 4 * i;
-          qf[n][4 * j + i][0] = half2_bits(x[0] * s1 * s2, x[2] * s1 * s2);
-          qf[n][4 * j + i][1] = half2_bits(x[1] * s1 * s2, x[3] * s1 * s2);
+          const float2 lo = mul2(make_float2(x[0], x[2]), make_float2(up, up));
+          const float2 hi = mul2(make_float2(x[1], x[3]), make_float2(up, up));
+          qf[n][4 * j + i][0] = half2_bits(lo.x, lo.y);
+          qf[n][4 * j + i][1] = half2_bits(hi.x, hi.y);
         }
       // this lane's softmax columns are 2t and 2t + 1: their factors sit in lanes g = 2t, 2t + 1
       const float f = a.scale_log2 * 0x1p-12f * __uint_as_float(static_cast<uint32_t>(ex + 127) << 23);
@@ -630,7 +626,7 @@ __global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, Cfg<WK, WV, NT
     const int heads = 1 << hs;
     const int tsh = n_cols > 4 ? 2 : n_cols > 2 ? 1 : 0;
     constexpr int FSH = NT * MT == 4 ? 5 : NT * MT == 8 ? 6 : NT * MT == 16 ? 7 : 8;
-    const int fsh = FSH + tsh, n_frag = 1 << fsh, all_frag = n_frag << hs;
+    const int fsh = FSH + tsh, n_frag = 1 << fsh, ash = fsh + hs, all_frag = 1 << ash;
     static_assert(NT * MT * 8 == 1 << FSH, "fragments");
     auto frag_at = [&](int v) { return (v >> (3 + tsh)) * 32 + ((v >> tsh) & 7) * 4 + (v & ((1 << tsh) - 1)); };
     auto col_of = [&](int f) { return 8 * (f / (MT * 32)) + 2 * (f & 3); };
@@ -641,18 +637,17 @@ __global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, Cfg<WK, WV, NT
       o.w = fmaf(w1, p.w, o.w);
     };
     // fragment f of head h0 + h: dims d, d + 1 of columns col, col + 1
+    const int64_t out0 = (static_cast<int64_t>(seq) * a.n_heads + h0 * a.group + c_base) * a.dv;
     auto put = [&](int h, int f, const float4 &o) {
       const int mt = (f / 32) % MT, fl = f & 31, col = col_of(f);
       const int d = 16 * mt + 2 * (fl >> 2);
       if (d >= a.dv) return;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        if (col + i >= n_cols) continue;
-        const float ls = s_l[h * NC + col + i], inv = ls != 0.f ? 1.f / ls : 0.f;
-        const int64_t at = (static_cast<int64_t>(seq) * a.n_heads + (h0 + h) * a.group + c_base + col + i) * a.dv + d;
-        store2(a.out, at, (i ? o.y : o.x) * inv, (i ? o.w : o.z) * inv, a.bf16);
-      }
+      const int64_t at = out0 + ((h * a.group + col) * a.dv + d);
+      const float i0 = s_inv[h * NC + col], i1 = s_inv[h * NC + col + 1];
+      if (col < n_cols) store2(a.out, at, o.x * i0, o.z * i0, a.bf16);
+      if (col + 1 < n_cols) store2(a.out, at + a.dv, o.y * i1, o.w * i1, a.bf16);
     };
+    auto inverse = [](float ls) { return ls != 0.f ? 1.f / ls : 0.f; };
     const bool whole = n_con == 1;
     float *mine = a.part + static_cast<int64_t>(2 * piece + (even || share0 >= ia ? 0 : 1)) * C::HEADS * C::PART;
     if (tid < heads * NC) {
@@ -670,7 +665,7 @@ __global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, Cfg<WK, WV, NT
         ls += f * rl[x].y;
         if (x < tiles_by) stat[(h + (x << hs)) * NC + col].x = f;           // the warp's weight
       }
-      s_l[tid] = ls;
+      s_inv[tid] = inverse(ls);
       if (!whole) reinterpret_cast<float2 *>(mine + h * C::PART)[col] = make_float2(M, ls);
     }
     __syncthreads();
@@ -699,21 +694,23 @@ __global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, Cfg<WK, WV, NT
           return a.part + (static_cast<int64_t>(2 * (c0 + c) + (c == 0 ? slot0 : 0)) * C::HEADS + h) * C::PART;
         };
         // shared memory: [CTA][head, column] weights and sums, then the fragments of as many CTAs as there is room for
-        const int hc = NC << hs;
+        constexpr int CSH = NT == 1 ? 3 : 4;
+        const int hsh = CSH + hs, hc = 1 << hsh;
+        static_assert(NC == 1 << CSH, "columns");
         float *cw = reinterpret_cast<float *>(smem), *cl = cw + n_con * hc;
         float4 *buf = reinterpret_cast<float4 *>(cl + n_con * hc);
-        const int room = (C::SMEM - n_con * hc * 8) / (all_frag * 16);
+        const int room = (C::SMEM - n_con * hc * 8) >> (ash + 4);
         auto fetch = [&](int c1) {                               // of CTAs c1 and on
           const int n = min(room, n_con - c1) * all_frag;
           for (int i = tid; i < n; i += C::THREADS) {
-            const int c = i / all_frag, v = i - c * all_frag;
+            const int c = i >> ash, v = i & (all_frag - 1);
             cp16(tc::smem_u32(buf + i), part_of(c1 + c, v >> fsh) + 2 * NC + 4 * (v & (n_frag - 1)));
           }
           tc::cp_async_commit();
         };
         fetch(0);                                                // on its way while the weights are worked out
         for (int i = tid; i < n_con * hc; i += C::THREADS) {
-          const int c = i / hc, col = i % hc;
+          const int c = i >> hsh, col = i & (hc - 1);
           const float2 r = __ldcg(reinterpret_cast<const float2 *>(part_of(c, col / NC)) + col % NC);
           cw[i] = r.x;
           cl[i] = r.y;
@@ -732,7 +729,7 @@ __global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, Cfg<WK, WV, NT
           }
 #pragma unroll
           for (int o = 1; o < 8; o <<= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
-          if ((tid & 7) == 0) s_l[col] = ls;
+          if ((tid & 7) == 0) s_inv[col] = inverse(ls);
         }
         constexpr int MOST = (C::HEADS * NT * MT * 32 + C::THREADS - 1) / C::THREADS;     // fragments of a thread
         float4 o[MOST];
