@@ -148,17 +148,19 @@ __device__ __forceinline__ int length_of(const AttnArgs &a, int s, bool report) 
   return len < 0 ? 0 : static_cast<int>(cap);
 }
 
-// What lies before this thread's sequence s0 + tid on a line where every sequence with cells takes its units and SET
-// more: `units` of them, and `seqs` such sequences.  Moves `at` past all sequences of the block.
+// What lies before a sequence on a line where every sequence with cells takes its units and SET more: `units` of them, and
+// `seqs` such sequences.
 struct Line {
   long long units;
   int seqs, longest;
 };
+// Sequence s0 + tid (few: s0 + lane, every warp for itself): its units, and what lies before it.  Moves `at` past all
+// sequences of the block (few: of the warp).
 template <int NW>
-__device__ __forceinline__ void scan_lengths(const AttnArgs &a, int s0, Line *sums, bool report, Line &at, Line &before,
-                                             int &own) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  own = s0 + tid < a.n_seq ? (length_of(a, s0 + tid, report) + UNIT - 1) / UNIT : 0;
+__device__ __forceinline__ void scan_lengths(const AttnArgs &a, int s0, bool few, Line *sums, bool report, Line &at,
+                                             Line &before, int &own) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, s = s0 + (few ? lane : tid);
+  own = s < a.n_seq ? (length_of(a, s, report) + UNIT - 1) / UNIT : 0;
   Line x = {own > 0 ? own + SET : 0, own > 0 ? 1 : 0, own};
   const Line v = x;
 #pragma unroll
@@ -171,19 +173,23 @@ __device__ __forceinline__ void scan_lengths(const AttnArgs &a, int s0, Line *su
     }
   }
   x.longest = __reduce_max_sync(0xffffffffu, own);
-  __syncthreads();
-  if (lane == 31) sums[warp] = x;
-  __syncthreads();
   Line all = {0, 0, 0};
+  if (few) {
+    all = {__shfl_sync(0xffffffffu, x.units, 31), __shfl_sync(0xffffffffu, x.seqs, 31), x.longest};
+  } else {
+    __syncthreads();
+    if (lane == 31) sums[warp] = x;
+    __syncthreads();
 #pragma unroll
-  for (int w = 0; w < NW; ++w) {
-    if (w == warp) {
-      x.units += all.units;
-      x.seqs += all.seqs;
+    for (int w = 0; w < NW; ++w) {
+      if (w == warp) {
+        x.units += all.units;
+        x.seqs += all.seqs;
+      }
+      all.units += sums[w].units;
+      all.seqs += sums[w].seqs;
+      all.longest = max(all.longest, sums[w].longest);
     }
-    all.units += sums[w].units;
-    all.seqs += sums[w].seqs;
-    all.longest = max(all.longest, sums[w].longest);
   }
   before = {at.units + x.units - v.units, at.seqs + x.seqs - v.seqs, 0};
   at = {at.units + all.units, at.seqs + all.seqs, max(at.longest, all.longest)};
@@ -209,7 +215,8 @@ __global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, Cfg<WK, WV, NT
   // ---- the work, as a line of units
   Line sum = {0, 0, 0}, before = {0, 0, 0};
   int own = 0;
-  for (int s0 = 0; s0 < a.n_seq; s0 += C::THREADS) scan_lengths<NW>(a, s0, s_scan, blockIdx.x == 0, sum, before, own);
+  const bool few = a.n_seq <= 32;         // every warp looks at all sequences: no barriers
+  for (int s0 = 0; s0 < a.n_seq; s0 += C::THREADS) scan_lengths<NW>(a, s0, few, s_scan, blockIdx.x == 0, sum, before, own);
   const int chunks = (a.group + NC - 1) / NC, grid = gridDim.x;
   const long long line1 = sum.units * chunks;             // (of one KV head)
   // Heads side by side: as many as the KV heads divide into, while the CTAs' shares stay LONG and whoever merges the
@@ -258,22 +265,29 @@ __global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, Cfg<WK, WV, NT
   if (piece < n_work) {
     cur = even ? piece / pieces : start_of(piece);
     end = even ? cur + 1 : start_of(piece + 1);
-    Line at = {0, 0, 0};
-    for (int s0 = 0; s0 < a.n_seq; s0 += C::THREADS) {
-      // (a batch of one block still has its sums in registers)
-      if (a.n_seq > C::THREADS) scan_lengths<NW>(a, s0, s_scan, false, at, before, own);
-      if (own > 0) {
-        const long long first = even ? static_cast<long long>(before.seqs) * per_seq : before.units * per_seq;
-        const long long n = even ? per_seq : static_cast<long long>(own + SET) * per_seq;
-        if (first <= cur && cur < first + n) {
+    auto has = [&](const Line &b, int n, long long &first) {   // whether the share begins in the n units after b
+      first = even ? static_cast<long long>(b.seqs) * per_seq : b.units * per_seq;
+      return n > 0 && first <= cur && cur < first + (even ? per_seq : static_cast<long long>(n + SET) * per_seq);
+    };
+    long long first;
+    if (few) {
+      const int from = __ffs(__ballot_sync(0xffffffffu, has(before, own, first))) - 1;
+      seq = from;
+      pre = __shfl_sync(0xffffffffu, first, from);
+    } else {
+      Line at = {0, 0, 0};
+      for (int s0 = 0; s0 < a.n_seq; s0 += C::THREADS) {
+        // (a batch of one block still has its sums in registers)
+        if (a.n_seq > C::THREADS) scan_lengths<NW>(a, s0, false, s_scan, false, at, before, own);
+        if (has(before, own, first)) {
           s_seq = s0 + tid;
           s_pre = first;
         }
       }
+      __syncthreads();
+      seq = s_seq;
+      pre = s_pre;
     }
-    __syncthreads();
-    seq = s_seq;
-    pre = s_pre;
   }
   const long long share0 = cur;
 
