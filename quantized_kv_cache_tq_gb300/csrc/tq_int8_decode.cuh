@@ -54,6 +54,9 @@ using p4::RAISE;
 
 constexpr int UNIT = 64;              // keys per unit of work
 constexpr int MIN_PIECE = 2;          // units of a piece at least: one tile for each of eight warps
+// Units that one CTA has sooner done alone than shared and merged, two tiles for each of eight warps (one sequence of 300
+// cells 6.4 against 7.8 us, of 440 6.8 against 7.8, of 570 7.7 against 8.0, of 700 8.2 against 7.9)
+constexpr int ALONE = 8;
 constexpr int SET = 6;                // units' worth of work that an item costs besides its keys
 // Heads side by side, two choices.  A share of few units has little to gain, and more heads a CTA means fewer CTAs per
 // head's keys (a sequence of 700 cells over 16-cell pages 8.5 us with one head at a time, 9.2 with two).  And the CTA
@@ -298,7 +301,7 @@ __global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, Cfg<WK, WV, NT
     int item, u0, u1, c0, n_con;
     if (even) {
       item = static_cast<int>(cur - pre);
-      const int n = max(1, min(pieces, units / least)), i = piece % pieces;
+      const int n = units <= ALONE >> hs ? 1 : max(1, min(pieces, units / least)), i = piece % pieces;
       if (i >= n) break;
       const int each = units / n, rest = units - each * n;    // (the first pieces take one unit of the rest each)
       u0 = i * each + min(i, rest);
