@@ -68,9 +68,15 @@ constexpr int MERGED = 72;            // partial results of a head, times heads,
 // Heads side by side whose partial results a CTA has room for in the workspace: 4 Ki values of fragments.
 constexpr int part_heads(int wv, int nt) { return 512 / (wv * nt) < 4 ? 512 / (wv * nt) : 4; }
 
+// Widths of rows: 64, 80, 96, 128, 192 (K), 256.  Those of 80 and 96 codes lie at odd numbers of 16-byte chunks.
+constexpr bool pow2(int w) { return (w & (w - 1)) == 0; }
+constexpr int pitch_of(int w) { return w == 96 ? 112 : w; }
+
 template <int WK, int WV, int NT, bool FINE>
 struct Cfg {
   static constexpr int KS = WK / 16, MT = WV / 16;        // k steps of the scores, m tiles of the values
+  static constexpr int KJ = WK / 64, KR = KS - 4 * KJ;    // fours of K chunks, and the chunks left, a word a lane
+  static constexpr int MP = MT <= 4 ? 4 : MT <= 8 ? 8 : 16;       // places of m tiles in merges
   static constexpr int KCH = WK / 16, VCH = WV / 16;      // 16-byte chunks of a row
   static constexpr int NW = 8;
   static constexpr int THREADS = NW * 32;
@@ -81,38 +87,44 @@ struct Cfg {
   static constexpr int HALVES = TILE / 16;
   // one stage: K rows, V rows, the words of the K and V scales, the halves of these that count, and the pages of the
   // tile that is to be copied when this one is read
-  static constexpr int K_BYTES = TILE * WK, V_BYTES = TILE * WV;
+  static constexpr int K_PITCH = pitch_of(WK), V_PITCH = pitch_of(WV);
+  static constexpr int K_BYTES = TILE * K_PITCH, V_BYTES = TILE * V_PITCH;
   static constexpr int SC = K_BYTES + V_BYTES;
   static constexpr int STAGE = (SC + TILE * 16 + 127) / 128 * 128;
   static constexpr int PREP = TILE * 16;                  // a warp's unpacked scales of one tile
-  static constexpr int MERGE = NW * NT * MT * 512 + NW * NC * 8 + NC * 8;       // CTA merge, in the same place
+  static constexpr int MERGE = NW * NT * MP * 512 + NW * NC * 8 + NC * 8;       // CTA merge, in the same place
   static constexpr int FIT = (222 * 1024 / CTAS / NW - PREP) / STAGE;
   static constexpr int STAGES = FIT > 4 ? 4 : FIT;
   static constexpr int RING = NW * (STAGES * STAGE + PREP);
   static constexpr int SMEM = RING > MERGE ? RING : MERGE;
-  static constexpr int PART = 2 * NC + NT * MT * 128;     // a head's partial result: (R, l) of every column, then fragments
-  static constexpr int HEADS = part_heads(WV, NT);        // heads side by side at most
+  static constexpr int PART = 2 * NC + NT * MP * 128;     // a head's partial result: (R, l) of every column, then fragments
+  static constexpr int HEADS = part_heads(16 * MP, NT);       // heads side by side at most
   // A merge: (weight, sum) of every CTA and column, and the fragments of one CTA at least.  The grid: one CTA per SM, as
   // far as the merge of an item that every one of them shares finds room.
-  static constexpr int merge_bytes(int ctas) { return ctas * NC * 8 + NT * MT * 512; }
+  static constexpr int merge_bytes(int ctas) { return ctas * NC * 8 + NT * MP * 512; }
   static constexpr int grid(int sms) {
-    const int room = (SMEM - NT * MT * 512) / (NC * 8), fit = room < p4::kMaxCtas ? room : p4::kMaxCtas;
+    const int room = (SMEM - NT * MP * 512) / (NC * 8), fit = room < p4::kMaxCtas ? room : p4::kMaxCtas;
     return sms < (fit + CTAS - 1) / CTAS ? sms * CTAS : fit;
   }
   static_assert(STAGES >= 2 && STAGE % 128 == 0, "stages");
   static_assert(HEADS * PART <= 4096 + 128, "partial results");
-  static_assert(2 * MERGED * NC * 8 + HEADS * NT * MT * 512 <= SMEM, "merge of heads side by side");
+  static_assert(2 * MERGED * NC * 8 + HEADS * NT * MP * 512 <= SMEM, "merge of heads side by side");
 };
 
 // Byte offset of 16-byte chunk c of row r.  K: one lane quad reads four chunks of a row, eight lanes those of rows r and
-// r + 1, which the turn of odd rows by four chunks puts on eight different places.  V: a matrix read takes one chunk of
-// eight rows.
+// r + 1, which lie on eight different places: odd rows are turned by four chunks, or (rows at odd numbers of chunks, P)
+// even ones by P - 4, or they are four chunks apart as they are (192).  V: a matrix read takes one chunk of eight rows.
 template <int W>
 __device__ __forceinline__ uint32_t k_chunk(int r, int c) {
-  return W == 64 ? r * 64 + c * 16 : r * W + ((c ^ ((r & 1) << 2)) * 16);
+  constexpr int P = pitch_of(W) / 16;
+  if (W == 64 || W == 192) return r * W + c * 16;
+  if (P & 1) return (r * P + (r & 1 ? c : c + P - 4 < P ? c + P - 4 : c - 4)) * 16;
+  return r * W + ((c ^ ((r & 1) << 2)) * 16);
 }
 template <int W>
 __device__ __forceinline__ uint32_t v_chunk(int r, int c) {
+  constexpr int P = pitch_of(W) / 16;
+  if (P & 1) return (r * P + c) * 16;
   return W == 64 ? (r >> 1) * 128 + (((((r & 1) << 2) + c) ^ ((r >> 1) & 3)) * 16) : r * W + ((c ^ (r & 7)) * 16);
 }
 // The turn's share of copy i in a V chunk's place: its rows are 32 / (W / 16) i and on.
@@ -249,12 +261,15 @@ __global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, Cfg<WK, WV, NT
   const uint32_t ring = tc::smem_u32(smem) + warp * (C::STAGES * C::STAGE + C::PREP), prep = ring + C::STAGES * C::STAGE;
   const uint32_t kc_at = k_chunk<WK>(lane / C::KCH, lane % C::KCH), vc_at = C::K_BYTES + v_chunk<WV>(lane / C::VCH, lane % C::VCH);
   const uint32_t k_size = (lane % C::KCH) * 16 < a.dk ? 16 : 0, v_size = (lane % C::VCH) * 16 < a.dv ? 16 : 0;
-  uint32_t k_at[C::KS / 4];                     // reads: K row g, chunks t + 4 j
+  uint32_t k_at[C::KJ], k_word[C::KR + 1];      // reads: K row g, chunks t + 4 j; words t of the chunks left
 #pragma unroll
-  for (int j = 0; j < C::KS / 4; ++j) k_at[j] = k_chunk<WK>(g, t + 4 * j);
-  uint32_t v_at[MT / 2];                        // matrices of keys 0-7 / 8-15 and chunks 2 j, 2 j + 1
+  for (int j = 0; j < C::KJ; ++j) k_at[j] = k_chunk<WK>(g, t + 4 * j);
 #pragma unroll
-  for (int j = 0; j < MT / 2; ++j) v_at[j] = C::K_BYTES + v_chunk<WV>(lane & 15, 2 * j + (lane >> 4));
+  for (int y = 0; y < C::KR; ++y) k_word[y] = k_chunk<WK>(g, 4 * C::KJ + y) + 4 * t;
+  uint32_t v_at[(MT + 1) / 2];                  // matrices of keys 0-7 / 8-15 and chunks 2 j, 2 j + 1 (an odd last one twice)
+#pragma unroll
+  for (int j = 0; j < (MT + 1) / 2; ++j) v_at[j] = C::K_BYTES + v_chunk<WV>(lane & 15, min(2 * j + (lane >> 4), MT - 1));
+  constexpr bool EVEN = pow2(WK) && pow2(WV);   // a copy's lanes take whole rows, the same chunks each time
   const int page_mask = (1 << a.page_shift) - 1;
   const bool apart = TILE / 2 >> a.page_shift > 1;        // half a tile lies in several pages
   const uint8_t *k_base = a.k_codes + (k_size ? 16 * (lane % C::KCH) : 0), *v_base = a.v_codes + (v_size ? 16 * (lane % C::VCH) : 0);
@@ -335,13 +350,14 @@ __global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, Cfg<WK, WV, NT
 
     // ---- query rows: column g of tile n, the dims of this lane's K chunks (converted further down, while the
     // first copies are on their way)
-    uint4 qraw[NT][C::KS / 4][2];
+    uint4 qraw[NT][C::KJ][2];
+    uint2 qword[NT][C::KR + 1];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int c = 8 * n + g;
       const int64_t qb = seq * a.q_stride + static_cast<int64_t>(hv * a.group + c_base + c) * a.dk;
 #pragma unroll
-      for (int j = 0; j < C::KS / 4; ++j)
+      for (int j = 0; j < C::KJ; ++j)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int d0 = 16 * (t + 4 * j) + 8 * i;
@@ -349,6 +365,13 @@ __global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, Cfg<WK, WV, NT
           if (c < n_cols && d0 < a.dk)
             qraw[n][j][i] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) + qb + d0));
         }
+#pragma unroll
+      for (int y = 0; y < C::KR; ++y) {
+        const int d0 = 16 * (4 * C::KJ + y) + 4 * t;
+        qword[n][y] = make_uint2(0, 0);
+        if (c < n_cols && d0 < a.dk)
+          qword[n][y] = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(a.q) + qb + d0));
+      }
     }
 
     // ---- the warp's tile copies.  Numbers of rows fit 32 bits (checked on the host); all ones: no row, zeros.
@@ -379,7 +402,7 @@ __global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, Cfg<WK, WV, NT
       const uint32_t row = ((static_cast<uint32_t>(page) << a.page_shift) + (key & page_mask)) * kv_heads + hv;
       const uint32_t there = __ballot_sync(0xffffffffu, ok);
       scales_in(ok ? row : 0, ok, st);
-      if (there == 0xffffffffu && !apart) {                     // half a tile lies in one page, its rows at even distances
+      if (EVEN && there == 0xffffffffu && !apart) {                     // half a tile lies in one page, its rows at even distances
         const uint32_t k_step = (32 / C::KCH) * kv_heads * a.dk, v_step = (32 / C::VCH) * kv_heads * a.dv;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -398,15 +421,19 @@ __global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, Cfg<WK, WV, NT
         const uint32_t mine = ok ? row : 0;
 #pragma unroll
         for (int i = 0; i < TILE * C::KCH / 32; ++i) {
-          const int k = i * (32 / C::KCH) + lane / C::KCH;
+          const int k = (32 * i + lane) / C::KCH, c = (32 * i + lane) % C::KCH;
           const uint32_t r = __shfl_sync(0xffffffffu, mine, k);
-          cp16(st + kc_at + i * 512, k_base + static_cast<uint64_t>(r) * a.dk, there >> k & 1 ? k_size : 0);
+          const uint32_t size = EVEN ? k_size : 16 * c < a.dk ? 16 : 0;
+          cp16(st + (EVEN ? kc_at + i * 512 : k_chunk<WK>(k, c)), (EVEN ? k_base : a.k_codes + (size ? 16 * c : 0)) + static_cast<uint64_t>(r) * a.dk,
+               there >> k & 1 ? size : 0);
         }
 #pragma unroll
         for (int i = 0; i < TILE * C::VCH / 32; ++i) {
-          const int k = i * (32 / C::VCH) + lane / C::VCH;
+          const int k = (32 * i + lane) / C::VCH, c = (32 * i + lane) % C::VCH;
           const uint32_t r = __shfl_sync(0xffffffffu, mine, k);
-          cp16(st + (vc_at ^ v_turn<WV>(i)) + i * 512, v_base + static_cast<uint64_t>(r) * a.dv, there >> k & 1 ? v_size : 0);
+          const uint32_t size = EVEN ? v_size : 16 * c < a.dv ? 16 : 0;
+          cp16(st + (EVEN ? (vc_at ^ v_turn<WV>(i)) + i * 512 : C::K_BYTES + v_chunk<WV>(k, c)),
+               (EVEN ? v_base : a.v_codes + (size ? 16 * c : 0)) + static_cast<uint64_t>(r) * a.dv, there >> k & 1 ? size : 0);
         }
       }
     };
@@ -429,29 +456,31 @@ __global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, Cfg<WK, WV, NT
     float2 fx[NT];                  // of columns 2t, 2t + 1: the score factor
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      float v[C::KS / 4][16], mx = 0.f;
+      float v[4 * C::KS], mx = 0.f;         // four of each k step
 #pragma unroll
-      for (int j = 0; j < C::KS / 4; ++j) {
-        unpack8(qraw[n][j][0], a.bf16, v[j]);
-        unpack8(qraw[n][j][1], a.bf16, v[j] + 8);
+      for (int j = 0; j < 2 * C::KJ; ++j) unpack8(qraw[n][j / 2][j & 1], a.bf16, v + 8 * j);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) mx = fmaxf(mx, fabsf(v[j][e]));
+      for (int y = 0; y < C::KR; ++y) {
+        float w[8];
+        unpack8(make_uint4(qword[n][y].x, qword[n][y].y, 0, 0), a.bf16, w);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[16 * C::KJ + 4 * y + e] = w[e];
       }
+#pragma unroll
+      for (int e = 0; e < 4 * C::KS; ++e) mx = fmaxf(mx, fabsf(v[e]));
 #pragma unroll
       for (int o = 1; o < 4; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
       // max in [2^ex, 2^(ex+1)) -> scaled to [2^12, 2^13) (below 2^-114 to less, exactly as well)
       const int ex = mx > 0x1p-114f ? static_cast<int>(__float_as_uint(mx) >> 23) - 127 : -114;
       const float up = __uint_as_float(static_cast<uint32_t>(12 - ex + 127) << 23);
 #pragma unroll
-      for (int j = 0; j < C::KS / 4; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float *x = v[j] + 4 * i;
-          const float2 lo = mul2(make_float2(x[0], x[2]), make_float2(up, up));
-          const float2 hi = mul2(make_float2(x[1], x[3]), make_float2(up, up));
-          qf[n][4 * j + i][0] = half2_bits(lo.x, lo.y);
-          qf[n][4 * j + i][1] = half2_bits(hi.x, hi.y);
-        }
+      for (int i = 0; i < C::KS; ++i) {
+        const float *x = v + 4 * i;
+        const float2 lo = mul2(make_float2(x[0], x[2]), make_float2(up, up));
+        const float2 hi = mul2(make_float2(x[1], x[3]), make_float2(up, up));
+        qf[n][i][0] = half2_bits(lo.x, lo.y);
+        qf[n][i][1] = half2_bits(hi.x, hi.y);
+      }
       // this lane's softmax columns are 2t and 2t + 1: their factors sit in lanes g = 2t, 2t + 1
       const float f = a.scale_log2 * 0x1p-12f * __uint_as_float(static_cast<uint32_t>(ex + 127) << 23);
       fx[n] = make_float2(__shfl_sync(0xffffffffu, f, 8 * t), __shfl_sync(0xffffffffu, f, 8 * t + 4));
@@ -511,12 +540,12 @@ __global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, Cfg<WK, WV, NT
 #pragma unroll
             for (int c = 0; c < 4; ++c) s[n][hf][c] = s2[n][hf][c] = 0.f;
 #pragma unroll
-        for (int j = 0; j < C::KS / 4; ++j) {
+        for (int j = 0; j < C::KJ; ++j) {
           uint32_t w0[H][4], w1[H][4];
 #pragma unroll
           for (int hf = 0; hf < H; ++hf) {
-            lds<4>(w0[hf], st + k_at[j] + hf * 16 * WK);
-            lds<4>(w1[hf], st + k_at[j] + (hf * 16 + 8) * WK);
+            lds<4>(w0[hf], st + k_at[j] + hf * 16 * C::K_PITCH);
+            lds<4>(w1[hf], st + k_at[j] + (hf * 16 + 8) * C::K_PITCH);
           }
 #pragma unroll
           for (int i = 0; i < 4; ++i)
@@ -529,6 +558,18 @@ __global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, Cfg<WK, WV, NT
                 mma16816((i & 1 ? s2 : s)[n][hf], x0, x1, x2, x3, qf[n][4 * j + i][0], qf[n][4 * j + i][1]);
             }
         }
+#pragma unroll
+        for (int y = 0; y < C::KR; ++y)
+#pragma unroll
+          for (int hf = 0; hf < H; ++hf) {
+            uint32_t w0, w1;
+            lds<1>(&w0, st + k_word[y] + hf * 16 * C::K_PITCH);
+            lds<1>(&w1, st + k_word[y] + (hf * 16 + 8) * C::K_PITCH);
+            const uint32_t x0 = codes_of(w0), x1 = codes_of(w1), x2 = codes_of(w0 >> 8), x3 = codes_of(w1 >> 8);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+              mma16816((y & 1 ? s2 : s)[n][hf], x0, x1, x2, x3, qf[n][4 * C::KJ + y][0], qf[n][4 * C::KJ + y][1]);
+          }
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -600,9 +641,9 @@ __global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, Cfg<WK, WV, NT
 #pragma unroll
         for (int c = 0; c < MT; c += 2) {
           uint32_t vw[4];                   // (chunk c: keys 0-7, 8-15), (chunk c + 1: the same)
-          ldsm4t(vw, st + v_at[c / 2] + hf * 16 * WV);
+          ldsm4t(vw, st + v_at[c / 2] + hf * 16 * C::V_PITCH);
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
+          for (int e = 0; e < (c + 1 < MT ? 2 : 1); ++e) {
             const uint32_t x0 = codes_of(vw[2 * e]), x1 = codes_of(vw[2 * e] >> 8);
             const uint32_t x2 = codes_of(vw[2 * e + 1]), x3 = codes_of(vw[2 * e + 1] >> 8);
 #pragma unroll
@@ -625,12 +666,12 @@ __global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, Cfg<WK, WV, NT
       }
     __syncthreads();                        // the ring is no longer read
     float4 *frag = reinterpret_cast<float4 *>(smem);
-    float2 *stat = reinterpret_cast<float2 *>(smem + NW * NT * MT * 512);      // [warp][column]: (R, l), then (weight, l)
+    float2 *stat = reinterpret_cast<float2 *>(smem + NW * NT * C::MP * 512);      // [warp][column]: (R, l), then (weight, l)
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
       for (int k = 0; k < MT; ++k)
-        frag[((warp * NT + n) * MT + k) * 32 + lane] =
+        frag[((warp * NT + n) * C::MP + k) * 32 + lane] =
             make_float4(acc[n][k][0], acc[n][k][1], acc[n][k][2], acc[n][k][3]);
       if (g == 0) {
         stat[warp * NC + 8 * n + 2 * t] = make_float2(R[n].x, l[n].x);
@@ -642,11 +683,12 @@ __global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, Cfg<WK, WV, NT
     // Fragments with columns that exist: of each (head, tile, m tile), lanes (g, t) with 1, 2 or 4 of the t.
     const int heads = 1 << hs;
     const int tsh = n_cols > 4 ? 2 : n_cols > 2 ? 1 : 0;
-    constexpr int FSH = NT * MT == 4 ? 5 : NT * MT == 8 ? 6 : NT * MT == 16 ? 7 : 8;
+    constexpr int FSH = NT * C::MP == 4 ? 5 : NT * C::MP == 8 ? 6 : NT * C::MP == 16 ? 7 : 8;
     const int fsh = FSH + tsh, n_frag = 1 << fsh, ash = fsh + hs, all_frag = 1 << ash;
-    static_assert(NT * MT * 8 == 1 << FSH, "fragments");
+    static_assert(NT * C::MP * 8 == 1 << FSH, "fragments");
     auto frag_at = [&](int v) { return (v >> (3 + tsh)) * 32 + ((v >> tsh) & 7) * 4 + (v & ((1 << tsh) - 1)); };
-    auto col_of = [&](int f) { return 8 * (f / (MT * 32)) + 2 * (f & 3); };
+    auto col_of = [&](int f) { return 8 * (f / (C::MP * 32)) + 2 * (f & 3); };
+    auto is_there = [&](int f) { return MT == C::MP || (f / 32) % C::MP < MT; };
     auto add = [](float4 &o, float w0, float w1, const float4 &p) {
       o.x = fmaf(w0, p.x, o.x);
       o.y = fmaf(w1, p.y, o.y);
@@ -656,7 +698,7 @@ __global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, Cfg<WK, WV, NT
     // fragment f of head h0 + h: dims d, d + 1 of columns col, col + 1
     const int64_t out0 = (static_cast<int64_t>(seq) * a.n_heads + h0 * a.group + c_base) * a.dv;
     auto put = [&](int h, int f, const float4 &o) {
-      const int mt = (f / 32) % MT, fl = f & 31, col = col_of(f);
+      const int mt = (f / 32) % C::MP, fl = f & 31, col = col_of(f);
       const int d = 16 * mt + 2 * (fl >> 2);
       if (d >= a.dv) return;
       const int64_t at = out0 + ((h * a.group + col) * a.dv + d);
@@ -688,12 +730,13 @@ __global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, Cfg<WK, WV, NT
     __syncthreads();
     for (int v = tid; v < all_frag; v += C::THREADS) {
       const int h = v >> fsh, u = v & (n_frag - 1), f = frag_at(u), col = col_of(f);
+      if (!is_there(f)) continue;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int k = 0; k < NW; ++k)
         if (k < tiles_by) {
           const int x = h + (k << hs);
-          add(o, stat[x * NC + col].x, stat[x * NC + col + 1].x, frag[x * (NT * MT * 32) + f]);
+          add(o, stat[x * NC + col].x, stat[x * NC + col + 1].x, frag[x * (NT * C::MP * 32) + f]);
         }
       if (whole) put(h, f, o);
       else reinterpret_cast<float4 *>(mine + h * C::PART + 2 * NC)[u] = o;
@@ -721,6 +764,7 @@ __global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, Cfg<WK, WV, NT
           const int n = min(room, n_con - c1) * all_frag;
           for (int i = tid; i < n; i += C::THREADS) {
             const int c = i >> ash, v = i & (all_frag - 1);
+            if (!is_there(frag_at(v & (n_frag - 1)))) continue;
             cp16(tc::smem_u32(buf + i), part_of(c1 + c, v >> fsh) + 2 * NC + 4 * (v & (n_frag - 1)));
           }
           tc::cp_async_commit();
@@ -748,7 +792,7 @@ __global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, Cfg<WK, WV, NT
           for (int o = 1; o < 8; o <<= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
           if ((tid & 7) == 0) s_inv[col] = inverse(ls);
         }
-        constexpr int MOST = (C::HEADS * NT * MT * 32 + C::THREADS - 1) / C::THREADS;     // fragments of a thread
+        constexpr int MOST = (C::HEADS * NT * C::MP * 32 + C::THREADS - 1) / C::THREADS;     // fragments of a thread
         float4 o[MOST];
 #pragma unroll
         for (int k = 0; k < MOST; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -759,6 +803,7 @@ __global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, Cfg<WK, WV, NT
           for (int k = 0; k < MOST; ++k) {
             const int v = tid + k * C::THREADS;
             if (v >= all_frag) break;
+            if (!is_there(frag_at(v & (n_frag - 1)))) continue;
             const int col = (v >> fsh) * NC + col_of(frag_at(v & (n_frag - 1)));
 #pragma unroll 8
             for (int c = c1; c < min(n_con, c1 + room); ++c) {

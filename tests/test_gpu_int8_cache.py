@@ -542,6 +542,19 @@ def test_decode(dtype, dk, dv, hkv, group, page):
     assert not out[1].any() and not out[7].any()
 
 
+@pytest.mark.parametrize("group", [1, 8, 9, 20])
+@pytest.mark.parametrize("page", [1, 16, 64])
+@pytest.mark.parametrize("dk,dv", [(80, 80), (96, 96), (96, 80), (80, 96), (112, 80), (160, 128), (192, 96), (192, 112),
+                                   (208, 128), (144, 144)])
+def test_decode_widths(dk, dv, page, group):
+    # rows that fill their kernel's width, or end before it; items alone and shared, one sequence of two pages' odd ends
+    import quantized_kv_cache_tq_gb300 as tq
+    b = Batch(dk + 3 * dv + group, [700, 0, 33, 2, 513], 2, dk, dv, page)
+    for dtype in ("bfloat16", "float16"):
+        q = b.query(2 * group, dtype)
+        b.check(tq.int8_decode(b.gk, b.gv, b.gt, b.gl, q, dk ** -0.5, page_size=page), q, dk ** -0.5, dtype)
+
+
 @pytest.mark.parametrize("n_seq,length", [(1, 1), (1, 15), (1, 16), (1, 4097), (1, 40000), (3, 9000), (300, 40), (700, 1)])
 def test_decode_splits(n_seq, length):
     import quantized_kv_cache_tq_gb300 as tq
