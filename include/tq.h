@@ -671,7 +671,7 @@ size_t tq_int8_decode_workspace(const tq_int8 *k, const tq_int8 *v, int n_q_head
  * with k_t, v_t the values of cell  block_table[s][t / page_size] * page_size + t % page_size  and query head h
  * reading KV head h / (n_q_heads / n_kv_heads).  Pages of one cell are lists of cells, as tq_int8_prompt_attn's
  * cell_of_pos.
- * page_size   a power of two, 1 .. 65536
+ * page_size   a power of two, 1 .. 65536; max_pages * page_size at most 2^31 - 65536
  * seq_len     device int32 [n_seq] (0: a zero output; beyond max_pages * page_size or below 0: cut to that range,
  *             and TQ_ERR_DEVICE_CHECK is stored in the workspace's status word)
  * block_table device int32 [n_seq][max_pages]; entries beyond a sequence's length are not read; a page that does not

@@ -3,23 +3,30 @@
 //   out[c] = sum_t p_t s^V_t v_t / sum_t p_t,   p_t = 2^(x_t - R),  x_t = scale log2(e) s^K_t (q . k_t)
 //
 // Columns are the query heads of a KV head, eight per tensor-core tile.  The work is reading the cache once, so
-// everything is arranged around the loads:
+// everything is arranged around the loads.  Batches of long sequences are bound by HBM (40 ragged sequences of up to
+// 32768 cells, 8 KV heads of 128, bf16: 190 us, 6.5 TB/s, 96% of a copy's rate; heads of 256 363 us, 99%; single
+// scattered cells 6 x 140000 254 us, 88%), short calls by the chain from the lengths to the merge (700 cells 7.9 us, 300
+// cells 6.4 us).
 //
 // - A warp streams its own tiles of 32 keys (16 where rows are wide) through a private ring of cp.async stages: it waits
 //   for its own copies only, and no CTA barrier stands in the loop.  Each lane looks up one key's cell, so that pages of
-//   any size, single cells among them, serve; where a tile lies in one page its rows lie at even distances, else the
-//   copying lanes get the row numbers by shuffles.  Rows are swizzled by 16-byte chunks so that copies and both kinds of
-//   reads spread over the banks.
+//   any size, single cells among them, serve; where half a tile lies in one page its rows lie at even distances, else the
+//   copying lanes get the row numbers by shuffles (40 ragged sequences over 16-cell pages: 203 us by shuffles, 195
+//   without).  Rows lie in such places that copies and both kinds of reads spread over the banks.
+// - The pages of the tile that is copied next are copied ahead as well, one ring turn before they are needed.
 // - Codes become binary16 operands exactly: (w & 0x00ff00ff) ^ 0x64806480 is the pair 1024 + (code + 128), and 1152 is
 //   taken off (two instructions for two codes, one more for the odd bytes).  Scores want pairs within a row: the words
 //   of a K row serve as they are, the head dim's order being free as long as q has the same.  The value operand wants
 //   pairs of neighbouring keys: a transposing ldmatrix over 16-bit units (two codes) delivers them so.
 //   (Codes + 128 as binary16 subnormals, 128 sum(q) and 128 sum(p) taken off at the end, save the subtractions and no
 //   time: they run on a pipe that is free.  They cost precision where a heavy key's values are near 0.)
-// - The pages of the tile that is copied next are copied ahead as well, one ring turn before they are needed.
 // - One CTA of eight warps per SM (two where rows have 64 codes), with registers for two score tiles at a time in four
-//   chains of products: with two CTAs of 16-key tiles an SM the per-tile work (455 against 315 instructions per 16 keys) and the wait for products
-//   kept memory idle, and the CTAs of a pair ended up to 50 us apart (40 ragged sequences: 218 against 190 us).
+//   chains of products: with two CTAs of 16-key tiles an SM the per-tile work (455 against 315 instructions per 16 keys)
+//   and the wait for products kept memory idle, and the CTAs of a pair ended up to 50 us apart (40 ragged sequences: 218
+//   against 190 us).
+// - Widths are those of the powers of two, and 80, 96 and 192 (K), since copies and products of zeros cost as much as
+//   those of codes (40 ragged sequences, heads of 80 as 128 wide: 190 us, as 80 wide 159; 192 / 128 as 256 / 128: 284,
+//   192 / 128 wide 265).
 // - Scores: q is scaled by a power of two per column, so that its binary16 form is exact for binary16 and bfloat16
 //   inputs down to 2^-23 of the column's largest entry.
 // - The value weights p_t s^V_t are rounded to binary16: R is a running maximum of x_t + exponent(s^V_t), so the
@@ -29,14 +36,16 @@
 //
 // Split of the work.  A CTA's warps take one, two or four KV heads (1 << hs) of the same cells side by side, so that what
 // it reads of a cell lies together (40 ragged sequences 217 -> 190 us, single scattered cells 362 -> 262 us against one
-// head at a time); the warps left take every so many-th tile.  An item is a (sequence, group of heads,
-// column chunk), its keys come in units of 64.  Nothing about lengths is needed on the host: every CTA works its share
-// out from the device's lengths.
+// head at a time); the warps left take every so many-th tile.  An item is a (sequence, group of heads, column chunk), its
+// keys come in units of 64.  Nothing about lengths is needed on the host: every CTA works its share out from the device's
+// lengths.
 // - Few items of like length: each is cut into as many pieces as there are CTAs per item, and a CTA has one piece.
 // - Else the items' units form one line that is cut into equal shares, one per CTA, however ragged the batch is; taking
 //   up an item counts as SET units.
 // An item that several CTAs share leaves partial results (R, sum, values) in the workspace, a CTA's first and last item
 // at most, and the last CTA to arrive merges them in the order of the CTAs, so that a repeated call gives the same bits.
+// An item costs some 5 us besides its keys, mostly instructions one after the other; sending off the next item's first
+// copies before the merge does not shorten that (256 sequences of 512 cells: 64 against 60 us).
 #pragma once
 
 #include <math.h>
@@ -97,7 +106,7 @@ struct Cfg {
   static constexpr int STAGES = FIT > 4 ? 4 : FIT;
   static constexpr int RING = NW * (STAGES * STAGE + PREP);
   static constexpr int SMEM = RING > MERGE ? RING : MERGE;
-  static constexpr int PART = 2 * NC + NT * MP * 128;     // a head's partial result: (R, l) of every column, then fragments
+  static constexpr int PART = 2 * NC + NT * MP * 128;     // a head's partial result: (R, l) by column, then fragments
   static constexpr int HEADS = part_heads(16 * MP, NT);       // heads side by side at most
   // A merge: (weight, sum) of every CTA and column, and the fragments of one CTA at least.  The grid: one CTA per SM, as
   // far as the merge of an item that every one of them shares finds room.
@@ -163,8 +172,8 @@ __device__ __forceinline__ int length_of(const AttnArgs &a, int s, bool report) 
   return len < 0 ? 0 : static_cast<int>(cap);
 }
 
-// What lies before a sequence on a line where every sequence with cells takes its units and SET more: `units` of them, and
-// `seqs` such sequences.
+// What lies before a sequence on a line where every sequence with cells takes its units and SET more: `units` of them,
+// and `seqs` such sequences.
 struct Line {
   long long units;
   int seqs, longest;
@@ -231,7 +240,8 @@ __global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, Cfg<WK, WV, NT
   Line sum = {0, 0, 0}, before = {0, 0, 0};
   int own = 0;
   const bool few = a.n_seq <= 32;         // every warp looks at all sequences: no barriers
-  for (int s0 = 0; s0 < a.n_seq; s0 += C::THREADS) scan_lengths<NW>(a, s0, few, s_scan, blockIdx.x == 0, sum, before, own);
+  for (int s0 = 0; s0 < a.n_seq; s0 += C::THREADS)
+    scan_lengths<NW>(a, s0, few, s_scan, blockIdx.x == 0, sum, before, own);
   const int chunks = (a.group + NC - 1) / NC, grid = gridDim.x;
   const long long line1 = sum.units * chunks;             // (of one KV head)
   // Heads side by side: as many as the KV heads divide into, while the CTAs' shares stay LONG and whoever merges the
@@ -250,7 +260,8 @@ __global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, Cfg<WK, WV, NT
   const int pieces = items > 0 && items <= grid ? grid / static_cast<int>(items) : 0;   // per item
   // (a line costs a CTA the taking up of a second item, which the even pieces may then take longer)
   const int least = max(1, MIN_PIECE >> hs);              // units of a piece: one tile for each warp
-  const bool even = pieces > 0 && static_cast<long long>(max(least, (sum.longest + pieces - 1) / pieces) - SET) * grid <= total;
+  const bool even = pieces > 0 &&
+                    static_cast<long long>(max(least, (sum.longest + pieces - 1) / pieces) - SET) * grid <= total;
   const int n_work = static_cast<int>(even ? pieces * items : min(static_cast<long long>(grid), total));     // shares
   // piece o of the line: where it begins, and which one unit x belongs to
   auto start_of = [&](int o) { return quotient(o * total, n_work); };
@@ -259,20 +270,22 @@ __global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, Cfg<WK, WV, NT
   // ---- the warp's ring, and the lane's places in its rows
   const int head_of = warp & ((1 << hs) - 1), tile0 = warp >> hs, tiles_by = NW >> hs;
   const uint32_t ring = tc::smem_u32(smem) + warp * (C::STAGES * C::STAGE + C::PREP), prep = ring + C::STAGES * C::STAGE;
-  const uint32_t kc_at = k_chunk<WK>(lane / C::KCH, lane % C::KCH), vc_at = C::K_BYTES + v_chunk<WV>(lane / C::VCH, lane % C::VCH);
+  const uint32_t kc_at = k_chunk<WK>(lane / C::KCH, lane % C::KCH);
+  const uint32_t vc_at = C::K_BYTES + v_chunk<WV>(lane / C::VCH, lane % C::VCH);
   const uint32_t k_size = (lane % C::KCH) * 16 < a.dk ? 16 : 0, v_size = (lane % C::VCH) * 16 < a.dv ? 16 : 0;
   uint32_t k_at[C::KJ], k_word[C::KR + 1];      // reads: K row g, chunks t + 4 j; words t of the chunks left
 #pragma unroll
   for (int j = 0; j < C::KJ; ++j) k_at[j] = k_chunk<WK>(g, t + 4 * j);
 #pragma unroll
   for (int y = 0; y < C::KR; ++y) k_word[y] = k_chunk<WK>(g, 4 * C::KJ + y) + 4 * t;
-  uint32_t v_at[(MT + 1) / 2];                  // matrices of keys 0-7 / 8-15 and chunks 2 j, 2 j + 1 (an odd last one twice)
+  uint32_t v_at[(MT + 1) / 2];                  // matrices of keys 0-7 / 8-15, chunks 2 j, 2 j + 1 (an odd last one twice)
 #pragma unroll
   for (int j = 0; j < (MT + 1) / 2; ++j) v_at[j] = C::K_BYTES + v_chunk<WV>(lane & 15, min(2 * j + (lane >> 4), MT - 1));
   constexpr bool EVEN = pow2(WK) && pow2(WV);   // a copy's lanes take whole rows, the same chunks each time
   const int page_mask = (1 << a.page_shift) - 1;
   const bool apart = TILE / 2 >> a.page_shift > 1;        // half a tile lies in several pages
-  const uint8_t *k_base = a.k_codes + (k_size ? 16 * (lane % C::KCH) : 0), *v_base = a.v_codes + (v_size ? 16 * (lane % C::VCH) : 0);
+  const uint8_t *k_base = a.k_codes + (k_size ? 16 * (lane % C::KCH) : 0);
+  const uint8_t *v_base = a.v_codes + (v_size ? 16 * (lane % C::VCH) : 0);
   // (the last scale of a plane with an odd number of them is half a word)
   const uint32_t last_row = static_cast<uint32_t>(a.n_rows_cache - 1);
 
@@ -390,7 +403,8 @@ __global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, Cfg<WK, WV, NT
       cp4(st + C::SC + lane * 4, a.k_scales + (row & ~1u), n);
       cp4(st + C::SC + (TILE + lane) * 4, a.v_scales + (row & ~1u), n);
       if (odd_cells)
-        asm volatile("st.shared.u32 [%0], %1;" ::"r"(st + C::SC + (2 * TILE + lane) * 4), "r"(row & 1 ? 0x4432u : 0x4410u) : "memory");
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(st + C::SC + (2 * TILE + lane) * 4), "r"(row & 1 ? 0x4432u : 0x4410u)
+                     : "memory");
     };
     auto issue = [&](int tile, int page, uint32_t st) {
       const int key = k_begin + tile * TILE + (lane & (TILE - 1));
@@ -402,7 +416,7 @@ __global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, Cfg<WK, WV, NT
       const uint32_t row = ((static_cast<uint32_t>(page) << a.page_shift) + (key & page_mask)) * kv_heads + hv;
       const uint32_t there = __ballot_sync(0xffffffffu, ok);
       scales_in(ok ? row : 0, ok, st);
-      if (EVEN && there == 0xffffffffu && !apart) {                     // half a tile lies in one page, its rows at even distances
+      if (EVEN && there == 0xffffffffu && !apart) {             // half a tile in one page: its rows at even distances
         const uint32_t k_step = (32 / C::KCH) * kv_heads * a.dk, v_step = (32 / C::VCH) * kv_heads * a.dv;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -416,24 +430,25 @@ __global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, Cfg<WK, WV, NT
           for (int i = 0; i < NV; ++i)
             cp16(st + (vc_at ^ v_turn<WV>(h * NV + i)) + (h * NV + i) * 512, ahead(vs, v_step, i), v_size);
         }
-      } else {                            // rows apart, the last tile, or a page outside the cache: zeros for what is not there
+      } else {                            // rows apart, the last tile, a page outside the cache: zeros for what is not there
         if (in && !ok) set_status(a.status, TQ_ERR_DEVICE_CHECK);
         const uint32_t mine = ok ? row : 0;
 #pragma unroll
         for (int i = 0; i < TILE * C::KCH / 32; ++i) {
           const int k = (32 * i + lane) / C::KCH, c = (32 * i + lane) % C::KCH;
-          const uint32_t r = __shfl_sync(0xffffffffu, mine, k);
-          const uint32_t size = EVEN ? k_size : 16 * c < a.dk ? 16 : 0;
-          cp16(st + (EVEN ? kc_at + i * 512 : k_chunk<WK>(k, c)), (EVEN ? k_base : a.k_codes + (size ? 16 * c : 0)) + static_cast<uint64_t>(r) * a.dk,
-               there >> k & 1 ? size : 0);
+          const uint32_t size = EVEN ? k_size : 16 * c < a.dk ? 16 : 0, to = EVEN ? kc_at + i * 512 : k_chunk<WK>(k, c);
+          const uint8_t *from = (EVEN ? k_base : a.k_codes + (size ? 16 * c : 0));
+          from += static_cast<uint64_t>(__shfl_sync(0xffffffffu, mine, k)) * a.dk;
+          cp16(st + to, from, there >> k & 1 ? size : 0);
         }
 #pragma unroll
         for (int i = 0; i < TILE * C::VCH / 32; ++i) {
           const int k = (32 * i + lane) / C::VCH, c = (32 * i + lane) % C::VCH;
-          const uint32_t r = __shfl_sync(0xffffffffu, mine, k);
           const uint32_t size = EVEN ? v_size : 16 * c < a.dv ? 16 : 0;
-          cp16(st + (EVEN ? (vc_at ^ v_turn<WV>(i)) + i * 512 : C::K_BYTES + v_chunk<WV>(k, c)),
-               (EVEN ? v_base : a.v_codes + (size ? 16 * c : 0)) + static_cast<uint64_t>(r) * a.dv, there >> k & 1 ? size : 0);
+          const uint32_t to = EVEN ? (vc_at ^ v_turn<WV>(i)) + i * 512 : C::K_BYTES + v_chunk<WV>(k, c);
+          const uint8_t *from = (EVEN ? v_base : a.v_codes + (size ? 16 * c : 0));
+          from += static_cast<uint64_t>(__shfl_sync(0xffffffffu, mine, k)) * a.dv;
+          cp16(st + to, from, there >> k & 1 ? size : 0);
         }
       }
     };
@@ -597,7 +612,8 @@ __global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, Cfg<WK, WV, NT
         }
 #pragma unroll
         for (int j = 0; j < 2 * H; j += 2) {
-          const float2 u = add2(x[j], make_float2(sc[j].z, sc[j].z)), w = add2(x[j + 1], make_float2(sc[j + 1].z, sc[j + 1].z));
+          const float2 u = add2(x[j], make_float2(sc[j].z, sc[j].z));
+          const float2 w = add2(x[j + 1], make_float2(sc[j + 1].z, sc[j + 1].z));
           mt[0] = max3(mt[0], u.x, w.x);
           mt[1] = max3(mt[1], u.y, w.y);
         }
