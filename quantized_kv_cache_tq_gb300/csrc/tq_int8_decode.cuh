@@ -25,8 +25,8 @@
 //   and the wait for products kept memory idle, and the CTAs of a pair ended up to 50 us apart (40 ragged sequences: 218
 //   against 190 us).
 // - Widths are those of the powers of two, and 80, 96 and 192 (K), since copies and products of zeros cost as much as
-//   those of codes (40 ragged sequences, heads of 80 as 128 wide: 190 us, as 80 wide 159; 192 / 128 as 256 / 128: 284,
-//   192 / 128 wide 265).
+//   those of codes (40 ragged sequences, heads of 80 as 128 wide: 190 us, as 80 wide 157; 192 / 128 as 256 / 128: 284,
+//   192 / 128 wide 256).
 // - Scores: q is scaled by a power of two per column, so that its binary16 form is exact for binary16 and bfloat16
 //   inputs down to 2^-23 of the column's largest entry.
 // - The value weights p_t s^V_t are rounded to binary16: R is a running maximum of x_t + exponent(s^V_t), so the
@@ -87,7 +87,7 @@ struct Cfg {
   static constexpr int KJ = WK / 64, KR = KS - 4 * KJ;    // fours of K chunks, and the chunks left, a word a lane
   static constexpr int MP = MT <= 4 ? 4 : MT <= 8 ? 8 : 16;       // places of m tiles in merges
   static constexpr int KCH = WK / 16, VCH = WV / 16;      // 16-byte chunks of a row
-  static constexpr int NW = 8;
+  static constexpr int NW = 8;                            // (3 bits)
   static constexpr int THREADS = NW * 32;
   static constexpr int NC = 8 * NT;                       // columns
   // CTAs per SM: two where registers and rings leave room (decode of 40 ragged sequences, heads of 64: 116 -> 108 us)
@@ -725,23 +725,24 @@ __global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, Cfg<WK, WV, NT
     auto inverse = [](float ls) { return ls != 0.f ? 1.f / ls : 0.f; };
     const bool whole = n_con == 1;
     float *mine = a.part + static_cast<int64_t>(2 * piece + (even || share0 >= ia ? 0 : 1)) * C::HEADS * C::PART;
-    if (tid < heads * NC) {
-      const int h = tid / NC, col = tid - h * NC;
-      float M = -INFINITY, ls = 0.f;
-      float2 rl[NW];
+    if (tid < NW * NC) {                    // (head, column, warp of the head): the warp's weight, and the sums
+      const int x = tid & (tiles_by - 1), hcol = tid >> (3 - hs), h = hcol / NC, col = hcol - h * NC;
+      float2 *at = stat + (h + (x << hs)) * NC + col;
+      const float2 rl = *at;
+      float M = rl.x;
 #pragma unroll
-      for (int x = 0; x < NW; ++x) {
-        rl[x] = x < tiles_by ? stat[(h + (x << hs)) * NC + col] : make_float2(-INFINITY, 0.f);
-        M = fmaxf(M, rl[x].x);
-      }
+      for (int o = 1; o < NW; o <<= 1)
+        if (o < tiles_by) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+      const float f = rl.x == -INFINITY ? 0.f : exp2f(rl.x - M);
+      float ls = f * rl.y;
 #pragma unroll
-      for (int x = 0; x < NW; ++x) {
-        const float f = rl[x].x == -INFINITY ? 0.f : exp2f(rl[x].x - M);
-        ls += f * rl[x].y;
-        if (x < tiles_by) stat[(h + (x << hs)) * NC + col].x = f;           // the warp's weight
+      for (int o = 1; o < NW; o <<= 1)
+        if (o < tiles_by) ls += __shfl_xor_sync(0xffffffffu, ls, o);
+      at->x = f;
+      if (x == 0) {
+        s_inv[hcol] = inverse(ls);
+        if (!whole) reinterpret_cast<float2 *>(mine + h * C::PART)[col] = make_float2(M, ls);
       }
-      s_inv[tid] = inverse(ls);
-      if (!whole) reinterpret_cast<float2 *>(mine + h * C::PART)[col] = make_float2(M, ls);
     }
     __syncthreads();
     for (int v = tid; v < all_frag; v += C::THREADS) {
