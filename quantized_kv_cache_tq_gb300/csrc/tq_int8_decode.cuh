@@ -66,12 +66,14 @@ constexpr int MIN_PIECE = 2;          // units of a piece at least: one tile for
 // Units that one CTA has sooner done alone than shared and merged, two tiles for each of eight warps (one sequence of 300
 // cells 6.4 against 7.8 us, of 440 6.8 against 7.8, of 570 7.7 against 8.0, of 700 8.2 against 7.9)
 constexpr int ALONE = 8;
-constexpr int SET = 6;                // units' worth of work that an item costs besides its keys
+// Units' worth of work that an item costs besides its keys (256 sequences of 512 cells, and 40 ragged ones with heads of
+// 80 and 16 columns: 57.5 and 205 us with 4, 58.3 and 197 with 6, 59.6 and 193 with 8)
+constexpr int SET = 6;
 // Heads side by side, two choices.  A share of few units has little to gain, and more heads a CTA means fewer CTAs per
 // head's keys (a sequence of 700 cells over 16-cell pages 8.5 us with one head at a time, 9.2 with two).  And the CTA
 // that merges an item reads all its partial results (a sequence of 32768 cells 21.2 us with 19 of one head, 24.4 with 40
 // of two).
-constexpr int LONG = 8;               // units of a share at least
+constexpr int LONG = 8;               // units of a share at least (100 short sequences: 4 26.0, 8 21.8, 16 24.3 us)
 constexpr int MERGED = 72;            // partial results of a head, times heads, at most
 
 // Heads side by side whose partial results a CTA has room for in the workspace: 4 Ki values of fragments.
@@ -278,7 +280,7 @@ __global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, Cfg<WK, WV, NT
   for (int j = 0; j < C::KJ; ++j) k_at[j] = k_chunk<WK>(g, t + 4 * j);
 #pragma unroll
   for (int y = 0; y < C::KR; ++y) k_word[y] = k_chunk<WK>(g, 4 * C::KJ + y) + 4 * t;
-  uint32_t v_at[(MT + 1) / 2];                  // matrices of keys 0-7 / 8-15, chunks 2 j, 2 j + 1 (an odd last one twice)
+  uint32_t v_at[(MT + 1) / 2];                  // matrices of keys 0-7 / 8-15, chunks 2 j, 2 j + 1 (a last one twice)
 #pragma unroll
   for (int j = 0; j < (MT + 1) / 2; ++j) v_at[j] = C::K_BYTES + v_chunk<WV>(lane & 15, min(2 * j + (lane >> 4), MT - 1));
   constexpr bool EVEN = pow2(WK) && pow2(WV);   // a copy's lanes take whole rows, the same chunks each time
@@ -430,7 +432,7 @@ __global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, Cfg<WK, WV, NT
           for (int i = 0; i < NV; ++i)
             cp16(st + (vc_at ^ v_turn<WV>(h * NV + i)) + (h * NV + i) * 512, ahead(vs, v_step, i), v_size);
         }
-      } else {                            // rows apart, the last tile, a page outside the cache: zeros for what is not there
+      } else {                            // rows apart, the last tile, a page outside the cache: zeros for the missing
         if (in && !ok) set_status(a.status, TQ_ERR_DEVICE_CHECK);
         const uint32_t mine = ok ? row : 0;
 #pragma unroll
@@ -682,7 +684,8 @@ __global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, Cfg<WK, WV, NT
       }
     __syncthreads();                        // the ring is no longer read
     float4 *frag = reinterpret_cast<float4 *>(smem);
-    float2 *stat = reinterpret_cast<float2 *>(smem + NW * NT * C::MP * 512);      // [warp][column]: (R, l), then (weight, l)
+    // [warp][column]: (R, l), then (weight, l)
+    float2 *stat = reinterpret_cast<float2 *>(smem + NW * NT * C::MP * 512);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
