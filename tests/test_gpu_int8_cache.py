@@ -565,6 +565,18 @@ def test_decode_splits(n_seq, length):
     b.check(tq.int8_decode(b.gk, b.gv, b.gt, b.gl, q, 0.125, page_size=16), q, 0.125, "float16")
 
 
+@pytest.mark.parametrize("lens", [[511], [512], [513], [576, 0, 512], [577, 65], [64] * 31 + [640], [130] * 32,
+                                  [130] * 33, [0] * 32, [0] * 40, [0] * 33 + [1], [700] + [0] * 254 + [3],
+                                  [5] * 256 + [900]])
+def test_decode_at_the_edges_of_the_split(lens):
+    # sequences that one CTA takes alone or several share, batches laid out by a warp, a CTA or in turns
+    import quantized_kv_cache_tq_gb300 as tq
+    for d, page in ((64, 16), (128, 1)):
+        b = Batch(len(lens) + lens[0] + d, lens, 2, d, d, page)
+        q = b.query(4, "float16")
+        b.check(tq.int8_decode(b.gk, b.gv, b.gt, b.gl, q, d ** -0.5, page_size=page), q, d ** -0.5, "float16")
+
+
 @pytest.mark.parametrize("dk,dv,hkv,group,page,dtype", [(128, 128, 8, 4, 32, "bfloat16"), (64, 64, 4, 8, 16, "float16"),
                                                         (128, 128, 4, 12, 1, "float16"), (256, 256, 2, 3, 16, "bfloat16"),
                                                         (192, 128, 6, 2, 8, "float16"), (80, 80, 8, 1, 64, "bfloat16")])
