@@ -94,7 +94,7 @@ def attention(kc: Cache, vc: Cache, tables, lens, page_size, q, scale, weight_bi
     ones of Dk terms, error 2^-22 of the largest sum there could be (four roundings' worth: the order is the tensor
     cores'), which a weight takes as a relative error; the exponent's argument is rounded once more.  Weights carry
     ``weight_bits`` bits, rounded to nearest: 2^-bits relative, and in any case in steps of binary16's smallest number:
-    the largest weight p s^V is at least 1, so each of them is off by 2^-25 at most against it.  Sums of weights and
+    the largest weight p s^V is at least 2^12, so each of them is off by 2^-37 at most against it.  Sums of weights and
     values are fp32, and the tensor cores cut theirs: 2^-13 in all (below 2^11 roundings in a row here)."""
     n, heads, _ = q.shape
     group = heads // vc.n_kv_heads
@@ -114,6 +114,6 @@ def attention(kc: Cache, vc: Cache, tables, lens, page_size, q, scale, weight_bi
             mag = np.max(np.abs(q[s, h])) * np.max(np.abs(k), initial=0.0)
             err = abs(scale) * 2.0 ** -22 * mag * kc.head_dim + 2.0 ** -23 * (np.max(np.abs(x)) + 1) + 2.0 ** -13
             a = p @ np.abs(v)
-            low = length * 2.0 ** -25 * np.max(np.abs(v))
+            low = length * 2.0 ** -37 * np.max(np.abs(v))
             bound[s, h] = 2.0 ** -weight_bits * a + err * (a + np.abs(out[s, h])) + low
     return out, bound

@@ -29,10 +29,14 @@
 //   192 / 128 wide 256).
 // - Scores: q is scaled by a power of two per column, so that its binary16 form is exact for binary16 and bfloat16
 //   inputs down to 2^-23 of the column's largest entry.
-// - The value weights p_t s^V_t are rounded to binary16: R is a running maximum of x_t + exponent(s^V_t), so the
-//   largest weight lies in [1, 2^13] whatever the scales, and the sum of p_t stays in fp32.  R is raised only when it
-//   would grow by more than 2^12.  Binary16 outputs (FINE) take what that rounding left in a second product, since it
-//   would cost them nearly as much again as their own rounding.
+// - The value weights p_t s^V_t are rounded to binary16: R + TOP follows the maximum of x_t + exponent(s^V_t), so the
+//   largest weight lies in [2^12, 2^15] whatever the scales, and the sum of p_t stays in fp32.  R is raised only when it
+//   would grow by more than 2^RAISE.  Weights end at 2^-25, that is 2^-37 of the largest: were the largest 1, those of
+//   100000 keys 16 nats below it, one percent of the sum, would lose a third of themselves, and one nat further all.
+//   The small step of R costs nothing up to 8 columns, and 4% at 16 (40 ragged sequences of 128 query heads: 213 -> 221
+//   us against steps of 2^8 or 2^12).
+//   Binary16 outputs (FINE) take what that rounding left in a second product, since it would cost them nearly as much
+//   again as their own rounding.
 //
 // Split of the work.  A CTA's warps take one, two or four KV heads (1 << hs) of the same cells side by side, so that what
 // it reads of a cell lies together (40 ragged sequences 217 -> 190 us, single scattered cells 362 -> 262 us against one
@@ -59,8 +63,11 @@ namespace tq {
 namespace i8 {
 
 using p4::AttnArgs;
-using p4::RAISE;
 
+// Log2 of the weight of a key that sets the running maximum (its value scale's mantissa makes it up to twice as much),
+// and of the growth that raises the maximum.  Even numbers, so that both are exact next to scores of 2^24 as well, and
+// their sum 14: the largest weight is then 2^14 (2 - 2^-10), and twice that, the maximum being rounded, still finite.
+constexpr float TOP = 12.f, RAISE = 2.f;
 constexpr int UNIT = 64;              // keys per unit of work
 constexpr int MIN_PIECE = 2;          // units of a piece at least: one tile for each of eight warps
 // Units that one CTA has sooner done alone than shared and merged, two tiles for each of eight warps (one sequence of 300
@@ -504,7 +511,7 @@ __global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, Cfg<WK, WV, NT
     }
 
     float acc[NT][MT][4];
-    // of columns 2t, 2t + 1; Ru: R + RAISE; Rs: R, or 0 as long as there is none
+    // of columns 2t, 2t + 1; Ru: R + TOP + RAISE; Rs: R, or 0 as long as there is none
     float2 R[NT], Ru[NT], Rs[NT], l[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -625,8 +632,8 @@ __global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, Cfg<WK, WV, NT
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
             if (m > ru) {
-              const float f = exp2f(r - m);             // 0 at the first raise
-              r = rs = m;
+              const float low = m - TOP, f = exp2f(r - low);    // 0 at the first raise
+              r = rs = low;
               ru = m + RAISE;
               lo *= f;
 #pragma unroll
@@ -639,11 +646,12 @@ __global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, Cfg<WK, WV, NT
           lift(mt[0], R[n].x, Ru[n].x, Rs[n].x, l[n].x, 0);
           lift(mt[1], R[n].y, Ru[n].y, Rs[n].y, l[n].y, 1);
         }
+        float2 lt;                // the tile's own sum: next to a heavy key's p, l rounds 1 addend of 4
 #pragma unroll
         for (int j = 0; j < 2 * H; ++j) {
           const float2 d = sub2(x[j], Rs[n]);
           const float2 p = make_float2(tc::ex2(d.x), tc::ex2(d.y));
-          l[n] = add2(l[n], p);
+          lt = j == 0 ? p : add2(lt, p);
           const float2 wv = mul2(p, make_float2(sc[j].y, sc[j].y));
           const __half2 h = __floats2half2_rn(wv.x, wv.y);
           pb[n][j] = transpose8(*reinterpret_cast<const uint32_t *>(&h));
@@ -652,6 +660,7 @@ __global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, Cfg<WK, WV, NT
             pl[n][j] = transpose8(half2_bits(left.x, left.y));
           }
         }
+        l[n] = add2(l[n], lt);
       }
       // values: m tile c holds dims 16 c + 2 g (rows g) and + 1 (rows g + 8)
 #pragma unroll
