@@ -680,8 +680,7 @@ size_t tq_int8_decode_workspace(const tq_int8 *k, const tq_int8 *v, int n_q_head
  *             contiguous; 16-byte aligned, q_stride a multiple of 8
  * out         device, q_type [n_seq][n_q_heads][v->head_dim], 16-byte aligned
  * Widths, the head dims rounded up to 64, 128 or 256 (K, V): (64, 64), (128, 128), (256, 128), (256, 256).  Weights
- * s_t^V softmax_t of binary16 results are kept to 22 bits, of bfloat16 results to 11, small ones to 2^-37 of the
- * largest; values are exact and sums fp32.
+ * s_t^V softmax_t are kept to 22 bits, small ones to 2^-37 of the largest; values are exact and sums fp32.
  * Scores beyond 2^24 in magnitude: results are not defined.
  * Errors: TQ_ERR_INVALID_ARG, TQ_ERR_UNSUPPORTED (widths, q_type), TQ_ERR_WORKSPACE, TQ_ERR_CUDA. */
 tq_status tq_int8_decode(const tq_int8 *k, const tq_int8 *v, int page_size, const int32_t *block_table, int max_pages,

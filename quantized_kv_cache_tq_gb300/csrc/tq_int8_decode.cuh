@@ -35,8 +35,10 @@
 //   100000 keys 16 nats below it, one percent of the sum, would lose a third of themselves, and one nat further all.
 //   The small step of R costs nothing up to 8 columns, and 4% at 16 (40 ragged sequences of 128 query heads: 213 -> 221
 //   us against steps of 2^8 or 2^12).
-//   Binary16 outputs (FINE) take what that rounding left in a second product, since it would cost them nearly as much
-//   again as their own rounding.
+//   What that rounding left is a second product, so that a weight has 22 bits: 11 would cost binary16 results as much
+//   again as their own rounding, and make every twentieth bfloat16 result another number than the exact one rounded
+//   (now one in a thousand).  That takes nothing where memory is the bound, and 3 to 13% of short and 16-column calls
+//   (one sequence of 700 cells 7.9 -> 8.05 us, 64 of 1024 28.1 -> 29.3, 40 ragged ones of 128 query heads 221 -> 241).
 //
 // Split of the work.  A CTA's warps take one, two or four KV heads (1 << hs) of the same cells side by side, so that what
 // it reads of a cell lies together (40 ragged sequences 217 -> 190 us, single scattered cells 362 -> 262 us against one
@@ -90,7 +92,7 @@ constexpr int part_heads(int wv, int nt) { return 512 / (wv * nt) < 4 ? 512 / (w
 constexpr bool pow2(int w) { return (w & (w - 1)) == 0; }
 constexpr int pitch_of(int w) { return w == 96 ? 112 : w; }
 
-template <int WK, int WV, int NT, bool FINE>
+template <int WK, int WV, int NT>
 struct Cfg {
   static constexpr int KS = WK / 16, MT = WV / 16;        // k steps of the scores, m tiles of the values
   static constexpr int KJ = WK / 64, KR = KS - 4 * KJ;    // fours of K chunks, and the chunks left, a word a lane
@@ -228,10 +230,10 @@ __device__ __forceinline__ void scan_lengths(const AttnArgs &a, int s0, bool few
   at = {at.units + all.units, at.seqs + all.seqs, max(at.longest, all.longest)};
 }
 
-template <int WK, int WV, int NT, bool FINE>
-__global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, Cfg<WK, WV, NT, FINE>::CTAS)
+template <int WK, int WV, int NT>
+__global__ void __launch_bounds__(Cfg<WK, WV, NT>::THREADS, Cfg<WK, WV, NT>::CTAS)
     decode_kernel(const AttnArgs a) {
-  using C = Cfg<WK, WV, NT, FINE>;
+  using C = Cfg<WK, WV, NT>;
   using namespace p4::few;
   constexpr int NW = C::NW, MT = C::MT, NC = C::NC, TILE = C::TILE;
   extern __shared__ __align__(128) unsigned char smem[];
@@ -655,10 +657,8 @@ __global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, Cfg<WK, WV, NT
           const float2 wv = mul2(p, make_float2(sc[j].y, sc[j].y));
           const __half2 h = __floats2half2_rn(wv.x, wv.y);
           pb[n][j] = transpose8(*reinterpret_cast<const uint32_t *>(&h));
-          if (FINE) {
-            const float2 left = sub2(wv, __half22float2(h));
-            pl[n][j] = transpose8(half2_bits(left.x, left.y));
-          }
+          const float2 left = sub2(wv, __half22float2(h));
+          pl[n][j] = transpose8(half2_bits(left.x, left.y));
         }
         l[n] = add2(l[n], lt);
       }
@@ -676,7 +676,7 @@ __global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, Cfg<WK, WV, NT
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
               mma16816(acc[n][c + e], x0, x1, x2, x3, pb[n][2 * hf], pb[n][2 * hf + 1]);
-              if (FINE) mma16816(acc[n][c + e], x0, x1, x2, x3, pl[n][2 * hf], pl[n][2 * hf + 1]);
+              mma16816(acc[n][c + e], x0, x1, x2, x3, pl[n][2 * hf], pl[n][2 * hf + 1]);
             }
           }
         }
@@ -864,22 +864,21 @@ __global__ void __launch_bounds__(Cfg<WK, WV, NT, FINE>::THREADS, Cfg<WK, WV, NT
   }
 }
 
-template <int WK, int WV, int NT, bool FINE>
+template <int WK, int WV, int NT>
 cudaError_t launch_t(const AttnArgs &a, cudaStream_t s) {
-  using C = Cfg<WK, WV, NT, FINE>;
+  using C = Cfg<WK, WV, NT>;
   static_assert(C::SMEM <= 227 * 1024, "shared memory");
   static_assert(C::merge_bytes(C::grid(1 << 20)) <= C::SMEM && C::grid(152) == 152 * C::CTAS, "merge");
-  auto kern = decode_kernel<WK, WV, NT, FINE>;
+  auto kern = decode_kernel<WK, WV, NT>;
   cudaError_t e = set_dynamic_smem(reinterpret_cast<const void *>(kern), C::SMEM);
   if (e != cudaSuccess) return e;
   return p4::launch_beside(kern, C::grid(sm_count()), C::THREADS, C::SMEM, s, a);
 }
 
-// up to eight columns in one tile, else two tiles at a time; binary16 outputs keep the weights to 22 bits
+// up to eight columns in one tile, else two tiles at a time
 template <int WK, int WV>
 cudaError_t launch_w(const AttnArgs &a, cudaStream_t s) {
-  if (a.group <= 8) return a.bf16 ? launch_t<WK, WV, 1, false>(a, s) : launch_t<WK, WV, 1, true>(a, s);
-  return a.bf16 ? launch_t<WK, WV, 2, false>(a, s) : launch_t<WK, WV, 2, true>(a, s);
+  return a.group <= 8 ? launch_t<WK, WV, 1>(a, s) : launch_t<WK, WV, 2>(a, s);
 }
 
 }  // namespace i8

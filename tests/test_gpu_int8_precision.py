@@ -54,3 +54,28 @@ def test_decode_faint_keys_beside_a_heavy_one(dtype, nats, first):
     tol = HALF[dtype] * (np.abs(ref) + bound) + bound
     worst = (np.abs(out - ref) / tol).max()
     assert worst <= 1.0, f"{worst:.2f} times the tolerance, in the mean {(out / ref - 1).mean():+.1e}"
+
+
+@pytest.mark.parametrize("dk,dv,group", [(128, 128, 4), (64, 64, 8), (128, 128, 16), (256, 256, 2)])
+def test_decode_in_bfloat16_is_the_exact_result_rounded(dk, dv, group):
+    """A result off by e rounds to another number with probability 2 e / step, and a step of bfloat16 is at least 2^-8 of
+    the number.  fp32 arithmetic and weights of 22 bits leave e at 2^-20 or so: 2^-11 of the results, and a few times
+    that for results near zero.  Weights of 11 bits, 2^-13 in the mean and independent: 2^-4."""
+    import torch
+    import quantized_kv_cache_tq_gb300 as tq
+    rng = np.random.default_rng(dk + group)
+    lens, hkv = [700, 3000, 9000], 2
+    k, v = I.Cache(hkv, dk, sum(lens)), I.Cache(hkv, dv, sum(lens))
+    for c in (k, v):
+        c.set_rows(rng.standard_normal((sum(lens), hkv, c.head_dim)), np.arange(sum(lens)))
+    table = np.zeros((3, 9000), np.int32)
+    at = rng.permutation(sum(lens))
+    for s, n in enumerate(lens):
+        table[s, :n], at = at[:n], at[n:]
+    q = _gpu(rng.standard_normal((3, hkv * group, dk)), "bfloat16")
+    gk, gv = (tq.Int8Cache.from_planes(_gpu(c.rows), _gpu(c.scales)) for c in (k, v))
+    out = tq.int8_decode(gk, gv, _gpu(table), _gpu(np.array(lens, np.int32)), q)
+    ref, _ = I.attention(k, v, table, lens, 1, _np(q), dk ** -0.5, 22)
+    want = torch.from_numpy(ref).to(torch.bfloat16)
+    off = (out.cpu() != want).double().mean().item()
+    assert off <= 2.0 ** -8, f"{off:.2%} of the results"
