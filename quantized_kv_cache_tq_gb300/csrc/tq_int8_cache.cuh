@@ -48,7 +48,7 @@ struct StepArgs {
   int32_t layout;
   float gain;                 // factor on what turns
   float sign;                 // -1: the other way round
-  float eps;
+  float eps, eps_root;        // and its square root
   Units units;                // (set at the launch)
 };
 cudaError_t launch_step_rows(int type, const StepArgs &a, cudaStream_t s);

@@ -61,6 +61,7 @@ static void set_rope(StepArgs &a, const tq_rope *r, int inverse, float eps, cons
   a.gain = r->magnitude;
   a.sign = inverse ? -1.f : 1.f;
   a.eps = eps;
+  a.eps_root = eps > 0.f ? sqrtf(eps) : 0.f;
   a.positions = positions;
 }
 

@@ -62,6 +62,11 @@ __device__ __forceinline__ uint4 lds16(uint32_t at) {
   asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "r"(at) : "memory");
   return u;
 }
+__device__ __forceinline__ uint32_t lds4b(uint32_t at) {
+  uint32_t u;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(u) : "r"(at) : "memory");
+  return u;
+}
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
@@ -152,6 +157,45 @@ __device__ __forceinline__ void codes16(const float2 *x, float s, uint32_t *w) {
   for (int i = 0; i < 4; ++i)
     w[i] = prmt_b32(prmt_b32(__float_as_uint(c[2 * i].x), __float_as_uint(c[2 * i].y), 0x0040u),
                     prmt_b32(__float_as_uint(c[2 * i + 1].x), __float_as_uint(c[2 * i + 1].y), 0x0040u), 0x5410u);
+}
+
+// The mean of a row's squares, `lanes` lanes a row.
+__device__ __forceinline__ float mean_square(const float2 *x, int lanes, int d) {
+  float2 s2 = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s2 = fma2(x[i], x[i], s2);
+  float ss = s2.x + s2.y;
+  for (int o = 1; o < lanes; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+  return ss / static_cast<float>(d);
+}
+// A row's elements in shared memory times a power of two, which is returned: the row's largest number or `root` comes to
+// lie in [1, 4), one of them at least.  Rows that do not ask for it stay as they are.  `at`: the thread's first word of
+// `words` that lie `step` bytes apart.
+template <int TYPE>
+__device__ __forceinline__ float rescale(uint32_t at, int words, uint32_t step, int lanes, float root, bool asked) {
+  constexpr int E = TYPE == TQ_F32 ? 1 : 2;       // elements of 32 bits (16-bit ones: bfloat16)
+  float top = root;
+#pragma unroll 1
+  for (int i = 0; i < 4 * words; ++i) {
+    const uint32_t u = lds4b(at + (i >> 2) * step + (i & 3) * 4);
+    top = fmaxf(top, fabsf(__uint_as_float(E == 1 ? u : u & 0xffff0000u)));
+    if (E == 2) top = fmaxf(top, fabsf(__uint_as_float(u << 16)));
+  }
+  for (int o = 1; o < lanes; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const float by = asked ? __uint_as_float((254 - min(__float_as_uint(top) >> 23, 253u)) << 23) : 1.f;
+#pragma unroll 1
+  for (int i = 0; i < 4 * words; ++i) {
+    const uint32_t to = at + (i >> 2) * step + (i & 3) * 4, u = lds4b(to);
+    uint32_t v;
+    if (E == 1) {
+      v = __float_as_uint(__uint_as_float(u) * by);
+    } else {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(u << 16) * by, __uint_as_float(u & 0xffff0000u) * by);
+      v = *reinterpret_cast<const uint32_t *>(&h);
+    }
+    asm volatile("st.shared.b32 [%0], %1;" ::"r"(to), "r"(v) : "memory");
+  }
+  return by;
 }
 
 // a / b of numbers below 2^32, as nearly all are, in 32 bits
@@ -317,24 +361,33 @@ __global__ void __launch_bounds__(RT, ctas_of(ROT)) step_rows_kernel(const StepA
       fresh = false;
       ++head;
       cp_wait<S - 2>();
-      Raw<TYPE> r0, r1;
-#pragma unroll
-      for (int i = 0; i < W; ++i) {
-        r0.u[i] = lds16(stage + i * kWord);
-        r1.u[i] = lds16(stage + (W + i) * kWord);
-      }
-      stage = stage == ring_at + (S - 1) * kStage ? ring_at : stage + kStage;
-      fetch();
       float2 x[8];                      // elements 8 c0 .. and 8 c1 ..
-      unpack8<TYPE>(r0, x);
-      unpack8<TYPE>(r1, x + 4);
-      if (p.norm) {
-        float2 s2 = make_float2(0.f, 0.f);
+      auto read = [&](uint32_t at) {
+        Raw<TYPE> r0, r1;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s2 = fma2(x[i], x[i], s2);
-        float ss = s2.x + s2.y;
-        for (int o = 1; o < lanes; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        const float mean = ss / static_cast<float>(d) + a.eps, r = mean != 0.f ? rsqrtf(mean) : 0.f;
+        for (int i = 0; i < W; ++i) {
+          r0.u[i] = lds16(at + i * kWord);
+          r1.u[i] = lds16(at + (W + i) * kWord);
+        }
+        unpack8<TYPE>(r0, x);
+        unpack8<TYPE>(r1, x + 4);
+      };
+      read(stage);
+      stage = stage == ring_at + (S - 1) * kStage ? ring_at : stage + kStage;
+      fetch();                          // (not to where this unit's elements are)
+      if (p.norm) {
+        float mean = mean_square(x, lanes, d) + a.eps;
+        if (TYPE != TQ_F16) {           // (its squares lie in [2^-48, 2^32])
+          // Rows whose squares may leave fp32's range, once more as multiples of a power of two: the norm is the same.
+          const bool far = !(mean >= 0x1p-80f && mean <= 0x1p80f);
+          if (__any_sync(0xffffffffu, far)) {
+            const uint32_t here_at = stage == ring_at ? ring_at + (S - 1) * kStage : stage - kStage;
+            const float root = a.eps_root * rescale<TYPE>(here_at, 2 * W, kWord, lanes, a.eps_root, far);
+            read(here_at);
+            mean = mean_square(x, lanes, d) + (far ? root * root : a.eps);
+          }
+        }
+        const float r = mean != 0.f ? rsqrtf(mean) : 0.f;
 #pragma unroll
         for (int k = 0; k < 2; ++k)
           if (k < n_in) {
@@ -342,8 +395,8 @@ __global__ void __launch_bounds__(RT, ctas_of(ROT)) step_rows_kernel(const StepA
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               const float4 n = __ldg(n4 + i);
-              x[4 * k + 2 * i] = mul2(x[4 * k + 2 * i], mul2(make_float2(n.x, n.y), make_float2(r, r)));
-              x[4 * k + 2 * i + 1] = mul2(x[4 * k + 2 * i + 1], mul2(make_float2(n.z, n.w), make_float2(r, r)));
+              x[4 * k + 2 * i] = mul2(mul2(x[4 * k + 2 * i], make_float2(r, r)), make_float2(n.x, n.y));
+              x[4 * k + 2 * i + 1] = mul2(mul2(x[4 * k + 2 * i + 1], make_float2(r, r)), make_float2(n.z, n.w));
             }
           }
       }

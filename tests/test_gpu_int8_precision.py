@@ -1,11 +1,10 @@
 """How many bits the int8 cache's calls and rotations keep: inputs on which one
 rounding too many, or a number that runs out of range, shows in the result."""
-import math
-
 import numpy as np
 import pytest
 
 from oracle import int8 as I
+from tests.test_gpu_int8_cache import _check_turned
 
 pytestmark = pytest.mark.gpu
 
@@ -79,3 +78,47 @@ def test_decode_in_bfloat16_is_the_exact_result_rounded(dk, dv, group):
     want = torch.from_numpy(ref).to(torch.bfloat16)
     off = (out.cpu() != want).double().mean().item()
     assert off <= 2.0 ** -8, f"{off:.2%} of the results"
+
+
+@pytest.mark.parametrize("layout,d,rot", [("half", 128, 128), ("half", 80, 20), ("interleaved", 96, 48)])
+@pytest.mark.parametrize("dtype,gain,eps", [("float32", 1e30, 1e-6), ("float32", 1e19, 0.0), ("float32", 1e-19, 0.0),
+                                            ("float32", 1e-30, 0.0), ("float32", 1e-41, 0.0), ("float32", 1e-25, 1e-44),
+                                            ("float32", 1e-7, 1e30), ("bfloat16", 1e30, 1e-6), ("bfloat16", 1e-30, 0.0),
+                                            ("float16", 5e3, 1e-6), ("float16", 6e-7, 0.0)])
+def test_norm_of_rows_whose_squares_leave_the_range(layout, d, rot, dtype, gain, eps):
+    # every other row as it mostly is, so that both kinds meet in a warp; tolerances as for those
+    import torch
+    import quantized_kv_cache_tq_gb300 as tq
+    rng = np.random.default_rng(d)
+    n, h, eps = 41, 3, float(np.float32(eps))
+    rows = rng.standard_normal((n, h, d))
+    rows[1::2] *= gain
+    x, pos = _gpu(rows.astype(np.float32), dtype), rng.integers(0, 9000, n).astype(np.int32)
+    w = 1 + rng.random(d).astype(np.float32)
+    rope, gp, gw = tq.Rope(rot, layout=layout), _gpu(pos), _gpu(w)
+    y = tq.rope_rows(rope, gp, x, q_norm=gw, eps=eps)
+    _check_turned(y, _np(x), pos, rope, dtype, w, eps)
+    assert torch.equal(tq.rope_rows(rope, gp[::2].contiguous(), x[::2].contiguous(), q_norm=gw, eps=eps), y[::2])
+    # and quantised: scales and codes of the exact rows, but next to a border between two of them
+    k, v = tq.Int8Cache(h, d, n), tq.Int8Cache(h, d, n)
+    tq.int8_rope_set_rows(k, v, rope, gp, None, x, x, torch.arange(n, device="cuda"), k_norm=gw, eps=eps)
+    want = I.turned(_np(x), pos, rope.frequencies, layout, 1.0, w, eps)
+    step = np.abs(want).max(-1, keepdims=True) / 127
+    scale, code = _np(k.scales)[..., None], k.rows.cpu().numpy().astype(np.float64)
+    assert np.all(np.abs(scale - step) <= 2.0 ** -11 * step * (1 + 2.0 ** -9) + 2.0 ** -25)
+    exact = np.clip(np.divide(want, scale, where=scale > 0, out=np.zeros_like(want)), -127, 127)
+    assert np.all(np.abs(code - exact) <= 0.5 + 127 * 2.0 ** -18)
+
+
+def test_norm_of_rows_that_are_not_finite_or_zero():
+    import torch
+    import quantized_kv_cache_tq_gb300 as tq
+    x = torch.ones((4, 2, 64), device="cuda")
+    x[0, 0, 3], x[1, 1, 5], x[2] = float("inf"), float("nan"), 0.0
+    y = tq.rope_rows(tq.Rope(64), torch.zeros(4, dtype=torch.int32, device="cuda"), x,
+                     q_norm=torch.ones(64, device="cuda"), eps=0.0)
+    assert bool(y[0, 0, 3].isnan()) and not y[0, 0, :3].any() and bool(y[1, 1].isnan().all()) and not y[2].any()
+    # (position 0 turns nothing; one root's 2^-22 and two products)
+    one = y.new_ones(64) * 1.0
+    for row in (y[0, 1], y[1, 0], y[3, 0], y[3, 1]):
+        assert bool(((row - one).abs() <= 2.0 ** -21).all())
