@@ -122,3 +122,25 @@ def test_norm_of_rows_that_are_not_finite_or_zero():
     one = y.new_ones(64) * 1.0
     for row in (y[0, 1], y[1, 0], y[3, 0], y[3, 1]):
         assert bool(((row - one).abs() <= 2.0 ** -21).all())
+
+
+@pytest.mark.parametrize("layout,d,rot", [("half", 128, 128), ("interleaved", 128, 128), ("half", 80, 20)])
+@pytest.mark.parametrize("magnitude", [1.0, 1.2079441547393799])
+@pytest.mark.parametrize("inverse", [False, True])
+def test_rotations_in_fp32_round_as_little_as_they_can(layout, d, rot, magnitude, inverse):
+    """Of N(0, 1) rows at all angles: a result is rounded once and one of its two products once; sine and cosine, each
+    rounded once, count as much again as a result.  A rounding of numbers spread evenly over the logarithm is 2.53e-8
+    rms (2^-23 / 12^0.5, times the rms of 1 / mantissa, 0.7355), of numbers just above a power of two 3.44e-8:
+    2.53e-8 (1 + 1/2 + 1)^0.5 = 4.0e-8, and with sine and cosine reaching into [1, 1.21) 4.63e-8 at most."""
+    import torch
+    import quantized_kv_cache_tq_gb300 as tq
+    rng = np.random.default_rng(rot)
+    n, h = 3000 * 128 // rot, 4
+    rope = tq.Rope(rot, frequencies=rng.uniform(0.1, 3.0, rot // 2), layout=layout, magnitude=magnitude)
+    x, pos = rng.standard_normal((n, h, d)).astype(np.float32), rng.integers(0, 1 << 20, n).astype(np.int32)
+    out = _np(tq.rope_rows(rope, _gpu(pos), _gpu(x), inverse=inverse))
+    ref = I.turned(x, pos, rope.frequencies, layout, float(np.float32(magnitude)), inverse=inverse)
+    first = np.arange(rot // 2) if layout == "half" else np.arange(0, rot, 2)
+    for at in (first, first + (rot // 2 if layout == "half" else 1)):
+        e = np.sqrt(((out - ref)[..., at] ** 2).mean() / (ref[..., at] ** 2).mean())
+        assert e <= (4.0e-8 if magnitude == 1.0 else 4.63e-8), f"{e:.3e}"
