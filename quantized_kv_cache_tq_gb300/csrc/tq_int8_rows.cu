@@ -13,7 +13,7 @@
 //   or 16 bytes and neighbouring lanes share sectors.  Which two eights: in the half layout those that turn together, so
 //   that no element looks for its partner in another lane (half_any, where half of rot_dim is no multiple of 8: by way of
 //   shared memory, 80-wide heads, 20 of them turned, 182 -> 75 us).  32-bit rows that nothing turns: four fours, since an
-//   eight is two halves of a sector there (20001 rows in 47 -> 37.5 us, out 50 -> 39.8).
+//   eight is two halves of a sector there (20001 rows in 47 -> 37.5 us, out 50 -> 39.8, now 36.7).
 // - The angle is an integer product: the position times the pair's 64-bit fraction of
 //   a turn, of which the upper 32 bits below the whole turns are kept.  Sine and cosine
 //   are then polynomials on an eighth of a turn either way (turn_sincos), eight per
@@ -37,8 +37,10 @@ constexpr int kStages = 3;          // units of a thread's ring
 // CTAs per SM: what the registers allow.  Rotations run best with 95 of them: six CTAs instead of five (rope of 20001
 // rows 71 instead of 65 us) leave the loads of positions and angles one after the other, four (67 us) too few of them
 // on their way.  More stages than three read no faster and hinder the writes (71 us with four).
-constexpr int kGet = 16;
 constexpr int ctas_of(int rot) { return rot == 0 ? 8 : rot == 3 ? 4 : 5; }
+// Rows out: 16 CTAs of 32 registers a thread; of fp32 rows ten, which spill nothing (20001 rows 36.7 us; sixteen spilled
+// and took 39.8, twelve 39.0).
+constexpr int get_ctas(int type) { return type == TQ_F32 ? 10 : 16; }
 constexpr float kTop = 127.f * 65504.f;
 
 enum Rot { kNone = 0, kHalf = 1, kInterleaved = 2, kHalfAny = 3 };
@@ -500,7 +502,7 @@ struct GetArgs {
 };
 
 template <int TYPE>
-__global__ void __launch_bounds__(RT, kGet) get_rows_kernel(const GetArgs args) {
+__global__ void __launch_bounds__(RT, get_ctas(TYPE)) get_rows_kernel(const GetArgs args) {
   const p4::RowsArgs &a = args.rows;
   after_earlier_launches();
   for (Share u = share_of(args.units); u.at < u.end;) {
@@ -620,7 +622,7 @@ cudaError_t launch_step_rows(int type, const StepArgs &args, cudaStream_t s) {
 cudaError_t launch_get_rows(int type, const p4::RowsArgs &a, cudaStream_t s) {
   GetArgs g;
   g.rows = a;
-  const unsigned grid = cut(g.units, a.n_heads, a.head_dim, 2, a.n_rows, kGet * sm_count());
+  const unsigned grid = cut(g.units, a.n_heads, a.head_dim, 2, a.n_rows, get_ctas(type) * sm_count());
   return type == TQ_F32   ? p4::launch_beside(get_rows_kernel<TQ_F32>, grid, RT, 0, s, g)
          : type == TQ_F16 ? p4::launch_beside(get_rows_kernel<TQ_F16>, grid, RT, 0, s, g)
                           : p4::launch_beside(get_rows_kernel<TQ_BF16>, grid, RT, 0, s, g);
