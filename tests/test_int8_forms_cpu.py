@@ -22,3 +22,12 @@ def test_polynomials_of_sine_and_cosine():
     assert len(numbers(sine)) == 3 and len(numbers(cosine)) == 4
     assert np.abs((t + t * u * s) / np.sin(t) - 1).max() <= float(stated.group(1)) <= 1e-8
     assert np.abs(1 + u * c - np.cos(t)).max() <= float(stated.group(2)) <= 1e-8
+
+
+def test_codes_and_scales_by_hand():
+    # 0.635 / binary16(0.01) = 63.49; -127 by 1.27 / binary16(0.01) = 126.97; ties go to the even code
+    c, s = I.quantise(np.array([[-1.27, 0.635, 0.0, 0.01, 1.27, -0.004], [31.75, 0.125, 0.375, 0.625, -0.125, -0.375]]))
+    assert s.dtype == np.float16 and c.dtype == np.int8
+    assert list(s) == [np.float16(0.01), np.float16(0.25)]
+    assert list(c[0]) == [-127, 63, 0, 1, 127, 0]
+    assert list(c[1]) == [127, 0, 2, 2, 0, -2]
