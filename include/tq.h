@@ -604,10 +604,12 @@ typedef struct tq_head_rows {
 
 /* Rotary positions of query and key rows, one launch.  For every row with a position p >= 0 and every head x:
  *   y = x                                             without norm_weight,
- *   y_i = norm_weight_i x_i / sqrt(mean(x^2) + eps)   with it (the mean over the head; a head of zeros stays one);
+ *   y_i = norm_weight_i x_i / sqrt(mean(x^2) + eps)   with it (the mean over the head, of whatever magnitude its
+ *                                                     elements are; a head of zeros stays one);
  *   pair (a, b) of y turns by t_j = p f_j:  a' = g (a cos t_j - b sin t_j),  b' = g (a sin t_j + b cos t_j)
  * with g = rope->magnitude; elements from rot_dim on are y.  fp32, rounded once to `type`.  inverse: by -t_j --
- * the gradient of the rotation, given that of its result, and for g = 1 the way back (norms are refused there).
+ * the gradient of the rotation, given that of its result, and for g = 1 the way back.  Norms are refused there: the
+ * gradient of a normed rotation is this call's result taken on through the norm by the caller.
  * q, k      either may be NULL
  * head_dim  multiple of 8, 8 .. 256, at least rope->rot_dim
  * type      TQ_F32, TQ_F16 or TQ_BF16, of both tensors
@@ -623,7 +625,7 @@ tq_status tq_rope_rows(const tq_rope *rope, const tq_head_rows *q, const tq_head
  *   rows   int8     [n_cells][n_kv_heads][head_dim]
  *   scales binary16 [n_cells][n_kv_heads]
  * head_dim: multiple of 16, 16 .. 256; n_cells * n_kv_heads below 2^32; planes 16-byte aligned.  A row stands for
- * scale * code. */
+ * scale * code.  (K and V of any two head_dims are written and read back; tq_int8_decode takes those that it lists.) */
 typedef struct tq_int8 {
   int32_t n_kv_heads;
   int32_t head_dim;
@@ -680,7 +682,8 @@ size_t tq_int8_decode_workspace(const tq_int8 *k, const tq_int8 *v, int n_q_head
  *             contiguous; 16-byte aligned, q_stride a multiple of 8
  * out         device, q_type [n_seq][n_q_heads][v->head_dim], 16-byte aligned
  * Widths, the head dims rounded up to 64, 128 or 256 (K, V): (64, 64), (128, 128), (256, 128), (256, 256).  Weights
- * s_t^V softmax_t are kept to 22 bits, small ones to 2^-37 of the largest; values are exact and sums fp32.
+ * s_t^V softmax_t are kept to 22 bits, small ones to 2^-37 of the largest; values are exact and sums fp32 (of the values,
+ * cut where it ends instead of rounded).
  * Scores beyond 2^24 in magnitude: results are not defined.
  * Errors: TQ_ERR_INVALID_ARG, TQ_ERR_UNSUPPORTED (widths, q_type), TQ_ERR_WORKSPACE, TQ_ERR_CUDA. */
 tq_status tq_int8_decode(const tq_int8 *k, const tq_int8 *v, int page_size, const int32_t *block_table, int max_pages,

@@ -588,7 +588,8 @@ def rope_rows(rope: Rope, positions, q, k=None, q_norm=None, k_norm=None, eps: f
               q_out=None, k_out=None, dev_status=None, stream=None):
     """Rotary positions (device int32 [n]) of rows q [n][n_q_heads][head_dim] and, if given, k, each head RMS-normed
     before where q_norm / k_norm (float32 [head_dim]) are given.  Rows may be strided, and q_out may be q (in place).
-    Rows whose position is -1 stay as they were (new outputs: zeros).  ``inverse`` turns the other way: the gradient.
+    Rows whose position is -1 stay as they were (new outputs: zeros).  ``inverse`` turns the other way: the gradient of
+    the rotation alone (refused with a norm).  Results carry no autograd graph, whatever q and k require.
     -> q_out, or (q_out, k_out) with k."""
     code, shape = _row_type(q, "q"), q.shape
     if len(shape) != 3:

@@ -4,9 +4,9 @@
 //
 // Columns are the query heads of a KV head, eight per tensor-core tile.  The work is reading the cache once, so
 // everything is arranged around the loads.  Batches of long sequences are bound by HBM (40 ragged sequences of up to
-// 32768 cells, 8 KV heads of 128, bf16: 190 us, 6.5 TB/s, 96% of a copy's rate; heads of 256 363 us, 99%; single
-// scattered cells 6 x 140000 254 us, 88%), short calls by the chain from the lengths to the merge (700 cells 7.9 us, 300
-// cells 6.4 us).
+// 32768 cells, 8 KV heads of 128: 188 to 197 us, 6.3 to 6.5 TB/s, 92 to 97% of a copy's rate; heads of 256 357 to 371
+// us, 97% and more; single scattered cells 6 x 140000 260 us, 86%), short calls by the chain from the lengths to the
+// merge (700 cells 8.1 us, 300 cells 6.6 us).
 //
 // - A warp streams its own tiles of 32 keys (16 where rows are wide) through a private ring of cp.async stages: it waits
 //   for its own copies only, and no CTA barrier stands in the loop.  Each lane looks up one key's cell, so that pages of
@@ -25,24 +25,26 @@
 //   and the wait for products kept memory idle, and the CTAs of a pair ended up to 50 us apart (40 ragged sequences: 218
 //   against 190 us).
 // - Widths are those of the powers of two, and 80, 96 and 192 (K), since copies and products of zeros cost as much as
-//   those of codes (40 ragged sequences, heads of 80 as 128 wide: 190 us, as 80 wide 157; 192 / 128 as 256 / 128: 284,
-//   192 / 128 wide 256).
+//   those of codes (40 ragged sequences, heads of 80 as 128 wide: 190 us, as 80 wide 158; 192 / 128 as 256 / 128: 284,
+//   192 / 128 wide 263).
 // - Scores: q is scaled by a power of two per column, so that its binary16 form is exact for binary16 and bfloat16
 //   inputs down to 2^-23 of the column's largest entry.
 // - The value weights p_t s^V_t are rounded to binary16: R + TOP follows the maximum of x_t + exponent(s^V_t), so the
 //   largest weight lies in [2^12, 2^15] whatever the scales, and the sum of p_t stays in fp32.  R is raised only when it
 //   would grow by more than 2^RAISE.  Weights end at 2^-25, that is 2^-37 of the largest: were the largest 1, those of
 //   100000 keys 16 nats below it, one percent of the sum, would lose a third of themselves, and one nat further all.
-//   The small step of R costs nothing up to 8 columns, and 4% at 16 (40 ragged sequences of 128 query heads: 213 -> 221
-//   us against steps of 2^8 or 2^12).
+//   The small step of R costs nothing up to 8 columns, and 4% at 16 (40 ragged sequences of 128 query heads: 221 us, with
+//   steps of 2^12 213, of 2^4 218, both before the second product).
 //   What that rounding left is a second product, so that a weight has 22 bits: 11 would cost binary16 results as much
 //   again as their own rounding, and make every twentieth bfloat16 result another number than the exact one rounded
-//   (now one in a thousand).  That takes nothing where memory is the bound, and 3 to 13% of short and 16-column calls
-//   (one sequence of 700 cells 7.9 -> 8.05 us, 64 of 1024 28.1 -> 29.3, 40 ragged ones of 128 query heads 221 -> 241).
+//   (now a few in a thousand).  That takes nothing where memory is the bound, and 2 to 13% of short and 16-column calls
+//   (one sequence of 700 cells 7.9 -> 8.1 us, 64 of 1024 28.1 -> 29.4, 40 ragged ones of 128 query heads 221 -> 241).
+// - Sums are fp32, but the matrix pipe cuts its own instead of rounding them: a warp that adds up 50000 keys one way gets
+//   3e-4 too little, next to a heavy key 6e-4.  Its share of a long sequence is mostly a few thousand.
 //
 // Split of the work.  A CTA's warps take one, two or four KV heads (1 << hs) of the same cells side by side, so that what
-// it reads of a cell lies together (40 ragged sequences 217 -> 190 us, single scattered cells 362 -> 262 us against one
-// head at a time); the warps left take every so many-th tile.  An item is a (sequence, group of heads, column chunk), its
+// it reads of a cell lies together (40 ragged sequences 241 us with one head at a time, 196 so; single scattered cells 362
+// and 262); the warps left take every so many-th tile.  An item is a (sequence, group of heads, column chunk), its
 // keys come in units of 64.  Nothing about lengths is needed on the host: every CTA works its share out from the device's
 // lengths.
 // - Few items of like length: each is cut into as many pieces as there are CTAs per item, and a CTA has one piece.
@@ -51,7 +53,7 @@
 // An item that several CTAs share leaves partial results (R, sum, values) in the workspace, a CTA's first and last item
 // at most, and the last CTA to arrive merges them in the order of the CTAs, so that a repeated call gives the same bits.
 // An item costs some 5 us besides its keys, mostly instructions one after the other; sending off the next item's first
-// copies before the merge does not shorten that (256 sequences of 512 cells: 64 against 60 us).
+// copies before the merge does not shorten that (256 sequences of 512 cells, then 60 us: 64).
 #pragma once
 
 #include <math.h>
@@ -71,18 +73,22 @@ using p4::AttnArgs;
 // their sum 14: the largest weight is then 2^14 (2 - 2^-10), and twice that, the maximum being rounded, still finite.
 constexpr float TOP = 12.f, RAISE = 2.f;
 constexpr int UNIT = 64;              // keys per unit of work
-constexpr int MIN_PIECE = 2;          // units of a piece at least: one tile for each of eight warps
+// Units of a piece at least.  Two are one tile of wide rows for each of eight warps, and of 32-key tiles only four: half of
+// the warps have none then.  Four units leave none without, and are slower up to 1500 cells (one sequence of 570 cells 8.0
+// us with two, 8.7 with four; of 700 8.2 and 8.9; of 1500 8.2 and 8.3; of 4096 9.1 and 8.8; 256-wide of 700 9.8 and 11.8):
+// a warp's tiles come one after the other, and half as many CTAs ask for them.
+constexpr int MIN_PIECE = 2;
 // Units that one CTA has sooner done alone than shared and merged, two tiles for each of eight warps (one sequence of 300
-// cells 6.4 against 7.8 us, of 440 6.8 against 7.8, of 570 7.7 against 8.0, of 700 8.2 against 7.9)
+// cells 6.6 against 7.8 us, of 440 7.1 against 7.9; of more units, shared: of 570 8.1)
 constexpr int ALONE = 8;
 // Units' worth of work that an item costs besides its keys (256 sequences of 512 cells, and 40 ragged ones with heads of
-// 80 and 16 columns: 57.5 and 205 us with 4, 58.3 and 197 with 6, 59.6 and 193 with 8)
+// 80 and 16 columns: 60.4 and 221 us with 4, 61.1 and 209 with 6, 62.3 and 206 with 8)
 constexpr int SET = 6;
 // Heads side by side, two choices.  A share of few units has little to gain, and more heads a CTA means fewer CTAs per
 // head's keys (a sequence of 700 cells over 16-cell pages 8.5 us with one head at a time, 9.2 with two).  And the CTA
 // that merges an item reads all its partial results (a sequence of 32768 cells 21.2 us with 19 of one head, 24.4 with 40
 // of two).
-constexpr int LONG = 8;               // units of a share at least (100 short sequences: 4 26.0, 8 21.8, 16 24.3 us)
+constexpr int LONG = 8;               // units of a share at least (100 short sequences: 4 26.5, 8 21.9, 16 24.5 us)
 constexpr int MERGED = 72;            // partial results of a head, times heads, at most
 
 // Heads side by side whose partial results a CTA has room for in the workspace: 4 Ki values of fragments.
@@ -270,7 +276,7 @@ __global__ void __launch_bounds__(Cfg<WK, WV, NT>::THREADS, Cfg<WK, WV, NT>::CTA
   const long long total = sum.units * per_seq, items = static_cast<long long>(sum.seqs) * per_seq;
   const int pieces = items > 0 && items <= grid ? grid / static_cast<int>(items) : 0;   // per item
   // (a line costs a CTA the taking up of a second item, which the even pieces may then take longer)
-  const int least = max(1, MIN_PIECE >> hs);              // units of a piece: one tile for each warp
+  const int least = max(1, MIN_PIECE >> hs);              // units of a piece
   const bool even = pieces > 0 &&
                     static_cast<long long>(max(least, (sum.longest + pieces - 1) / pieces) - SET) * grid <= total;
   const int n_work = static_cast<int>(even ? pieces * items : min(static_cast<long long>(grid), total));     // shares

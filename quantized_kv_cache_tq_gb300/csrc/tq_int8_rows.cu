@@ -7,12 +7,12 @@
 //
 // 2 to 8 bytes an element are read or written and some 10 operations done: memory is what bounds long calls, latency
 // short ones.  20001 rows of 32 + 8 heads of 128, 16-bit, rotated: 65 us, 6.3 TB/s (92% of a copy's rate), normed first
-// 70; 16001 rows of which K and V go into the cache 63 us (84%; normed 81, held by its instructions: 59% of the issue
-// slots are busy without the norm); 20001 rows of 8 heads into the cache 22.4 and out of it 22.8 (80%).  48 rows 2.4 us.
+// 71; 16001 rows of which K and V go into the cache 64 us (83%; normed 84, held by its instructions: 58% of the issue
+// slots are busy without the norm); 20001 rows of 8 heads into the cache 22.5 and out of it 22.8 (80%).  48 rows 2.4 us.
 // - A lane holds twice 8 elements of a row, 4, 8 or 16 lanes a row (widths 64, 128, 256), so that every access is of 8
 //   or 16 bytes and neighbouring lanes share sectors.  Which two eights: in the half layout those that turn together, so
 //   that no element looks for its partner in another lane (half_any, where half of rot_dim is no multiple of 8: by way of
-//   shared memory, 80-wide heads, 20 of them turned, 182 -> 75 us).  32-bit rows that nothing turns: four fours, since an
+//   shared memory, 80-wide heads, 20 of them turned, 182 -> 73 us).  32-bit rows that nothing turns: four fours, since an
 //   eight is two halves of a sector there (20001 rows in 47 -> 37.5 us, out 50 -> 39.8, now 36.7).
 // - The angle is an integer product: the position times the pair's 64-bit fraction of
 //   a turn, of which the upper 32 bits below the whole turns are kept.  Sine and cosine
