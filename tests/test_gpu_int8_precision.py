@@ -144,3 +144,32 @@ def test_rotations_in_fp32_round_as_little_as_they_can(layout, d, rot, magnitude
     for at in (first, first + (rot // 2 if layout == "half" else 1)):
         e = np.sqrt(((out - ref)[..., at] ** 2).mean() / (ref[..., at] ** 2).mean())
         assert e <= (4.0e-8 if magnitude == 1.0 else 4.63e-8), f"{e:.3e}"
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
+@pytest.mark.parametrize("v_scale", [0x3fff, 0x43ff, 0x03ff, 0x7bff])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_decode_scores_at_the_end_of_the_range(dtype, v_scale, sign):
+    """Scores next to 2^24, growing from key to key by what fp32 resolves there, value scales just below a power of two:
+    weights stay finite.  All keys have the same values, so that whatever the weights are, these are the result: weights
+    of 22 bits, sums over 40 tiles of a warp at most."""
+    import torch
+    import quantized_kv_cache_tq_gb300 as tq
+    n, h, d = 3000, 2, 64
+    rng = np.random.default_rng(3)
+    k, v = I.Cache(h, d, n), I.Cache(h, d, n)
+    k.rows[:, :, 0], k.rows[:, :, 1], k.scales[:] = 127, (np.arange(n) * 127 // n)[:, None], 1.0
+    v.rows[:] = rng.integers(-126, 127, (1, h, d))
+    v.rows[:, :, 0] = 127
+    v.scales[:] = np.uint16(v_scale).view(np.float16)
+    q = torch.zeros((1, 4, d), dtype=getattr(torch, dtype), device="cuda")
+    q[..., 0], q[..., 1] = sign, 3e-5
+    gk, gv = (tq.Int8Cache.from_planes(_gpu(c.rows), _gpu(c.scales)) for c in (k, v))
+    out = tq.int8_decode(gk, gv, torch.arange(n, dtype=torch.int32, device="cuda")[None],
+                         torch.tensor([n], dtype=torch.int32, device="cuda"), q, (2.0 ** 24 - 2.0 ** 14) / 127)
+    want = I.values(v.rows[0], v.scales[0]).repeat(2, 0)[None]
+    over = np.abs(want) >= 65520 if dtype == "float16" else np.zeros_like(want, bool)
+    got = _np(out)
+    # (a binary16 result has steps of 2^-24 at least)
+    tol = (HALF[dtype] + 2.0 ** -13) * np.abs(want) + (2.0 ** -25 if dtype == "float16" else 0.0)
+    assert np.all(np.isfinite(got) | over) and np.all((np.abs(got - want) <= tol) | over)
